@@ -35,7 +35,8 @@ EXPORTS = ("gdn_prefill_chunked", "gdn_decode_step", "gdn_verify_block",
            "gdn_input_prologue", "gdn_gated_rmsnorm", "gdn_verify_block_capture",
            "gdn_state_rollback", "gdn_conv_state_rollback", "gdn_prefill_split",
            "gdn_prefill_split_workspace_size", "gdn_device_status", "gdn_selftest_wait_timeout",
-           "gdn_decode_block_step")
+           "gdn_decode_block_step", "gdn_add_rmsnorm", "gdn_kv_append", "gdn_paged_attention",
+           "gdn_shared_prefix_attention", "gdn_attn_workspace_size")
 GDN_STATUS_WAIT_TIMEOUT = 1
 
 
@@ -108,6 +109,17 @@ def lib() -> ctypes.CDLL:
         L.gdn_device_status.restype = ctypes.c_int
         L.gdn_selftest_wait_timeout.argtypes = [I32, P]
         L.gdn_selftest_wait_timeout.restype = ctypes.c_int
+        # the attention layers (attention.py); shape structs go in as pointers
+        L.gdn_kv_append.argtypes = [P] * 6 + [F] + [P] * 10
+        L.gdn_kv_append.restype = ctypes.c_int
+        L.gdn_paged_attention.argtypes = [P] * 11 + [S, P]
+        L.gdn_paged_attention.restype = ctypes.c_int
+        L.gdn_shared_prefix_attention.argtypes = [P] * 12 + [S, P]
+        L.gdn_shared_prefix_attention.restype = ctypes.c_int
+        L.gdn_attn_workspace_size.argtypes = [P]
+        L.gdn_attn_workspace_size.restype = S
+        L.gdn_add_rmsnorm.argtypes = [ctypes.c_int64, I32, I32, P, P, P, F, P, P, P, I32, P]
+        L.gdn_add_rmsnorm.restype = ctypes.c_int
         _lib = L
     return _lib
 
@@ -437,3 +449,20 @@ def gdn_conv_state_rollback(q_raw, k_raw, v_raw, conv_state_in, prefix_len, conv
     if st != GDN_OK:
         raise GdnError(st, "gdn_conv_state_rollback")
     return conv_state_out
+
+
+# ------------------------------------------------------------------ the attention layers
+
+_ATTENTION = ("GdnAttnShape", "make_attn_shape", "gdn_attn_workspace_size", "gdn_attn_workspace",
+              "gdn_kv_append", "gdn_paged_attention", "gdn_shared_prefix_attention",
+              "gdn_add_rmsnorm")
+
+
+def __getattr__(name):
+    """The attention-layer calls live in attention.py, which imports torch: loaded on use."""
+    if name in _ATTENTION:
+        from . import attention
+        for n in _ATTENTION:
+            globals()[n] = getattr(attention, n)
+        return globals()[name]
+    raise AttributeError("module %r has no attribute %r" % (__name__, name))

@@ -1,0 +1,290 @@
+"""Binding of the attention-layer operators: residual + RMS norm, rotary positions and the
+append to the paged cache, attention over the cache, and the same behind a shared prefix.
+
+Argument marshalling only, as in the package itself; include/gdn.h has the contract of each
+call.  The shape structs are kept by sizes and strides, so that a decode loop builds them
+once.
+"""
+from __future__ import annotations
+
+import ctypes
+import functools
+import math
+from typing import Optional
+
+import torch
+
+from . import (GDN_BF16, GDN_ERR_INVALID_ARG, GDN_F32, GDN_OK, GdnError, lib)
+
+I64x2 = ctypes.c_int64 * 2
+
+
+class GdnAttnShape(ctypes.Structure):
+    """gdn_attn_shape (include/gdn.h)."""
+    _fields_ = [("num_seqs", ctypes.c_int32), ("total_tokens", ctypes.c_int32),
+                ("num_q_heads", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("num_pages", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+                ("prefix_len", ctypes.c_int32), ("rotary_dim", ctypes.c_int32),
+                ("num_axes", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("scale", ctypes.c_float),
+                ("q_stride", I64x2), ("k_stride", I64x2), ("v_stride", I64x2),
+                ("gate_stride", I64x2), ("page_stride", ctypes.c_int64)]
+
+
+def make_attn_shape(num_seqs: int, total_tokens: int, num_q_heads: int, num_kv_heads: int,
+                    head_dim: int = 128, page_size: int = 64, num_pages: int = 0,
+                    max_pages: int = 0, prefix_len: int = 0, rotary_dim: int = 0,
+                    num_axes: int = 1, scale: Optional[float] = None,
+                    dtype: int = GDN_BF16) -> GdnAttnShape:
+    """A shape with contiguous tensors; the stride fields may be changed afterwards."""
+    s = GdnAttnShape(num_seqs, total_tokens, num_q_heads, num_kv_heads, head_dim, page_size,
+                     num_pages, max_pages, prefix_len, rotary_dim, num_axes, dtype,
+                     1.0 / math.sqrt(max(head_dim, 1)) if scale is None else scale)
+    s.q_stride[:] = s.gate_stride[:] = (num_q_heads * head_dim, head_dim)
+    s.k_stride[:] = s.v_stride[:] = (num_kv_heads * head_dim, head_dim)
+    s.page_stride = num_kv_heads * page_size * head_dim
+    return s
+
+
+@functools.lru_cache(maxsize=4096)
+def _shape(n, tokens, hq, hkv, d, page_size, num_pages, max_pages, prefix_len, rotary_dim, axes,
+           scale, page_stride, q_stride, k_stride=None, v_stride=None, gate_stride=None):
+    """The C struct for these sizes and strides (never changed once made)."""
+    s = make_attn_shape(n, tokens, hq, hkv, d, page_size, num_pages, max_pages, prefix_len,
+                        rotary_dim, axes, scale)
+    s.page_stride = page_stride
+    for field, st in (("q_stride", q_stride), ("k_stride", k_stride), ("v_stride", v_stride),
+                      ("gate_stride", gate_stride)):
+        if st is not None:
+            getattr(s, field)[:] = st
+    return s, ctypes.byref(s)
+
+
+def gdn_attn_workspace_size(shape: GdnAttnShape) -> int:
+    n = lib().gdn_attn_workspace_size(ctypes.byref(shape))
+    if n == ctypes.c_size_t(-1).value:
+        raise GdnError(GDN_ERR_INVALID_ARG, "gdn_attn_workspace_size")
+    return n
+
+
+def gdn_attn_workspace(num_seqs: int, total_tokens: int, num_q_heads: int, num_kv_heads: int,
+                       head_dim: int, prefix_len: int = 0, device="cuda"):
+    """A zeroed workspace for the attention calls up to these sizes, to be kept and given to
+    every call (one per stream)."""
+    shape = make_attn_shape(num_seqs, total_tokens, num_q_heads, num_kv_heads, head_dim,
+                            prefix_len=prefix_len)
+    # the caching allocator's blocks start on 512-byte boundaries
+    return torch.zeros(max(gdn_attn_workspace_size(shape), 1), dtype=torch.uint8, device=device)
+
+
+def _strides3(t, what):
+    """(token, head) strides of a [T, H, D] bf16 CUDA tensor whose rows are contiguous."""
+    if t.dtype != torch.bfloat16:
+        raise TypeError("%s must be bfloat16, got %s" % (what, t.dtype))
+    st = t.stride()
+    if len(st) != 3 or not t.is_cuda or st[2] != 1:
+        raise ValueError("%s must be a [tokens, heads, head_dim] CUDA tensor with contiguous rows"
+                         % what)
+    if t.shape[0] <= 1 or t.shape[1] <= 1:  # torch leaves the stride of a size of 1 open
+        d = t.shape[2]
+        head = st[1] if t.shape[1] > 1 else d
+        return (st[0] if t.shape[0] > 1 else max(t.shape[1] * head, d), head)
+    return st[:2]
+
+
+def _cache(k_cache, v_cache):
+    """(num_pages, hkv, page_size, d, page_stride) of a pair of caches."""
+    shape, st = k_cache.shape, k_cache.stride()
+    if (len(shape) != 4 or v_cache.shape != shape or v_cache.stride() != st or not k_cache.is_cuda
+            or not v_cache.is_cuda or k_cache.dtype != torch.bfloat16
+            or v_cache.dtype != torch.bfloat16):
+        raise ValueError("the caches must be two alike [pages, kv_heads, page_size, head_dim] "
+                         "bfloat16 CUDA tensors")
+    pages, hkv, size, d = shape
+    if st[3] != 1 or (size > 1 and st[2] != d) or (hkv > 1 and st[1] != size * d):
+        raise ValueError("a page's heads must be contiguous in the caches")
+    return pages, hkv, size, d, (st[0] if pages > 1 else hkv * size * d)
+
+
+def _index(t, what, dtype=torch.int32):
+    if t.dtype != dtype or not t.is_cuda or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous %s CUDA tensor" % (what, dtype))
+    return t.data_ptr()
+
+
+def _float(t, shape, what):
+    if t.dtype != torch.float32 or not t.is_cuda or not t.is_contiguous() or t.shape != shape:
+        raise ValueError("%s must be a contiguous float32 CUDA tensor of shape %s"
+                         % (what, tuple(shape)))
+    return t.data_ptr()
+
+
+def _stream(stream, t):
+    return (torch.cuda.current_stream(t.device) if stream is None else stream).cuda_stream
+
+
+def _sequences(q, page_table, kv_lens, cu_seqlens):
+    """(num_seqs, max_pages) after checking the index tensors' shapes against each other."""
+    n = kv_lens.shape[0]
+    if page_table.dim() != 2 or page_table.shape[0] != n or kv_lens.dim() != 1:
+        raise ValueError("page_table must be [num_seqs, max_pages] and kv_lens [num_seqs]")
+    if cu_seqlens is not None and tuple(cu_seqlens.shape) != (n + 1,):
+        raise ValueError("cu_seqlens must be [num_seqs + 1]")
+    return n, page_table.shape[1]
+
+
+def gdn_kv_append(q, k, v, k_cache, v_cache, page_table, kv_lens, inv_freq=None, cu_seqlens=None,
+                  positions=None, rope_axis=None, q_norm=None, k_norm=None, eps: float = 1e-6,
+                  q_out=None, prefix_len: int = 0, stream=None):
+    """Per-head RMS norm of q and k (with q_norm / k_norm [D] fp32), rotation of their first
+    2 * len(inv_freq) elements, q to q_out, k and v to their place in the paged cache.
+    q [T, Hq, D], k, v [T, Hkv, D] bf16, any token and head strides; caches
+    [pages, Hkv, page_size, D]; page_table [N, max_pages], kv_lens [N] (the call's tokens
+    included), cu_seqlens [N+1] int32 or None (one token per sequence); inv_freq [R/2] fp64
+    or None (no rotation); positions [T] or [axes, T] int32 (None: prefix_len + place) with
+    rope_axis [R/2] int32.  q_out None: a new tensor.  Returns q_out."""
+    pages, hkv, size, d, page_stride = _cache(k_cache, v_cache)
+    tokens, hq = q.shape[0], q.shape[1]
+    n, max_pages = _sequences(q, page_table, kv_lens, cu_seqlens)
+    if q.shape[2] != d or k.shape != (tokens, hkv, d) or v.shape != (tokens, hkv, d):
+        raise ValueError("q, k, v and the caches must agree in tokens, kv heads and head_dim")
+    axes = 1
+    if positions is not None:
+        axes = 1 if positions.dim() == 1 else positions.shape[0]
+        if positions.shape[-1] != tokens or positions.dim() > 2:
+            raise ValueError("positions must be [tokens] or [axes, tokens]")
+    rot = 0
+    if inv_freq is not None:
+        rot = 2 * inv_freq.shape[0]
+        if rope_axis is not None and rope_axis.shape != inv_freq.shape:
+            raise ValueError("rope_axis must have one entry per frequency")
+    if q_out is None:
+        q_out = torch.empty((tokens, hq, d), dtype=torch.bfloat16, device=q.device)
+    elif q_out.shape != q.shape or not q_out.is_contiguous() or q_out.dtype != torch.bfloat16 \
+            or not q_out.is_cuda:
+        raise ValueError("q_out must be a contiguous bfloat16 CUDA tensor of q's shape")
+    _, ref = _shape(n, tokens, hq, hkv, d, size, pages, max_pages, prefix_len, rot, axes, None,
+                    page_stride, _strides3(q, "q"), _strides3(k, "k"), _strides3(v, "v"))
+    st = lib().gdn_kv_append(
+        ref, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+        None if q_norm is None else _float(q_norm, (d,), "q_norm"),
+        None if k_norm is None else _float(k_norm, (d,), "k_norm"), eps,
+        None if inv_freq is None else _index(inv_freq, "inv_freq", torch.float64),
+        None if rope_axis is None else _index(rope_axis, "rope_axis"),
+        None if positions is None else _index(positions, "positions"),
+        _index(page_table, "page_table"), _index(kv_lens, "kv_lens"),
+        None if cu_seqlens is None else _index(cu_seqlens, "cu_seqlens"),
+        q_out.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), _stream(stream, q))
+    if st != GDN_OK:
+        raise GdnError(st, "gdn_kv_append")
+    return q_out
+
+
+def _attend(name, q, k_cache, v_cache, prefix_table, prefix_len, page_table, kv_lens, cu_seqlens,
+            gate, scale, o, lse, workspace, stream):
+    pages, hkv, size, d, page_stride = _cache(k_cache, v_cache)
+    tokens, hq = q.shape[0], q.shape[1]
+    n, max_pages = _sequences(q, page_table, kv_lens, cu_seqlens)
+    if q.shape[2] != d:
+        raise ValueError("q and the caches must agree in head_dim")
+    gate_stride = None
+    if gate is not None:
+        if gate.shape != q.shape:
+            raise ValueError("gate must have q's shape")
+        gate_stride = _strides3(gate, "gate")
+    if o is None:
+        o = torch.empty((tokens, hq, d), dtype=torch.bfloat16, device=q.device)
+    elif o.shape != q.shape or not o.is_contiguous() or o.dtype != torch.bfloat16 or not o.is_cuda:
+        raise ValueError("o must be a contiguous bfloat16 CUDA tensor of q's shape")
+    s, ref = _shape(n, tokens, hq, hkv, d, size, pages, max_pages, prefix_len, 0, 1, scale,
+                    page_stride, _strides3(q, "q"), None, None, gate_stride)
+    if workspace is None:
+        workspace = torch.zeros(max(gdn_attn_workspace_size(s), 1), dtype=torch.uint8,
+                                device=q.device)
+    args = [ref, q.data_ptr(), None if gate is None else gate.data_ptr(), k_cache.data_ptr(),
+            v_cache.data_ptr()]
+    if prefix_table is not None:
+        if prefix_table.numel() * size < prefix_len:
+            raise ValueError("prefix_table must cover prefix_len keys")
+        args.append(_index(prefix_table, "prefix_table"))
+    st = getattr(lib(), name)(
+        *args, _index(page_table, "page_table"), _index(kv_lens, "kv_lens"),
+        None if cu_seqlens is None else _index(cu_seqlens, "cu_seqlens"), o.data_ptr(),
+        None if lse is None else _float(lse, (tokens, hq), "lse"), workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), _stream(stream, q))
+    if st != GDN_OK:
+        raise GdnError(st, name)
+    return o
+
+
+def gdn_paged_attention(q, k_cache, v_cache, page_table, kv_lens, cu_seqlens=None, gate=None,
+                        scale: Optional[float] = None, o=None, lse=None, workspace=None,
+                        stream=None):
+    """Causal attention of q [T, Hq, D] over each sequence's keys in the paged cache, times
+    sigmoid(gate) with a gate.  cu_seqlens None: one token per sequence.  scale None:
+    1 / sqrt(D).  lse (fp32 [T, Hq], optional) receives ln of each row's sum of exp(scores).
+    workspace: from gdn_attn_workspace, kept by the caller (None: a fresh zeroed one per
+    call).  Returns o."""
+    return _attend("gdn_paged_attention", q, k_cache, v_cache, None, 0, page_table, kv_lens,
+                   cu_seqlens, gate, scale, o, lse, workspace, stream)
+
+
+def gdn_shared_prefix_attention(q, k_cache, v_cache, prefix_table, prefix_len: int, page_table,
+                                kv_lens, cu_seqlens=None, gate=None,
+                                scale: Optional[float] = None, o=None, lse=None, workspace=None,
+                                stream=None):
+    """gdn_paged_attention with prefix_len keys in front that every sequence shares: the pages
+    in prefix_table [ceil(prefix_len / page_size)] int32.  kv_lens counts the sequences' own
+    keys alone.  Returns o."""
+    return _attend("gdn_shared_prefix_attention", q, k_cache, v_cache, prefix_table, prefix_len,
+                   page_table, kv_lens, cu_seqlens, gate, scale, o, lse, workspace, stream)
+
+
+def gdn_add_rmsnorm(x, residual, weight, eps: float = 1e-6, residual_out=None, y=None, scale=None,
+                    out: str = "same", group: int = 0, stream=None):
+    """h = x + residual (rounded to x's type; x itself with residual None) and its RMS norm
+    y = h / sqrt(mean(h^2) + eps) * weight over the last dimension.  out "same": y in x's
+    type, returns (y, h); out "e4m3": y in float8_e4m3fn with fp32 scales per row (group 0) or
+    per 128 columns (group 128), returns (y, scale, h).  x, residual bf16 or fp32; weight
+    fp32.  residual_out may be residual or x."""
+    cols = x.shape[-1]
+    rows = x.numel() // max(cols, 1)
+    if x.dtype == torch.bfloat16:
+        code = GDN_BF16
+    elif x.dtype == torch.float32:
+        code = GDN_F32
+    else:
+        raise TypeError("x must be bfloat16 or float32, got %s" % x.dtype)
+    if out not in ("same", "e4m3"):
+        raise ValueError("out must be 'same' or 'e4m3'")
+    for t in (x, residual, residual_out):
+        if t is not None and (t.dtype != x.dtype or t.shape != x.shape or not t.is_cuda
+                              or not t.is_contiguous()):
+            raise ValueError("x, residual and residual_out must be alike, contiguous CUDA tensors")
+    if residual is not None and residual_out is None:
+        residual_out = torch.empty_like(x)
+    kind = x.dtype if out == "same" else torch.float8_e4m3fn
+    if y is None:
+        y = torch.empty_like(x, dtype=kind)
+    elif y.dtype != kind or y.shape != x.shape or not y.is_cuda or not y.is_contiguous():
+        raise ValueError("y must be a contiguous %s CUDA tensor of x's shape" % kind)
+    sp = None
+    if out == "e4m3":
+        if group and (group != 128 or cols % 128):
+            raise ValueError("group must be 0, or 128 and divide the columns")
+        shape = x.shape[:-1] + ((cols // group if group else 1),)
+        if scale is None:
+            scale = torch.empty(shape, dtype=torch.float32, device=x.device)
+        sp = _float(scale, shape, "scale")
+    elif group:
+        raise ValueError("groups go with out='e4m3'")
+    st = lib().gdn_add_rmsnorm(
+        rows, cols, code, x.data_ptr(), None if residual is None else residual.data_ptr(),
+        _float(weight, (cols,), "weight"), eps,
+        None if residual_out is None else residual_out.data_ptr(), y.data_ptr(), sp,
+        group, _stream(stream, x))
+    if st != GDN_OK:
+        raise GdnError(st, "gdn_add_rmsnorm")
+    h = x if residual_out is None else residual_out
+    return (y, h) if out == "same" else (y, scale, h)

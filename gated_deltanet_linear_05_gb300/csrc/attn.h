@@ -1,0 +1,61 @@
+// Internal launch interface of the attention-layer operators.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "gdn.h"
+
+namespace gdn {
+
+struct AppendParams {
+  int num_seqs, tokens, hq, hkv, d, page_size, num_pages, max_pages, rot, axes, pos0;
+  float eps;
+  int64_t qs[2], ks[2], vs[2], page_stride;
+  const void *q, *k, *v;
+  const float *q_norm, *k_norm;
+  const double *inv_freq;
+  const int32_t *rope_axis, *positions, *page_table, *kv_lens, *cu_seqlens;
+  void *q_out, *k_cache, *v_cache;
+};
+cudaError_t launch_kv_append(const AppendParams &p, cudaStream_t stream);
+
+struct AddNormParams {
+  long long rows;
+  int cols, group;
+  float eps;
+  const void *x, *residual;
+  const float *weight;
+  void *residual_out, *y;
+  float *scale;
+};
+cudaError_t launch_add_rmsnorm(const AddNormParams &p, gdn_dtype dtype, cudaStream_t stream);
+
+struct AttnParams {
+  int num_seqs, tokens, hq, hkv, d, page_size, num_pages, max_pages, prefix_len;
+  float scale;
+  int64_t qs[2], gs[2], page_stride;
+  const void *q, *gate, *k_cache, *v_cache;
+  const int32_t *prefix_table, *page_table, *kv_lens, *cu_seqlens;
+  void *o;
+  float *lse;
+};
+cudaError_t launch_attn_simple(const AttnParams &p, cudaStream_t stream);
+
+// Sequence that token t belongs to: the n with cu[n] <= t < cu[n + 1], by a warp that probes
+// 32 places at a time (cu non-decreasing, cu[0] = 0; a malformed cu gives some n in range).
+__device__ __forceinline__ int find_seq(const int32_t *cu, int num_seqs, int t, int lane) {
+  int lo = 0, hi = num_seqs;  // cu[lo] <= t (taken), answer in [lo, hi)
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 31) / 32;
+    const int at = lo + (lane + 1) * step;
+    const bool le = at < hi && cu[at] <= t;
+    const int m = __popc(__ballot_sync(0xffffffffu, le));  // probes at or below t
+    lo += m * step;
+    hi = min(hi, lo + step);
+  }
+  return lo;
+}
+
+}  // namespace gdn

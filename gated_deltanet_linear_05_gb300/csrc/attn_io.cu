@@ -1,0 +1,302 @@
+// The attention layer's steps around its products: rotary positions + append to the paged
+// cache, and the residual addition + RMS norm.  Both move each byte once and are bound by
+// HBM, or at a few rows by the latency of a launch and of a chain of loads.
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+
+#include "attn.h"
+#include "common.cuh"
+
+namespace gdn {
+namespace {
+
+// Eight consecutive elements as floats.
+__device__ __forceinline__ void unpack8(const uint4 &u, float (&x)[8]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = __uint_as_float(w[i] << 16);
+    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
+  return make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]),
+                    pack_bf16(x[6], x[7]));
+}
+
+// ------------------------------------------------------------------ append
+
+// f / (2 pi) as a binary fraction of a turn, modulo 1, in 64 bits: f = m 2^e exactly (m < 2^53),
+// 2^64 / (2 pi) = C, so the fraction is the low 64 bits of (m C) 2^e.  Integer arithmetic:
+// the 64-bit floating units of this GPU are too slow for it, and 32-bit floats lose the
+// angle (pos * f at pos = 10^6 has an error of 0.06 rad).
+__device__ __forceinline__ uint64_t turn_fraction(double f) {
+  constexpr uint64_t C = 0x28BE60DB9391054Aull;
+  const uint64_t b = (uint64_t)__double_as_longlong(f);
+  const int ex = (int)((b >> 52) & 0x7ff);
+  const uint64_t m = (b & 0xfffffffffffffull) | (ex ? 1ull << 52 : 0);
+  const int e = (ex ? ex : 1) - 1075;
+  const uint64_t lo = m * C, hi = __umul64hi(m, C);
+  uint64_t r;
+  if (e >= 0) r = e < 64 ? lo << e : 0;
+  else if (e > -64) r = (lo >> -e) | (hi << (64 + e));
+  else r = e > -128 ? hi >> (-e - 64) : 0;
+  return (b >> 63) ? 0 - r : r;
+}
+
+constexpr int kAppendWarps = 8;
+
+// One warp per (token, share of its head rows): a row takes D / 8 lanes of 8 elements, the
+// token's cosines and sines stay in registers for all its rows.  `share`: warps per token.
+template <int D>
+__global__ void __launch_bounds__(32 * kAppendWarps) append_kernel(AppendParams p, int share) {
+  constexpr int LPR = D / 8, RPW = 32 / LPR;
+  const int lane = threadIdx.x & 31;
+  const long long w = (long long)blockIdx.x * kAppendWarps + (threadIdx.x >> 5);
+  const int tok = (int)(w / share), part = (int)(w % share);
+  if (tok >= p.tokens) return;
+  const int col = (lane % LPR) * 8;
+  const int half = p.rot >> 1;
+  // the token's place
+  int n = tok, back = 1;  // back: tokens from this one to the sequence's end
+  if (p.cu_seqlens) {
+    n = find_seq(p.cu_seqlens, p.num_seqs, tok, lane);
+    int bos, eos;
+    seq_range(p.cu_seqlens, n, p.tokens, bos, eos);
+    back = eos - tok;
+  }
+  const long long cap = (long long)p.max_pages * p.page_size;
+  const int len = (int)min(max((long long)p.kv_lens[n], 0ll), cap);
+  const int place = len - back;
+  long long dst = -1;  // element offset of the token's rows of head 0
+  if (place >= 0 && back > 0) {
+    const int pg = p.page_table[(long long)n * p.max_pages + place / p.page_size];
+    if ((unsigned)pg < (unsigned)p.num_pages)
+      dst = (long long)pg * p.page_stride + (long long)(place % p.page_size) * D;
+  }
+  float cs[8], sn[8];
+  const bool rot = col < p.rot;
+  if (rot) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int f = (col + i) % half;
+      int pos = p.pos0 + place;
+      if (p.positions) {
+        const int ax = p.rope_axis ? min(max(p.rope_axis[f], 0), p.axes - 1) : 0;
+        pos = p.positions[(long long)ax * p.tokens + tok];
+      }
+      const uint64_t turn = turn_fraction(p.inv_freq[f]) * (uint64_t)(int64_t)pos;
+      sincospif((float)(int32_t)(turn >> 32) * 0x1p-31f, &sn[i], &cs[i]);
+      if (col + i < half) sn[i] = -sn[i];  // out = x cos + partner * sn
+    }
+  }
+  const int shift = half / 8;
+  const int peer = (lane & ~(LPR - 1)) + ((col < half ? lane % LPR + shift : lane % LPR - shift) & (LPR - 1));
+  const int rows = p.hq + 2 * p.hkv;
+  const __nv_bfloat16 *q = (const __nv_bfloat16 *)p.q + tok * p.qs[0] + col;
+  const __nv_bfloat16 *k = (const __nv_bfloat16 *)p.k + tok * p.ks[0] + col;
+  const __nv_bfloat16 *v = (const __nv_bfloat16 *)p.v + tok * p.vs[0] + col;
+  for (int r0 = part * RPW; r0 < rows; r0 += share * RPW) {
+    const int r = r0 + lane / LPR;
+    const bool on = r < rows;
+    const int kind = r < p.hq ? 0 : r < p.hq + p.hkv ? 1 : 2;
+    const int h = r - (kind == 0 ? 0 : kind == 1 ? p.hq : p.hq + p.hkv);
+    uint4 u = make_uint4(0, 0, 0, 0);
+    if (on)
+      u = *(const uint4 *)(kind == 0 ? q + h * p.qs[1] : kind == 1 ? k + h * p.ks[1] : v + h * p.vs[1]);
+    float x[8];
+    unpack8(u, x);
+    const float *nw = kind == 0 ? p.q_norm : kind == 1 ? p.k_norm : nullptr;
+    if (p.q_norm || p.k_norm) {
+      float s = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s = fmaf(x[i], x[i], s);
+#pragma unroll
+      for (int o = LPR / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+      if (nw) {
+        const float inv = 1.f / sqrtf(s * (1.f / D) + p.eps);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = x[i] * inv * nw[col + i];
+      }
+    }
+    float y[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = __shfl_sync(0xffffffffu, x[i], peer);
+    if (kind < 2 && rot) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = fmaf(x[i], cs[i], y[i] * sn[i]);
+    }
+    if (kind < 2) u = pack8(x);
+    if (!on) continue;
+    if (kind == 0)
+      *(uint4 *)((__nv_bfloat16 *)p.q_out + ((long long)tok * p.hq + h) * D + col) = u;
+    else if (dst >= 0)
+      *(uint4 *)((__nv_bfloat16 *)(kind == 1 ? p.k_cache : p.v_cache) + dst +
+                 (long long)h * p.page_size * D + col) = u;
+  }
+}
+
+// ------------------------------------------------------------------ add + norm
+
+template <typename T>
+__device__ __forceinline__ void load8(const T *p, float (&x)[8]);
+template <>
+__device__ __forceinline__ void load8<__nv_bfloat16>(const __nv_bfloat16 *p, float (&x)[8]) {
+  unpack8(*(const uint4 *)p, x);
+}
+template <>
+__device__ __forceinline__ void load8<float>(const float *p, float (&x)[8]) {
+  const float4 a = *(const float4 *)p, b = *(const float4 *)(p + 4);
+  x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+  x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+}
+__device__ __forceinline__ void store8(__nv_bfloat16 *p, const float (&x)[8]) { *(uint4 *)p = pack8(x); }
+__device__ __forceinline__ void store8(float *p, const float (&x)[8]) {
+  *(float4 *)p = make_float4(x[0], x[1], x[2], x[3]);
+  *(float4 *)(p + 4) = make_float4(x[4], x[5], x[6], x[7]);
+}
+__device__ __forceinline__ void round8(__nv_bfloat16 *, float (&x)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] = __bfloat162float(__float2bfloat16_rn(x[i]));
+}
+__device__ __forceinline__ void round8(float *, float (&)[8]) {}
+
+// Sum of squares / largest magnitude over the block.  Magnitudes as their bits: an
+// unsigned maximum that keeps NaN (fmaxf would drop it).
+__device__ __forceinline__ float block_sum(float s, float *sh, int warps) {
+  s = warp_sum(s);
+  if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = s;
+  __syncthreads();
+  const int l = threadIdx.x & 31;
+  return warp_sum(l < warps ? sh[l] : 0.f);
+}
+__device__ __forceinline__ uint32_t block_max(uint32_t m, uint32_t *sh, int warps) {
+  m = __reduce_max_sync(0xffffffffu, m);
+  if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = m;
+  __syncthreads();
+  const int l = threadIdx.x & 31;
+  return __reduce_max_sync(0xffffffffu, l < warps ? sh[l] : 0u);
+}
+__device__ __forceinline__ float scale_of(uint32_t amax_bits) {
+  const float a = __uint_as_float(amax_bits);
+  return (a < 1e-12f ? 1e-12f : a) / 448.f;  // NaN stays
+}
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
+  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
+  return lo | hi << 16;
+}
+
+// One CTA per row; a thread keeps NV vectors of 8 values of the row in registers, so x and
+// the residual are read once and h, y written once.
+template <typename T, int NV>
+__global__ void __launch_bounds__(1024) add_rmsnorm_kernel(AddNormParams p) {
+  __shared__ float sh_sum[32];
+  __shared__ uint32_t sh_max[32];
+  const int warps = blockDim.x >> 5;
+  const long long at = (long long)blockIdx.x * p.cols;
+  float v[NV][8];
+  float s = 0.f;
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int c = (j * blockDim.x + threadIdx.x) * 8;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[j][i] = 0.f;
+    if (c < p.cols) {
+      load8((const T *)p.x + at + c, v[j]);
+      if (p.residual) {
+        float r[8];
+        load8((const T *)p.residual + at + c, r);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[j][i] += r[i];
+        round8((T *)nullptr, v[j]);
+      }
+      if (p.residual_out) store8((T *)p.residual_out + at + c, v[j]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s = fmaf(v[j][i], v[j][i], s);
+    }
+  }
+  s = block_sum(s, sh_sum, warps);
+  const float inv = 1.f / sqrtf(s / p.cols + p.eps);
+  uint32_t amax = 0;
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int c = (j * blockDim.x + threadIdx.x) * 8;
+    if (c < p.cols) {
+      float w[8];
+      load8(p.weight + c, w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        v[j][i] = v[j][i] * inv * w[i];
+        amax = max(amax, __float_as_uint(fabsf(v[j][i])));
+      }
+      if (!p.scale) store8((T *)p.y + at + c, v[j]);
+    }
+  }
+  if (!p.scale) return;
+  float scale = 0.f;
+  if (p.group == 0) {
+    scale = scale_of(block_max(amax, sh_max, warps));
+    if (threadIdx.x == 0) p.scale[blockIdx.x] = scale;
+  }
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int c = (j * blockDim.x + threadIdx.x) * 8;
+    if (p.group) {  // 16 lanes hold a group of 128 columns
+      uint32_t m = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(fabsf(v[j][i])));
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+      scale = scale_of(m);
+      if (c < p.cols && (threadIdx.x & 15) == 0)
+        p.scale[(long long)blockIdx.x * (p.cols >> 7) + (c >> 7)] = scale;
+    }
+    if (c < p.cols) {
+      const float q = 1.f / scale;
+      uint2 u;
+      u.x = e4m3x4(v[j][0] * q, v[j][1] * q, v[j][2] * q, v[j][3] * q);
+      u.y = e4m3x4(v[j][4] * q, v[j][5] * q, v[j][6] * q, v[j][7] * q);
+      *(uint2 *)((uint8_t *)p.y + at + c) = u;
+    }
+  }
+}
+
+template <typename T>
+cudaError_t launch_norm_t(const AddNormParams &p, cudaStream_t stream) {
+  const int vecs = p.cols / 8;
+  // vectors per thread: as few threads as hold the row with 2 each, so that several rows share
+  // an SM; 1 each while there are too few rows to fill the SMs; more for very wide rows
+  const int want = p.rows < 304 && vecs <= 1024 ? 1 : vecs <= 2048 ? 2 : vecs <= 4096 ? 4 : 8;
+  const int threads = ((vecs + want - 1) / want + 31) / 32 * 32;
+  const unsigned grid = (unsigned)p.rows;
+  switch (want) {
+    case 1: add_rmsnorm_kernel<T, 1><<<grid, threads, 0, stream>>>(p); break;
+    case 2: add_rmsnorm_kernel<T, 2><<<grid, threads, 0, stream>>>(p); break;
+    case 4: add_rmsnorm_kernel<T, 4><<<grid, threads, 0, stream>>>(p); break;
+    default: add_rmsnorm_kernel<T, 8><<<grid, threads, 0, stream>>>(p); break;
+  }
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_kv_append(const AppendParams &p, cudaStream_t stream) {
+  const int rpw = 32 / (p.d / 8);
+  const int rows = p.hq + 2 * p.hkv;
+  // warps per token: enough to fill 152 SMs with 16 warps each, while each has rows to do
+  int share = 1;
+  while (share < kAppendWarps && (long long)p.tokens * share < 152 * 16 && share * rpw < rows) share *= 2;
+  const long long blocks = ((long long)p.tokens * share + kAppendWarps - 1) / kAppendWarps;
+  if (p.d == 128)
+    append_kernel<128><<<(unsigned)blocks, 32 * kAppendWarps, 0, stream>>>(p, share);
+  else
+    append_kernel<256><<<(unsigned)blocks, 32 * kAppendWarps, 0, stream>>>(p, share);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_add_rmsnorm(const AddNormParams &p, gdn_dtype dtype, cudaStream_t stream) {
+  return dtype == GDN_BF16 ? launch_norm_t<__nv_bfloat16>(p, stream) : launch_norm_t<float>(p, stream);
+}
+
+}  // namespace gdn

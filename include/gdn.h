@@ -428,6 +428,140 @@ gdn_status gdn_prefill_split(const gdn_shape *shape, const void *q, const void *
 /* Workspace bytes of gdn_prefill_split; (size_t)-1 for an invalid shape or segment_len. */
 size_t gdn_prefill_split_workspace_size(const gdn_shape *shape, int32_t segment_len);
 
+/* ------------------------------------------------------------------------------------
+ * The attention layers of the hybrid decoders
+ * ------------------------------------------------------------------------------------
+ * The decoders alternate delta-rule layers with gated softmax-attention layers.  These
+ * entry points are such a layer's steps beside its matrix products, for serving:
+ *   gdn_add_rmsnorm              residual addition + RMS norm, optional 8-bit output
+ *   gdn_kv_append                q/k head norms, rotary positions, scatter into the cache
+ *   gdn_paged_attention          attention over the paged cache
+ *   gdn_shared_prefix_attention  the same behind a prefix that the whole batch shares
+ *
+ * Device pointers; 16-byte aligned unless said otherwise (page_table, prefix_table, kv_lens,
+ * cu_seqlens, positions, rope_axis and lse: 4 bytes; inv_freq: 8 bytes).
+ *     q            [total_tokens, Hq, D]   bf16, with the strides of the shape
+ *     k, v         [total_tokens, Hkv, D]  bf16, with the strides of the shape
+ *     gate         [total_tokens, Hq, D]   bf16, with the strides of the shape
+ *     o            [total_tokens, Hq, D]   bf16, contiguous
+ *     lse          [total_tokens, Hq]      float32 or NULL: ln of each row's sum of
+ *                                          exp(scores), -inf for a row that sees no key
+ *     k_cache, v_cache [num_pages, Hkv, page_size, D] bf16, page_stride elements from page
+ *                                          to page (a page's heads contiguous)
+ *     page_table   [num_seqs, max_pages]   int32: the pages of each sequence in order
+ *     kv_lens      [num_seqs]              int32: keys of each sequence in its own pages,
+ *                                          the call's tokens included
+ *     cu_seqlens   [num_seqs + 1]          int32, as for the delta-rule calls; NULL: one
+ *                                          token per sequence (total_tokens == num_seqs)
+ * Token t of the T_n tokens of sequence n has place kv_lens[n] - T_n + t in the sequence's
+ * own keys: key c is row c % page_size of page page_table[n][c / page_size].  q-head h
+ * reads kv-head h / (Hq / Hkv).
+ *
+ * kv_lens is clamped to [0, max_pages * page_size].  A page-table entry outside
+ * [0, num_pages) never makes a kernel access memory outside the cache: gdn_kv_append drops
+ * the row, the attention calls give unspecified results for that sequence alone.  Entries past a
+ * sequence's last page are not read.  Cache rows at or past kv_lens may hold anything,
+ * infinities and NaN included; keys below kv_lens must be finite. */
+typedef struct {
+  int32_t num_seqs;     /* N >= 0                                                        */
+  int32_t total_tokens; /* query tokens of the call                                      */
+  int32_t num_q_heads;  /* Hq, a multiple of Hkv, Hq / Hkv <= 128                         */
+  int32_t num_kv_heads; /* Hkv                                                           */
+  int32_t head_dim;     /* D: 128 or 256                                                 */
+  int32_t page_size;    /* tokens per page: 16, 32, 64 or 128                            */
+  int32_t num_pages;    /* pages in the cache                                            */
+  int32_t max_pages;    /* entries in a row of page_table                                */
+  int32_t prefix_len;   /* keys of the shared prefix; 0 without one                      */
+  int32_t rotary_dim;   /* R: the first R of D elements are rotated; a multiple of 16,   */
+                        /* 0 <= R <= D (gdn_kv_append)                                   */
+  int32_t num_axes;     /* rows of positions, 1..8 (gdn_kv_append)                       */
+  gdn_dtype dtype;      /* GDN_BF16                                                      */
+  float scale;          /* scores are scale * q.k (the attention calls); finite          */
+  /* element strides {token, head}; multiples of 8, head stride >= D                      */
+  int64_t q_stride[2], k_stride[2], v_stride[2], gate_stride[2];
+  int64_t page_stride;  /* >= Hkv * page_size * D, a multiple of 8                       */
+} gdn_attn_shape;
+
+/*
+ * Rotary positions and append: for every token and head row x of q and k
+ *     x <- x / sqrt(mean(x^2) + eps) * w             (with q_norm / k_norm; else unchanged)
+ *     (x_i, x_{i+R/2}) <- (x_i cos a - x_{i+R/2} sin a, x_{i+R/2} cos a + x_i sin a),
+ *         i < R/2,  a = pos * inv_freq[i]
+ * in float32, rounded once to bf16; q rows go to q_out, k rows and the unchanged v rows to
+ * their place in the cache (a token whose place is negative is not stored).
+ *     q_norm, k_norm [D] float32, 16-byte aligned, or NULL
+ *     inv_freq     [R/2] float64: angle per position in radians
+ *     positions    [num_axes, total_tokens] int32, or NULL: pos = prefix_len + place
+ *     rope_axis    [R/2] int32: the row of positions that frequency i takes (clamped to
+ *                  [0, num_axes)); NULL: row 0.  Several axes (time, height, width) give
+ *                  image and video tokens their positions.
+ *     q_out        [total_tokens, Hq, D] bf16 contiguous; may be q exactly when q is
+ *                  contiguous, other overlap is GDN_ERR_ALIAS
+ * pos * inv_freq is taken modulo a full turn in 64-bit fixed point, so far positions lose
+ * nothing.  One launch, no workspace.
+ */
+gdn_status gdn_kv_append(const gdn_attn_shape *shape, const void *q, const void *k, const void *v,
+                         const float *q_norm, const float *k_norm, float eps,
+                         const double *inv_freq, const int32_t *rope_axis,
+                         const int32_t *positions, const int32_t *page_table,
+                         const int32_t *kv_lens, const int32_t *cu_seqlens, void *q_out,
+                         void *k_cache, void *v_cache, void *stream);
+
+/*
+ * Attention of every token over its sequence's keys up to its own place:
+ *     o = softmax(scale q K^T) V, and o <- o * sigmoid(gate) with a gate (not NULL).
+ * Scores, softmax statistics and sums in float32, the probabilities rounded to bf16 for
+ * their product with V (as V is held), o rounded once.  A row that sees no key is 0.
+ * o must not overlap q or gate (GDN_ERR_ALIAS).  shape->prefix_len must be 0.
+ * workspace: gdn_attn_workspace_size(shape) bytes, 256-byte aligned, zero before the first
+ * call that uses it; every call leaves it ready for the next.  Calls sharing a workspace must
+ * not overlap on the GPU.  The results do not depend on the order of execution.
+ */
+gdn_status gdn_paged_attention(const gdn_attn_shape *shape, const void *q, const void *gate,
+                               const void *k_cache, const void *v_cache,
+                               const int32_t *page_table, const int32_t *kv_lens,
+                               const int32_t *cu_seqlens, void *o, float *lse, void *workspace,
+                               size_t workspace_bytes, void *stream);
+
+/*
+ * The same with shape->prefix_len > 0 keys in front that all sequences share: key c of the
+ * prefix is row c % page_size of page prefix_table[c / page_size], and every token sees all
+ * of it before its own sequence's keys.  kv_lens counts the sequences' own keys alone (it
+ * may be 0).  The prefix is read once for the batch, not once per sequence.
+ *     prefix_table [ceil(prefix_len / page_size)] int32
+ */
+gdn_status gdn_shared_prefix_attention(const gdn_attn_shape *shape, const void *q,
+                                       const void *gate, const void *k_cache,
+                                       const void *v_cache, const int32_t *prefix_table,
+                                       const int32_t *page_table, const int32_t *kv_lens,
+                                       const int32_t *cu_seqlens, void *o, float *lse,
+                                       void *workspace, size_t workspace_bytes, void *stream);
+
+/* Workspace bytes that either attention call needs for `shape`, with or without cu_seqlens
+ * (num_seqs, total_tokens, the heads, head_dim and prefix_len decide; larger values of any
+ * of the first two never need less); (size_t)-1 for an invalid shape. */
+size_t gdn_attn_workspace_size(const gdn_attn_shape *shape);
+
+/*
+ * Residual addition and RMS norm of rows of `cols` values:
+ *     h = x + residual, rounded to dtype (x itself when residual is NULL)
+ *     y = h / sqrt(mean(h^2) + eps) * weight, in float32
+ * y is rounded to dtype, or with scale != NULL held in 8 bits (e4m3):
+ *     scale = max(max|y|, 1e-12) / 448 over the row (group == 0) or over each 128 columns
+ *     (group == 128), y8 = round(y / scale).  A NaN in a row (group) gives it a NaN scale.
+ *     x, residual, residual_out [rows, cols] dtype (float32 or bf16), 16-byte aligned
+ *     weight [cols] float32, 16-byte aligned
+ *     y      [rows, cols] dtype, or e4m3 bytes, 16-byte aligned
+ *     scale  [rows] (group == 0) or [rows, cols / 128] float32, or NULL
+ * residual_out receives h (may be NULL when residual is NULL); it may be residual or x
+ * exactly, y in dtype may be x exactly when residual_out is not; other overlaps are
+ * GDN_ERR_ALIAS.  cols: a multiple of 8 (128 with group == 128), at most 65536.
+ */
+gdn_status gdn_add_rmsnorm(int64_t rows, int32_t cols, gdn_dtype dtype, const void *x,
+                           const void *residual, const float *weight, float eps,
+                           void *residual_out, void *y, float *scale, int32_t group,
+                           void *stream);
+
 /* Bits of the device status word. */
 #define GDN_STATUS_WAIT_TIMEOUT 1u /* a kernel gave up a bounded wait on a barrier */
 
