@@ -41,7 +41,27 @@ struct AttnParams {
   void *o;
   float *lse;
 };
-cudaError_t launch_attn_simple(const AttnParams &p, cudaStream_t stream);
+
+constexpr int kSms = 152;          // persistent CTAs, and the shares that work is cut into
+constexpr int kSplitSlots = 304;   // partial results of split tiles, over all kv-heads
+size_t attn_tile_workspace(int num_seqs, int tokens, int hq, int hkv, int d, int prefix_len);
+cudaError_t launch_attn_tile(const AttnParams &p, void *ws, unsigned int *err, cudaStream_t stream);
+
+// The library's device status word on the current device (gdn_api.cu), or NULL.
+unsigned int *device_status_word();
+
+// x <- x * sigmoid(gate), gate in bf16.
+__device__ __forceinline__ float sigmoid(float g) { return __fdividef(1.f, 1.f + __expf(-g)); }
+__device__ __forceinline__ void gate4(float *x, const uint2 &g) {
+  x[0] *= sigmoid(__uint_as_float(g.x << 16));
+  x[1] *= sigmoid(__uint_as_float(g.x & 0xffff0000u));
+  x[2] *= sigmoid(__uint_as_float(g.y << 16));
+  x[3] *= sigmoid(__uint_as_float(g.y & 0xffff0000u));
+}
+__device__ __forceinline__ void gate8(float (&x)[8], const uint4 &g) {
+  gate4(x, make_uint2(g.x, g.y));
+  gate4(x + 4, make_uint2(g.z, g.w));
+}
 
 // Sequence that token t belongs to: the n with cu[n] <= t < cu[n + 1], by a warp that probes
 // 32 places at a time (cu non-decreasing, cu[0] = 0; a malformed cu gives some n in range).

@@ -21,7 +21,7 @@ bool overlap(const void *a, size_t na, const void *b, size_t nb) {
 }
 
 gdn_status check_stride(const int64_t (&st)[2], int d) {
-  if (st[0] < 0 || st[1] < d || (st[0] & 7) || (st[1] & 7)) return GDN_ERR_INVALID_ARG;
+  if (st[0] < d || st[1] < d || (st[0] & 7) || (st[1] & 7)) return GDN_ERR_INVALID_ARG;
   // what a tensor map can hold: 40-bit byte strides
   if (st[0] > (1ll << 38) || st[1] > (1ll << 38)) return GDN_ERR_UNSUPPORTED;
   return GDN_OK;
@@ -76,7 +76,8 @@ gdn_status attention(const gdn_attn_shape *s, const void *q, const void *gate, c
   if ((st = check_stride(s->q_stride, s->head_dim)) != GDN_OK) return st;
   if (gate && (st = check_stride(s->gate_stride, s->head_dim)) != GDN_OK) return st;
   if ((st = check_tables(s, k_cache, v_cache, page_table, kv_lens, cu_seqlens)) != GDN_OK) return st;
-  if (s->prefix_len > 0 && (!prefix_table || !aligned(prefix_table, 4))) return GDN_ERR_INVALID_ARG;
+  if (s->prefix_len > 0 && (!prefix_table || !aligned(prefix_table, 4) || s->num_pages == 0))
+    return GDN_ERR_INVALID_ARG;
   if (s->total_tokens > 0 && (!q || !o)) return GDN_ERR_INVALID_ARG;
   if (!aligned(q, 16) || !aligned(gate, 16) || !aligned(o, 16) || !aligned(lse, 4))
     return GDN_ERR_INVALID_ARG;
@@ -96,7 +97,7 @@ gdn_status attention(const gdn_attn_shape *s, const void *q, const void *gate, c
   p.d = s->head_dim;
   p.page_size = s->page_size;
   p.num_pages = s->num_pages;
-  p.max_pages = s->max_pages;
+  p.max_pages = s->num_pages > 0 ? s->max_pages : 0;  // no page: no key
   p.prefix_len = s->prefix_len;
   p.scale = s->scale;
   for (int i = 0; i < 2; ++i) p.qs[i] = s->q_stride[i], p.gs[i] = s->gate_stride[i];
@@ -111,7 +112,8 @@ gdn_status attention(const gdn_attn_shape *s, const void *q, const void *gate, c
   p.cu_seqlens = cu_seqlens;
   p.o = o;
   p.lse = lse;
-  return cuda_status(gdn::launch_attn_simple(p, static_cast<cudaStream_t>(stream)));
+  return cuda_status(gdn::launch_attn_tile(p, workspace, gdn::device_status_word(),
+                                           static_cast<cudaStream_t>(stream)));
 }
 
 }  // namespace
@@ -120,7 +122,8 @@ extern "C" {
 
 size_t gdn_attn_workspace_size(const gdn_attn_shape *shape) {
   if (check_shape(shape) != GDN_OK) return (size_t)-1;
-  return 256;  // reserved
+  return gdn::attn_tile_workspace(shape->num_seqs, shape->total_tokens, shape->num_q_heads,
+                                  shape->num_kv_heads, shape->head_dim, shape->prefix_len);
 }
 
 gdn_status gdn_paged_attention(const gdn_attn_shape *shape, const void *q, const void *gate,

@@ -1,0 +1,897 @@
+// Attention over the paged cache on the tcgen05 tensor cores, for prompts, drafts and shared
+// prefixes: tiles of query rows against the keys, one pass with a running maximum and sum.
+//
+// Rows.  A kv-head's G = Hq / Hkv query heads share its keys, so a tile packs (token, head)
+// rows: row r of a 128-row sub-tile is token r / G, head r % G, tpt = 128 / G tokens in all.
+//
+// Per tile of BN keys, with S = Q K^T in tensor memory and one thread per row:
+//     m' = max(m, scale max_c S_c);  p_c = 2^(scale S_c - m');  l = l 2^(m - m') + sum p_c
+//     O <- O 2^(m - m') + P V
+// (scale includes log2 e).  The reference m only moves when it would rise by more than 8, so
+// that O is rescaled a few times per row at most: p then stays below 2^8 and the result is the
+// same, as l and O share the reference.  P goes to tensor memory as bf16 (V is held in
+// bf16: the product's other operand has no more bits) and l sums the unrounded p in float32.
+//
+// D = 128: two sub-tiles of 128 rows share each K and V tile of 128 keys; while the softmax
+// warps of one work, the tensor cores run the other's products.  Tensor memory: S 2 x 128
+// columns (P over S), O 2 x 128.  D = 256: O of two sub-tiles would fill tensor memory, so one
+// sub-tile, K and V tiles of 64 keys, and two S buffers of 64 columns: the next tile's scores
+// are computed while this one's softmax runs.  Both: 64 KB of Q and a ring of five 32 KB
+// tiles of K and V in shared memory, loaded by TMA page by page.
+//
+// Warps: 4 per sub-tile for the softmax and the epilogue, one for the loads, one for the MMAs.
+#include <cuda.h>
+#include <math_constants.h>
+#include <string.h>
+
+#include "attn.h"
+#include "tc.cuh"
+
+namespace gdn {
+namespace {
+
+constexpr float kLn2 = 0.6931471805599453f;
+
+template <int D_>
+struct Cfg {
+  static constexpr int D = D_;
+  static constexpr int BN = D == 128 ? 128 : 64;    // keys per tile
+  static constexpr int NSUB = D == 128 ? 2 : 1;     // sub-tiles of 128 rows
+  static constexpr int NBUF = D == 128 ? 1 : 2;     // S buffers of a sub-tile
+  static constexpr int STAGES = 5;
+  static constexpr int CH = D / 64;                 // 128-byte column chunks of a row
+  static constexpr int Q_BYTES = 128 * D * 2;       // one sub-tile
+  static constexpr int KV_BYTES = BN * D * 2;
+  static constexpr int SMEM = NSUB * Q_BYTES + STAGES * KV_BYTES;
+  static constexpr int THREADS = 128 * NSUB + 64;
+  static constexpr int ROWS = 128 * NSUB;
+};
+
+// ------------------------------------------------------------------ waits
+
+// Bounded wait that remembers a lost signal: after the first time-out of a CTA every later
+// wait returns at once, so the kernel ends.
+__device__ __forceinline__ void wait_bar(uint64_t *bar, uint32_t parity, volatile int *dead,
+                                         unsigned int *err) {
+  for (int it = 0; it < (1 << 20); ++it) {
+    uint32_t done;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+        " selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(done)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    if (done) return;
+    if ((it & 255) == 255 && *dead) return;
+  }
+  *dead = 1;
+  report_status(err, GDN_STATUS_WAIT_TIMEOUT);
+}
+
+__device__ __forceinline__ void tma_4d(void *dst, const void *map, int x, int y, int z, int w,
+                                       uint64_t *bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, "
+      "{%2, %3, %4, %5}], [%6];\n" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// Descriptors of 128-byte-swizzled operands: K-major (rows of 128 bytes, eight rows per
+// 1024-byte atom) and MN-major (rows along K; `mn` bytes from one 64-column chunk to the next).
+__device__ __forceinline__ uint64_t desc_k(uint32_t saddr) {
+  return (uint64_t)((saddr >> 4) & 0x3FFF) | (1ull << 16) | ((uint64_t)(1024 >> 4) << 32) | (1ull << 46) |
+         (2ull << 61);
+}
+__device__ __forceinline__ uint64_t desc_mn(uint32_t saddr, uint32_t mn) {
+  return (uint64_t)((saddr >> 4) & 0x3FFF) | ((uint64_t)(mn >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+         (1ull << 46) | (2ull << 61);
+}
+
+// Ties loaded registers to the wait before them, so that no use moves above it.
+__device__ __forceinline__ void tie32(uint32_t (&r)[32]) {
+  asm volatile(""
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
+                 "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]),
+                 "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]),
+                 "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]),
+                 "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31]));
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// ------------------------------------------------------------------ plan
+
+// One piece of work of a kv-head: tokens tok0 .. tok0 + ntok - 1 of a sequence against its
+// key tiles kt0 .. kt1 - 1.
+struct Entry {
+  int tok0, ntok, seq, place0;  // place0: place of tok0 (INT_MAX / 2: every key is seen)
+  int kt0, kt1, slot, kvlen;    // slot: partial result's (of kv-head 0, then Hkv apart), -1: final
+};
+struct Split {  // a tile whose parts are joined afterwards
+  int tok0, ntok, slot, parts;
+};
+
+// The plan and the partial results, in the caller's workspace.
+struct TilePlan {
+  int *head;      // [0] entries, [1] tiles to join
+  int *base;      // first tile of each sequence
+  Entry *rec;     // tiles
+  Entry *entry;   // pieces of work, longest first
+  Split *split;   // tiles to join
+  float *ml;      // [slot][row] {m, l}
+  float *part;    // [slot][row][D]
+  int max_tiles, sms, all_slots;
+  int uniform_parts, uniform_kt;  // > 0: no plan, equal parts of equal tiles (shared prefix)
+  unsigned int *err;
+};
+
+__host__ __device__ inline size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+
+// Keys that the last of `ntok` tokens from place0 on sees.
+__device__ __forceinline__ int visible(int place0, int ntok, int kvlen) {
+  return min(max(place0 + ntok, 0), kvlen);
+}
+
+__device__ __forceinline__ void seq_info(const AttnParams &p, int n, int &bos, int &t, int &len) {
+  bos = n;
+  t = 1;
+  if (p.cu_seqlens) {
+    int eos;
+    seq_range(p.cu_seqlens, n, p.tokens, bos, eos);
+    t = eos - bos;
+  }
+  len = (int)min(max((long long)p.kv_lens[n], 0ll), (long long)p.max_pages * p.page_size);
+}
+
+constexpr int kPlanThreads = 1024;
+constexpr int kCand = 16;
+
+// Cuts the batch into entries, one block.  Tiles with many key tiles are split so that the
+// SMs get even shares: of kCand chunk lengths the one with the smallest
+//     max(chunk, ceil(entries / SMs) * mean entry) + 3 ceil(entries / SMs)
+// (in key tiles; 3 is about what starting and ending an entry costs).  Entries are ordered by
+// length, longest first, in 64 classes, for the kernel's back-and-forth assignment to CTAs.
+__global__ void __launch_bounds__(kPlanThreads) plan_kernel(AttnParams p, TilePlan w, int tt, int bn) {
+  __shared__ int sh_scan[32], sh_total, sh_kvmax, sh_cnt[kCand], sh_spl[kCand], sh_hist[64], sh_chunk;
+  __shared__ int sh_slot, sh_nsplit, sh_big[kPlanThreads], sh_nbig;
+  __shared__ unsigned long long sh_work;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");
+  if (tid == 0) sh_total = sh_kvmax = sh_slot = sh_nsplit = 0, sh_work = 0;
+  if (tid < kCand) sh_cnt[tid] = sh_spl[tid] = 0;
+  if (tid < 64) sh_hist[tid] = 0;
+  Entry *rec = w.rec;
+  unsigned long long work = 0;
+  int kvmax = 0;
+  auto put = [&](int at, int bos, int t, int len, int i) {
+    if (at >= w.max_tiles) return;  // only with a malformed cu_seqlens
+    const int tok0 = i * tt, ntok = min(tt, t - tok0);
+    const int kvt = (visible(len - t + tok0, ntok, len) + bn - 1) / bn;
+    rec[at] = Entry{bos + tok0, ntok, 0, len - t + tok0, 0, kvt, 0, len};
+    work += kvt;
+    kvmax = max(kvmax, kvt);
+  };
+  for (int n0 = 0; n0 < p.num_seqs; n0 += kPlanThreads) {
+    const int n = n0 + tid;
+    int bos = 0, t = 0, len = 0;
+    if (n < p.num_seqs) seq_info(p, n, bos, t, len);
+    const int tiles = (t + tt - 1) / tt;
+    int s = tiles;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, s, o);
+      if (lane >= o) s += v;
+    }
+    __syncthreads();
+    if (tid == 0) sh_nbig = 0;
+    if (lane == 31) sh_scan[warp] = s;
+    __syncthreads();
+    int before = sh_total;
+    for (int i = 0; i < warp; ++i) before += sh_scan[i];
+    const int at = before + s - tiles;
+    if (n < p.num_seqs) {
+      w.base[n] = at;
+      if (tiles <= 4) {
+        for (int i = 0; i < tiles; ++i) {
+          put(at + i, bos, t, len, i);
+          if (at + i < w.max_tiles) rec[at + i].seq = n;
+        }
+      } else {
+        sh_big[atomicAdd(&sh_nbig, 1)] = n;
+      }
+    }
+    __syncthreads();
+    if (tid == kPlanThreads - 1) sh_total = before + s;
+    for (int b = 0; b < sh_nbig; ++b) {  // long sequences: all threads over the tiles
+      const int m = sh_big[b];
+      int bos2, t2, len2;
+      seq_info(p, m, bos2, t2, len2);
+      const int at2 = w.base[m];
+      for (int i = tid; i < (t2 + tt - 1) / tt; i += kPlanThreads) {
+        put(at2 + i, bos2, t2, len2, i);
+        if (at2 + i < w.max_tiles) rec[at2 + i].seq = m;
+      }
+    }
+  }
+  atomicAdd(&sh_work, work);
+  atomicMax(&sh_kvmax, kvmax);
+  __syncthreads();
+  const int tiles = min(sh_total, w.max_tiles);
+  kvmax = max(sh_kvmax, 1);
+  // candidates
+  constexpr int parts_of[kCand] = {1, 2, 3, 4, 5, 6, 8, 10, 12, 16, 19, 25, 38, 50, 76, 152};
+  {
+    int cnt[kCand], spl[kCand];
+#pragma unroll
+    for (int j = 0; j < kCand; ++j) cnt[j] = spl[j] = 0;
+    for (int i = tid; i < tiles; i += kPlanThreads) {
+      const int kvt = rec[i].kt1;
+#pragma unroll
+      for (int j = 0; j < kCand; ++j) {
+        const int chunk = (kvmax + parts_of[j] - 1) / parts_of[j];
+        const int parts = max(1, (kvt + chunk - 1) / chunk);
+        cnt[j] += parts;
+        spl[j] += parts > 1 ? parts : 0;
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kCand; ++j) {
+      cnt[j] = __reduce_add_sync(0xffffffffu, cnt[j]);
+      spl[j] = __reduce_add_sync(0xffffffffu, spl[j]);
+      if (lane == 0 && cnt[j]) atomicAdd(&sh_cnt[j], cnt[j]), atomicAdd(&sh_spl[j], spl[j]);
+    }
+  }
+  __syncthreads();
+  if (tid == 0) {
+    float best = CUDART_INF_F;
+    int chunk = kvmax;
+    for (int j = 0; j < kCand; ++j) {
+      const int c = (kvmax + parts_of[j] - 1) / parts_of[j];
+      if (j > 0 && (long long)sh_spl[j] * p.hkv > kSplitSlots) break;
+      const float items = (float)sh_cnt[j] * p.hkv;
+      const float rounds = ceilf(items / w.sms);
+      const float cost = fmaxf((float)c, rounds * ((float)sh_work * p.hkv / fmaxf(items, 1.f))) + 3.f * rounds;
+      if (cost < best) best = cost, chunk = c;
+    }
+    sh_chunk = chunk;
+  }
+  __syncthreads();
+  const int chunk = sh_chunk;
+  auto cls = [&](int len) { return 63 - min(63, len * 63 / chunk); };
+  for (int i = tid; i < tiles; i += kPlanThreads) {
+    const int kvt = rec[i].kt1, parts = max(1, (kvt + chunk - 1) / chunk);
+    for (int q = 0; q < parts; ++q) {
+      const int a = (int)((long long)kvt * q / parts), b = (int)((long long)kvt * (q + 1) / parts);
+      atomicAdd(&sh_hist[cls(b - a)], 1);
+    }
+  }
+  __syncthreads();
+  if (warp == 0) {  // exclusive scan of the 64 classes
+    int a = sh_hist[2 * lane], b = sh_hist[2 * lane + 1], s = a + b;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, s, o);
+      if (lane >= o) s += v;
+    }
+    sh_hist[2 * lane] = s - a - b;
+    sh_hist[2 * lane + 1] = s - b;
+    if (lane == 31) w.head[0] = s;  // number of entries
+  }
+  __syncthreads();
+  for (int i = tid; i < tiles; i += kPlanThreads) {
+    Entry e = rec[i];
+    const int kvt = e.kt1, parts = max(1, (kvt + chunk - 1) / chunk);
+    int slot = -1;
+    if (parts > 1 || w.all_slots) {
+      slot = atomicAdd(&sh_slot, parts) * p.hkv;
+      w.split[atomicAdd(&sh_nsplit, 1)] = Split{e.tok0, e.ntok, slot, parts};
+    }
+    for (int q = 0; q < parts; ++q) {
+      const int a = (int)((long long)kvt * q / parts), b = (int)((long long)kvt * (q + 1) / parts);
+      e.kt0 = a;
+      e.kt1 = b;
+      e.slot = slot < 0 ? -1 : slot + q * p.hkv;
+      w.entry[atomicAdd(&sh_hist[cls(b - a)], 1)] = e;
+    }
+  }
+  __syncthreads();
+  if (tid == 0) w.head[1] = sh_nsplit;
+}
+
+// ------------------------------------------------------------------ the tile kernel
+
+struct Barriers {
+  uint64_t q_full, q_empty, kv_full[5], kv_empty[5], s_full[2], p_full[2], pv_done[2];
+  uint32_t tmem;
+  int dead;
+};
+
+// Work item `i` of this launch: the entry and its kv-head.
+__device__ __forceinline__ bool item_at(const AttnParams &p, const TilePlan &w, int round, int tt, Entry &e,
+                                        int &h) {
+  // back and forth over the CTAs, so that who had the longest entry gets the shortest next
+  const int c = (round & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x;
+  const long long i = (long long)round * gridDim.x + c;
+  if (w.uniform_parts > 0) {  // shared prefix: equal parts of equal tiles
+    const int tiles = (p.tokens + tt - 1) / tt;
+    if (i >= (long long)tiles * w.uniform_parts * p.hkv) return false;
+    h = (int)(i % p.hkv);
+    const int at = (int)(i / p.hkv), tile = at / w.uniform_parts, q = at % w.uniform_parts;
+    const int kvt = w.uniform_kt;
+    e.tok0 = tile * tt;
+    e.ntok = min(tt, p.tokens - e.tok0);
+    e.seq = 0;
+    e.place0 = 0x3fffffff;
+    e.kt0 = (int)((long long)kvt * q / w.uniform_parts);
+    e.kt1 = (int)((long long)kvt * (q + 1) / w.uniform_parts);
+    e.slot = at * p.hkv;
+    e.kvlen = p.prefix_len;
+    return true;
+  }
+  if (i >= (long long)w.head[0] * p.hkv) return false;
+  h = (int)(i % p.hkv);
+  const int4 *src = reinterpret_cast<const int4 *>(w.entry + i / p.hkv);
+  const int4 a = src[0], b = src[1];
+  e = Entry{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  return true;
+}
+
+// Key tiles that sub-tile `i` of an entry takes part in.
+template <int BN>
+__device__ __forceinline__ int sub_tiles(const Entry &e, int i, int tpt) {
+  const int first = i * tpt;
+  if (first >= e.ntok) return 0;
+  const int vis = visible(e.place0, min(e.ntok, first + tpt), e.kvlen);
+  return max(0, min((vis + BN - 1) / BN, e.kt1) - e.kt0);
+}
+
+template <int D>
+__global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
+    tile_kernel(AttnParams p, TilePlan w, const __grid_constant__ CUtensorMap qmap,
+                const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
+  using C = Cfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ Barriers bars;
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  uint8_t *sq = smem, *skv = smem + C::NSUB * C::Q_BYTES;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  volatile int *dead = &bars.dead;
+  const int G = p.hq / p.hkv, tpt = 128 / G, tt = tpt * C::NSUB;
+
+  if (threadIdx.x == 0) {
+    mbar_init(&bars.q_full, 1);
+    mbar_init(&bars.q_empty, 1);
+    for (int i = 0; i < C::STAGES; ++i) mbar_init(&bars.kv_full[i], 1), mbar_init(&bars.kv_empty[i], 1);
+    for (int i = 0; i < 2; ++i)
+      mbar_init(&bars.s_full[i], 1), mbar_init(&bars.p_full[i], 128), mbar_init(&bars.pv_done[i], 1);
+    mbar_fence_init();
+    bars.dead = 0;
+  }
+  if (warp == 4 * C::NSUB) tc::alloc<512>(&bars.tmem);
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  const uint32_t tmem = bars.tmem;
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+
+  Entry e;
+  int h;
+  if (warp < 4 * C::NSUB) {
+    // ---------------------------------------------------------------- softmax, epilogue
+    const int sub = warp >> 2;
+    const int row = threadIdx.x & 127;
+    const float asl = p.scale == 0.f ? 1.f : fabsf(p.scale) * 1.4426950408889634f;
+    uint32_t cnt = 0;  // tiles of this sub-tile so far, over all items
+    for (int round = 0; item_at(p, w, round, tt, e, h); ++round) {
+      const int n = sub_tiles<C::BN>(e, sub, tpt);
+      const int dt = sub * tpt + row / G;
+      const bool live = row < tpt * G && dt < e.ntok;
+      // keys this row sees, counted from the entry's first
+      const int limit = (live ? visible(e.place0, dt + 1, e.kvlen) : 0) - e.kt0 * C::BN;
+      float m = -CUDART_INF_F, l = 0.f;
+      const uint32_t o_base = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + 256 + sub * 128;
+      for (int j = 0; j < n; ++j, ++cnt) {
+        const int b = C::NBUF == 2 ? (cnt & 1) : sub;
+        const uint32_t s_addr = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + (C::NBUF == 2 ? b * 64 : sub * 128);
+        wait_bar(&bars.s_full[b], C::NBUF == 2 ? (cnt >> 1) & 1 : cnt & 1, dead, w.err);
+        // Every completion of P V is waited for in its turn (it has come, or is about to: these
+        // scores were issued after it), so that no wait mistakes an older phase for its own.
+        if (C::NBUF == 2 && j >= 2) wait_bar(&bars.pv_done[b], ((cnt - 2) >> 1) & 1, dead, w.err);
+        if (C::NBUF == 1 && j >= 1) wait_bar(&bars.pv_done[b], (cnt - 1) & 1, dead, w.err);
+        tc::fence_after();
+        uint32_t s[C::BN / 32][32];
+#pragma unroll
+        for (int c = 0; c < C::BN / 32; ++c) tc::ld32(s_addr + 32 * c, s[c]);
+        tc::wait_ld();
+#pragma unroll
+        for (int c = 0; c < C::BN / 32; ++c) tie32(s[c]);
+        if (p.scale <= 0.f) {
+#pragma unroll
+          for (int c = 0; c < C::BN; ++c) {
+            const float x = __uint_as_float(s[c / 32][c % 32]);
+            s[c / 32][c % 32] = __float_as_uint(p.scale == 0.f ? 0.f : -x);
+          }
+        }
+        const int lim = limit - j * C::BN;
+        if (__any_sync(0xffffffffu, lim < C::BN)) {
+#pragma unroll
+          for (int c = 0; c < C::BN; ++c)
+            if (c >= lim) s[c / 32][c % 32] = 0xff800000u;
+        }
+        float mx[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) mx[c] = __uint_as_float(s[0][c]);
+#pragma unroll
+        for (int c = 4; c < C::BN; ++c) mx[c & 3] = fmaxf(mx[c & 3], __uint_as_float(s[c / 32][c % 32]));
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * asl;
+        if (__any_sync(0xffffffffu, top > m + 8.f)) {
+          const float m1 = fmaxf(m, top);
+          const float a = m1 == -CUDART_INF_F ? 1.f : ex2(m - m1);
+          if (j > 0) {
+            if (C::NBUF == 2) {
+              wait_bar(&bars.pv_done[b ^ 1], ((cnt - 1) >> 1) & 1, dead, w.err);
+              tc::fence_after();
+            }
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+              uint32_t o[32];
+              tc::ld32(o_base + c, o);
+              tc::wait_ld();
+              tie32(o);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * a);
+              tc::st32(o_base + c, o);
+            }
+          }
+          l *= a;
+          m = m1;
+        }
+        const float ref = m == -CUDART_INF_F ? 0.f : m;
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < C::BN / 32; ++c) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float x = ex2(fmaf(__uint_as_float(s[c][2 * i]), asl, -ref));
+            const float y = ex2(fmaf(__uint_as_float(s[c][2 * i + 1]), asl, -ref));
+            sum[i & 1] += x;
+            sum[2 + (i & 1)] += y;
+            pk[i] = pack_bf16(x, y);
+          }
+          tc::st16(s_addr + 16 * c, pk);
+        }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        tc::wait_st();
+        tc::fence_before();
+        mbar_arrive(&bars.p_full[b]);
+      }
+      // epilogue
+      if (n > 0) {
+        if (C::NBUF == 2) {
+          if (n > 1) wait_bar(&bars.pv_done[cnt & 1], ((cnt - 2) >> 1) & 1, dead, w.err);
+          wait_bar(&bars.pv_done[(cnt - 1) & 1], ((cnt - 1) >> 1) & 1, dead, w.err);
+        } else {
+          wait_bar(&bars.pv_done[sub], (cnt - 1) & 1, dead, w.err);
+        }
+        tc::fence_after();
+      }
+      const int tok = e.tok0 + dt, head = h * G + row % G;
+      const float inv = l > 0.f ? 1.f / l : 0.f;
+      const long long orow = (long long)tok * p.hq + head;
+      float *part = nullptr;
+      if (e.slot >= 0) {
+        const long long at = (long long)(e.slot + h) * C::ROWS + sub * 128 + row;
+        part = w.part + at * D;
+        if (live) *reinterpret_cast<float2 *>(w.ml + 2 * at) = make_float2(m, l);
+      } else if (live && p.lse) {
+        p.lse[orow] = l > 0.f ? (m + log2f(l)) * kLn2 : -CUDART_INF_F;
+      }
+#pragma unroll 1
+      for (int c = 0; c < D; c += 32) {
+        uint32_t o[32];
+        if (n > 0) {
+          tc::ld32(o_base + c, o);
+          tc::wait_ld();
+          tie32(o);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = 0;
+        }
+        if (!live) continue;
+        if (part) {
+#pragma unroll
+          for (int i = 0; i < 32; i += 4)
+            *reinterpret_cast<uint4 *>(part + c + i) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+          continue;
+        }
+        const __nv_bfloat16 *gate =
+            p.gate ? (const __nv_bfloat16 *)p.gate + tok * p.gs[0] + head * p.gs[1] + c : nullptr;
+        __nv_bfloat16 *out = (__nv_bfloat16 *)p.o + orow * D + c;
+#pragma unroll
+        for (int i = 0; i < 32; i += 8) {
+          float x[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) x[k] = __uint_as_float(o[i + k]) * inv;
+          if (gate) gate8(x, *reinterpret_cast<const uint4 *>(gate + i));
+          *reinterpret_cast<uint4 *>(out + i) = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]),
+                                                           pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+        }
+      }
+      tc::fence_before();
+    }
+  } else if (warp == 4 * C::NSUB) {
+    // ---------------------------------------------------------------- loads
+    const int box = min(p.page_size, C::BN);       // rows of a load
+    const int boxes = C::BN / box;                 // loads of a tile per column chunk
+    const int pi = lane / C::CH, ch = lane % C::CH;  // this lane's box and chunk
+    uint32_t ld = 0, items = 0;
+    for (int round = 0; item_at(p, w, round, tt, e, h); ++round) {
+      int n = 0, nsub = 0;
+#pragma unroll
+      for (int i = 0; i < C::NSUB; ++i) {
+        const int ni = sub_tiles<C::BN>(e, i, tpt);
+        n = max(n, ni);
+        nsub += ni > 0;
+      }
+      if (n == 0) continue;
+      const int32_t *table = w.uniform_parts > 0 ? p.prefix_table : p.page_table + (long long)e.seq * p.max_pages;
+      auto page_of = [&](int j) {  // page of this lane's box of tile j, -1: past the last key
+        const int key = (e.kt0 + j) * C::BN + pi * box;
+        if (pi >= boxes || j >= n || key >= e.kvlen) return -1;
+        const int pg = table[key / p.page_size];
+        return (unsigned)pg < (unsigned)p.num_pages ? pg : p.num_pages;  // out of range: zeros
+      };
+      int next = page_of(0);
+      wait_bar(&bars.q_empty, (items & 1) ^ 1, dead, w.err);
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&bars.q_full, (uint32_t)nsub * C::CH * tpt * G * 128);
+        for (int i = 0; i < C::NSUB; ++i)
+          if (sub_tiles<C::BN>(e, i, tpt) > 0)
+            for (int c = 0; c < C::CH; ++c)
+              tma_load_3d(sq + i * C::Q_BYTES + c * 16384, &qmap, c * 64, h * G, e.tok0 + i * tpt, &bars.q_full);
+      }
+      ++items;
+      for (int j = 0; j < n; ++j) {
+        const int pg = next;
+        next = page_of(j + 1);
+        const int key = (e.kt0 + j) * C::BN + pi * box;
+        const int count = __popc(__ballot_sync(0xffffffffu, pg >= 0));
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv, ++ld) {
+          const uint32_t st = ld % C::STAGES;
+          wait_bar(&bars.kv_empty[st], ((ld / C::STAGES) & 1) ^ 1, dead, w.err);
+          if (lane == 0) mbar_arrive_expect_tx(&bars.kv_full[st], (uint32_t)count * box * 128);
+          __syncwarp();
+          if (pg >= 0)
+            tma_4d(skv + st * C::KV_BYTES + ch * (C::BN * 128) + pi * box * 128, kv ? &vmap : &kmap, ch * 64,
+                   key % p.page_size, h, pg, &bars.kv_full[st]);
+        }
+      }
+    }
+  } else {
+    // ---------------------------------------------------------------- products
+    constexpr uint32_t id_qk = tc::idesc(128, C::BN, 1, 0, 0), id_pv = tc::idesc(128, D, 1, 0, 1);
+    uint32_t ld = 0, items = 0;
+    uint32_t cnt[2] = {0, 0};
+    const uint32_t q_addr = smem_u32(sq), kv_addr = smem_u32(skv);
+    auto qk = [&](int i, uint32_t st, uint32_t c) {
+      const uint32_t d = tmem + (C::NBUF == 2 ? (c & 1) * 64 : i * 128);
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k)
+        tc::mma_ss(d, desc_k(q_addr + i * C::Q_BYTES + (k / 4) * 16384 + (k % 4) * 32),
+                   desc_k(kv_addr + st * C::KV_BYTES + (k / 4) * (C::BN * 128) + (k % 4) * 32), id_qk, k > 0);
+      tc::commit(&bars.s_full[C::NBUF == 2 ? (c & 1) : i]);
+    };
+    for (int round = 0; item_at(p, w, round, tt, e, h); ++round) {
+      int n[2] = {0, 0};
+#pragma unroll
+      for (int i = 0; i < C::NSUB; ++i) n[i] = sub_tiles<C::BN>(e, i, tpt);
+      const int nmax = max(n[0], n[1]);
+      if (nmax == 0) continue;
+      wait_bar(&bars.q_full, items & 1, dead, w.err);
+      ++items;
+      const uint32_t ld0 = ld;
+      auto full = [&](uint32_t at) { wait_bar(&bars.kv_full[at % C::STAGES], (at / C::STAGES) & 1, dead, w.err); };
+      full(ld0);
+      tc::fence_after();
+      if (lane == 0) {
+#pragma unroll
+        for (int i = 0; i < C::NSUB; ++i)
+          if (n[i] > 0) qk(i, ld0 % C::STAGES, cnt[i]);
+        tc::commit(&bars.kv_empty[ld0 % C::STAGES]);
+        if (nmax == 1) tc::commit(&bars.q_empty);
+      }
+      __syncwarp();
+      for (int j = 0; j < nmax; ++j) {
+        const uint32_t lv = ld0 + 2 * j + 1, lk = lv + 1;
+        const uint32_t sv = lv % C::STAGES, sk = lk % C::STAGES;
+        if (C::NBUF == 2 && j + 1 < nmax) {
+          full(lk);
+          tc::fence_after();
+          if (lane == 0) {
+            qk(0, sk, cnt[0] + 1);
+            tc::commit(&bars.kv_empty[sk]);
+            if (j + 2 == nmax) tc::commit(&bars.q_empty);
+          }
+          __syncwarp();
+        }
+        full(lv);
+        const int valid = e.kvlen - (e.kt0 + j) * C::BN;
+        if (valid < C::BN) {  // rows of V past the last key: 0 * NaN is not 0
+          for (int x = lane; x < (C::BN - valid) * C::CH * 8; x += 32) {
+            const int r = valid + x / (C::CH * 8), y = x % (C::CH * 8);
+            *reinterpret_cast<uint4 *>(skv + sv * C::KV_BYTES + (y >> 3) * (C::BN * 128) + r * 128 + (y & 7) * 16) =
+                make_uint4(0, 0, 0, 0);
+          }
+          tc::fence_proxy_async();
+          __syncwarp();
+        }
+#pragma unroll
+        for (int i = 0; i < C::NSUB; ++i) {
+          if (C::NBUF == 1 && i == 0 && j + 1 < nmax) full(lk);
+          if (j >= n[i]) continue;
+          const uint32_t c = cnt[i]++;
+          wait_bar(&bars.p_full[C::NBUF == 2 ? (c & 1) : i], C::NBUF == 2 ? (c >> 1) & 1 : c & 1, dead, w.err);
+          tc::fence_after();
+          if (lane == 0) {
+            const uint32_t pa = tmem + (C::NBUF == 2 ? (c & 1) * 64 : i * 128);
+#pragma unroll
+            for (int k = 0; k < C::BN / 16; ++k)
+              tc::mma_ts(tmem + 256 + i * 128, pa + k * 8, desc_mn(kv_addr + sv * C::KV_BYTES + k * 2048, C::BN * 128),
+                         id_pv, j > 0 || k > 0);
+            tc::commit(&bars.pv_done[C::NBUF == 2 ? (c & 1) : i]);
+            if (C::NBUF == 1 && j + 1 < n[i]) qk(i, sk, c + 1);
+          }
+          __syncwarp();
+        }
+        if (lane == 0) {
+          tc::commit(&bars.kv_empty[sv]);
+          if (C::NBUF == 1 && j + 1 < nmax) {
+            tc::commit(&bars.kv_empty[sk]);
+            if (j + 2 == nmax) tc::commit(&bars.q_empty);
+          }
+        }
+        __syncwarp();
+      }
+      ld = ld0 + 2 * nmax;
+    }
+  }
+  if (*dead) __nanosleep(1000000);  // copies in flight land before shared memory is given up
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  if (warp == 4 * C::NSUB) tc::dealloc<512>(tmem);
+}
+
+// ------------------------------------------------------------------ join
+
+// One warp per row: the row's partial results (m_i, l_i, O_i) to
+//     M = max m_i,  o = sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i.
+// Rows: those of the split tiles in the plan's table, plus for each the shared prefix's parts.
+template <int D>
+__global__ void __launch_bounds__(256) join_kernel(AttnParams p, TilePlan w, TilePlan pre, int tpt) {
+  constexpr int E = D / 32, ROWS = Cfg<D>::ROWS;
+  const int lane = threadIdx.x & 31;
+  const int G = p.hq / p.hkv, tt = tpt * Cfg<D>::NSUB;
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+  const long long rows = (long long)w.head[1] * p.hkv * (tt * G);
+  const long long step = (long long)gridDim.x * 8;
+  for (long long i = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); i < rows; i += step) {
+    const int r = (int)(i % (tt * G)), h = (int)(i / (tt * G) % p.hkv);
+    const Split s = w.split[i / (tt * G) / p.hkv];
+    const int dt = r / G, g = r % G;
+    if (dt >= s.ntok) continue;
+    const int tok = s.tok0 + dt, head = h * G + g;
+    float acc[E] = {}, m = -CUDART_INF_F, l = 0.f;
+    auto take = [&](const TilePlan &src, int slot, int parts, int off) {
+      const int srow = off / tpt * 128 + (off % tpt) * G + g;
+      for (int q = 0; q < parts; ++q) {
+        const long long at = (long long)(slot + q * p.hkv + h) * ROWS + srow;
+        const float2 ml = *reinterpret_cast<const float2 *>(src.ml + 2 * at);
+        if (!(ml.y > 0.f)) continue;
+        const float m1 = fmaxf(m, ml.x), a = ex2(m - m1), b = ex2(ml.x - m1);
+        m = m1;
+        l = l * a + ml.y * b;
+        const float *o = src.part + at * D + lane * 4;
+#pragma unroll
+        for (int k = 0; k < E / 4; ++k) {
+          const float4 v = *reinterpret_cast<const float4 *>(o + 128 * k);
+          acc[4 * k] = acc[4 * k] * a + v.x * b;
+          acc[4 * k + 1] = acc[4 * k + 1] * a + v.y * b;
+          acc[4 * k + 2] = acc[4 * k + 2] * a + v.z * b;
+          acc[4 * k + 3] = acc[4 * k + 3] * a + v.w * b;
+        }
+      }
+    };
+    if (pre.uniform_parts > 0) take(pre, tok / tt * pre.uniform_parts * p.hkv, pre.uniform_parts, tok % tt);
+    take(w, s.slot, s.parts, dt);
+    const long long orow = (long long)tok * p.hq + head;
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+#pragma unroll
+    for (int k = 0; k < E / 4; ++k) {
+      float x[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) x[q] = acc[4 * k + q] * inv;
+      if (p.gate)
+        gate4(x, *reinterpret_cast<const uint2 *>((const __nv_bfloat16 *)p.gate + tok * p.gs[0] + head * p.gs[1] +
+                                                  lane * 4 + 128 * k));
+      *reinterpret_cast<uint2 *>((__nv_bfloat16 *)p.o + orow * D + lane * 4 + 128 * k) =
+          make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
+    }
+    if (p.lse && lane == 0) p.lse[orow] = l > 0.f ? (m + log2f(l)) * kLn2 : -CUDART_INF_F;
+  }
+}
+
+// ------------------------------------------------------------------ host
+
+using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
+                                   const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
+                                   const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiledFn encode_tiled() {
+  static EncodeTiledFn fn = []() -> EncodeTiledFn {
+    void *f = nullptr;
+    cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) !=
+            cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      return nullptr;
+    return reinterpret_cast<EncodeTiledFn>(f);
+  }();
+  return fn;
+}
+
+cudaError_t encode(CUtensorMap *map, const void *x, int rank, const cuuint64_t *dims, const cuuint64_t *strides,
+                   const cuuint32_t *box) {
+  EncodeTiledFn enc = encode_tiled();
+  if (!enc) return cudaErrorNotSupported;
+  const cuuint32_t one[4] = {1, 1, 1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void *>(x), dims, strides, box, one,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? cudaSuccess
+             : cudaErrorInvalidValue;
+}
+
+struct Maps {
+  CUtensorMap q, k, v;
+};
+
+template <int D>
+cudaError_t make_maps(Maps &m, const AttnParams &p) {
+  memset(&m, 0, sizeof(m));
+  const int G = p.hq / p.hkv, tpt = 128 / G;
+  {
+    const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)p.hq, (cuuint64_t)p.tokens};
+    const cuuint64_t strides[2] = {(cuuint64_t)p.qs[1] * 2, (cuuint64_t)p.qs[0] * 2};
+    const cuuint32_t box[3] = {64, (cuuint32_t)G, (cuuint32_t)tpt};
+    const cudaError_t err = encode(&m.q, p.q, 3, dims, strides, box);
+    if (err != cudaSuccess) return err;
+  }
+  if (p.num_pages == 0) return cudaSuccess;  // no key, no load
+  const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)p.page_size, (cuuint64_t)p.hkv, (cuuint64_t)p.num_pages};
+  const cuuint64_t strides[3] = {(cuuint64_t)D * 2, (cuuint64_t)p.page_size * D * 2, (cuuint64_t)p.page_stride * 2};
+  const cuuint32_t box[4] = {64, (cuuint32_t)(p.page_size < Cfg<D>::BN ? p.page_size : Cfg<D>::BN), 1, 1};
+  const cudaError_t err = encode(&m.k, p.k_cache, 4, dims, strides, box);
+  return err != cudaSuccess ? err : encode(&m.v, p.v_cache, 4, dims, strides, box);
+}
+
+// Launch as a programmatic dependent of the work before it on the stream.
+template <typename... Args>
+cudaError_t launch(void (*kernel)(Args...), unsigned grid, unsigned threads, size_t smem, cudaStream_t stream,
+                   Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// Tokens of a tile, tiles of a call at most, tiles of the shared prefix's pass.
+template <int D>
+struct Sizes {
+  int tpt, tt, max_tiles, prefix_tiles;
+  Sizes(int tokens, int num_seqs, int hq, int hkv) {
+    tpt = 128 / (hq / hkv);
+    tt = tpt * Cfg<D>::NSUB;
+    max_tiles = tokens / tt + num_seqs;
+    prefix_tiles = (tokens + tt - 1) / tt;
+  }
+};
+
+// Parts that each tile of the prefix pass is cut into: as many as fill the SMs once, of at
+// least two key tiles each.
+template <int D>
+int prefix_parts(int tiles, int hkv, int prefix_len) {
+  const int kt = (prefix_len + Cfg<D>::BN - 1) / Cfg<D>::BN;
+  const int fill = kSms / (int)(((long long)tiles * hkv < kSms) ? tiles * hkv : kSms);
+  const int most = (kt + 1) / 2;
+  return fill < 1 ? 1 : fill < most ? fill : most;
+}
+
+template <int D>
+size_t layout(TilePlan *own, TilePlan *pre, char *ws, int num_seqs, int tokens, int hq, int hkv, int prefix_len) {
+  const Sizes<D> z(tokens, num_seqs, hq, hkv);
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    char *r = ws ? ws + at : nullptr;
+    at += up256(bytes);
+    return r;
+  };
+  const int entries = z.max_tiles + kSplitSlots;
+  const size_t own_slots = prefix_len > 0 ? (size_t)z.max_tiles * hkv + kSplitSlots : kSplitSlots;
+  const size_t slot = (size_t)Cfg<D>::ROWS * sizeof(float);
+  TilePlan a{}, b{};
+  a.head = (int *)take(256);
+  a.base = (int *)take(sizeof(int) * (size_t)(num_seqs + 1));
+  a.rec = (Entry *)take(sizeof(Entry) * (size_t)z.max_tiles);
+  a.entry = (Entry *)take(sizeof(Entry) * (size_t)entries);
+  a.split = (Split *)take(sizeof(Split) * (size_t)(prefix_len > 0 ? z.max_tiles : kSplitSlots));
+  a.ml = (float *)take(own_slots * slot * 2);
+  a.part = (float *)take(own_slots * slot * D);
+  a.max_tiles = z.max_tiles;
+  if (prefix_len > 0) {
+    b.uniform_parts = prefix_parts<D>(z.prefix_tiles, hkv, prefix_len);
+    b.uniform_kt = (prefix_len + Cfg<D>::BN - 1) / Cfg<D>::BN;
+    const size_t slots = (size_t)z.prefix_tiles * b.uniform_parts * hkv;
+    b.ml = (float *)take(slots * slot * 2);
+    b.part = (float *)take(slots * slot * D);
+    a.all_slots = 1;
+  }
+  if (own) *own = a;
+  if (pre) *pre = b;
+  return at;
+}
+
+template <int D>
+cudaError_t run(const AttnParams &p, char *ws, unsigned int *errw, cudaStream_t stream) {
+  using C = Cfg<D>;
+  const Sizes<D> z(p.tokens, p.num_seqs, p.hq, p.hkv);
+  TilePlan own, pre;
+  layout<D>(&own, &pre, ws, p.num_seqs, p.tokens, p.hq, p.hkv, p.prefix_len);
+  own.err = pre.err = errw;
+  own.sms = pre.sms = kSms;
+  Maps m;
+  cudaError_t err = make_maps<D>(m, p);
+  if (err != cudaSuccess) return err;
+  const size_t smem = C::SMEM + 1024;
+  err = cudaFuncSetAttribute(tile_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (err != cudaSuccess) return err;
+  err = launch(plan_kernel, 1, kPlanThreads, 0, stream, p, own, z.tt, C::BN);
+  if (err != cudaSuccess) return err;
+  if (p.prefix_len > 0) {
+    err = launch(tile_kernel<D>, kSms, C::THREADS, smem, stream, p, pre, m.q, m.k, m.v);
+    if (err != cudaSuccess) return err;
+  }
+  err = launch(tile_kernel<D>, kSms, C::THREADS, smem, stream, p, own, m.q, m.k, m.v);
+  if (err != cudaSuccess) return err;
+  return launch(join_kernel<D>, 4 * kSms, 256, 0, stream, p, own, pre, z.tpt);
+}
+
+}  // namespace
+
+size_t attn_tile_workspace(int num_seqs, int tokens, int hq, int hkv, int d, int prefix_len) {
+  return d == 128 ? layout<128>(nullptr, nullptr, nullptr, num_seqs, tokens, hq, hkv, prefix_len)
+                  : layout<256>(nullptr, nullptr, nullptr, num_seqs, tokens, hq, hkv, prefix_len);
+}
+
+cudaError_t launch_attn_tile(const AttnParams &p, void *ws, unsigned int *err, cudaStream_t stream) {
+  return p.d == 128 ? run<128>(p, static_cast<char *>(ws), err, stream)
+                    : run<256>(p, static_cast<char *>(ws), err, stream);
+}
+
+}  // namespace gdn

@@ -233,6 +233,10 @@ gdn_status check_split(const gdn_shape *s, int32_t seg_len) {
 
 }  // namespace
 
+namespace gdn {
+unsigned int *device_status_word() { return status_word(); }
+}  // namespace gdn
+
 extern "C" {
 
 size_t gdn_prefill_split_workspace_size(const gdn_shape *shape, int32_t segment_len) {
