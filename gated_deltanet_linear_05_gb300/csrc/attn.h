@@ -44,8 +44,14 @@ struct AttnParams {
 
 constexpr int kSms = 152;          // persistent CTAs, and the shares that work is cut into
 constexpr int kSplitSlots = 304;   // partial results of split tiles, over all kv-heads
-size_t attn_tile_workspace(int num_seqs, int tokens, int hq, int hkv, int d, int prefix_len);
-cudaError_t launch_attn_tile(const AttnParams &p, void *ws, unsigned int *err, cudaStream_t stream);
+constexpr int kStepRows = 16;      // query heads per kv-head that the decode kernel takes
+// Either attention call: picks the kernels and lays out the workspace (attn_tile.cu).
+size_t attn_workspace(int num_seqs, int tokens, int hq, int hkv, int d, int prefix_len);
+cudaError_t launch_attention(const AttnParams &p, void *ws, unsigned int *err, cudaStream_t stream);
+// One token per sequence (attn_step.cu); with `dense` the rows' {m, l} and sums go there.
+size_t attn_step_workspace(int d);
+cudaError_t launch_attn_step(const AttnParams &p, void *ws, float *dense_ml, float *dense, unsigned int *err,
+                             cudaStream_t stream);
 
 // The library's device status word on the current device (gdn_api.cu), or NULL.
 unsigned int *device_status_word();

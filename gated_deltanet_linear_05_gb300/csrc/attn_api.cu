@@ -112,7 +112,7 @@ gdn_status attention(const gdn_attn_shape *s, const void *q, const void *gate, c
   p.cu_seqlens = cu_seqlens;
   p.o = o;
   p.lse = lse;
-  return cuda_status(gdn::launch_attn_tile(p, workspace, gdn::device_status_word(),
+  return cuda_status(gdn::launch_attention(p, workspace, gdn::device_status_word(),
                                            static_cast<cudaStream_t>(stream)));
 }
 
@@ -122,8 +122,8 @@ extern "C" {
 
 size_t gdn_attn_workspace_size(const gdn_attn_shape *shape) {
   if (check_shape(shape) != GDN_OK) return (size_t)-1;
-  return gdn::attn_tile_workspace(shape->num_seqs, shape->total_tokens, shape->num_q_heads,
-                                  shape->num_kv_heads, shape->head_dim, shape->prefix_len);
+  return gdn::attn_workspace(shape->num_seqs, shape->total_tokens, shape->num_q_heads,
+                             shape->num_kv_heads, shape->head_dim, shape->prefix_len);
 }
 
 gdn_status gdn_paged_attention(const gdn_attn_shape *shape, const void *q, const void *gate,

@@ -1,0 +1,460 @@
+// Attention of one token per sequence over the paged cache (decode): bound by reading every
+// key and value once from HBM.
+//
+// The batch's key tiles of 64, over all sequences and kv-heads in a row, are dealt out to the
+// CTAs in equal runs, so that ragged contexts load every SM alike; a run may begin and end
+// inside a sequence.  A (sequence, kv-head) pair that lies in one run is finished there; else
+// each run leaves a partial result (m, l, O) in the workspace and the CTA that arrives last
+// joins them in the order of the keys.
+//
+// The G <= 16 query heads of a kv-head are the rows of m16n8k16 products.  A warp takes 16
+// keys of each tile with a running maximum and sum of its own, so that the warps meet only
+// at the end of a pair; with D = 256 a second set of warps takes the upper half of V's
+// columns (and repeats the scores: the shared memory they are read from has the bandwidth to spare).
+// One warp keeps a ring of K and V tiles full by TMA: 160 KB in flight per SM.
+#include <cuda.h>
+#include <math_constants.h>
+#include <string.h>
+
+#include "attn.h"
+#include "attn_tma.cuh"
+
+namespace gdn {
+namespace {
+
+constexpr int kTile = 64;  // keys
+
+template <int D_>
+struct StepCfg {
+  static constexpr int D = D_;
+  static constexpr int HALVES = D / 128;
+  static constexpr int WARPS = 4 * HALVES;             // consumers
+  static constexpr int THREADS = 32 * (WARPS + 1);
+  static constexpr int CTAS = kSms * (D == 128 ? 2 : 1);
+  static constexpr int UNIT = kTile * D * 2;           // bytes of a K or V tile
+  static constexpr int STAGES = 5;
+  static constexpr int CH = D / 64;
+  static constexpr int RP = 132;                       // padded row of the join buffers (floats)
+  static constexpr int R_BYTES = HALVES * 2 * 16 * RP * 4;
+  static constexpr int SMEM = STAGES * UNIT + 16 * D * 2 + R_BYTES;
+};
+
+struct StepPlan {
+  unsigned int *arrived;  // [CTAS] parts finished of the pair that begins in that CTA's run
+  float *ml, *part;       // [2 CTAS][16] {m, l}, [2 CTAS][16][D]
+  float *dense_ml, *dense;  // rows' results left for a join (shared prefix), or NULL
+  unsigned int *err;
+};
+
+__device__ __forceinline__ int seq_len(const AttnParams &p, int n) {
+  return (int)min(max((long long)p.kv_lens[n], 0ll), (long long)p.max_pages * p.page_size);
+}
+__device__ __forceinline__ int tiles_of(int len) { return max(1, (len + kTile - 1) / kTile); }
+
+// Byte offset of (row, col) in a tile of 64 rows: 64-column chunks in TMA's 128-byte swizzle.
+__device__ __forceinline__ uint32_t sw_off(int row, int col) {
+  return (uint32_t)((col >> 6) * (kTile * 128) + row * 128 + ((((col >> 3) & 7) ^ (row & 7)) << 4));
+}
+
+template <int D>
+__global__ void __launch_bounds__(StepCfg<D>::THREADS, D == 128 ? 2 : 1)
+    step_kernel(AttnParams p, StepPlan w, const __grid_constant__ CUtensorMap kmap,
+                const __grid_constant__ CUtensorMap vmap) {
+  using C = StepCfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ uint64_t full[C::STAGES], empty[C::STAGES];
+  __shared__ int sh_dead, sh_last, sh_n, sh_scan[C::WARPS + 1];
+  __shared__ long long sh_base, sh_total;
+  __shared__ float sh_m[C::WARPS][16], sh_l[C::WARPS][16];
+  uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  uint8_t *sq = ring + C::STAGES * C::UNIT;
+  float *sr = reinterpret_cast<float *>(sq + 16 * D * 2);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int G = p.hq / p.hkv;
+  volatile int *dead = &sh_dead;
+  if (tid == 0) {
+    for (int i = 0; i < C::STAGES; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], C::WARPS);
+    mbar_fence_init();
+    sh_dead = 0;
+    sh_total = 0;
+  }
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+  __syncthreads();
+
+  // The run of this CTA: tiles [x0, x1) of all, and the sequence that x0 lies in.
+  long long mine = 0;
+  for (int n = tid; n < p.num_seqs; n += C::THREADS) mine += tiles_of(seq_len(p, n));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+  if (lane == 0) atomicAdd(reinterpret_cast<unsigned long long *>(&sh_total), (unsigned long long)mine);
+  __syncthreads();
+  const long long total = sh_total * p.hkv;
+  const long long ctas = min((long long)gridDim.x, total);
+  if (blockIdx.x >= ctas) return;
+  const long long x0 = total * blockIdx.x / ctas, x1 = total * (blockIdx.x + 1) / ctas;
+  {
+    long long before = 0;  // tiles of one kv-head before the chunk of sequences
+    for (int n0 = 0; n0 < p.num_seqs; n0 += C::THREADS) {
+      const int n = n0 + tid;
+      const int t = n < p.num_seqs ? tiles_of(seq_len(p, n)) : 0;
+      int s = t;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, s, o);
+        if (lane >= o) s += v;
+      }
+      if (lane == 31) sh_scan[warp] = s;
+      __syncthreads();
+      long long at = before;
+      for (int i = 0; i < warp; ++i) at += sh_scan[i];
+      at += s - t;
+      if (t > 0 && at * p.hkv <= x0 && x0 < (at + t) * p.hkv) sh_n = n, sh_base = at * p.hkv;
+      for (int i = 0; i <= C::WARPS; ++i) before += sh_scan[i];
+      __syncthreads();
+      if (before * p.hkv > x0) break;
+    }
+  }
+  int n = sh_n;
+  long long base = sh_base;  // first tile of sequence n
+  const float asl = p.scale == 0.f ? 1.f : fabsf(p.scale) * 1.4426950408889634f;
+  const float flip = p.scale == 0.f ? 0.f : p.scale < 0.f ? -1.f : 1.f;
+  uint32_t ld = 0;
+
+  if (warp == C::WARPS) {
+    // ---------------------------------------------------------------- loads
+    const int box = min(p.page_size, kTile), boxes = kTile / box;
+    const int pi = lane / C::CH, ch = lane % C::CH;
+    for (long long x = x0; x < x1;) {
+      const int len = seq_len(p, n), tiles = tiles_of(len);
+      const long long rem = x - base;
+      const int h = (int)(rem / tiles), j0 = (int)(rem % tiles);
+      const int j1 = (int)min((long long)tiles, j0 + (x1 - x));
+      const int32_t *table = p.page_table + (long long)n * p.max_pages;
+      auto page_of = [&](int j) {
+        const int key = j * kTile + pi * box;
+        if (pi >= boxes || j >= j1 || key >= len) return -1;
+        const int pg = table[key / p.page_size];
+        return (unsigned)pg < (unsigned)p.num_pages ? pg : p.num_pages;  // out of range: zeros
+      };
+      if (len > 0) {
+        int next = page_of(j0);
+        for (int j = j0; j < j1; ++j) {
+          const int pg = next;
+          next = page_of(j + 1);
+          const int count = __popc(__ballot_sync(0xffffffffu, pg >= 0));
+#pragma unroll
+          for (int kv = 0; kv < 2; ++kv, ++ld) {
+            const uint32_t st = ld % C::STAGES;
+            wait_bar(&empty[st], ((ld / C::STAGES) & 1) ^ 1, dead, w.err);
+            if (lane == 0) mbar_arrive_expect_tx(&full[st], (uint32_t)count * box * 128);
+            __syncwarp();
+            if (pg >= 0)
+              tma_4d(ring + st * C::UNIT + ch * (kTile * 128) + pi * box * 128, kv ? &vmap : &kmap, ch * 64,
+                     (j * kTile + pi * box) % p.page_size, h, pg, &full[st]);
+          }
+        }
+      }
+      x += j1 - j0;
+      if (j1 == tiles && h == p.hkv - 1) base += (long long)tiles * p.hkv, ++n;
+    }
+    if (*dead) __nanosleep(1000000);  // copies in flight land before shared memory is given up
+    return;
+  }
+
+  // ------------------------------------------------------------------ scores, softmax, sums
+  const int kg = warp & 3, hf = warp >> 2;
+  const int gid = lane >> 2, tig = lane & 3;
+  const int kr = kg * 16;                                       // this warp's keys in a tile
+  const int nthr = 32 * C::WARPS;
+  for (long long x = x0; x < x1;) {
+    const int len = seq_len(p, n), tiles = tiles_of(len);
+    const long long rem = x - base;
+    const int h = (int)(rem / tiles), j0 = (int)(rem % tiles);
+    const int j1 = (int)min((long long)tiles, j0 + (x1 - x));
+    const long long pair0 = base + (long long)h * tiles;  // first tile of the pair
+    // the pair's query rows, zero past G, in the layout that ldmatrix reads (the last pair's
+    // rows were done with before its join)
+    for (int i = tid; i < 16 * (D / 8); i += nthr) {
+      const int r = i / (D / 8), c = (i % (D / 8)) * 8;
+      uint4 u = make_uint4(0, 0, 0, 0);
+      if (r < G)
+        u = *reinterpret_cast<const uint4 *>((const __nv_bfloat16 *)p.q + n * p.qs[0] + (h * G + r) * p.qs[1] + c);
+      *reinterpret_cast<uint4 *>(sq + (c >> 6) * 2048 + r * 128 + ((((c >> 3) & 7) ^ (r & 7)) << 4)) = u;
+    }
+    bar_sync(1, nthr);
+    const int qrow = (lane & 7) + ((lane >> 3) & 1) * 8;
+    auto q_frag = [&](uint32_t (&a)[4], int k) {
+      const int c = k * 16 + (lane >> 4) * 8;
+      ldsm_x4(a, sq + (c >> 6) * 2048 + qrow * 128 + ((((c >> 3) & 7) ^ (qrow & 7)) << 4));
+    };
+    uint32_t qa[D == 128 ? 8 : 1][4];
+    if (D == 128)
+#pragma unroll
+      for (int k = 0; k < (D == 128 ? 8 : 1); ++k) q_frag(qa[k], k);
+    float o[16][4] = {};
+    float m[2] = {-CUDART_INF_F, -CUDART_INF_F}, l[2] = {0.f, 0.f};
+    for (int j = j0; j < j1 && len > 0; ++j) {
+      // scores of 16 rows and this warp's 16 keys
+      uint32_t st = ld % C::STAGES;
+      wait_bar(&full[st], (ld / C::STAGES) & 1, dead, w.err);
+      const uint8_t *kt = ring + st * C::UNIT;
+      float s[2][4] = {};
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+        uint32_t b[4];
+        ldsm_x4(b, kt + sw_off(kr + (lane & 7) + (lane >> 4) * 8, k * 16 + ((lane >> 3) & 1) * 8));
+        if (D == 128) {
+          mma_bf16(s[0], qa[k & 7], b[0], b[1]);
+          mma_bf16(s[1], qa[k & 7], b[2], b[3]);
+        } else {
+          uint32_t a[4];
+          q_frag(a, k);
+          mma_bf16(s[0], a, b[0], b[1]);
+          mma_bf16(s[1], a, b[2], b[3]);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[st]);
+      ++ld;
+      const int left = len - j * kTile - kr;  // live keys among the warp's 16
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          s[t][i] *= flip;
+          if (t * 8 + 2 * tig + (i & 1) >= left) s[t][i] = -CUDART_INF_F;
+        }
+      float top[2];
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        top[r] = fmaxf(fmaxf(s[0][2 * r], s[0][2 * r + 1]), fmaxf(s[1][2 * r], s[1][2 * r + 1]));
+        top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 1));
+        top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 2)) * asl;
+      }
+      // the reference moves when it would rise by more than 8 (2^8 is far from overflow)
+      if (__any_sync(0xffffffffu, top[0] > m[0] + 8.f || top[1] > m[1] + 8.f)) {
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const float m1 = fmaxf(m[r], top[r]);
+          const float a = m1 == -CUDART_INF_F ? 1.f : ex2(m[r] - m1);
+          m[r] = m1;
+          l[r] *= a;
+#pragma unroll
+          for (int t = 0; t < 16; ++t) o[t][2 * r] *= a, o[t][2 * r + 1] *= a;
+        }
+      }
+      uint32_t pa[4];
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const float ref = m[r] == -CUDART_INF_F ? 0.f : m[r];
+        float e[2][2];
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            e[t][i] = ex2(fmaf(s[t][2 * r + i], asl, -ref));
+            l[r] += e[t][i];
+          }
+        pa[r] = pack_bf16(e[0][0], e[0][1]);
+        pa[2 + r] = pack_bf16(e[1][0], e[1][1]);
+      }
+      // O += P V over the 16 keys; V rows past the last key count as zero whatever they hold
+      st = ld % C::STAGES;
+      wait_bar(&full[st], (ld / C::STAGES) & 1, dead, w.err);
+      const uint8_t *vt = ring + st * C::UNIT;
+      uint32_t keep[2] = {0xffffffffu, 0xffffffffu};
+      if (left < 16) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int k = 2 * tig + 8 * i;
+          keep[i] = (k < left ? 0xffffu : 0u) | (k + 1 < left ? 0xffff0000u : 0u);
+        }
+      }
+#pragma unroll
+      for (int t = 0; t < 8; ++t) {
+        uint32_t b[4];
+        ldsm_x4_t(b, vt + sw_off(kr + (lane & 7) + ((lane >> 3) & 1) * 8, hf * 128 + t * 16 + (lane >> 4) * 8));
+        mma_bf16(o[2 * t], pa, b[0] & keep[0], b[1] & keep[1]);
+        mma_bf16(o[2 * t + 1], pa, b[2] & keep[0], b[3] & keep[1]);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[st]);
+      ++ld;
+    }
+
+    // join the warps: one maximum per row, then O in a tree over the four key groups
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+      if (tig == 0) sh_m[warp][gid + 8 * r] = m[r];
+    }
+    bar_sync(1, nthr);
+    float top[2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int row = gid + 8 * r;
+      top[r] = fmaxf(fmaxf(sh_m[hf * 4][row], sh_m[hf * 4 + 1][row]),
+                     fmaxf(sh_m[hf * 4 + 2][row], sh_m[hf * 4 + 3][row]));
+      const float a = top[r] == -CUDART_INF_F ? 0.f : ex2(m[r] - top[r]);
+      if (tig == 0) sh_l[warp][row] = l[r] * a;
+#pragma unroll
+      for (int t = 0; t < 16; ++t) o[t][2 * r] *= a, o[t][2 * r + 1] *= a;
+    }
+    auto put = [&](float *buf) {
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+        if (gid + 8 * r < G)
+#pragma unroll
+          for (int t = 0; t < 16; ++t)
+            *reinterpret_cast<float2 *>(buf + (gid + 8 * r) * C::RP + 8 * t + 2 * tig) =
+                make_float2(o[t][2 * r], o[t][2 * r + 1]);
+    };
+    auto add = [&](const float *buf) {
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+        if (gid + 8 * r < G)
+#pragma unroll
+          for (int t = 0; t < 16; ++t) {
+            const float2 v = *reinterpret_cast<const float2 *>(buf + (gid + 8 * r) * C::RP + 8 * t + 2 * tig);
+            o[t][2 * r] += v.x;
+            o[t][2 * r + 1] += v.y;
+          }
+    };
+    float *r0 = sr + hf * 2 * 16 * C::RP, *r1 = r0 + 16 * C::RP;
+    if (kg >= 2) put(kg == 2 ? r0 : r1);
+    bar_sync(1, nthr);
+    if (kg < 2) add(kg == 0 ? r0 : r1);
+    bar_sync(1, nthr);
+    if (kg == 1) put(r1);
+    bar_sync(1, nthr);
+    if (kg == 0) add(r1), put(r0);
+    bar_sync(1, nthr);
+
+    // a row of the pair to its place: final, or left for a join
+    auto emit = [&](int r, float mm, float ll, const float (&v)[D / 32]) {
+      const long long row = (long long)n * p.hq + h * G + r;
+      if (w.dense) {
+        if (lane == 0) *reinterpret_cast<float2 *>(w.dense_ml + 2 * row) = make_float2(mm, ll);
+#pragma unroll
+        for (int k = 0; k < D / 128; ++k)
+          *reinterpret_cast<float4 *>(w.dense + row * D + 128 * k + 4 * lane) =
+              make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+        return;
+      }
+      emit_row<D>(p, n, h * G + r, lane, mm, ll, v);
+    };
+    const bool whole = j0 == 0 && j1 == tiles;
+    const long long slot = 2ll * blockIdx.x + (j0 == 0);
+    for (int r = warp; r < G; r += C::WARPS) {
+      const float mm = fmaxf(fmaxf(sh_m[0][r], sh_m[1][r]), fmaxf(sh_m[2][r], sh_m[3][r]));
+      const float ll = (sh_l[0][r] + sh_l[1][r]) + (sh_l[2][r] + sh_l[3][r]);
+      float v[D / 32];
+#pragma unroll
+      for (int k = 0; k < D / 128; ++k) {
+        const float4 u = *reinterpret_cast<const float4 *>(sr + k * 2 * 16 * C::RP + r * C::RP + 4 * lane);
+        v[4 * k] = u.x, v[4 * k + 1] = u.y, v[4 * k + 2] = u.z, v[4 * k + 3] = u.w;
+      }
+      if (whole) {
+        emit(r, mm, ll, v);
+      } else {
+        if (lane == 0) *reinterpret_cast<float2 *>(w.ml + 2 * (slot * 16 + r)) = make_float2(mm, ll);
+#pragma unroll
+        for (int k = 0; k < D / 128; ++k)
+          *reinterpret_cast<float4 *>(w.part + (slot * 16 + r) * D + 128 * k + 4 * lane) =
+              make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+      }
+    }
+    if (!whole) {
+      // the runs that the pair lies in: c owns tile x iff total c / ctas <= x < total (c + 1) / ctas
+      const int c0 = (int)(((pair0 + 1) * ctas - 1) / total), c1 = (int)(((pair0 + tiles) * ctas - 1) / total);
+      __threadfence();
+      bar_sync(1, nthr);
+      if (tid == 0) {
+        sh_last = atomicAdd(&w.arrived[c0], 1u) == (unsigned)(c1 - c0);
+        if (sh_last) w.arrived[c0] = 0;  // ready for the next call
+      }
+      bar_sync(1, nthr);
+      if (sh_last) {
+        __threadfence();
+        for (int r = warp; r < G; r += C::WARPS) {
+          // parts c0 (which began the pair, slot 2 c0 + 1) to c1 (slots 2 c)
+          auto at = [&](int c) { return (2ll * c + (c == c0)) * 16 + r; };
+          float mm = -CUDART_INF_F;
+          for (int c = c0 + lane; c <= c1; c += 32) mm = fmaxf(mm, __ldcg(w.ml + 2 * at(c)));
+#pragma unroll
+          for (int k = 16; k > 0; k >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, k));
+          float ll = 0.f, v[D / 32] = {};
+          if (mm > -CUDART_INF_F) {
+#pragma unroll 4
+            for (int c = c0; c <= c1; ++c) {
+              const float2 q = __ldcg(reinterpret_cast<const float2 *>(w.ml + 2 * at(c)));
+              const float a = ex2(q.x - mm);
+              ll = fmaf(q.y, a, ll);
+#pragma unroll
+              for (int k = 0; k < D / 128; ++k) {
+                const float4 u = __ldcg(reinterpret_cast<const float4 *>(w.part + at(c) * D + 128 * k + 4 * lane));
+                v[4 * k] = fmaf(u.x, a, v[4 * k]);
+                v[4 * k + 1] = fmaf(u.y, a, v[4 * k + 1]);
+                v[4 * k + 2] = fmaf(u.z, a, v[4 * k + 2]);
+                v[4 * k + 3] = fmaf(u.w, a, v[4 * k + 3]);
+              }
+            }
+          }
+          emit(r, mm, ll, v);
+        }
+      }
+    }
+    x += j1 - j0;
+    if (j1 == tiles && h == p.hkv - 1) base += (long long)tiles * p.hkv, ++n;
+  }
+}
+
+template <int D>
+size_t layout(StepPlan *out, char *ws) {
+  using C = StepCfg<D>;
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    char *r = ws ? ws + at : nullptr;
+    at += up256(bytes);
+    return r;
+  };
+  StepPlan a{};
+  a.arrived = (unsigned int *)take(kArrivedBytes);
+  a.ml = (float *)take(sizeof(float) * 2 * 16 * 2 * C::CTAS);
+  a.part = (float *)take(sizeof(float) * 16 * D * 2 * C::CTAS);
+  if (out) *out = a;
+  return at;
+}
+
+template <int D>
+cudaError_t run(const AttnParams &p, char *ws, float *dense_ml, float *dense, unsigned int *errw,
+                cudaStream_t stream) {
+  using C = StepCfg<D>;
+  static_assert(C::CTAS * sizeof(unsigned int) <= kArrivedBytes, "counters");
+  StepPlan w;
+  layout<D>(&w, ws);
+  w.dense_ml = dense_ml;
+  w.dense = dense;
+  w.err = errw;
+  CUtensorMap k, v;
+  cudaError_t err = cache_maps(&k, &v, p, kTile);
+  if (err != cudaSuccess) return err;
+  const size_t smem = C::SMEM + 1024;
+  err = cudaFuncSetAttribute(step_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (err != cudaSuccess) return err;
+  return launch_dependent(step_kernel<D>, C::CTAS, C::THREADS, smem, stream, p, w, k, v);
+}
+
+}  // namespace
+
+size_t attn_step_workspace(int d) { return d == 128 ? layout<128>(nullptr, nullptr) : layout<256>(nullptr, nullptr); }
+
+cudaError_t launch_attn_step(const AttnParams &p, void *ws, float *dense_ml, float *dense, unsigned int *err,
+                             cudaStream_t stream) {
+  return p.d == 128 ? run<128>(p, static_cast<char *>(ws), dense_ml, dense, err, stream)
+                    : run<256>(p, static_cast<char *>(ws), dense_ml, dense, err, stream);
+}
+
+}  // namespace gdn

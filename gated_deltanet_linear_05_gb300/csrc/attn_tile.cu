@@ -25,12 +25,11 @@
 #include <string.h>
 
 #include "attn.h"
+#include "attn_tma.cuh"
 #include "tc.cuh"
 
 namespace gdn {
 namespace {
-
-constexpr float kLn2 = 0.6931471805599453f;
 
 template <int D_>
 struct Cfg {
@@ -47,35 +46,7 @@ struct Cfg {
   static constexpr int ROWS = 128 * NSUB;
 };
 
-// ------------------------------------------------------------------ waits
-
-// Bounded wait that remembers a lost signal: after the first time-out of a CTA every later
-// wait returns at once, so the kernel ends.
-__device__ __forceinline__ void wait_bar(uint64_t *bar, uint32_t parity, volatile int *dead,
-                                         unsigned int *err) {
-  for (int it = 0; it < (1 << 20); ++it) {
-    uint32_t done;
-    asm volatile(
-        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
-        " selp.u32 %0, 1, 0, p;\n}\n"
-        : "=r"(done)
-        : "r"(smem_u32(bar)), "r"(parity)
-        : "memory");
-    if (done) return;
-    if ((it & 255) == 255 && *dead) return;
-  }
-  *dead = 1;
-  report_status(err, GDN_STATUS_WAIT_TIMEOUT);
-}
-
-__device__ __forceinline__ void tma_4d(void *dst, const void *map, int x, int y, int z, int w,
-                                       uint64_t *bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, "
-      "{%2, %3, %4, %5}], [%6];\n" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
-      : "memory");
-}
+// ------------------------------------------------------------------ operands
 
 // Descriptors of 128-byte-swizzled operands: K-major (rows of 128 bytes, eight rows per
 // 1024-byte atom) and MN-major (rows along K; `mn` bytes from one 64-column chunk to the next).
@@ -96,12 +67,6 @@ __device__ __forceinline__ void tie32(uint32_t (&r)[32]) {
                  "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]),
                  "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]),
                  "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31]));
-}
-
-__device__ __forceinline__ float ex2(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(r) : "f"(x));
-  return r;
 }
 
 // ------------------------------------------------------------------ plan
@@ -125,12 +90,11 @@ struct TilePlan {
   Split *split;   // tiles to join
   float *ml;      // [slot][row] {m, l}
   float *part;    // [slot][row][D]
+  float *dense_ml, *dense;  // one result per row of the call instead (attn_step.cu), or NULL
   int max_tiles, sms, all_slots;
   int uniform_parts, uniform_kt;  // > 0: no plan, equal parts of equal tiles (shared prefix)
   unsigned int *err;
 };
-
-__host__ __device__ inline size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
 // Keys that the last of `ntok` tokens from place0 on sees.
 __device__ __forceinline__ int visible(int place0, int ntok, int kvlen) {
@@ -674,7 +638,8 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
 
 // One warp per row: the row's partial results (m_i, l_i, O_i) to
 //     M = max m_i,  o = sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i.
-// Rows: those of the split tiles in the plan's table, plus for each the shared prefix's parts.
+// Rows: those of the split tiles in the plan's table, or with own results in `dense` (one
+// per row) all rows of the call; for each also the shared prefix's parts.
 template <int D>
 __global__ void __launch_bounds__(256) join_kernel(AttnParams p, TilePlan w, TilePlan pre, int tpt) {
   constexpr int E = D / 32, ROWS = Cfg<D>::ROWS;
@@ -682,123 +647,62 @@ __global__ void __launch_bounds__(256) join_kernel(AttnParams p, TilePlan w, Til
   const int G = p.hq / p.hkv, tt = tpt * Cfg<D>::NSUB;
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
-  const long long rows = (long long)w.head[1] * p.hkv * (tt * G);
+  const long long rows = w.dense ? (long long)p.tokens * p.hq : (long long)w.head[1] * p.hkv * (tt * G);
   const long long step = (long long)gridDim.x * 8;
   for (long long i = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); i < rows; i += step) {
-    const int r = (int)(i % (tt * G)), h = (int)(i / (tt * G) % p.hkv);
-    const Split s = w.split[i / (tt * G) / p.hkv];
-    const int dt = r / G, g = r % G;
-    if (dt >= s.ntok) continue;
-    const int tok = s.tok0 + dt, head = h * G + g;
+    int tok, h, g, dt = 0;
+    Split s{};
+    if (w.dense) {
+      tok = (int)(i / p.hq);
+      h = (int)(i % p.hq) / G;
+      g = (int)(i % p.hq) % G;
+    } else {
+      const int r = (int)(i % (tt * G));
+      h = (int)(i / (tt * G) % p.hkv);
+      s = w.split[i / (tt * G) / p.hkv];
+      dt = r / G;
+      g = r % G;
+      if (dt >= s.ntok) continue;
+      tok = s.tok0 + dt;
+    }
     float acc[E] = {}, m = -CUDART_INF_F, l = 0.f;
-    auto take = [&](const TilePlan &src, int slot, int parts, int off) {
-      const int srow = off / tpt * 128 + (off % tpt) * G + g;
-      for (int q = 0; q < parts; ++q) {
-        const long long at = (long long)(slot + q * p.hkv + h) * ROWS + srow;
-        const float2 ml = *reinterpret_cast<const float2 *>(src.ml + 2 * at);
-        if (!(ml.y > 0.f)) continue;
-        const float m1 = fmaxf(m, ml.x), a = ex2(m - m1), b = ex2(ml.x - m1);
-        m = m1;
-        l = l * a + ml.y * b;
-        const float *o = src.part + at * D + lane * 4;
+    auto take = [&](const float *ml_of, const float *part_of, long long at) {
+      const float2 ml = *reinterpret_cast<const float2 *>(ml_of + 2 * at);
+      if (!(ml.y > 0.f)) return;
+      const float m1 = fmaxf(m, ml.x), a = ex2(m - m1), b = ex2(ml.x - m1);
+      m = m1;
+      l = l * a + ml.y * b;
+      const float *o = part_of + at * D + lane * 4;
 #pragma unroll
-        for (int k = 0; k < E / 4; ++k) {
-          const float4 v = *reinterpret_cast<const float4 *>(o + 128 * k);
-          acc[4 * k] = acc[4 * k] * a + v.x * b;
-          acc[4 * k + 1] = acc[4 * k + 1] * a + v.y * b;
-          acc[4 * k + 2] = acc[4 * k + 2] * a + v.z * b;
-          acc[4 * k + 3] = acc[4 * k + 3] * a + v.w * b;
-        }
+      for (int k = 0; k < E / 4; ++k) {
+        const float4 v = *reinterpret_cast<const float4 *>(o + 128 * k);
+        acc[4 * k] = acc[4 * k] * a + v.x * b;
+        acc[4 * k + 1] = acc[4 * k + 1] * a + v.y * b;
+        acc[4 * k + 2] = acc[4 * k + 2] * a + v.z * b;
+        acc[4 * k + 3] = acc[4 * k + 3] * a + v.w * b;
       }
     };
-    if (pre.uniform_parts > 0) take(pre, tok / tt * pre.uniform_parts * p.hkv, pre.uniform_parts, tok % tt);
-    take(w, s.slot, s.parts, dt);
-    const long long orow = (long long)tok * p.hq + head;
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-#pragma unroll
-    for (int k = 0; k < E / 4; ++k) {
-      float x[4];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) x[q] = acc[4 * k + q] * inv;
-      if (p.gate)
-        gate4(x, *reinterpret_cast<const uint2 *>((const __nv_bfloat16 *)p.gate + tok * p.gs[0] + head * p.gs[1] +
-                                                  lane * 4 + 128 * k));
-      *reinterpret_cast<uint2 *>((__nv_bfloat16 *)p.o + orow * D + lane * 4 + 128 * k) =
-          make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
-    }
-    if (p.lse && lane == 0) p.lse[orow] = l > 0.f ? (m + log2f(l)) * kLn2 : -CUDART_INF_F;
+    auto take_parts = [&](const TilePlan &src, int slot, int parts, int off) {
+      const int srow = off / tpt * 128 + (off % tpt) * G + g;
+      for (int q = 0; q < parts; ++q)
+        take(src.ml, src.part, (long long)(slot + q * p.hkv + h) * ROWS + srow);
+    };
+    if (pre.uniform_parts > 0) take_parts(pre, tok / tt * pre.uniform_parts * p.hkv, pre.uniform_parts, tok % tt);
+    if (w.dense) take(w.dense_ml, w.dense, i);
+    else take_parts(w, s.slot, s.parts, dt);
+    emit_row<D>(p, tok, h * G + g, lane, m, l, acc);
   }
 }
 
 // ------------------------------------------------------------------ host
 
-using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
-                                   const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
-                                   const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-EncodeTiledFn encode_tiled() {
-  static EncodeTiledFn fn = []() -> EncodeTiledFn {
-    void *f = nullptr;
-    cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) !=
-            cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      return nullptr;
-    return reinterpret_cast<EncodeTiledFn>(f);
-  }();
-  return fn;
-}
-
-cudaError_t encode(CUtensorMap *map, const void *x, int rank, const cuuint64_t *dims, const cuuint64_t *strides,
-                   const cuuint32_t *box) {
-  EncodeTiledFn enc = encode_tiled();
-  if (!enc) return cudaErrorNotSupported;
-  const cuuint32_t one[4] = {1, 1, 1, 1};
-  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void *>(x), dims, strides, box, one,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
-             ? cudaSuccess
-             : cudaErrorInvalidValue;
-}
-
-struct Maps {
-  CUtensorMap q, k, v;
-};
-
-template <int D>
-cudaError_t make_maps(Maps &m, const AttnParams &p) {
-  memset(&m, 0, sizeof(m));
-  const int G = p.hq / p.hkv, tpt = 128 / G;
-  {
-    const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)p.hq, (cuuint64_t)p.tokens};
-    const cuuint64_t strides[2] = {(cuuint64_t)p.qs[1] * 2, (cuuint64_t)p.qs[0] * 2};
-    const cuuint32_t box[3] = {64, (cuuint32_t)G, (cuuint32_t)tpt};
-    const cudaError_t err = encode(&m.q, p.q, 3, dims, strides, box);
-    if (err != cudaSuccess) return err;
-  }
-  if (p.num_pages == 0) return cudaSuccess;  // no key, no load
-  const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)p.page_size, (cuuint64_t)p.hkv, (cuuint64_t)p.num_pages};
-  const cuuint64_t strides[3] = {(cuuint64_t)D * 2, (cuuint64_t)p.page_size * D * 2, (cuuint64_t)p.page_stride * 2};
-  const cuuint32_t box[4] = {64, (cuuint32_t)(p.page_size < Cfg<D>::BN ? p.page_size : Cfg<D>::BN), 1, 1};
-  const cudaError_t err = encode(&m.k, p.k_cache, 4, dims, strides, box);
-  return err != cudaSuccess ? err : encode(&m.v, p.v_cache, 4, dims, strides, box);
-}
-
-// Launch as a programmatic dependent of the work before it on the stream.
-template <typename... Args>
-cudaError_t launch(void (*kernel)(Args...), unsigned grid, unsigned threads, size_t smem, cudaStream_t stream,
-                   Args... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
+// Tensor map of q for boxes of one sub-tile's rows: tpt tokens x G heads x 64 columns.
+cudaError_t q_map(CUtensorMap *map, const AttnParams &p) {
+  const int G = p.hq / p.hkv;
+  const cuuint64_t dims[3] = {(cuuint64_t)p.d, (cuuint64_t)p.hq, (cuuint64_t)p.tokens};
+  const cuuint64_t strides[2] = {(cuuint64_t)p.qs[1] * 2, (cuuint64_t)p.qs[0] * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)G, (cuuint32_t)(128 / G)};
+  return bf16_map(map, p.q, 3, dims, strides, box);
 }
 
 // Tokens of a tile, tiles of a call at most, tiles of the shared prefix's pass.
@@ -824,7 +728,8 @@ int prefix_parts(int tiles, int hkv, int prefix_len) {
 }
 
 template <int D>
-size_t layout(TilePlan *own, TilePlan *pre, char *ws, int num_seqs, int tokens, int hq, int hkv, int prefix_len) {
+size_t layout(TilePlan *own, TilePlan *pre, char *ws, int num_seqs, int tokens, int hq, int hkv, int prefix_len,
+              bool dense) {
   const Sizes<D> z(tokens, num_seqs, hq, hkv);
   size_t at = 0;
   auto take = [&](size_t bytes) {
@@ -836,6 +741,11 @@ size_t layout(TilePlan *own, TilePlan *pre, char *ws, int num_seqs, int tokens, 
   const size_t own_slots = prefix_len > 0 ? (size_t)z.max_tiles * hkv + kSplitSlots : kSplitSlots;
   const size_t slot = (size_t)Cfg<D>::ROWS * sizeof(float);
   TilePlan a{}, b{};
+  if (dense) {
+    const size_t rows = (size_t)tokens * hq;
+    a.dense_ml = (float *)take(rows * 2 * sizeof(float));
+    a.dense = (float *)take(rows * D * sizeof(float));
+  }
   a.head = (int *)take(256);
   a.base = (int *)take(sizeof(int) * (size_t)(num_seqs + 1));
   a.rec = (Entry *)take(sizeof(Entry) * (size_t)z.max_tiles);
@@ -859,39 +769,92 @@ size_t layout(TilePlan *own, TilePlan *pre, char *ws, int num_seqs, int tokens, 
 
 template <int D>
 cudaError_t run(const AttnParams &p, char *ws, unsigned int *errw, cudaStream_t stream) {
+  // one token per sequence: the decode kernel does the sequences' own keys
+  const bool step = !p.cu_seqlens && p.hq / p.hkv <= kStepRows;
+  char *tile_ws = ws + attn_step_workspace(D);
   using C = Cfg<D>;
   const Sizes<D> z(p.tokens, p.num_seqs, p.hq, p.hkv);
+  if (step && p.prefix_len == 0) return launch_attn_step(p, ws, nullptr, nullptr, errw, stream);
   TilePlan own, pre;
-  layout<D>(&own, &pre, ws, p.num_seqs, p.tokens, p.hq, p.hkv, p.prefix_len);
+  layout<D>(&own, &pre, tile_ws, p.num_seqs, p.tokens, p.hq, p.hkv, p.prefix_len, step && p.prefix_len > 0);
   own.err = pre.err = errw;
   own.sms = pre.sms = kSms;
-  Maps m;
-  cudaError_t err = make_maps<D>(m, p);
+  CUtensorMap q, k, v;
+  cudaError_t err = q_map(&q, p);
+  if (err == cudaSuccess) err = cache_maps(&k, &v, p, C::BN);
   if (err != cudaSuccess) return err;
   const size_t smem = C::SMEM + 1024;
   err = cudaFuncSetAttribute(tile_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (err != cudaSuccess) return err;
-  err = launch(plan_kernel, 1, kPlanThreads, 0, stream, p, own, z.tt, C::BN);
-  if (err != cudaSuccess) return err;
   if (p.prefix_len > 0) {
-    err = launch(tile_kernel<D>, kSms, C::THREADS, smem, stream, p, pre, m.q, m.k, m.v);
+    err = launch_dependent(tile_kernel<D>, kSms, C::THREADS, smem, stream, p, pre, q, k, v);
     if (err != cudaSuccess) return err;
   }
-  err = launch(tile_kernel<D>, kSms, C::THREADS, smem, stream, p, own, m.q, m.k, m.v);
+  if (step) {
+    err = launch_attn_step(p, ws, own.dense_ml, own.dense, errw, stream);
+  } else {
+    err = launch_dependent(plan_kernel, 1, kPlanThreads, 0, stream, p, own, z.tt, C::BN);
+    if (err != cudaSuccess) return err;
+    err = launch_dependent(tile_kernel<D>, kSms, C::THREADS, smem, stream, p, own, q, k, v);
+  }
   if (err != cudaSuccess) return err;
-  return launch(join_kernel<D>, 4 * kSms, 256, 0, stream, p, own, pre, z.tpt);
+  return launch_dependent(join_kernel<D>, 4 * kSms, 256, 0, stream, p, own, pre, z.tpt);
 }
 
 }  // namespace
 
-size_t attn_tile_workspace(int num_seqs, int tokens, int hq, int hkv, int d, int prefix_len) {
-  return d == 128 ? layout<128>(nullptr, nullptr, nullptr, num_seqs, tokens, hq, hkv, prefix_len)
-                  : layout<256>(nullptr, nullptr, nullptr, num_seqs, tokens, hq, hkv, prefix_len);
+size_t attn_workspace(int num_seqs, int tokens, int hq, int hkv, int d, int prefix_len) {
+  // the decode kernel's part first (its counters stay in one place), then the larger of the
+  // layouts with and without cu_seqlens
+  const bool dense = prefix_len > 0;
+  return d == 128 ? attn_step_workspace(128) +
+                        layout<128>(nullptr, nullptr, nullptr, num_seqs, tokens, hq, hkv, prefix_len, dense)
+                  : attn_step_workspace(256) +
+                        layout<256>(nullptr, nullptr, nullptr, num_seqs, tokens, hq, hkv, prefix_len, dense);
 }
 
-cudaError_t launch_attn_tile(const AttnParams &p, void *ws, unsigned int *err, cudaStream_t stream) {
+cudaError_t launch_attention(const AttnParams &p, void *ws, unsigned int *err, cudaStream_t stream) {
   return p.d == 128 ? run<128>(p, static_cast<char *>(ws), err, stream)
                     : run<256>(p, static_cast<char *>(ws), err, stream);
+}
+
+using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
+                                   const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
+                                   const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+cudaError_t bf16_map(CUtensorMap *map, const void *x, int rank, const cuuint64_t *dims,
+                     const cuuint64_t *strides, const cuuint32_t *box) {
+  // cuTensorMapEncodeTiled from the driver, looked up once (no link against libcuda)
+  static EncodeTiledFn enc = []() -> EncodeTiledFn {
+    void *f = nullptr;
+    cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) !=
+            cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      return nullptr;
+    return reinterpret_cast<EncodeTiledFn>(f);
+  }();
+  if (!enc) return cudaErrorNotSupported;
+  const cuuint32_t one[4] = {1, 1, 1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void *>(x), dims, strides, box, one,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? cudaSuccess
+             : cudaErrorInvalidValue;
+}
+
+cudaError_t cache_maps(CUtensorMap *k, CUtensorMap *v, const AttnParams &p, int tile) {
+  memset(k, 0, sizeof(*k));
+  memset(v, 0, sizeof(*v));
+  if (p.num_pages == 0) return cudaSuccess;
+  const cuuint64_t dims[4] = {(cuuint64_t)p.d, (cuuint64_t)p.page_size, (cuuint64_t)p.hkv,
+                              (cuuint64_t)p.num_pages};
+  const cuuint64_t strides[3] = {(cuuint64_t)p.d * 2, (cuuint64_t)p.page_size * p.d * 2,
+                                 (cuuint64_t)p.page_stride * 2};
+  const cuuint32_t box[4] = {64, (cuuint32_t)(p.page_size < tile ? p.page_size : tile), 1, 1};
+  const cudaError_t err = bf16_map(k, p.k_cache, 4, dims, strides, box);
+  return err != cudaSuccess ? err : bf16_map(v, p.v_cache, 4, dims, strides, box);
 }
 
 }  // namespace gdn

@@ -1,0 +1,100 @@
+// What the attention kernels share: bounded waits, TMA loads and tensor maps of the paged
+// cache, the output of a row, launches.
+#pragma once
+
+#include <cuda.h>
+#include <math_constants.h>
+#include <string.h>
+
+#include "attn.h"
+#include "common.cuh"
+
+namespace gdn {
+
+constexpr float kLn2 = 0.6931471805599453f;
+// Counters at the start of an attention workspace: zero before the first call and after
+// every one, at the same place for all shapes.
+constexpr size_t kArrivedBytes = 2048;
+
+__host__ __device__ inline size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+
+// Bounded wait that remembers a lost signal: after the first time-out of a CTA every later
+// wait returns soon, so the kernel ends.
+__device__ __forceinline__ void wait_bar(uint64_t *bar, uint32_t parity, volatile int *dead,
+                                         unsigned int *err) {
+  for (int it = 0; it < (1 << 20); ++it) {
+    uint32_t done;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+        " selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(done)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    if (done) return;
+    if ((it & 255) == 255 && *dead) return;
+  }
+  *dead = 1;
+  report_status(err, GDN_STATUS_WAIT_TIMEOUT);
+}
+
+__device__ __forceinline__ void tma_4d(void *dst, const void *map, int x, int y, int z, int w,
+                                       uint64_t *bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, "
+      "{%2, %3, %4, %5}], [%6];\n" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
+      : "memory");
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// A row (token, head) of the output by one warp: lane l has columns 128 k + 4 l .. + 3 of the
+// sum O (v[4 k ..]) with the maximum m (base 2) and the sum l.
+template <int D>
+__device__ __forceinline__ void emit_row(const AttnParams &p, int tok, int head, int lane, float m, float l,
+                                         const float (&v)[D / 32]) {
+  const long long row = (long long)tok * p.hq + head;
+  const float inv = l > 0.f ? 1.f / l : 0.f;
+#pragma unroll
+  for (int k = 0; k < D / 128; ++k) {
+    float x[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) x[q] = v[4 * k + q] * inv;
+    if (p.gate)
+      gate4(x, *reinterpret_cast<const uint2 *>((const __nv_bfloat16 *)p.gate + tok * p.gs[0] + head * p.gs[1] +
+                                                lane * 4 + 128 * k));
+    *reinterpret_cast<uint2 *>((__nv_bfloat16 *)p.o + row * D + lane * 4 + 128 * k) =
+        make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
+  }
+  if (p.lse && lane == 0) p.lse[row] = l > 0.f ? (m + log2f(l)) * kLn2 : -CUDART_INF_F;
+}
+
+// Tensor map of a bf16 tensor with 128-byte swizzle (boxes of 64 columns).
+cudaError_t bf16_map(CUtensorMap *map, const void *x, int rank, const cuuint64_t *dims,
+                     const cuuint64_t *strides, const cuuint32_t *box);
+// Maps of K and V, [page][head][row][column], for boxes of min(page_size, tile) rows; zero
+// (and never used) for a cache without pages.
+cudaError_t cache_maps(CUtensorMap *k, CUtensorMap *v, const AttnParams &p, int tile);
+
+// Launch as a programmatic dependent of the work before it on the stream.
+template <typename... Args>
+cudaError_t launch_dependent(void (*kernel)(Args...), unsigned grid, unsigned threads, size_t smem,
+                             cudaStream_t stream, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+}  // namespace gdn
