@@ -69,7 +69,7 @@ __global__ void __launch_bounds__(StepCfg<D>::THREADS, D == 128 ? 2 : 1)
   uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   uint8_t *sq = ring + C::STAGES * C::UNIT;
   float *sr = reinterpret_cast<float *>(sq + 16 * D * 2);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
   const int G = p.hq / p.hkv;
   volatile int *dead = &sh_dead;
   if (tid == 0) {

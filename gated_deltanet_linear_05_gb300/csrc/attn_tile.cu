@@ -42,7 +42,8 @@ struct Cfg {
   static constexpr int Q_BYTES = 128 * D * 2;       // one sub-tile
   static constexpr int KV_BYTES = BN * D * 2;
   static constexpr int SMEM = NSUB * Q_BYTES + STAGES * KV_BYTES;
-  static constexpr int THREADS = 128 * NSUB + 64;
+  static constexpr int THREADS = D == 128 ? 384 : 192;  // (two warps idle with D = 128)
+  static constexpr int PARTS = D == 128 ? 2 : 1;    // P is handed over in so many pieces
   static constexpr int ROWS = 128 * NSUB;
 };
 
@@ -67,6 +68,33 @@ __device__ __forceinline__ void tie32(uint32_t (&r)[32]) {
                  "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]),
                  "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]),
                  "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31]));
+}
+
+// Pairs of floats in one instruction.
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};\n" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;\n" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.ftz.f32x2 %0, %1, %2, %3;\n" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.ftz.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;\n" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
 }
 
 // ------------------------------------------------------------------ plan
@@ -270,7 +298,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(AttnParams p, TilePl
 // ------------------------------------------------------------------ the tile kernel
 
 struct Barriers {
-  uint64_t q_full, q_empty, kv_full[5], kv_empty[5], s_full[2], p_full[2], pv_done[2];
+  uint64_t q_full, q_empty, kv_full[5], kv_empty[5], s_full[2], p_full[2][2], pv_done[2];
   uint32_t tmem;
   int dead;
 };
@@ -323,7 +351,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
   __shared__ Barriers bars;
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   uint8_t *sq = smem, *skv = smem + C::NSUB * C::Q_BYTES;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   volatile int *dead = &bars.dead;
   const int G = p.hq / p.hkv, tpt = 128 / G, tt = tpt * C::NSUB;
 
@@ -332,7 +360,8 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
     mbar_init(&bars.q_empty, 1);
     for (int i = 0; i < C::STAGES; ++i) mbar_init(&bars.kv_full[i], 1), mbar_init(&bars.kv_empty[i], 1);
     for (int i = 0; i < 2; ++i)
-      mbar_init(&bars.s_full[i], 1), mbar_init(&bars.p_full[i], 128), mbar_init(&bars.pv_done[i], 1);
+      mbar_init(&bars.s_full[i], 1), mbar_init(&bars.p_full[i][0], 128), mbar_init(&bars.p_full[i][1], 128),
+          mbar_init(&bars.pv_done[i], 1);
     mbar_fence_init();
     bars.dead = 0;
   }
@@ -346,6 +375,12 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
 
   Entry e;
   int h;
+  // D = 128: 12 warps start with 168 registers each; the eight softmax warps take 224 and the
+  // other four keep 56 (8 x 224 + 4 x 56 = 12 x 168)
+  if (D == 128) {
+    if (warp < 8) asm volatile("setmaxnreg.inc.sync.aligned.u32 224;\n");
+    else asm volatile("setmaxnreg.dec.sync.aligned.u32 56;\n");
+  }
   if (warp < 4 * C::NSUB) {
     // ---------------------------------------------------------------- softmax, epilogue
     const int sub = warp >> 2;
@@ -392,8 +427,10 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
 #pragma unroll
         for (int c = 0; c < 4; ++c) mx[c] = __uint_as_float(s[0][c]);
 #pragma unroll
-        for (int c = 4; c < C::BN; ++c) mx[c & 3] = fmaxf(mx[c & 3], __uint_as_float(s[c / 32][c % 32]));
-        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * asl;
+        for (int c = 4; c < C::BN; c += 2)
+          mx[(c >> 1) & 3] = max3(mx[(c >> 1) & 3], __uint_as_float(s[c / 32][c % 32]),
+                                  __uint_as_float(s[c / 32][c % 32 + 1]));
+        const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * asl;
         if (__any_sync(0xffffffffu, top > m + 8.f)) {
           const float m1 = fmaxf(m, top);
           const float a = m1 == -CUDART_INF_F ? 1.f : ex2(m - m1);
@@ -417,24 +454,28 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
           m = m1;
         }
         const float ref = m == -CUDART_INF_F ? 0.f : m;
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        const uint64_t asl2 = pack2(asl, asl), ref2 = pack2(-ref, -ref);
+        uint64_t sum[2] = {0, 0};
 #pragma unroll
         for (int c = 0; c < C::BN / 32; ++c) {
           uint32_t pk[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            const float x = ex2(fmaf(__uint_as_float(s[c][2 * i]), asl, -ref));
-            const float y = ex2(fmaf(__uint_as_float(s[c][2 * i + 1]), asl, -ref));
-            sum[i & 1] += x;
-            sum[2 + (i & 1)] += y;
-            pk[i] = pack_bf16(x, y);
+            const float2 x =
+                unpack2(fma2(pack2(__uint_as_float(s[c][2 * i]), __uint_as_float(s[c][2 * i + 1])), asl2, ref2));
+            const float a = ex2(x.x), b2 = ex2(x.y);
+            sum[i & 1] = add2(sum[i & 1], pack2(a, b2));
+            pk[i] = pack_bf16(a, b2);
           }
           tc::st16(s_addr + 16 * c, pk);
+          if ((c + 1) % (C::BN / 32 / C::PARTS) == 0) {
+            tc::wait_st();
+            tc::fence_before();
+            mbar_arrive(&bars.p_full[b][C::PARTS == 2 ? c / 2 : 0]);
+          }
         }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-        tc::wait_st();
-        tc::fence_before();
-        mbar_arrive(&bars.p_full[b]);
+        const float2 su = unpack2(add2(sum[0], sum[1]));
+        l += su.x + su.y;
       }
       // epilogue
       if (n > 0) {
@@ -539,55 +580,70 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
         }
       }
     }
-  } else {
+  } else if (warp == 4 * C::NSUB + 1) {
     // ---------------------------------------------------------------- products
+    // All values here are the same in every lane and known as such (uniform()): the
+    // instruction takes its descriptors from uniform registers, and building them from
+    // lane-varying ones made issuing a product (95 cycles) slower than the product (64).
     constexpr uint32_t id_qk = tc::idesc(128, C::BN, 1, 0, 0), id_pv = tc::idesc(128, D, 1, 0, 1);
-    uint32_t ld = 0, items = 0;
+    constexpr uint32_t kStage = C::KV_BYTES >> 4;
+    const uint32_t tm = uniform(tmem);
+    const uint64_t dq = desc_k(uniform(smem_u32(sq))), dk = desc_k(uniform(smem_u32(skv))),
+                   dv = desc_mn(uniform(smem_u32(skv)), C::BN * 128);
+    uint32_t st = 0, ph = 0, items = 0;  // ring position of the next K or V tile, its parity
     uint32_t cnt[2] = {0, 0};
-    const uint32_t q_addr = smem_u32(sq), kv_addr = smem_u32(skv);
-    auto qk = [&](int i, uint32_t st, uint32_t c) {
-      const uint32_t d = tmem + (C::NBUF == 2 ? (c & 1) * 64 : i * 128);
+    auto qk = [&](int i, uint32_t at, uint32_t c) {
+      const uint32_t d = tm + (C::NBUF == 2 ? (c & 1) * 64 : i * 128);
+      const uint64_t a = dq + i * (C::Q_BYTES >> 4), b = dk + at * kStage;
+      if (elect_one()) {
 #pragma unroll
-      for (int k = 0; k < D / 16; ++k)
-        tc::mma_ss(d, desc_k(q_addr + i * C::Q_BYTES + (k / 4) * 16384 + (k % 4) * 32),
-                   desc_k(kv_addr + st * C::KV_BYTES + (k / 4) * (C::BN * 128) + (k % 4) * 32), id_qk, k > 0);
-      tc::commit(&bars.s_full[C::NBUF == 2 ? (c & 1) : i]);
+        for (int k = 0; k < D / 16; ++k)
+          tc::mma_ss(d, a + (((k / 4) * 16384 + (k % 4) * 32) >> 4),
+                     b + (((k / 4) * (C::BN * 128) + (k % 4) * 32) >> 4), id_qk, k > 0);
+        tc::commit(&bars.s_full[C::NBUF == 2 ? (c & 1) : i]);
+      }
+      __syncwarp();
+    };
+    auto done = [&](uint64_t *bar) {
+      if (elect_one()) tc::commit(bar);
+      __syncwarp();
     };
     for (int round = 0; item_at(p, w, round, tt, e, h); ++round) {
       int n[2] = {0, 0};
 #pragma unroll
-      for (int i = 0; i < C::NSUB; ++i) n[i] = sub_tiles<C::BN>(e, i, tpt);
+      for (int i = 0; i < C::NSUB; ++i) n[i] = uniform(sub_tiles<C::BN>(e, i, tpt));
       const int nmax = max(n[0], n[1]);
+      const int keys = uniform(e.kvlen - e.kt0 * C::BN);
       if (nmax == 0) continue;
       wait_bar(&bars.q_full, items & 1, dead, w.err);
       ++items;
-      const uint32_t ld0 = ld;
-      auto full = [&](uint32_t at) { wait_bar(&bars.kv_full[at % C::STAGES], (at / C::STAGES) & 1, dead, w.err); };
-      full(ld0);
+      auto next = [&](uint32_t &at, uint32_t &parity) {  // takes the ring's next tile
+        at = st;
+        parity = ph;
+        if (++st == C::STAGES) st = 0, ph ^= 1;
+      };
+      uint32_t sk, pk, sv, pv;
+      next(sk, pk);
+      wait_bar(&bars.kv_full[sk], pk, dead, w.err);
       tc::fence_after();
-      if (lane == 0) {
 #pragma unroll
-        for (int i = 0; i < C::NSUB; ++i)
-          if (n[i] > 0) qk(i, ld0 % C::STAGES, cnt[i]);
-        tc::commit(&bars.kv_empty[ld0 % C::STAGES]);
-        if (nmax == 1) tc::commit(&bars.q_empty);
-      }
-      __syncwarp();
+      for (int i = 0; i < C::NSUB; ++i)
+        if (n[i] > 0) qk(i, sk, cnt[i]);
+      done(&bars.kv_empty[sk]);
+      if (nmax == 1) done(&bars.q_empty);
       for (int j = 0; j < nmax; ++j) {
-        const uint32_t lv = ld0 + 2 * j + 1, lk = lv + 1;
-        const uint32_t sv = lv % C::STAGES, sk = lk % C::STAGES;
-        if (C::NBUF == 2 && j + 1 < nmax) {
-          full(lk);
+        const bool more = j + 1 < nmax;
+        next(sv, pv);
+        if (more) next(sk, pk);
+        if (C::NBUF == 2 && more) {
+          wait_bar(&bars.kv_full[sk], pk, dead, w.err);
           tc::fence_after();
-          if (lane == 0) {
-            qk(0, sk, cnt[0] + 1);
-            tc::commit(&bars.kv_empty[sk]);
-            if (j + 2 == nmax) tc::commit(&bars.q_empty);
-          }
-          __syncwarp();
+          qk(0, sk, cnt[0] + 1);
+          done(&bars.kv_empty[sk]);
+          if (j + 2 == nmax) done(&bars.q_empty);
         }
-        full(lv);
-        const int valid = e.kvlen - (e.kt0 + j) * C::BN;
+        wait_bar(&bars.kv_full[sv], pv, dead, w.err);
+        const int valid = keys - j * C::BN;
         if (valid < C::BN) {  // rows of V past the last key: 0 * NaN is not 0
           for (int x = lane; x < (C::BN - valid) * C::CH * 8; x += 32) {
             const int r = valid + x / (C::CH * 8), y = x % (C::CH * 8);
@@ -597,34 +653,36 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
           tc::fence_proxy_async();
           __syncwarp();
         }
+        if (C::NBUF == 1 && more) wait_bar(&bars.kv_full[sk], pk, dead, w.err);
 #pragma unroll
         for (int i = 0; i < C::NSUB; ++i) {
-          if (C::NBUF == 1 && i == 0 && j + 1 < nmax) full(lk);
           if (j >= n[i]) continue;
           const uint32_t c = cnt[i]++;
-          wait_bar(&bars.p_full[C::NBUF == 2 ? (c & 1) : i], C::NBUF == 2 ? (c >> 1) & 1 : c & 1, dead, w.err);
-          tc::fence_after();
-          if (lane == 0) {
-            const uint32_t pa = tmem + (C::NBUF == 2 ? (c & 1) * 64 : i * 128);
+          const uint32_t pa = tm + (C::NBUF == 2 ? (c & 1) * 64 : i * 128);
+          const uint64_t b = dv + sv * kStage;
 #pragma unroll
-            for (int k = 0; k < C::BN / 16; ++k)
-              tc::mma_ts(tmem + 256 + i * 128, pa + k * 8, desc_mn(kv_addr + sv * C::KV_BYTES + k * 2048, C::BN * 128),
-                         id_pv, j > 0 || k > 0);
-            tc::commit(&bars.pv_done[C::NBUF == 2 ? (c & 1) : i]);
-            if (C::NBUF == 1 && j + 1 < n[i]) qk(i, sk, c + 1);
+          for (int part = 0; part < C::PARTS; ++part) {
+            wait_bar(&bars.p_full[C::NBUF == 2 ? (c & 1) : i][part], C::NBUF == 2 ? (c >> 1) & 1 : c & 1, dead,
+                     w.err);
+            tc::fence_after();
+            if (elect_one()) {
+#pragma unroll
+              for (int k = 0; k < C::BN / 16 / C::PARTS; ++k) {
+                const int kk = part * (C::BN / 16 / C::PARTS) + k;
+                tc::mma_ts(tm + 256 + i * 128, pa + kk * 8, b + (kk * 2048 >> 4), id_pv, j > 0 || kk > 0);
+              }
+              if (part == C::PARTS - 1) tc::commit(&bars.pv_done[C::NBUF == 2 ? (c & 1) : i]);
+            }
+            __syncwarp();
           }
-          __syncwarp();
+          if (C::NBUF == 1 && j + 1 < n[i]) qk(i, sk, c + 1);
         }
-        if (lane == 0) {
-          tc::commit(&bars.kv_empty[sv]);
-          if (C::NBUF == 1 && j + 1 < nmax) {
-            tc::commit(&bars.kv_empty[sk]);
-            if (j + 2 == nmax) tc::commit(&bars.q_empty);
-          }
+        done(&bars.kv_empty[sv]);
+        if (C::NBUF == 1 && more) {
+          done(&bars.kv_empty[sk]);
+          if (j + 2 == nmax) done(&bars.q_empty);
         }
-        __syncwarp();
       }
-      ld = ld0 + 2 * nmax;
     }
   }
   if (*dead) __nanosleep(1000000);  // copies in flight land before shared memory is given up

@@ -18,24 +18,40 @@ constexpr size_t kArrivedBytes = 2048;
 
 __host__ __device__ inline size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
+__device__ __forceinline__ bool try_bar(uint64_t *bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      " selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(done)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return done != 0;
+}
 // Bounded wait that remembers a lost signal: after the first time-out of a CTA every later
 // wait returns soon, so the kernel ends.
-__device__ __forceinline__ void wait_bar(uint64_t *bar, uint32_t parity, volatile int *dead,
-                                         unsigned int *err) {
+__device__ __forceinline__ void wait_slow(uint64_t *bar, uint32_t parity, volatile int *dead,
+                                          unsigned int *err) {
   for (int it = 0; it < (1 << 20); ++it) {
-    uint32_t done;
-    asm volatile(
-        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
-        " selp.u32 %0, 1, 0, p;\n}\n"
-        : "=r"(done)
-        : "r"(smem_u32(bar)), "r"(parity)
-        : "memory");
-    if (done) return;
+    if (try_bar(bar, parity)) return;
     if ((it & 255) == 255 && *dead) return;
   }
   *dead = 1;
   report_status(err, GDN_STATUS_WAIT_TIMEOUT);
 }
+__device__ __forceinline__ void wait_bar(uint64_t *bar, uint32_t parity, volatile int *dead,
+                                         unsigned int *err) {
+  if (!try_bar(bar, parity)) wait_slow(bar, parity, dead, err);
+}
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+  return p != 0;
+}
+// A value that all lanes hold, known to the compiler as such (uniform registers).
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
 
 __device__ __forceinline__ void tma_4d(void *dst, const void *map, int x, int y, int z, int w,
                                        uint64_t *bar) {
