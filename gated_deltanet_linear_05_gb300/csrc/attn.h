@@ -43,7 +43,6 @@ struct AttnParams {
 };
 
 constexpr int kSms = 152;          // persistent CTAs, and the shares that work is cut into
-constexpr int kSplitSlots = 304;   // partial results of split tiles, over all kv-heads
 constexpr int kStepRows = 16;      // query heads per kv-head that the decode kernel takes
 // Either attention call: picks the kernels and lays out the workspace (attn_tile.cu).
 size_t attn_workspace(int num_seqs, int tokens, int hq, int hkv, int d, int prefix_len);

@@ -444,7 +444,7 @@ cudaError_t run(const AttnParams &p, char *ws, float *dense_ml, float *dense, un
   const size_t smem = C::SMEM + 1024;
   err = cudaFuncSetAttribute(step_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (err != cudaSuccess) return err;
-  return launch_dependent(step_kernel<D>, C::CTAS, C::THREADS, smem, stream, p, w, k, v);
+  return launch_dependent(step_kernel<D>, C::CTAS, C::THREADS, smem, stream, 1, p, w, k, v);
 }
 
 }  // namespace

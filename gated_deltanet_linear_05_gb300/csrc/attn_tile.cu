@@ -12,14 +12,16 @@
 // same, as l and O share the reference.  P goes to tensor memory as bf16 (V is held in
 // bf16: the product's other operand has no more bits) and l sums the unrounded p in float32.
 //
-// D = 128: two sub-tiles of 128 rows share each K and V tile of 128 keys; while the softmax
-// warps of one work, the tensor cores run the other's products.  Tensor memory: S 2 x 128
-// columns (P over S), O 2 x 128.  D = 256: O of two sub-tiles would fill tensor memory, so one
-// sub-tile, K and V tiles of 64 keys, and two S buffers of 64 columns: the next tile's scores
-// are computed while this one's softmax runs.  Both: 64 KB of Q and a ring of five 32 KB
-// tiles of K and V in shared memory, loaded by TMA page by page.
+// A tile has two sub-tiles of 128 rows that share each K and V tile of 128 keys.
+// D = 128: one CTA; while the softmax warps of one sub-tile work, the tensor cores run the
+// other's products.  Tensor memory: S 2 x 128 columns (P over S), O 2 x 128.
+// D = 256: a pair of CTAs with a sub-tile each (O takes 256 of the 512 columns) and the
+// products of cta_group::2, so that each CTA loads and reads half of every K and V tile (one CTA
+// alone had 64-key tiles, whose score products are bound by shared memory: 48 cycles for 32).
+// Two S buffers: the next tile's scores are computed while this one's softmax runs.
+// Both: 64 KB of Q and a ring of five 32 KB tiles in shared memory, loaded by TMA page by page.
 //
-// Warps: 4 per sub-tile for the softmax and the epilogue, one for the loads, one for the MMAs.
+// Warps: 4 per sub-tile for the softmax and the epilogue, one for the loads, one for the products.
 #include <cuda.h>
 #include <math_constants.h>
 #include <string.h>
@@ -31,20 +33,26 @@
 namespace gdn {
 namespace {
 
+constexpr int kBN = 128;        // keys per tile
+constexpr int kTileRows = 256;  // rows per tile: two sub-tiles
+
 template <int D_>
 struct Cfg {
   static constexpr int D = D_;
-  static constexpr int BN = D == 128 ? 128 : 64;    // keys per tile
-  static constexpr int NSUB = D == 128 ? 2 : 1;     // sub-tiles of 128 rows
-  static constexpr int NBUF = D == 128 ? 1 : 2;     // S buffers of a sub-tile
+  static constexpr bool PAIR = D == 256;            // two CTAs share a tile, one sub-tile each
+  static constexpr int GRP = PAIR ? 2 : 1;          // tcgen05 cta_group
+  static constexpr int SUBS = PAIR ? 1 : 2;         // sub-tiles of 128 rows in a CTA
+  static constexpr int NBUF = PAIR ? 2 : 1;         // S buffers of a sub-tile
   static constexpr int STAGES = 5;
-  static constexpr int CH = D / 64;                 // 128-byte column chunks of a row
+  static constexpr int CH = D / 64;                 // 128-byte column chunks of a row of q or K
+  static constexpr int KROWS = PAIR ? 64 : kBN;     // keys of a K tile in this CTA
   static constexpr int Q_BYTES = 128 * D * 2;       // one sub-tile
-  static constexpr int KV_BYTES = BN * D * 2;
-  static constexpr int SMEM = NSUB * Q_BYTES + STAGES * KV_BYTES;
-  static constexpr int THREADS = D == 128 ? 384 : 192;  // (two warps idle with D = 128)
-  static constexpr int PARTS = D == 128 ? 2 : 1;    // P is handed over in so many pieces
-  static constexpr int ROWS = 128 * NSUB;
+  static constexpr int KV_BYTES = 32768;            // a CTA's part of a K or V tile
+  static constexpr int SMEM = SUBS * Q_BYTES + STAGES * KV_BYTES;
+  static constexpr int LOADER = 4 * SUBS;           // warp that loads; the next issues products
+  static constexpr int THREADS = PAIR ? 192 : 384;  // (two warps idle with D = 128)
+  static constexpr int UNITS = kSms / GRP;          // CTAs, or pairs of them
+  static constexpr int SLOTS = 2 * UNITS;           // partial results of split tiles
 };
 
 // ------------------------------------------------------------------ operands
@@ -58,6 +66,113 @@ __device__ __forceinline__ uint64_t desc_k(uint32_t saddr) {
 __device__ __forceinline__ uint64_t desc_mn(uint32_t saddr, uint32_t mn) {
   return (uint64_t)((saddr >> 4) & 0x3FFF) | ((uint64_t)(mn >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
          (1ull << 46) | (2ull << 61);
+}
+
+// tcgen05 of one CTA (GRP = 1) or of a pair (2): there the CTA of even rank issues for both,
+// each holding its 128 rows of A and of the result and half of B's N, at the same addresses.
+template <int GRP>
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t accumulate) {
+  if (GRP == 1) {
+    tc::mma_ss(d, a, b, id, accumulate);
+  } else {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(id), "r"(accumulate)
+        : "memory");
+  }
+}
+template <int GRP>
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t accumulate) {
+  if (GRP == 1) {
+    tc::mma_ts(d, a, b, id, accumulate);
+  } else {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+        "r"(a), "l"(b), "r"(id), "r"(accumulate)
+        : "memory");
+  }
+}
+// Arrive on `bar` (of both CTAs of a pair) once every product issued so far has completed.
+template <int GRP>
+__device__ __forceinline__ void commit(uint64_t *bar) {
+  if (GRP == 1) {
+    tc::commit(bar);
+  } else {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n" ::"r"(
+            smem_u32(bar)),
+        "h"((uint16_t)3)
+        : "memory");
+  }
+}
+template <int GRP>
+__device__ __forceinline__ void tmem_alloc(uint32_t *slot) {
+  if (GRP == 1) {
+    tc::alloc<512>(slot);
+  } else {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;\n" ::"r"(smem_u32(slot)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;\n" ::: "memory");
+  }
+}
+template <int GRP>
+__device__ __forceinline__ void tmem_dealloc(uint32_t base) {
+  if (GRP == 1) tc::dealloc<512>(base);
+  else asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;\n" ::"r"(base) : "memory");
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
+}
+// The address of a shared-memory object of this CTA in the pair's first CTA.
+__device__ __forceinline__ uint32_t in_first(const void *p) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, 0;\n" : "=r"(r) : "r"(smem_u32(p)));
+  return r;
+}
+// Arrive in the first CTA.  The second form also orders this thread's writes to shared memory
+// before it for the cluster; what the first one signals lies in tensor memory and is ordered by
+// tcgen05's own fences (with .release.cluster a tile's softmax took 2000 cycles longer).
+__device__ __forceinline__ void arrive_first(uint64_t *bar) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];\n" ::"r"(in_first(bar)) : "memory");
+}
+__device__ __forceinline__ void release_first(uint64_t *bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];\n" ::"r"(in_first(bar)) : "memory");
+}
+// TMA loads; in a pair they count on the first CTA's barrier.
+template <bool PAIR>
+__device__ __forceinline__ void load_q(void *dst, const void *map, int x, int y, int z, uint64_t *bar) {
+  if (!PAIR) {
+    tma_load_3d(dst, map, x, y, z, bar);
+  } else {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, "
+        "{%2, %3, %4}], [%5];\n" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(in_first(bar))
+        : "memory");
+  }
+}
+template <bool PAIR>
+__device__ __forceinline__ void load_kv(void *dst, const void *map, int x, int y, int z, int w, uint64_t *bar) {
+  if (!PAIR) {
+    tma_4d(dst, map, x, y, z, w, bar);
+  } else {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, "
+        "{%2, %3, %4, %5}], [%6];\n" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(in_first(bar))
+        : "memory");
+  }
+}
+// Rows of a V tile (two 64-column chunks of 128 rows) from `valid` on to zero, by one warp:
+// they lie past the last key, and 0 * NaN is not 0.
+__device__ __forceinline__ void clear_rows(uint8_t *tile, int valid, int lane) {
+  for (int x = lane; x < (128 - valid) * 16; x += 32) {
+    const int r = valid + (x >> 4), y = x & 15;
+    *reinterpret_cast<uint4 *>(tile + (y >> 3) * 16384 + r * 128 + (y & 7) * 16) = make_uint4(0, 0, 0, 0);
+  }
+  tc::fence_proxy_async();
+  __syncwarp();
 }
 
 // Ties loaded registers to the wait before them, so that no use moves above it.
@@ -119,7 +234,7 @@ struct TilePlan {
   float *ml;      // [slot][row] {m, l}
   float *part;    // [slot][row][D]
   float *dense_ml, *dense;  // one result per row of the call instead (attn_step.cu), or NULL
-  int max_tiles, sms, all_slots;
+  int max_tiles, units, slots, all_slots;
   int uniform_parts, uniform_kt;  // > 0: no plan, equal parts of equal tiles (shared prefix)
   unsigned int *err;
 };
@@ -148,7 +263,7 @@ constexpr int kCand = 16;
 //     max(chunk, ceil(entries / SMs) * mean entry) + 3 ceil(entries / SMs)
 // (in key tiles; 3 is about what starting and ending an entry costs).  Entries are ordered by
 // length, longest first, in 64 classes, for the kernel's back-and-forth assignment to CTAs.
-__global__ void __launch_bounds__(kPlanThreads) plan_kernel(AttnParams p, TilePlan w, int tt, int bn) {
+__global__ void __launch_bounds__(kPlanThreads) plan_kernel(AttnParams p, TilePlan w, int tt) {
   __shared__ int sh_scan[32], sh_total, sh_kvmax, sh_cnt[kCand], sh_spl[kCand], sh_hist[64], sh_chunk;
   __shared__ int sh_slot, sh_nsplit, sh_big[kPlanThreads], sh_nbig;
   __shared__ unsigned long long sh_work;
@@ -163,7 +278,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(AttnParams p, TilePl
   auto put = [&](int at, int bos, int t, int len, int i) {
     if (at >= w.max_tiles) return;  // only with a malformed cu_seqlens
     const int tok0 = i * tt, ntok = min(tt, t - tok0);
-    const int kvt = (visible(len - t + tok0, ntok, len) + bn - 1) / bn;
+    const int kvt = (visible(len - t + tok0, ntok, len) + kBN - 1) / kBN;
     rec[at] = Entry{bos + tok0, ntok, 0, len - t + tok0, 0, kvt, 0, len};
     work += kvt;
     kvmax = max(kvmax, kvt);
@@ -244,9 +359,9 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(AttnParams p, TilePl
     int chunk = kvmax;
     for (int j = 0; j < kCand; ++j) {
       const int c = (kvmax + parts_of[j] - 1) / parts_of[j];
-      if (j > 0 && (long long)sh_spl[j] * p.hkv > kSplitSlots) break;
+      if (j > 0 && (long long)sh_spl[j] * p.hkv > w.slots) break;
       const float items = (float)sh_cnt[j] * p.hkv;
-      const float rounds = ceilf(items / w.sms);
+      const float rounds = ceilf(items / w.units);
       const float cost = fmaxf((float)c, rounds * ((float)sh_work * p.hkv / fmaxf(items, 1.f))) + 3.f * rounds;
       if (cost < best) best = cost, chunk = c;
     }
@@ -299,16 +414,18 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(AttnParams p, TilePl
 
 struct Barriers {
   uint64_t q_full, q_empty, kv_full[5], kv_empty[5], s_full[2], p_full[2][2], pv_done[2];
+  uint64_t v_tail, tail_ok[5];  // D = 256: a last V tile has come; it has been cleared past the last key
   uint32_t tmem;
   int dead;
 };
 
-// Work item `i` of this launch: the entry and its kv-head.
-__device__ __forceinline__ bool item_at(const AttnParams &p, const TilePlan &w, int round, int tt, Entry &e,
-                                        int &h) {
-  // back and forth over the CTAs, so that who had the longest entry gets the shortest next
-  const int c = (round & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x;
-  const long long i = (long long)round * gridDim.x + c;
+// Work item of this round: the entry and its kv-head.
+template <int UNITS>
+__device__ __forceinline__ bool item_at(const AttnParams &p, const TilePlan &w, int unit, int round, int tt,
+                                        Entry &e, int &h) {
+  // back and forth over the units, so that who had the longest entry gets the shortest next
+  const int c = (round & 1) ? UNITS - 1 - unit : unit;
+  const long long i = (long long)round * UNITS + c;
   if (w.uniform_parts > 0) {  // shared prefix: equal parts of equal tiles
     const int tiles = (p.tokens + tt - 1) / tt;
     if (i >= (long long)tiles * w.uniform_parts * p.hkv) return false;
@@ -334,12 +451,11 @@ __device__ __forceinline__ bool item_at(const AttnParams &p, const TilePlan &w, 
 }
 
 // Key tiles that sub-tile `i` of an entry takes part in.
-template <int BN>
 __device__ __forceinline__ int sub_tiles(const Entry &e, int i, int tpt) {
   const int first = i * tpt;
   if (first >= e.ntok) return 0;
   const int vis = visible(e.place0, min(e.ntok, first + tpt), e.kvlen);
-  return max(0, min((vis + BN - 1) / BN, e.kt1) - e.kt0);
+  return max(0, min((vis + kBN - 1) / kBN, e.kt1) - e.kt0);
 }
 
 template <int D>
@@ -350,24 +466,29 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
   extern __shared__ uint8_t smem_raw[];
   __shared__ Barriers bars;
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-  uint8_t *sq = smem, *skv = smem + C::NSUB * C::Q_BYTES;
+  uint8_t *sq = smem, *skv = smem + C::SUBS * C::Q_BYTES;
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   volatile int *dead = &bars.dead;
-  const int G = p.hq / p.hkv, tpt = 128 / G, tt = tpt * C::NSUB;
+  const int G = p.hq / p.hkv, tpt = 128 / G, tt = tpt * 2;
+  const int rank = C::PAIR ? (int)(blockIdx.x & 1) : 0;  // CTA of the pair
+  const int unit = C::PAIR ? (int)(blockIdx.x >> 1) : (int)blockIdx.x;
 
   if (threadIdx.x == 0) {
     mbar_init(&bars.q_full, 1);
     mbar_init(&bars.q_empty, 1);
-    for (int i = 0; i < C::STAGES; ++i) mbar_init(&bars.kv_full[i], 1), mbar_init(&bars.kv_empty[i], 1);
+    for (int i = 0; i < C::STAGES; ++i)
+      mbar_init(&bars.kv_full[i], 1), mbar_init(&bars.kv_empty[i], 1), mbar_init(&bars.tail_ok[i], 2);
     for (int i = 0; i < 2; ++i)
-      mbar_init(&bars.s_full[i], 1), mbar_init(&bars.p_full[i][0], 128), mbar_init(&bars.p_full[i][1], 128),
-          mbar_init(&bars.pv_done[i], 1);
+      mbar_init(&bars.s_full[i], 1), mbar_init(&bars.p_full[i][0], 4 * C::GRP),
+          mbar_init(&bars.p_full[i][1], 4 * C::GRP), mbar_init(&bars.pv_done[i], 1);
+    mbar_init(&bars.v_tail, 1);
     mbar_fence_init();
     bars.dead = 0;
   }
-  if (warp == 4 * C::NSUB) tc::alloc<512>(&bars.tmem);
+  if (warp == C::LOADER) tmem_alloc<C::GRP>(&bars.tmem);
   tc::fence_before();
   __syncthreads();
+  if (C::PAIR) cluster_sync();  // the other CTA's barriers are ready
   tc::fence_after();
   const uint32_t tmem = bars.tmem;
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
@@ -377,57 +498,59 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
   int h;
   // D = 128: 12 warps start with 168 registers each; the eight softmax warps take 224 and the
   // other four keep 56 (8 x 224 + 4 x 56 = 12 x 168)
-  if (D == 128) {
+  if (!C::PAIR) {
     if (warp < 8) asm volatile("setmaxnreg.inc.sync.aligned.u32 224;\n");
     else asm volatile("setmaxnreg.dec.sync.aligned.u32 56;\n");
   }
-  if (warp < 4 * C::NSUB) {
+  if (warp < C::LOADER) {
     // ---------------------------------------------------------------- softmax, epilogue
-    const int sub = warp >> 2;
+    const int sub = C::PAIR ? rank : warp >> 2;
     const int row = threadIdx.x & 127;
     const float asl = p.scale == 0.f ? 1.f : fabsf(p.scale) * 1.4426950408889634f;
+    const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+    const uint32_t o_base = lanes + 256 + (C::PAIR ? 0 : sub * 128);
     uint32_t cnt = 0;  // tiles of this sub-tile so far, over all items
-    for (int round = 0; item_at(p, w, round, tt, e, h); ++round) {
-      const int n = sub_tiles<C::BN>(e, sub, tpt);
+    for (int round = 0; item_at<C::UNITS>(p, w, unit, round, tt, e, h); ++round) {
+      // (a pair's sub-tiles run through the same tiles: one product is for both)
+      const int n = C::PAIR ? max(sub_tiles(e, 0, tpt), sub_tiles(e, 1, tpt)) : sub_tiles(e, sub, tpt);
       const int dt = sub * tpt + row / G;
       const bool live = row < tpt * G && dt < e.ntok;
       // keys this row sees, counted from the entry's first
-      const int limit = (live ? visible(e.place0, dt + 1, e.kvlen) : 0) - e.kt0 * C::BN;
+      const int limit = (live ? visible(e.place0, dt + 1, e.kvlen) : 0) - e.kt0 * kBN;
       float m = -CUDART_INF_F, l = 0.f;
-      const uint32_t o_base = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + 256 + sub * 128;
       for (int j = 0; j < n; ++j, ++cnt) {
         const int b = C::NBUF == 2 ? (cnt & 1) : sub;
-        const uint32_t s_addr = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + (C::NBUF == 2 ? b * 64 : sub * 128);
+        const uint32_t s_addr = lanes + b * 128;
         wait_bar(&bars.s_full[b], C::NBUF == 2 ? (cnt >> 1) & 1 : cnt & 1, dead, w.err);
         // Every completion of P V is waited for in its turn (it has come, or is about to: these
         // scores were issued after it), so that no wait mistakes an older phase for its own.
         if (C::NBUF == 2 && j >= 2) wait_bar(&bars.pv_done[b], ((cnt - 2) >> 1) & 1, dead, w.err);
         if (C::NBUF == 1 && j >= 1) wait_bar(&bars.pv_done[b], (cnt - 1) & 1, dead, w.err);
         tc::fence_after();
-        uint32_t s[C::BN / 32][32];
+        uint32_t s[4][32];
 #pragma unroll
-        for (int c = 0; c < C::BN / 32; ++c) tc::ld32(s_addr + 32 * c, s[c]);
+        for (int c = 0; c < 4; ++c) tc::ld32(s_addr + 32 * c, s[c]);
         tc::wait_ld();
 #pragma unroll
-        for (int c = 0; c < C::BN / 32; ++c) tie32(s[c]);
+        for (int c = 0; c < 4; ++c) tie32(s[c]);
         if (p.scale <= 0.f) {
 #pragma unroll
-          for (int c = 0; c < C::BN; ++c) {
+          for (int c = 0; c < kBN; ++c) {
             const float x = __uint_as_float(s[c / 32][c % 32]);
             s[c / 32][c % 32] = __float_as_uint(p.scale == 0.f ? 0.f : -x);
           }
         }
-        const int lim = limit - j * C::BN;
-        if (__any_sync(0xffffffffu, lim < C::BN)) {
+        const int lim = limit - j * kBN;
+        if (__any_sync(0xffffffffu, lim < kBN)) {
 #pragma unroll
-          for (int c = 0; c < C::BN; ++c)
+          for (int c = 0; c < kBN; ++c)
             if (c >= lim) s[c / 32][c % 32] = 0xff800000u;
         }
         float mx[4];
 #pragma unroll
         for (int c = 0; c < 4; ++c) mx[c] = __uint_as_float(s[0][c]);
 #pragma unroll
-        for (int c = 4; c < C::BN; c += 2)
+        for (int c = 4; c < kBN; c += 2)
           mx[(c >> 1) & 3] = max3(mx[(c >> 1) & 3], __uint_as_float(s[c / 32][c % 32]),
                                   __uint_as_float(s[c / 32][c % 32 + 1]));
         const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * asl;
@@ -457,7 +580,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
         const uint64_t asl2 = pack2(asl, asl), ref2 = pack2(-ref, -ref);
         uint64_t sum[2] = {0, 0};
 #pragma unroll
-        for (int c = 0; c < C::BN / 32; ++c) {
+        for (int c = 0; c < 4; ++c) {
           uint32_t pk[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
@@ -468,10 +591,14 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
             pk[i] = pack_bf16(a, b2);
           }
           tc::st16(s_addr + 16 * c, pk);
-          if ((c + 1) % (C::BN / 32 / C::PARTS) == 0) {
+          if (c & 1) {  // 64 keys of P are handed over
             tc::wait_st();
             tc::fence_before();
-            mbar_arrive(&bars.p_full[b][C::PARTS == 2 ? c / 2 : 0]);
+            __syncwarp();
+            if (lane == 0) {
+              if (C::PAIR) arrive_first(&bars.p_full[b][c >> 1]);
+              else mbar_arrive(&bars.p_full[b][c >> 1]);
+            }
           }
         }
         const float2 su = unpack2(add2(sum[0], sum[1]));
@@ -492,7 +619,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
       const long long orow = (long long)tok * p.hq + head;
       float *part = nullptr;
       if (e.slot >= 0) {
-        const long long at = (long long)(e.slot + h) * C::ROWS + sub * 128 + row;
+        const long long at = (long long)(e.slot + h) * kTileRows + sub * 128 + row;
         part = w.part + at * D;
         if (live) *reinterpret_cast<float2 *>(w.ml + 2 * at) = make_float2(m, l);
       } else if (live && p.lse) {
@@ -531,89 +658,111 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
       }
       tc::fence_before();
     }
-  } else if (warp == 4 * C::NSUB) {
+  } else if (warp == C::LOADER) {
     // ---------------------------------------------------------------- loads
-    const int box = min(p.page_size, C::BN);       // rows of a load
-    const int boxes = C::BN / box;                 // loads of a tile per column chunk
-    const int pi = lane / C::CH, ch = lane % C::CH;  // this lane's box and chunk
-    uint32_t ld = 0, items = 0;
-    for (int round = 0; item_at(p, w, round, tt, e, h); ++round) {
-      int n = 0, nsub = 0;
-#pragma unroll
-      for (int i = 0; i < C::NSUB; ++i) {
-        const int ni = sub_tiles<C::BN>(e, i, tpt);
-        n = max(n, ni);
-        nsub += ni > 0;
-      }
+    // A lane has one box of a K tile (box rows of a 64-column chunk of this CTA's keys) and one of
+    // a V tile.  In a pair, CTA r holds keys 64 r .. + 63 of K and columns 128 r .. + 127 of V.
+    const int box = min(p.page_size, C::KROWS);
+    const int kp = lane / C::CH, kc = lane % C::CH, vp = lane >> 1, vc = lane & 1;
+    const int kr = rank * (C::PAIR ? 64 : 0) + kp * box, vr = vp * box;  // first key in the tile
+    const bool k_on = kp * box < C::KROWS, v_on = vp * box < kBN;
+    uint32_t st = 0, ph = 1, items = 0, tails = 0;
+    for (int round = 0; item_at<C::UNITS>(p, w, unit, round, tt, e, h); ++round) {
+      const int n0 = sub_tiles(e, 0, tpt), n1 = sub_tiles(e, 1, tpt), n = max(n0, n1);
       if (n == 0) continue;
       const int32_t *table = w.uniform_parts > 0 ? p.prefix_table : p.page_table + (long long)e.seq * p.max_pages;
-      auto page_of = [&](int j) {  // page of this lane's box of tile j, -1: past the last key
-        const int key = (e.kt0 + j) * C::BN + pi * box;
-        if (pi >= boxes || j >= n || key >= e.kvlen) return -1;
+      auto page_of = [&](bool on, int j, int r) {  // page of a lane's box in tile j, -1: past the last key
+        const int key = (e.kt0 + j) * kBN + r;
+        if (!on || j >= n || key >= e.kvlen) return -1;
         const int pg = table[key / p.page_size];
         return (unsigned)pg < (unsigned)p.num_pages ? pg : p.num_pages;  // out of range: zeros
       };
-      int next = page_of(0);
+      int kpg = page_of(k_on, 0, kr), vpg = page_of(v_on, 0, vr);
       wait_bar(&bars.q_empty, (items & 1) ^ 1, dead, w.err);
       if (lane == 0) {
-        mbar_arrive_expect_tx(&bars.q_full, (uint32_t)nsub * C::CH * tpt * G * 128);
-        for (int i = 0; i < C::NSUB; ++i)
-          if (sub_tiles<C::BN>(e, i, tpt) > 0)
+        const uint32_t sub_bytes = (uint32_t)C::CH * tpt * G * 128;
+        if (rank == 0) mbar_arrive_expect_tx(&bars.q_full, ((n0 > 0) + (n1 > 0)) * sub_bytes);
+        for (int i = 0; i < 2; ++i)
+          if ((i ? n1 : n0) > 0 && (!C::PAIR || i == rank))
             for (int c = 0; c < C::CH; ++c)
-              tma_load_3d(sq + i * C::Q_BYTES + c * 16384, &qmap, c * 64, h * G, e.tok0 + i * tpt, &bars.q_full);
+              load_q<C::PAIR>(sq + (C::PAIR ? 0 : i * C::Q_BYTES) + c * 16384, &qmap, c * 64, h * G, e.tok0 + i * tpt,
+                              &bars.q_full);
       }
       ++items;
       for (int j = 0; j < n; ++j) {
-        const int pg = next;
-        next = page_of(j + 1);
-        const int key = (e.kt0 + j) * C::BN + pi * box;
-        const int count = __popc(__ballot_sync(0xffffffffu, pg >= 0));
+        const int kpg0 = kpg, vpg0 = vpg;
+        kpg = page_of(k_on, j + 1, kr);
+        vpg = page_of(v_on, j + 1, vr);
+        const int key0 = (e.kt0 + j) * kBN;
+        const int left = e.kvlen - key0;
+        // bytes of the tile (of both CTAs'): whole boxes up to the last key, all columns
+        const uint32_t bytes = (uint32_t)((min(left, kBN) + box - 1) / box * box) * D * 2;
 #pragma unroll
-        for (int kv = 0; kv < 2; ++kv, ++ld) {
-          const uint32_t st = ld % C::STAGES;
-          wait_bar(&bars.kv_empty[st], ((ld / C::STAGES) & 1) ^ 1, dead, w.err);
-          if (lane == 0) mbar_arrive_expect_tx(&bars.kv_full[st], (uint32_t)count * box * 128);
+        for (int kv = 0; kv < 2; ++kv) {
+          wait_bar(&bars.kv_empty[st], ph, dead, w.err);
+          const bool tail = C::PAIR && kv && left < kBN;
+          if (lane == 0) {
+            if (rank == 0) {
+              if (tail) mbar_arrive(&bars.kv_full[st]);
+              else mbar_arrive_expect_tx(&bars.kv_full[st], bytes);
+            }
+            if (tail) mbar_arrive_expect_tx(&bars.v_tail, bytes / 2);
+          }
           __syncwarp();
-          if (pg >= 0)
-            tma_4d(skv + st * C::KV_BYTES + ch * (C::BN * 128) + pi * box * 128, kv ? &vmap : &kmap, ch * 64,
-                   key % p.page_size, h, pg, &bars.kv_full[st]);
+          uint8_t *dst = skv + st * C::KV_BYTES;
+          if (kv == 0 && kpg0 >= 0)
+            load_kv<C::PAIR>(dst + kc * (C::KROWS * 128) + kp * box * 128, &kmap, kc * 64, (key0 + kr) % p.page_size, h,
+                             kpg0, &bars.kv_full[st]);
+          if (kv == 1 && vpg0 >= 0) {
+            const int x = (C::PAIR ? rank * 128 : 0) + vc * 64;
+            uint8_t *at = dst + vc * (kBN * 128) + vr * 128;
+            if (tail) tma_4d(at, &vmap, x, (key0 + vr) % p.page_size, h, vpg0, &bars.v_tail);
+            else load_kv<C::PAIR>(at, &vmap, x, (key0 + vr) % p.page_size, h, vpg0, &bars.kv_full[st]);
+          }
+          if (tail) {  // both CTAs clear their columns past the last key, then the products may start
+            wait_bar(&bars.v_tail, tails & 1, dead, w.err);
+            ++tails;
+            clear_rows(dst, left, lane);
+            if (lane == 0) release_first(&bars.tail_ok[st]);
+          }
+          if (++st == C::STAGES) st = 0, ph ^= 1;
         }
       }
     }
-  } else if (warp == 4 * C::NSUB + 1) {
+  } else if (warp == C::LOADER + 1 && rank == 0) {
     // ---------------------------------------------------------------- products
     // All values here are the same in every lane and known as such (uniform()): the
     // instruction takes its descriptors from uniform registers, and building them from
     // lane-varying ones made issuing a product (95 cycles) slower than the product (64).
-    constexpr uint32_t id_qk = tc::idesc(128, C::BN, 1, 0, 0), id_pv = tc::idesc(128, D, 1, 0, 1);
+    constexpr int M = 128 * C::GRP;
+    constexpr uint32_t id_qk = tc::idesc(M, kBN, 1, 0, 0), id_pv = tc::idesc(M, D, 1, 0, 1);
     constexpr uint32_t kStage = C::KV_BYTES >> 4;
     const uint32_t tm = uniform(tmem);
     const uint64_t dq = desc_k(uniform(smem_u32(sq))), dk = desc_k(uniform(smem_u32(skv))),
-                   dv = desc_mn(uniform(smem_u32(skv)), C::BN * 128);
-    uint32_t st = 0, ph = 0, items = 0;  // ring position of the next K or V tile, its parity
+                   dv = desc_mn(uniform(smem_u32(skv)), kBN * 128);
+    uint32_t st = 0, ph = 0, items = 0, tails = 0;  // ring position of the next K or V tile, its parity
     uint32_t cnt[2] = {0, 0};
     auto qk = [&](int i, uint32_t at, uint32_t c) {
-      const uint32_t d = tm + (C::NBUF == 2 ? (c & 1) * 64 : i * 128);
+      const int buf = C::NBUF == 2 ? (c & 1) : i;
       const uint64_t a = dq + i * (C::Q_BYTES >> 4), b = dk + at * kStage;
       if (elect_one()) {
 #pragma unroll
         for (int k = 0; k < D / 16; ++k)
-          tc::mma_ss(d, a + (((k / 4) * 16384 + (k % 4) * 32) >> 4),
-                     b + (((k / 4) * (C::BN * 128) + (k % 4) * 32) >> 4), id_qk, k > 0);
-        tc::commit(&bars.s_full[C::NBUF == 2 ? (c & 1) : i]);
+          mma_ss<C::GRP>(tm + buf * 128, a + (((k / 4) * 16384 + (k % 4) * 32) >> 4),
+                         b + (((k / 4) * (C::KROWS * 128) + (k % 4) * 32) >> 4), id_qk, k > 0);
+        commit<C::GRP>(&bars.s_full[buf]);
       }
       __syncwarp();
     };
     auto done = [&](uint64_t *bar) {
-      if (elect_one()) tc::commit(bar);
+      if (elect_one()) commit<C::GRP>(bar);
       __syncwarp();
     };
-    for (int round = 0; item_at(p, w, round, tt, e, h); ++round) {
-      int n[2] = {0, 0};
-#pragma unroll
-      for (int i = 0; i < C::NSUB; ++i) n[i] = uniform(sub_tiles<C::BN>(e, i, tpt));
+    for (int round = 0; item_at<C::UNITS>(p, w, unit, round, tt, e, h); ++round) {
+      int n[2] = {uniform(sub_tiles(e, 0, tpt)), uniform(sub_tiles(e, 1, tpt))};
       const int nmax = max(n[0], n[1]);
-      const int keys = uniform(e.kvlen - e.kt0 * C::BN);
+      if (C::PAIR) n[0] = nmax, n[1] = 0;  // one product for both sub-tiles
+      const int keys = uniform(e.kvlen - e.kt0 * kBN);
       if (nmax == 0) continue;
       wait_bar(&bars.q_full, items & 1, dead, w.err);
       ++items;
@@ -627,7 +776,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
       wait_bar(&bars.kv_full[sk], pk, dead, w.err);
       tc::fence_after();
 #pragma unroll
-      for (int i = 0; i < C::NSUB; ++i)
+      for (int i = 0; i < C::SUBS; ++i)
         if (n[i] > 0) qk(i, sk, cnt[i]);
       done(&bars.kv_empty[sk]);
       if (nmax == 1) done(&bars.q_empty);
@@ -643,35 +792,32 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
           if (j + 2 == nmax) done(&bars.q_empty);
         }
         wait_bar(&bars.kv_full[sv], pv, dead, w.err);
-        const int valid = keys - j * C::BN;
-        if (valid < C::BN) {  // rows of V past the last key: 0 * NaN is not 0
-          for (int x = lane; x < (C::BN - valid) * C::CH * 8; x += 32) {
-            const int r = valid + x / (C::CH * 8), y = x % (C::CH * 8);
-            *reinterpret_cast<uint4 *>(skv + sv * C::KV_BYTES + (y >> 3) * (C::BN * 128) + r * 128 + (y & 7) * 16) =
-                make_uint4(0, 0, 0, 0);
+        const int valid = keys - j * kBN;
+        if (valid < kBN) {
+          if (C::PAIR) {
+            wait_bar(&bars.tail_ok[sv], tails >> sv & 1, dead, w.err);
+            tails ^= 1u << sv;  // parity of each stage's own
+          } else {
+            clear_rows(skv + sv * C::KV_BYTES, valid, lane);
           }
-          tc::fence_proxy_async();
-          __syncwarp();
         }
         if (C::NBUF == 1 && more) wait_bar(&bars.kv_full[sk], pk, dead, w.err);
 #pragma unroll
-        for (int i = 0; i < C::NSUB; ++i) {
+        for (int i = 0; i < C::SUBS; ++i) {
           if (j >= n[i]) continue;
           const uint32_t c = cnt[i]++;
-          const uint32_t pa = tm + (C::NBUF == 2 ? (c & 1) * 64 : i * 128);
+          const int buf = C::NBUF == 2 ? (c & 1) : i;
+          const uint32_t pa = tm + buf * 128;
           const uint64_t b = dv + sv * kStage;
 #pragma unroll
-          for (int part = 0; part < C::PARTS; ++part) {
-            wait_bar(&bars.p_full[C::NBUF == 2 ? (c & 1) : i][part], C::NBUF == 2 ? (c >> 1) & 1 : c & 1, dead,
-                     w.err);
+          for (int part = 0; part < 2; ++part) {
+            wait_bar(&bars.p_full[buf][part], C::NBUF == 2 ? (c >> 1) & 1 : c & 1, dead, w.err);
             tc::fence_after();
             if (elect_one()) {
 #pragma unroll
-              for (int k = 0; k < C::BN / 16 / C::PARTS; ++k) {
-                const int kk = part * (C::BN / 16 / C::PARTS) + k;
-                tc::mma_ts(tm + 256 + i * 128, pa + kk * 8, b + (kk * 2048 >> 4), id_pv, j > 0 || kk > 0);
-              }
-              if (part == C::PARTS - 1) tc::commit(&bars.pv_done[C::NBUF == 2 ? (c & 1) : i]);
+              for (int k = 4 * part; k < 4 * part + 4; ++k)
+                mma_ts<C::GRP>(tm + 256 + i * 128, pa + k * 8, b + (k * 2048 >> 4), id_pv, j > 0 || k > 0);
+              if (part) commit<C::GRP>(&bars.pv_done[buf]);
             }
             __syncwarp();
           }
@@ -688,8 +834,9 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
   if (*dead) __nanosleep(1000000);  // copies in flight land before shared memory is given up
   tc::fence_before();
   __syncthreads();
+  if (C::PAIR) cluster_sync();  // no signal is on its way to a CTA that has gone
   tc::fence_after();
-  if (warp == 4 * C::NSUB) tc::dealloc<512>(tmem);
+  if (warp == C::LOADER) tmem_dealloc<C::GRP>(tmem);
 }
 
 // ------------------------------------------------------------------ join
@@ -700,9 +847,9 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
 // per row) all rows of the call; for each also the shared prefix's parts.
 template <int D>
 __global__ void __launch_bounds__(256) join_kernel(AttnParams p, TilePlan w, TilePlan pre, int tpt) {
-  constexpr int E = D / 32, ROWS = Cfg<D>::ROWS;
+  constexpr int E = D / 32;
   const int lane = threadIdx.x & 31;
-  const int G = p.hq / p.hkv, tt = tpt * Cfg<D>::NSUB;
+  const int G = p.hq / p.hkv, tt = tpt * 2;
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   const long long rows = w.dense ? (long long)p.tokens * p.hq : (long long)w.head[1] * p.hkv * (tt * G);
@@ -743,7 +890,7 @@ __global__ void __launch_bounds__(256) join_kernel(AttnParams p, TilePlan w, Til
     auto take_parts = [&](const TilePlan &src, int slot, int parts, int off) {
       const int srow = off / tpt * 128 + (off % tpt) * G + g;
       for (int q = 0; q < parts; ++q)
-        take(src.ml, src.part, (long long)(slot + q * p.hkv + h) * ROWS + srow);
+        take(src.ml, src.part, (long long)(slot + q * p.hkv + h) * kTileRows + srow);
     };
     if (pre.uniform_parts > 0) take_parts(pre, tok / tt * pre.uniform_parts * p.hkv, pre.uniform_parts, tok % tt);
     if (w.dense) take(w.dense_ml, w.dense, i);
@@ -769,7 +916,7 @@ struct Sizes {
   int tpt, tt, max_tiles, prefix_tiles;
   Sizes(int tokens, int num_seqs, int hq, int hkv) {
     tpt = 128 / (hq / hkv);
-    tt = tpt * Cfg<D>::NSUB;
+    tt = tpt * 2;
     max_tiles = tokens / tt + num_seqs;
     prefix_tiles = (tokens + tt - 1) / tt;
   }
@@ -779,8 +926,9 @@ struct Sizes {
 // least two key tiles each.
 template <int D>
 int prefix_parts(int tiles, int hkv, int prefix_len) {
-  const int kt = (prefix_len + Cfg<D>::BN - 1) / Cfg<D>::BN;
-  const int fill = kSms / (int)(((long long)tiles * hkv < kSms) ? tiles * hkv : kSms);
+  constexpr int units = Cfg<D>::UNITS;
+  const int kt = (prefix_len + kBN - 1) / kBN;
+  const int fill = units / (int)(((long long)tiles * hkv < units) ? tiles * hkv : units);
   const int most = (kt + 1) / 2;
   return fill < 1 ? 1 : fill < most ? fill : most;
 }
@@ -795,9 +943,10 @@ size_t layout(TilePlan *own, TilePlan *pre, char *ws, int num_seqs, int tokens, 
     at += up256(bytes);
     return r;
   };
-  const int entries = z.max_tiles + kSplitSlots;
-  const size_t own_slots = prefix_len > 0 ? (size_t)z.max_tiles * hkv + kSplitSlots : kSplitSlots;
-  const size_t slot = (size_t)Cfg<D>::ROWS * sizeof(float);
+  constexpr int split_slots = Cfg<D>::SLOTS;
+  const int entries = z.max_tiles + split_slots;
+  const size_t own_slots = prefix_len > 0 ? (size_t)z.max_tiles * hkv + split_slots : split_slots;
+  const size_t slot = (size_t)kTileRows * sizeof(float);
   TilePlan a{}, b{};
   if (dense) {
     const size_t rows = (size_t)tokens * hq;
@@ -808,13 +957,13 @@ size_t layout(TilePlan *own, TilePlan *pre, char *ws, int num_seqs, int tokens, 
   a.base = (int *)take(sizeof(int) * (size_t)(num_seqs + 1));
   a.rec = (Entry *)take(sizeof(Entry) * (size_t)z.max_tiles);
   a.entry = (Entry *)take(sizeof(Entry) * (size_t)entries);
-  a.split = (Split *)take(sizeof(Split) * (size_t)(prefix_len > 0 ? z.max_tiles : kSplitSlots));
+  a.split = (Split *)take(sizeof(Split) * (size_t)(prefix_len > 0 ? z.max_tiles : split_slots));
   a.ml = (float *)take(own_slots * slot * 2);
   a.part = (float *)take(own_slots * slot * D);
   a.max_tiles = z.max_tiles;
   if (prefix_len > 0) {
     b.uniform_parts = prefix_parts<D>(z.prefix_tiles, hkv, prefix_len);
-    b.uniform_kt = (prefix_len + Cfg<D>::BN - 1) / Cfg<D>::BN;
+    b.uniform_kt = (prefix_len + kBN - 1) / kBN;
     const size_t slots = (size_t)z.prefix_tiles * b.uniform_parts * hkv;
     b.ml = (float *)take(slots * slot * 2);
     b.part = (float *)take(slots * slot * D);
@@ -836,27 +985,28 @@ cudaError_t run(const AttnParams &p, char *ws, unsigned int *errw, cudaStream_t 
   TilePlan own, pre;
   layout<D>(&own, &pre, tile_ws, p.num_seqs, p.tokens, p.hq, p.hkv, p.prefix_len, step && p.prefix_len > 0);
   own.err = pre.err = errw;
-  own.sms = pre.sms = kSms;
+  own.units = C::UNITS;
+  own.slots = C::SLOTS;
   CUtensorMap q, k, v;
   cudaError_t err = q_map(&q, p);
-  if (err == cudaSuccess) err = cache_maps(&k, &v, p, C::BN);
+  if (err == cudaSuccess) err = cache_maps(&k, &v, p, C::KROWS);
   if (err != cudaSuccess) return err;
   const size_t smem = C::SMEM + 1024;
   err = cudaFuncSetAttribute(tile_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (err != cudaSuccess) return err;
   if (p.prefix_len > 0) {
-    err = launch_dependent(tile_kernel<D>, kSms, C::THREADS, smem, stream, p, pre, q, k, v);
+    err = launch_dependent(tile_kernel<D>, kSms, C::THREADS, smem, stream, C::GRP, p, pre, q, k, v);
     if (err != cudaSuccess) return err;
   }
   if (step) {
     err = launch_attn_step(p, ws, own.dense_ml, own.dense, errw, stream);
   } else {
-    err = launch_dependent(plan_kernel, 1, kPlanThreads, 0, stream, p, own, z.tt, C::BN);
+    err = launch_dependent(plan_kernel, 1, kPlanThreads, 0, stream, 1, p, own, z.tt);
     if (err != cudaSuccess) return err;
-    err = launch_dependent(tile_kernel<D>, kSms, C::THREADS, smem, stream, p, own, q, k, v);
+    err = launch_dependent(tile_kernel<D>, kSms, C::THREADS, smem, stream, C::GRP, p, own, q, k, v);
   }
   if (err != cudaSuccess) return err;
-  return launch_dependent(join_kernel<D>, 4 * kSms, 256, 0, stream, p, own, pre, z.tpt);
+  return launch_dependent(join_kernel<D>, 4 * kSms, 256, 0, stream, 1, p, own, pre, z.tpt);
 }
 
 }  // namespace

@@ -21,7 +21,7 @@ __host__ __device__ inline size_t up256(size_t x) { return (x + 255) / 256 * 256
 __device__ __forceinline__ bool try_bar(uint64_t *bar, uint32_t parity) {
   uint32_t done;
   asm volatile(
-      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
       " selp.u32 %0, 1, 0, p;\n}\n"
       : "=r"(done)
       : "r"(smem_u32(bar)), "r"(parity)
@@ -96,20 +96,24 @@ cudaError_t bf16_map(CUtensorMap *map, const void *x, int rank, const cuuint64_t
 // (and never used) for a cache without pages.
 cudaError_t cache_maps(CUtensorMap *k, CUtensorMap *v, const AttnParams &p, int tile);
 
-// Launch as a programmatic dependent of the work before it on the stream.
+// Launch, in clusters of `cluster` CTAs, as a programmatic dependent of the work before it on
+// the stream.
 template <typename... Args>
 cudaError_t launch_dependent(void (*kernel)(Args...), unsigned grid, unsigned threads, size_t smem,
-                             cudaStream_t stream, Args... args) {
+                             cudaStream_t stream, int cluster, Args... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
