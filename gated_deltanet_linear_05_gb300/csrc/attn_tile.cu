@@ -660,73 +660,93 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
     }
   } else if (warp == C::LOADER) {
     // ---------------------------------------------------------------- loads
-    // A lane has one box of a K tile (box rows of a 64-column chunk of this CTA's keys) and one of
-    // a V tile.  In a pair, CTA r holds keys 64 r .. + 63 of K and columns 128 r .. + 127 of V.
-    const int box = min(p.page_size, C::KROWS);
-    const int kp = lane / C::CH, kc = lane % C::CH, vp = lane >> 1, vc = lane & 1;
-    const int kr = rank * (C::PAIR ? 64 : 0) + kp * box, vr = vp * box;  // first key in the tile
-    const bool k_on = kp * box < C::KROWS, v_on = vp * box < kBN;
+    // A tile comes in boxes of box rows x 64 columns; lane b keeps the page of box b of the tile
+    // after the present one, so that no load waits for the table.  In a pair, CTA r holds keys
+    // 64 r .. + 63 of K and columns 128 r .. + 127 of V.  Uniform values for the same reason
+    // as in the products.
+    const int lps = 31 - __clz(p.page_size), box = min(p.page_size, C::KROWS);
+    const int kb0 = C::PAIR ? rank * (64 / box) : 0, kb1 = kb0 + C::KROWS / box;  // this CTA's boxes of K
     uint32_t st = 0, ph = 1, items = 0, tails = 0;
     for (int round = 0; item_at<C::UNITS>(p, w, unit, round, tt, e, h); ++round) {
-      const int n0 = sub_tiles(e, 0, tpt), n1 = sub_tiles(e, 1, tpt), n = max(n0, n1);
+      const int n0 = uniform(sub_tiles(e, 0, tpt)), n1 = uniform(sub_tiles(e, 1, tpt)), n = max(n0, n1);
       if (n == 0) continue;
       const int32_t *table = w.uniform_parts > 0 ? p.prefix_table : p.page_table + (long long)e.seq * p.max_pages;
-      auto page_of = [&](bool on, int j, int r) {  // page of a lane's box in tile j, -1: past the last key
-        const int key = (e.kt0 + j) * kBN + r;
-        if (!on || j >= n || key >= e.kvlen) return -1;
-        const int pg = table[key / p.page_size];
-        return (unsigned)pg < (unsigned)p.num_pages ? pg : p.num_pages;  // out of range: zeros
+      const int kvlen = uniform(e.kvlen), first = uniform(e.kt0 * kBN), head = uniform(h);
+      auto page_of = [&](int j) {
+        const int key = first + j * kBN + lane * box;
+        return j < n && lane * box < kBN && key < kvlen ? table[key >> lps] : 0;
       };
-      int kpg = page_of(k_on, 0, kr), vpg = page_of(v_on, 0, vr);
+      int ahead = page_of(0);
       wait_bar(&bars.q_empty, (items & 1) ^ 1, dead, w.err);
-      if (lane == 0) {
+      if (elect_one()) {
         const uint32_t sub_bytes = (uint32_t)C::CH * tpt * G * 128;
         if (rank == 0) mbar_arrive_expect_tx(&bars.q_full, ((n0 > 0) + (n1 > 0)) * sub_bytes);
         for (int i = 0; i < 2; ++i)
           if ((i ? n1 : n0) > 0 && (!C::PAIR || i == rank))
             for (int c = 0; c < C::CH; ++c)
-              load_q<C::PAIR>(sq + (C::PAIR ? 0 : i * C::Q_BYTES) + c * 16384, &qmap, c * 64, h * G, e.tok0 + i * tpt,
-                              &bars.q_full);
+              load_q<C::PAIR>(sq + (C::PAIR ? 0 : i * C::Q_BYTES) + c * 16384, &qmap, c * 64, head * G,
+                              e.tok0 + i * tpt, &bars.q_full);
       }
+      __syncwarp();
       ++items;
       for (int j = 0; j < n; ++j) {
-        const int kpg0 = kpg, vpg0 = vpg;
-        kpg = page_of(k_on, j + 1, kr);
-        vpg = page_of(v_on, j + 1, vr);
-        const int key0 = (e.kt0 + j) * kBN;
-        const int left = e.kvlen - key0;
-        // bytes of the tile (of both CTAs'): whole boxes up to the last key, all columns
-        const uint32_t bytes = (uint32_t)((min(left, kBN) + box - 1) / box * box) * D * 2;
+        const int page = ahead;
+        ahead = page_of(j + 1);
+        const int key0 = first + j * kBN, left = kvlen - key0;
+        const int boxes = (min(left, kBN) + box - 1) / box;        // up to the last key
+        const uint32_t bytes = (uint32_t)boxes * box * D * 2;      // of both CTAs
+        auto page_in = [&](int b) {  // (a page out of range reads as zeros)
+          const int pg = __shfl_sync(0xffffffffu, page, b);
+          return (unsigned)pg < (unsigned)p.num_pages ? pg : p.num_pages;
+        };
+        // K
+        wait_bar(&bars.kv_empty[st], ph, dead, w.err);
+        uint8_t *dst = skv + st * C::KV_BYTES;
+        if (rank == 0 && elect_one()) mbar_arrive_expect_tx(&bars.kv_full[st], bytes);
+        __syncwarp();
+        for (int b = kb0; b < min(boxes, kb1); ++b) {
+          const int pg = page_in(b), row = (key0 + b * box) & (p.page_size - 1);
+          if (elect_one()) {
 #pragma unroll
-        for (int kv = 0; kv < 2; ++kv) {
-          wait_bar(&bars.kv_empty[st], ph, dead, w.err);
-          const bool tail = C::PAIR && kv && left < kBN;
-          if (lane == 0) {
-            if (rank == 0) {
-              if (tail) mbar_arrive(&bars.kv_full[st]);
-              else mbar_arrive_expect_tx(&bars.kv_full[st], bytes);
-            }
-            if (tail) mbar_arrive_expect_tx(&bars.v_tail, bytes / 2);
+            for (int c = 0; c < C::CH; ++c)
+              load_kv<C::PAIR>(dst + c * (C::KROWS * 128) + (b - kb0) * box * 128, &kmap, c * 64, row, head, pg,
+                               &bars.kv_full[st]);
           }
           __syncwarp();
-          uint8_t *dst = skv + st * C::KV_BYTES;
-          if (kv == 0 && kpg0 >= 0)
-            load_kv<C::PAIR>(dst + kc * (C::KROWS * 128) + kp * box * 128, &kmap, kc * 64, (key0 + kr) % p.page_size, h,
-                             kpg0, &bars.kv_full[st]);
-          if (kv == 1 && vpg0 >= 0) {
-            const int x = (C::PAIR ? rank * 128 : 0) + vc * 64;
-            uint8_t *at = dst + vc * (kBN * 128) + vr * 128;
-            if (tail) tma_4d(at, &vmap, x, (key0 + vr) % p.page_size, h, vpg0, &bars.v_tail);
-            else load_kv<C::PAIR>(at, &vmap, x, (key0 + vr) % p.page_size, h, vpg0, &bars.kv_full[st]);
-          }
-          if (tail) {  // both CTAs clear their columns past the last key, then the products may start
-            wait_bar(&bars.v_tail, tails & 1, dead, w.err);
-            ++tails;
-            clear_rows(dst, left, lane);
-            if (lane == 0) release_first(&bars.tail_ok[st]);
-          }
-          if (++st == C::STAGES) st = 0, ph ^= 1;
         }
+        if (++st == C::STAGES) st = 0, ph ^= 1;
+        // V
+        wait_bar(&bars.kv_empty[st], ph, dead, w.err);
+        dst = skv + st * C::KV_BYTES;
+        const bool tail = C::PAIR && left < kBN;
+        if (elect_one()) {
+          if (tail) mbar_arrive_expect_tx(&bars.v_tail, bytes / 2);
+          if (rank == 0) {
+            if (tail) mbar_arrive(&bars.kv_full[st]);
+            else mbar_arrive_expect_tx(&bars.kv_full[st], bytes);
+          }
+        }
+        __syncwarp();
+        for (int b = 0; b < boxes; ++b) {
+          const int pg = page_in(b), row = (key0 + b * box) & (p.page_size - 1);
+          if (elect_one()) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              const int x = (C::PAIR ? rank * 128 : 0) + c * 64;
+              uint8_t *at = dst + c * (kBN * 128) + b * box * 128;
+              if (tail) tma_4d(at, &vmap, x, row, head, pg, &bars.v_tail);
+              else load_kv<C::PAIR>(at, &vmap, x, row, head, pg, &bars.kv_full[st]);
+            }
+          }
+          __syncwarp();
+        }
+        if (tail) {  // both CTAs clear their columns past the last key, then the products may start
+          wait_bar(&bars.v_tail, tails & 1, dead, w.err);
+          ++tails;
+          clear_rows(dst, left, lane);
+          if (lane == 0) release_first(&bars.tail_ok[st]);
+        }
+        if (++st == C::STAGES) st = 0, ph ^= 1;
       }
     }
   } else if (warp == C::LOADER + 1 && rank == 0) {
