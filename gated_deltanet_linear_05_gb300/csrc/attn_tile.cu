@@ -164,6 +164,23 @@ __device__ __forceinline__ void load_kv(void *dst, const void *map, int x, int y
         : "memory");
   }
 }
+// Four lanes' 16-byte units: unit k of lane i to unit i of lane k.
+__device__ __forceinline__ void swap_units(uint4 &a, uint4 &b, bool up, int mask) {
+  uint4 s = up ? a : b;
+  s.x = __shfl_xor_sync(0xffffffffu, s.x, mask);
+  s.y = __shfl_xor_sync(0xffffffffu, s.y, mask);
+  s.z = __shfl_xor_sync(0xffffffffu, s.z, mask);
+  s.w = __shfl_xor_sync(0xffffffffu, s.w, mask);
+  if (up) a = s;
+  else b = s;
+}
+__device__ __forceinline__ void transpose4(uint4 (&u)[4], int lane) {
+  swap_units(u[0], u[1], lane & 1, 1);
+  swap_units(u[2], u[3], lane & 1, 1);
+  swap_units(u[0], u[2], lane & 2, 2);
+  swap_units(u[1], u[3], lane & 2, 2);
+}
+
 // Rows of a V tile (two 64-column chunks of 128 rows) from `valid` on to zero, by one warp:
 // they lie past the last key, and 0 * NaN is not 0.
 __device__ __forceinline__ void clear_rows(uint8_t *tile, int valid, int lane) {
@@ -206,6 +223,17 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   asm("add.rn.ftz.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
+// 32 columns of O, or zeros where no product was taken.
+__device__ __forceinline__ void read_o(uint32_t (&o)[32], uint32_t addr, bool some) {
+  if (some) {
+    tc::ld32(addr, o);
+    tc::wait_ld();
+    tie32(o);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) o[i] = 0;
+  }
+}
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;\n" : "=f"(r) : "f"(a), "f"(b), "f"(c));
@@ -244,6 +272,12 @@ __device__ __forceinline__ int visible(int place0, int ntok, int kvlen) {
   return min(max(place0 + ntok, 0), kvlen);
 }
 
+// Parts of a tile of kvt key tiles in chunks of `chunk` (inv = 1 / chunk): about
+// ceil(kvt / chunk), at least 1; every user computes the same.
+__device__ __forceinline__ int parts_in(int kvt, int chunk, float inv) {
+  return kvt <= chunk ? 1 : (int)ceilf(kvt * inv * 0.999999f);
+}
+
 __device__ __forceinline__ void seq_info(const AttnParams &p, int n, int &bos, int &t, int &len) {
   bos = n;
   t = 1;
@@ -255,34 +289,35 @@ __device__ __forceinline__ void seq_info(const AttnParams &p, int n, int &bos, i
   len = (int)min(max((long long)p.kv_lens[n], 0ll), (long long)p.max_pages * p.page_size);
 }
 
-constexpr int kPlanThreads = 1024;
+constexpr int kPlanThreads = 512;
 constexpr int kCand = 16;
+constexpr int kPlanTiles = 4096;  // tiles whose lengths are kept in shared memory
 
 // Cuts the batch into entries, one block.  Tiles with many key tiles are split so that the
 // SMs get even shares: of kCand chunk lengths the one with the smallest
-//     max(chunk, ceil(entries / SMs) * mean entry) + 3 ceil(entries / SMs)
+//     max(chunk, ceil(entries / units) * mean entry) + 3 ceil(entries / units)
 // (in key tiles; 3 is about what starting and ending an entry costs).  Entries are ordered by
-// length, longest first, in 64 classes, for the kernel's back-and-forth assignment to CTAs.
+// length, longest first, in 64 classes, for the kernel's back-and-forth assignment.  All of it
+// is latency: the lengths stay in shared memory and a warp tries each chunk length.
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(AttnParams p, TilePlan w, int tt) {
-  __shared__ int sh_scan[32], sh_total, sh_kvmax, sh_cnt[kCand], sh_spl[kCand], sh_hist[64], sh_chunk;
-  __shared__ int sh_slot, sh_nsplit, sh_big[kPlanThreads], sh_nbig;
-  __shared__ unsigned long long sh_work;
+  constexpr int kWarps = kPlanThreads / 32;
+  __shared__ int sh_scan[kWarps], sh_total, sh_kvmax, sh_hist[64], sh_slot, sh_nsplit, sh_nbig;
+  __shared__ int sh_big[kPlanThreads], sh_kvt[kPlanTiles];
+  __shared__ float sh_cost[kCand];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
-  if (tid == 0) sh_total = sh_kvmax = sh_slot = sh_nsplit = 0, sh_work = 0;
-  if (tid < kCand) sh_cnt[tid] = sh_spl[tid] = 0;
+  if (tid == 0) sh_total = sh_kvmax = sh_slot = sh_nsplit = sh_nbig = 0;
   if (tid < 64) sh_hist[tid] = 0;
-  Entry *rec = w.rec;
-  unsigned long long work = 0;
-  int kvmax = 0;
-  auto put = [&](int at, int bos, int t, int len, int i) {
+  int kvmax = 1;
+  auto put = [&](int at, int n, int bos, int t, int len, int i) {
     if (at >= w.max_tiles) return;  // only with a malformed cu_seqlens
     const int tok0 = i * tt, ntok = min(tt, t - tok0);
     const int kvt = (visible(len - t + tok0, ntok, len) + kBN - 1) / kBN;
-    rec[at] = Entry{bos + tok0, ntok, 0, len - t + tok0, 0, kvt, 0, len};
-    work += kvt;
+    w.rec[at] = Entry{bos + tok0, ntok, n, len - t + tok0, 0, kvt, 0, len};
+    if (at < kPlanTiles) sh_kvt[at] = kvt;
     kvmax = max(kvmax, kvt);
   };
+  auto length = [&](int i) { return i < kPlanTiles ? sh_kvt[i] : w.rec[i].kt1; };
   for (int n0 = 0; n0 < p.num_seqs; n0 += kPlanThreads) {
     const int n = n0 + tid;
     int bos = 0, t = 0, len = 0;
@@ -294,88 +329,66 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(AttnParams p, TilePl
       const int v = __shfl_up_sync(0xffffffffu, s, o);
       if (lane >= o) s += v;
     }
-    __syncthreads();
-    if (tid == 0) sh_nbig = 0;
     if (lane == 31) sh_scan[warp] = s;
     __syncthreads();
-    int before = sh_total;
-    for (int i = 0; i < warp; ++i) before += sh_scan[i];
-    const int at = before + s - tiles;
-    if (n < p.num_seqs) {
+    int at = sh_total + s - tiles;
+    for (int i = 0; i < warp; ++i) at += sh_scan[i];
+    if (tiles > 4) {  // long sequences: all threads over the tiles, below
+      sh_big[atomicAdd(&sh_nbig, 1)] = n;
       w.base[n] = at;
-      if (tiles <= 4) {
-        for (int i = 0; i < tiles; ++i) {
-          put(at + i, bos, t, len, i);
-          if (at + i < w.max_tiles) rec[at + i].seq = n;
-        }
-      } else {
-        sh_big[atomicAdd(&sh_nbig, 1)] = n;
-      }
+    } else {
+      for (int i = 0; i < tiles; ++i) put(at + i, n, bos, t, len, i);
     }
     __syncthreads();
-    if (tid == kPlanThreads - 1) sh_total = before + s;
-    for (int b = 0; b < sh_nbig; ++b) {  // long sequences: all threads over the tiles
+    if (tid == kPlanThreads - 1) sh_total = at + tiles;
+    for (int b = 0; b < sh_nbig; ++b) {
       const int m = sh_big[b];
-      int bos2, t2, len2;
-      seq_info(p, m, bos2, t2, len2);
-      const int at2 = w.base[m];
-      for (int i = tid; i < (t2 + tt - 1) / tt; i += kPlanThreads) {
-        put(at2 + i, bos2, t2, len2, i);
-        if (at2 + i < w.max_tiles) rec[at2 + i].seq = m;
-      }
+      seq_info(p, m, bos, t, len);
+      const int first = w.base[m];
+      for (int i = tid; i < (t + tt - 1) / tt; i += kPlanThreads) put(first + i, m, bos, t, len, i);
     }
+    __syncthreads();
+    if (tid == 0) sh_nbig = 0;
   }
-  atomicAdd(&sh_work, work);
-  atomicMax(&sh_kvmax, kvmax);
+  kvmax = __reduce_max_sync(0xffffffffu, kvmax);
+  if (lane == 0) atomicMax(&sh_kvmax, kvmax);
   __syncthreads();
   const int tiles = min(sh_total, w.max_tiles);
-  kvmax = max(sh_kvmax, 1);
-  // candidates
+  kvmax = sh_kvmax;
   constexpr int parts_of[kCand] = {1, 2, 3, 4, 5, 6, 8, 10, 12, 16, 19, 25, 38, 50, 76, 152};
-  {
-    int cnt[kCand], spl[kCand];
-#pragma unroll
-    for (int j = 0; j < kCand; ++j) cnt[j] = spl[j] = 0;
-    for (int i = tid; i < tiles; i += kPlanThreads) {
-      const int kvt = rec[i].kt1;
-#pragma unroll
-      for (int j = 0; j < kCand; ++j) {
-        const int chunk = (kvmax + parts_of[j] - 1) / parts_of[j];
-        const int parts = max(1, (kvt + chunk - 1) / chunk);
-        cnt[j] += parts;
-        spl[j] += parts > 1 ? parts : 0;
-      }
+  for (int c = warp; c < kCand; c += kWarps) {
+    const int chunk = (kvmax + parts_of[c] - 1) / parts_of[c];
+    const float inv = 1.f / chunk;
+    int cnt = 0, spl = 0;
+    float work = 0.f;
+    for (int i = lane; i < tiles; i += 32) {
+      const int kvt = length(i), parts = parts_in(kvt, chunk, inv);
+      cnt += parts;
+      spl += parts > 1 ? parts : 0;
+      work += kvt;
     }
-#pragma unroll
-    for (int j = 0; j < kCand; ++j) {
-      cnt[j] = __reduce_add_sync(0xffffffffu, cnt[j]);
-      spl[j] = __reduce_add_sync(0xffffffffu, spl[j]);
-      if (lane == 0 && cnt[j]) atomicAdd(&sh_cnt[j], cnt[j]), atomicAdd(&sh_spl[j], spl[j]);
+    cnt = __reduce_add_sync(0xffffffffu, cnt);
+    spl = __reduce_add_sync(0xffffffffu, spl);
+    work = warp_sum(work);
+    if (lane == 0) {
+      const float items = (float)cnt * p.hkv, rounds = ceilf(items / w.units);
+      sh_cost[c] = c > 0 && (long long)spl * p.hkv > w.slots
+                       ? CUDART_INF_F
+                       : fmaxf((float)chunk, rounds * (work * p.hkv / fmaxf(items, 1.f))) + 3.f * rounds;
     }
   }
   __syncthreads();
-  if (tid == 0) {
-    float best = CUDART_INF_F;
-    int chunk = kvmax;
-    for (int j = 0; j < kCand; ++j) {
-      const int c = (kvmax + parts_of[j] - 1) / parts_of[j];
-      if (j > 0 && (long long)sh_spl[j] * p.hkv > w.slots) break;
-      const float items = (float)sh_cnt[j] * p.hkv;
-      const float rounds = ceilf(items / w.units);
-      const float cost = fmaxf((float)c, rounds * ((float)sh_work * p.hkv / fmaxf(items, 1.f))) + 3.f * rounds;
-      if (cost < best) best = cost, chunk = c;
-    }
-    sh_chunk = chunk;
-  }
-  __syncthreads();
-  const int chunk = sh_chunk;
-  auto cls = [&](int len) { return 63 - min(63, len * 63 / chunk); };
+  int best = 0;
+#pragma unroll
+  for (int c = 1; c < kCand; ++c)
+    if (sh_cost[c] < sh_cost[best]) best = c;
+  const int chunk = (kvmax + parts_of[best] - 1) / parts_of[best];
+  const float inv = 1.f / chunk;
+  auto cls = [&](int len) { return 63 - min(63, (int)(len * 63 * inv)); };
+  auto cut = [&](int kvt, int q, int parts) { return parts == 1 ? q * kvt : (int)((long long)kvt * q / parts); };
   for (int i = tid; i < tiles; i += kPlanThreads) {
-    const int kvt = rec[i].kt1, parts = max(1, (kvt + chunk - 1) / chunk);
-    for (int q = 0; q < parts; ++q) {
-      const int a = (int)((long long)kvt * q / parts), b = (int)((long long)kvt * (q + 1) / parts);
-      atomicAdd(&sh_hist[cls(b - a)], 1);
-    }
+    const int kvt = length(i), parts = parts_in(kvt, chunk, inv);
+    for (int q = 0; q < parts; ++q) atomicAdd(&sh_hist[cls(cut(kvt, q + 1, parts) - cut(kvt, q, parts))], 1);
   }
   __syncthreads();
   if (warp == 0) {  // exclusive scan of the 64 classes
@@ -391,19 +404,18 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(AttnParams p, TilePl
   }
   __syncthreads();
   for (int i = tid; i < tiles; i += kPlanThreads) {
-    Entry e = rec[i];
-    const int kvt = e.kt1, parts = max(1, (kvt + chunk - 1) / chunk);
+    Entry e = w.rec[i];
+    const int kvt = length(i), parts = parts_in(kvt, chunk, inv);
     int slot = -1;
     if (parts > 1 || w.all_slots) {
       slot = atomicAdd(&sh_slot, parts) * p.hkv;
       w.split[atomicAdd(&sh_nsplit, 1)] = Split{e.tok0, e.ntok, slot, parts};
     }
     for (int q = 0; q < parts; ++q) {
-      const int a = (int)((long long)kvt * q / parts), b = (int)((long long)kvt * (q + 1) / parts);
-      e.kt0 = a;
-      e.kt1 = b;
+      e.kt0 = cut(kvt, q, parts);
+      e.kt1 = cut(kvt, q + 1, parts);
       e.slot = slot < 0 ? -1 : slot + q * p.hkv;
-      w.entry[atomicAdd(&sh_hist[cls(b - a)], 1)] = e;
+      w.entry[atomicAdd(&sh_hist[cls(e.kt1 - e.kt0)], 1)] = e;
     }
   }
   __syncthreads();
@@ -614,46 +626,76 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
         }
         tc::fence_after();
       }
+      // A lane has a row; for global memory four lanes exchange 16-byte units (transpose4), so that
+      // an access covers 64 bytes of eight rows and not 16 of 32 (a line a cycle is the limit).
       const int tok = e.tok0 + dt, head = h * G + row % G;
-      const float inv = l > 0.f ? 1.f / l : 0.f;
-      const long long orow = (long long)tok * p.hq + head;
-      float *part = nullptr;
+      const int orow = live ? tok * p.hq + head : -1;
+      const int unit4 = lane & 3;
+      int rowk[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) rowk[k] = __shfl_sync(0xffffffffu, orow, (lane & 28) + k);
       if (e.slot >= 0) {
         const long long at = (long long)(e.slot + h) * kTileRows + sub * 128 + row;
-        part = w.part + at * D;
         if (live) *reinterpret_cast<float2 *>(w.ml + 2 * at) = make_float2(m, l);
-      } else if (live && p.lse) {
-        p.lse[orow] = l > 0.f ? (m + log2f(l)) * kLn2 : -CUDART_INF_F;
-      }
+        float *part = w.part + (at - unit4) * D + 4 * unit4;
 #pragma unroll 1
-      for (int c = 0; c < D; c += 32) {
-        uint32_t o[32];
-        if (n > 0) {
-          tc::ld32(o_base + c, o);
-          tc::wait_ld();
-          tie32(o);
-        } else {
+        for (int c = 0; c < D; c += 32) {
+          uint32_t o[32];
+          read_o(o, o_base + c, n > 0);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = 0;
+          for (int i = 0; i < 32; i += 16) {
+            uint4 u[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              u[k] = make_uint4(o[i + 4 * k], o[i + 4 * k + 1], o[i + 4 * k + 2], o[i + 4 * k + 3]);
+            transpose4(u, lane);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if (rowk[k] >= 0) *reinterpret_cast<uint4 *>(part + k * D + c + i) = u[k];
+          }
         }
-        if (!live) continue;
-        if (part) {
+      } else {
+        if (live && p.lse) p.lse[orow] = l > 0.f ? (m + log2f(l)) * kLn2 : -CUDART_INF_F;
+        const float inv = l > 0.f ? 1.f / l : 0.f;
+        const __nv_bfloat16 *gk[4];
+        uint4 gate[4];
+        if (p.gate) {
+          const long long off = live ? tok * p.gs[0] + head * p.gs[1] : 0;
 #pragma unroll
-          for (int i = 0; i < 32; i += 4)
-            *reinterpret_cast<uint4 *>(part + c + i) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
-          continue;
+          for (int k = 0; k < 4; ++k)
+            gk[k] = (const __nv_bfloat16 *)p.gate + __shfl_sync(0xffffffffu, off, (lane & 28) + k) + 8 * unit4;
         }
-        const __nv_bfloat16 *gate =
-            p.gate ? (const __nv_bfloat16 *)p.gate + tok * p.gs[0] + head * p.gs[1] + c : nullptr;
-        __nv_bfloat16 *out = (__nv_bfloat16 *)p.o + orow * D + c;
+        auto fetch = [&](int c) {
 #pragma unroll
-        for (int i = 0; i < 32; i += 8) {
-          float x[8];
+          for (int k = 0; k < 4; ++k)
+            gate[k] = rowk[k] >= 0 ? *reinterpret_cast<const uint4 *>(gk[k] + c) : make_uint4(0, 0, 0, 0);
+        };
+        if (p.gate) fetch(0);
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          uint32_t o[32];
+          read_o(o, o_base + c, n > 0);
+          uint4 g[4], u[4];
+          if (p.gate) {
 #pragma unroll
-          for (int k = 0; k < 8; ++k) x[k] = __uint_as_float(o[i + k]) * inv;
-          if (gate) gate8(x, *reinterpret_cast<const uint4 *>(gate + i));
-          *reinterpret_cast<uint4 *>(out + i) = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]),
-                                                           pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+            for (int k = 0; k < 4; ++k) g[k] = gate[k];
+            if (c + 32 < D) fetch(c + 32);
+            transpose4(g, lane);
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            float x[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(o[8 * k + i]) * inv;
+            if (p.gate) gate8(x, g[k]);
+            u[k] = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]),
+                              pack_bf16(x[6], x[7]));
+          }
+          transpose4(u, lane);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (rowk[k] >= 0)
+              *reinterpret_cast<uint4 *>((__nv_bfloat16 *)p.o + (long long)rowk[k] * D + c + 8 * unit4) = u[k];
         }
       }
       tc::fence_before();
