@@ -56,7 +56,12 @@ cudaError_t launch_attn_step(const AttnParams &p, void *ws, float *dense_ml, flo
 unsigned int *device_status_word();
 
 // x <- x * sigmoid(gate), gate in bf16.
-__device__ __forceinline__ float sigmoid(float g) { return __fdividef(1.f, 1.f + __expf(-g)); }
+__device__ __forceinline__ float sigmoid(float g) {
+  float e, r;  // 1 / (1 + 2^(-g log2 e)); 0 where the power overflows
+  asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(e) : "f"(g * -1.4426950408889634f));
+  asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(r) : "f"(1.f + e));
+  return r;
+}
 __device__ __forceinline__ void gate4(float *x, const uint2 &g) {
   x[0] *= sigmoid(__uint_as_float(g.x << 16));
   x[1] *= sigmoid(__uint_as_float(g.x & 0xffff0000u));

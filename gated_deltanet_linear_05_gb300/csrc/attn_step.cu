@@ -78,6 +78,7 @@ __global__ void __launch_bounds__(StepCfg<D>::THREADS, D == 128 ? 2 : 1)
     sh_dead = 0;
     sh_total = 0;
   }
+  if (tid == 0) prefetch_map(&kmap), prefetch_map(&vmap);
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   __syncthreads();

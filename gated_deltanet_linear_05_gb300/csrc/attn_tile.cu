@@ -34,6 +34,7 @@ namespace gdn {
 namespace {
 
 constexpr int kBN = 128;        // keys per tile
+constexpr int kAhead = 2;       // 32-column chunks of the gate fetched ahead in the epilogue
 constexpr int kTileRows = 256;  // rows per tile: two sub-tiles
 
 template <int D_>
@@ -164,6 +165,12 @@ __device__ __forceinline__ void load_kv(void *dst, const void *map, int x, int y
         : "memory");
   }
 }
+// A load that stays where it stands (the compiler would move it down to its use).
+__device__ __forceinline__ uint4 load_now(const void *p) {
+  uint4 v;
+  asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];\n" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
 // Four lanes' 16-byte units: unit k of lane i to unit i of lane k.
 __device__ __forceinline__ void swap_units(uint4 &a, uint4 &b, bool up, int mask) {
   uint4 s = up ? a : b;
@@ -262,7 +269,7 @@ struct TilePlan {
   float *ml;      // [slot][row] {m, l}
   float *part;    // [slot][row][D]
   float *dense_ml, *dense;  // one result per row of the call instead (attn_step.cu), or NULL
-  int max_tiles, units, slots, all_slots;
+  int max_tiles, max_entries, units, slots, all_slots;
   int uniform_parts, uniform_kt;  // > 0: no plan, equal parts of equal tiles (shared prefix)
   unsigned int *err;
 };
@@ -454,10 +461,11 @@ __device__ __forceinline__ bool item_at(const AttnParams &p, const TilePlan &w, 
     e.kvlen = p.prefix_len;
     return true;
   }
-  if (i >= (long long)w.head[0] * p.hkv) return false;
+  if (i / p.hkv >= w.max_entries) return false;
   h = (int)(i % p.hkv);
   const int4 *src = reinterpret_cast<const int4 *>(w.entry + i / p.hkv);
   const int4 a = src[0], b = src[1];
+  if (i / p.hkv >= w.head[0]) return false;  // (three loads side by side, not one after another)
   e = Entry{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
   return true;
 }
@@ -497,7 +505,15 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
     mbar_fence_init();
     bars.dead = 0;
   }
-  if (warp == C::LOADER) tmem_alloc<C::GRP>(&bars.tmem);
+  if (warp == C::LOADER) {
+    if (lane == 0) {
+      prefetch_map(&qmap);
+      prefetch_map(&kmap);
+      prefetch_map(&vmap);
+    }
+    __syncwarp();
+    tmem_alloc<C::GRP>(&bars.tmem);
+  }
   tc::fence_before();
   __syncthreads();
   if (C::PAIR) cluster_sync();  // the other CTA's barriers are ready
@@ -617,7 +633,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
         l += su.x + su.y;
       }
       // epilogue
-      if (n > 0) {
+      auto settle = [&]() {  // the last P V
         if (C::NBUF == 2) {
           if (n > 1) wait_bar(&bars.pv_done[cnt & 1], ((cnt - 2) >> 1) & 1, dead, w.err);
           wait_bar(&bars.pv_done[(cnt - 1) & 1], ((cnt - 1) >> 1) & 1, dead, w.err);
@@ -625,7 +641,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
           wait_bar(&bars.pv_done[sub], (cnt - 1) & 1, dead, w.err);
         }
         tc::fence_after();
-      }
+      };
       // A lane has a row; for global memory four lanes exchange 16-byte units (transpose4), so that
       // an access covers 64 bytes of eight rows and not 16 of 32 (a line a cycle is the limit).
       const int tok = e.tok0 + dt, head = h * G + row % G;
@@ -638,6 +654,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
         const long long at = (long long)(e.slot + h) * kTileRows + sub * 128 + row;
         if (live) *reinterpret_cast<float2 *>(w.ml + 2 * at) = make_float2(m, l);
         float *part = w.part + (at - unit4) * D + 4 * unit4;
+        if (n > 0) settle();
 #pragma unroll 1
         for (int c = 0; c < D; c += 32) {
           uint32_t o[32];
@@ -658,30 +675,37 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
         if (live && p.lse) p.lse[orow] = l > 0.f ? (m + log2f(l)) * kLn2 : -CUDART_INF_F;
         const float inv = l > 0.f ? 1.f / l : 0.f;
         const __nv_bfloat16 *gk[4];
-        uint4 gate[4];
+        uint4 gate[kAhead][4];
         if (p.gate) {
           const long long off = live ? tok * p.gs[0] + head * p.gs[1] : 0;
 #pragma unroll
           for (int k = 0; k < 4; ++k)
             gk[k] = (const __nv_bfloat16 *)p.gate + __shfl_sync(0xffffffffu, off, (lane & 28) + k) + 8 * unit4;
         }
-        auto fetch = [&](int c) {
+        auto fetch = [&](uint4 (&to)[4], int c) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            gate[k] = rowk[k] >= 0 ? *reinterpret_cast<const uint4 *>(gk[k] + c) : make_uint4(0, 0, 0, 0);
+          for (int k = 0; k < 4; ++k) {
+            to[k] = make_uint4(0, 0, 0, 0);
+            if (rowk[k] >= 0) to[k] = load_now(gk[k] + c);
+          }
         };
-        if (p.gate) fetch(0);
-#pragma unroll 1
+        if (p.gate) {
+#pragma unroll
+          for (int b = 0; b < kAhead; ++b) fetch(gate[b], 32 * b);
+        }
+        if (n > 0) settle();
+#pragma unroll (kAhead)
         for (int c = 0; c < D; c += 32) {
           uint32_t o[32];
-          read_o(o, o_base + c, n > 0);
           uint4 g[4], u[4];
           if (p.gate) {
+            uint4 (&mine)[4] = gate[c / 32 % kAhead];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) g[k] = gate[k];
-            if (c + 32 < D) fetch(c + 32);
+            for (int k = 0; k < 4; ++k) g[k] = mine[k];
+            if (c + 32 * kAhead < D) fetch(mine, c + 32 * kAhead);
             transpose4(g, lane);
           }
+          read_o(o, o_base + c, n > 0);
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             float x[8];
@@ -1023,6 +1047,7 @@ size_t layout(TilePlan *own, TilePlan *pre, char *ws, int num_seqs, int tokens, 
   a.ml = (float *)take(own_slots * slot * 2);
   a.part = (float *)take(own_slots * slot * D);
   a.max_tiles = z.max_tiles;
+  a.max_entries = entries;
   if (prefix_len > 0) {
     b.uniform_parts = prefix_parts<D>(z.prefix_tiles, hkv, prefix_len);
     b.uniform_kt = (prefix_len + kBN - 1) / kBN;
