@@ -5,6 +5,7 @@
 #include <cuda_fp8.h>
 
 #include "attn.h"
+#include "attn_tma.cuh"
 #include "common.cuh"
 
 namespace gdn {
@@ -45,94 +46,125 @@ __device__ __forceinline__ uint64_t turn_fraction(double f) {
 }
 
 constexpr int kAppendWarps = 8;
+constexpr int kAppendRows = 4;  // rows that a warp has in flight per lane group
 
-// One warp per (token, share of its head rows): a row takes D / 8 lanes of 8 elements, the
-// token's cosines and sines stay in registers for all its rows.  `share`: warps per token.
-template <int D>
+// A warp takes one token's head rows (or, with few tokens, `share` warps a token), a row in D / 8
+// lanes of 8 elements.  The turns per position of a lane's frequencies are kept over the warp's
+// tokens, cosines and sines over a token's rows; rows come kAppendRows at a time, so that
+// loads are in flight while the ones before are rotated.  The rotation's other half reaches a
+// lane as the raw bf16 words of the lane that has it.  Sine and cosine by the fast
+// instructions on an angle already reduced to half a turn: 2^-21 absolute, against 2^-9 of bf16.
+template <int D, bool NORM>
 __global__ void __launch_bounds__(32 * kAppendWarps) append_kernel(AppendParams p, int share) {
-  constexpr int LPR = D / 8, RPW = 32 / LPR;
+  constexpr int LPR = D / 8, RPW = 32 / LPR, U = kAppendRows;
   const int lane = threadIdx.x & 31;
-  const long long w = (long long)blockIdx.x * kAppendWarps + (threadIdx.x >> 5);
-  const int tok = (int)(w / share), part = (int)(w % share);
-  if (tok >= p.tokens) return;
+  const int part = (int)((blockIdx.x * kAppendWarps + (threadIdx.x >> 5)) % share);
+  const int tokens_at_once = (int)(gridDim.x * kAppendWarps / share);
   const int col = (lane % LPR) * 8;
   const int half = p.rot >> 1;
-  // the token's place
-  int n = tok, back = 1;  // back: tokens from this one to the sequence's end
-  if (p.cu_seqlens) {
-    n = find_seq(p.cu_seqlens, p.num_seqs, tok, lane);
-    int bos, eos;
-    seq_range(p.cu_seqlens, n, p.tokens, bos, eos);
-    back = eos - tok;
-  }
-  const long long cap = (long long)p.max_pages * p.page_size;
-  const int len = (int)min(max((long long)p.kv_lens[n], 0ll), cap);
-  const int place = len - back;
-  long long dst = -1;  // element offset of the token's rows of head 0
-  if (place >= 0 && back > 0) {
-    const int pg = p.page_table[(long long)n * p.max_pages + place / p.page_size];
-    if ((unsigned)pg < (unsigned)p.num_pages)
-      dst = (long long)pg * p.page_stride + (long long)(place % p.page_size) * D;
-  }
-  float cs[8], sn[8];
-  const bool rot = col < p.rot;
+  const bool rot = col < p.rot, low = col < half;
+  const int f0 = rot ? (low ? col : col - half) : 0;  // first frequency of this lane's eight
+  const int peer = (lane & ~(LPR - 1)) + ((low ? lane + half / 8 : lane - half / 8) & (LPR - 1));
+  const int rows = p.hq + 2 * p.hkv;
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+  uint64_t turn[8];
+  int axis[8];
   if (rot) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const int f = (col + i) % half;
-      int pos = p.pos0 + place;
-      if (p.positions) {
-        const int ax = p.rope_axis ? min(max(p.rope_axis[f], 0), p.axes - 1) : 0;
-        pos = p.positions[(long long)ax * p.tokens + tok];
-      }
-      const uint64_t turn = turn_fraction(p.inv_freq[f]) * (uint64_t)(int64_t)pos;
-      sincospif((float)(int32_t)(turn >> 32) * 0x1p-31f, &sn[i], &cs[i]);
-      if (col + i < half) sn[i] = -sn[i];  // out = x cos + partner * sn
+      turn[i] = turn_fraction(p.inv_freq[f0 + i]);
+      axis[i] = p.rope_axis ? min(max(p.rope_axis[f0 + i], 0), p.axes - 1) : 0;
     }
   }
-  const int shift = half / 8;
-  const int peer = (lane & ~(LPR - 1)) + ((col < half ? lane % LPR + shift : lane % LPR - shift) & (LPR - 1));
-  const int rows = p.hq + 2 * p.hkv;
-  const __nv_bfloat16 *q = (const __nv_bfloat16 *)p.q + tok * p.qs[0] + col;
-  const __nv_bfloat16 *k = (const __nv_bfloat16 *)p.k + tok * p.ks[0] + col;
-  const __nv_bfloat16 *v = (const __nv_bfloat16 *)p.v + tok * p.vs[0] + col;
-  for (int r0 = part * RPW; r0 < rows; r0 += share * RPW) {
-    const int r = r0 + lane / LPR;
-    const bool on = r < rows;
-    const int kind = r < p.hq ? 0 : r < p.hq + p.hkv ? 1 : 2;
-    const int h = r - (kind == 0 ? 0 : kind == 1 ? p.hq : p.hq + p.hkv);
-    uint4 u = make_uint4(0, 0, 0, 0);
-    if (on)
-      u = *(const uint4 *)(kind == 0 ? q + h * p.qs[1] : kind == 1 ? k + h * p.ks[1] : v + h * p.vs[1]);
-    float x[8];
-    unpack8(u, x);
-    const float *nw = kind == 0 ? p.q_norm : kind == 1 ? p.k_norm : nullptr;
-    if (p.q_norm || p.k_norm) {
-      float s = 0.f;
+  for (int tok = (int)((blockIdx.x * kAppendWarps + (threadIdx.x >> 5)) / share); tok < p.tokens;
+       tok += tokens_at_once) {
+    const __nv_bfloat16 *q = (const __nv_bfloat16 *)p.q + tok * p.qs[0] + col;
+    const __nv_bfloat16 *k = (const __nv_bfloat16 *)p.k + tok * p.ks[0] + col;
+    const __nv_bfloat16 *v = (const __nv_bfloat16 *)p.v + tok * p.vs[0] + col;
+    uint4 u[U];
+    auto fetch = [&](int r0) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) s = fmaf(x[i], x[i], s);
+      for (int i = 0; i < U; ++i) {
+        const int r = r0 + i * share * RPW + lane / LPR;
+        const __nv_bfloat16 *src = r < p.hq ? q + r * p.qs[1] : r < p.hq + p.hkv ? k + (r - p.hq) * p.ks[1]
+                                                                                 : v + (r - p.hq - p.hkv) * p.vs[1];
+        u[i] = r < rows ? *(const uint4 *)src : make_uint4(0, 0, 0, 0);
+      }
+    };
+    fetch(part * RPW);
+    // the token's place
+    int n = tok, back = 1;  // back: tokens from this one to the sequence's end
+    if (p.cu_seqlens) {
+      n = find_seq(p.cu_seqlens, p.num_seqs, tok, lane);
+      int bos, eos;
+      seq_range(p.cu_seqlens, n, p.tokens, bos, eos);
+      back = eos - tok;
+    }
+    const long long cap = (long long)p.max_pages * p.page_size;
+    const int len = (int)min(max((long long)p.kv_lens[n], 0ll), cap);
+    const int place = len - back;
+    long long dst = -1;  // element offset of the token's rows of head 0
+    if (place >= 0 && back > 0) {
+      const int lps = 31 - __clz(p.page_size);
+      const int pg = p.page_table[(long long)n * p.max_pages + (place >> lps)];
+      if ((unsigned)pg < (unsigned)p.num_pages)
+        dst = (long long)pg * p.page_stride + (long long)(place & (p.page_size - 1)) * D;
+    }
+    float cs[8], sn[8];
+    if (rot) {
 #pragma unroll
-      for (int o = LPR / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-      if (nw) {
-        const float inv = 1.f / sqrtf(s * (1.f / D) + p.eps);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = x[i] * inv * nw[col + i];
+      for (int i = 0; i < 8; ++i) {
+        const int pos = p.positions ? p.positions[(long long)axis[i] * p.tokens + tok] : p.pos0 + place;
+        const int32_t t = (int32_t)((turn[i] * (uint64_t)(int64_t)pos) >> 32);
+        __sincosf((float)t * 1.4629180792671596e-9f, &sn[i], &cs[i]);  // 2 pi 2^-32
+        if (low) sn[i] = -sn[i];  // out = x cos + other * sn
       }
     }
-    float y[8];
+    for (int r0 = part * RPW; r0 < rows; r0 += U * share * RPW) {
+      uint4 raw[U];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = __shfl_sync(0xffffffffu, x[i], peer);
-    if (kind < 2 && rot) {
+      for (int i = 0; i < U; ++i) raw[i] = u[i];
+      if (r0 + U * share * RPW < rows) fetch(r0 + U * share * RPW);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = fmaf(x[i], cs[i], y[i] * sn[i]);
+      for (int i = 0; i < U; ++i) {
+        const int r = r0 + i * share * RPW + lane / LPR;
+        const int kind = r < p.hq ? 0 : r < p.hq + p.hkv ? 1 : 2;
+        uint4 o;
+        o.x = __shfl_sync(0xffffffffu, raw[i].x, peer);
+        o.y = __shfl_sync(0xffffffffu, raw[i].y, peer);
+        o.z = __shfl_sync(0xffffffffu, raw[i].z, peer);
+        o.w = __shfl_sync(0xffffffffu, raw[i].w, peer);
+        float x[8], y[8];
+        unpack8(raw[i], x);
+        unpack8(o, y);
+        if (NORM) {
+          float s = 0.f;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) s = fmaf(x[e], x[e], s);
+#pragma unroll
+          for (int m = LPR / 2; m > 0; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
+          const float *nw = kind == 0 ? p.q_norm : kind == 1 ? p.k_norm : nullptr;
+          if (nw) {
+            const float inv = rsqrtf(s * (1.f / D) + p.eps);
+            const int other = rot ? (low ? col + half : col - half) : col;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = x[e] * inv * nw[col + e], y[e] = y[e] * inv * nw[other + e];
+          }
+        }
+        if (rot) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[e] = fmaf(x[e], cs[e], y[e] * sn[e]);
+        }
+        if (r >= rows) continue;
+        if (kind == 0)
+          *(uint4 *)((__nv_bfloat16 *)p.q_out + ((long long)tok * p.hq + r) * D + col) = pack8(x);
+        else if (kind == 1 && dst >= 0)
+          *(uint4 *)((__nv_bfloat16 *)p.k_cache + dst + (long long)(r - p.hq) * p.page_size * D + col) = pack8(x);
+        else if (kind == 2 && dst >= 0)
+          *(uint4 *)((__nv_bfloat16 *)p.v_cache + dst + (long long)(r - p.hq - p.hkv) * p.page_size * D + col) = raw[i];
+      }
     }
-    if (kind < 2) u = pack8(x);
-    if (!on) continue;
-    if (kind == 0)
-      *(uint4 *)((__nv_bfloat16 *)p.q_out + ((long long)tok * p.hq + h) * D + col) = u;
-    else if (dst >= 0)
-      *(uint4 *)((__nv_bfloat16 *)(kind == 1 ? p.k_cache : p.v_cache) + dst +
-                 (long long)h * p.page_size * D + col) = u;
   }
 }
 
@@ -193,6 +225,8 @@ template <typename T, int NV>
 __global__ void __launch_bounds__(1024) add_rmsnorm_kernel(AddNormParams p) {
   __shared__ float sh_sum[32];
   __shared__ uint32_t sh_max[32];
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   const int warps = blockDim.x >> 5;
   const long long at = (long long)blockIdx.x * p.cols;
   float v[NV][8];
@@ -270,13 +304,11 @@ cudaError_t launch_norm_t(const AddNormParams &p, cudaStream_t stream) {
   const int want = p.rows < 304 && vecs <= 1024 ? 1 : vecs <= 2048 ? 2 : vecs <= 4096 ? 4 : 8;
   const int threads = ((vecs + want - 1) / want + 31) / 32 * 32;
   const unsigned grid = (unsigned)p.rows;
-  switch (want) {
-    case 1: add_rmsnorm_kernel<T, 1><<<grid, threads, 0, stream>>>(p); break;
-    case 2: add_rmsnorm_kernel<T, 2><<<grid, threads, 0, stream>>>(p); break;
-    case 4: add_rmsnorm_kernel<T, 4><<<grid, threads, 0, stream>>>(p); break;
-    default: add_rmsnorm_kernel<T, 8><<<grid, threads, 0, stream>>>(p); break;
-  }
-  return cudaGetLastError();
+  auto *kernel = want == 1   ? add_rmsnorm_kernel<T, 1>
+                 : want == 2 ? add_rmsnorm_kernel<T, 2>
+                 : want == 4 ? add_rmsnorm_kernel<T, 4>
+                             : add_rmsnorm_kernel<T, 8>;
+  return launch_dependent(kernel, grid, threads, 0, stream, 1, p);
 }
 
 }  // namespace
@@ -288,11 +320,11 @@ cudaError_t launch_kv_append(const AppendParams &p, cudaStream_t stream) {
   int share = 1;
   while (share < kAppendWarps && (long long)p.tokens * share < 152 * 16 && share * rpw < rows) share *= 2;
   const long long blocks = ((long long)p.tokens * share + kAppendWarps - 1) / kAppendWarps;
-  if (p.d == 128)
-    append_kernel<128><<<(unsigned)blocks, 32 * kAppendWarps, 0, stream>>>(p, share);
-  else
-    append_kernel<256><<<(unsigned)blocks, 32 * kAppendWarps, 0, stream>>>(p, share);
-  return cudaGetLastError();
+  const unsigned grid = (unsigned)(blocks < 152 * 8 ? blocks : 152 * 8);
+  const bool norm = p.q_norm || p.k_norm;
+  auto *kernel = p.d == 128 ? (norm ? append_kernel<128, true> : append_kernel<128, false>)
+                            : (norm ? append_kernel<256, true> : append_kernel<256, false>);
+  return launch_dependent(kernel, grid, 32 * kAppendWarps, 0, stream, 1, p, share);
 }
 
 cudaError_t launch_add_rmsnorm(const AddNormParams &p, gdn_dtype dtype, cudaStream_t stream) {
