@@ -8,7 +8,6 @@ once.
 from __future__ import annotations
 
 import ctypes
-import functools
 import math
 from typing import Optional
 
@@ -47,7 +46,6 @@ def make_attn_shape(num_seqs: int, total_tokens: int, num_q_heads: int, num_kv_h
     return s
 
 
-@functools.lru_cache(maxsize=4096)
 def _shape(n, tokens, hq, hkv, d, page_size, num_pages, max_pages, prefix_len, rotary_dim, axes,
            scale, page_stride, q_stride, k_stride=None, v_stride=None, gate_stride=None):
     """The C struct for these sizes and strides (never changed once made)."""
@@ -79,11 +77,9 @@ def gdn_attn_workspace(num_seqs: int, total_tokens: int, num_q_heads: int, num_k
 
 
 def _strides3(t, what):
-    """(token, head) strides of a [T, H, D] bf16 CUDA tensor whose rows are contiguous."""
-    if t.dtype != torch.bfloat16:
-        raise TypeError("%s must be bfloat16, got %s" % (what, t.dtype))
+    """(token, head) strides of a [T, H, D] bf16 tensor whose rows are contiguous."""
     st = t.stride()
-    if len(st) != 3 or not t.is_cuda or st[2] != 1:
+    if len(st) != 3 or st[2] != 1:
         raise ValueError("%s must be a [tokens, heads, head_dim] CUDA tensor with contiguous rows"
                          % what)
     if t.shape[0] <= 1 or t.shape[1] <= 1:  # torch leaves the stride of a size of 1 open
@@ -96,9 +92,7 @@ def _strides3(t, what):
 def _cache(k_cache, v_cache):
     """(num_pages, hkv, page_size, d, page_stride) of a pair of caches."""
     shape, st = k_cache.shape, k_cache.stride()
-    if (len(shape) != 4 or v_cache.shape != shape or v_cache.stride() != st or not k_cache.is_cuda
-            or not v_cache.is_cuda or k_cache.dtype != torch.bfloat16
-            or v_cache.dtype != torch.bfloat16):
+    if len(shape) != 4 or v_cache.shape != shape or v_cache.stride() != st:
         raise ValueError("the caches must be two alike [pages, kv_heads, page_size, head_dim] "
                          "bfloat16 CUDA tensors")
     pages, hkv, size, d = shape
@@ -107,24 +101,51 @@ def _cache(k_cache, v_cache):
     return pages, hkv, size, d, (st[0] if pages > 1 else hkv * size * d)
 
 
-def _index(t, what, dtype=torch.int32):
-    if t.dtype != dtype or not t.is_cuda or not t.is_contiguous():
-        raise ValueError("%s must be a contiguous %s CUDA tensor" % (what, dtype))
+_BF16, _I32, _F32 = torch.bfloat16, torch.int32, torch.float32
+_DENSE = torch.contiguous_format
+
+
+def _bf16(device, what, *tensors):
+    for t in tensors:
+        if t.dtype is not _BF16:
+            raise TypeError("%s must be bfloat16, got %s" % (what, t.dtype))
+        if t.get_device() != device or device < 0:
+            raise ValueError("%s must be CUDA tensors of one device" % what)
+
+
+def _index(device, t, what, dtype=_I32):
+    """The address of a contiguous tensor of indices (or frequencies)."""
+    if t.dtype is not dtype or t.get_device() != device or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous %s CUDA tensor on the queries' device"
+                         % (what, dtype))
     return t.data_ptr()
 
 
-def _float(t, shape, what):
-    if t.dtype != torch.float32 or not t.is_cuda or not t.is_contiguous() or t.shape != shape:
+def _float(device, t, shape, what):
+    if t.dtype is not _F32 or t.get_device() != device or not t.is_contiguous() or t.shape != shape:
         raise ValueError("%s must be a contiguous float32 CUDA tensor of shape %s"
                          % (what, tuple(shape)))
     return t.data_ptr()
 
 
-def _stream(stream, t):
-    return (torch.cuda.current_stream(t.device) if stream is None else stream).cuda_stream
+def _output(device, t, like, what):
+    if t.shape != like.shape or t.dtype is not _BF16 or t.get_device() != device \
+            or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous bfloat16 CUDA tensor of q's shape" % what)
+    return t
 
 
-def _sequences(q, page_table, kv_lens, cu_seqlens):
+def _stream(stream, device):
+    """The stream's handle: the current one of the device (a raw handle, as making a Stream
+    object costs as much as the rest of the marshalling), or the given Stream's."""
+    return _raw_stream(device) if stream is None else stream.cuda_stream
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda device: torch.cuda.current_stream(device).cuda_stream)
+
+
+def _sequences(page_table, kv_lens, cu_seqlens):
     """(num_seqs, max_pages) after checking the index tensors' shapes against each other."""
     n = kv_lens.shape[0]
     if page_table.dim() != 2 or page_table.shape[0] != n or kv_lens.dim() != 1:
@@ -134,19 +155,24 @@ def _sequences(q, page_table, kv_lens, cu_seqlens):
     return n, page_table.shape[1]
 
 
-def gdn_kv_append(q, k, v, k_cache, v_cache, page_table, kv_lens, inv_freq=None, cu_seqlens=None,
-                  positions=None, rope_axis=None, q_norm=None, k_norm=None, eps: float = 1e-6,
-                  q_out=None, prefix_len: int = 0, stream=None):
-    """Per-head RMS norm of q and k (with q_norm / k_norm [D] fp32), rotation of their first
-    2 * len(inv_freq) elements, q to q_out, k and v to their place in the paged cache.
-    q [T, Hq, D], k, v [T, Hkv, D] bf16, any token and head strides; caches
-    [pages, Hkv, page_size, D]; page_table [N, max_pages], kv_lens [N] (the call's tokens
-    included), cu_seqlens [N+1] int32 or None (one token per sequence); inv_freq [R/2] fp64
-    or None (no rotation); positions [T] or [axes, T] int32 (None: prefix_len + place) with
-    rope_axis [R/2] int32.  q_out None: a new tensor.  Returns q_out."""
+# What follows from the tensors' sizes and strides alone is checked and built once for each
+# combination of them: (shape struct, pointer to it).
+_made = {}
+
+
+def _remember(key, value):
+    if len(_made) >= 4096:
+        _made.clear()
+    _made[key] = value
+    return value
+
+
+def _append_shape(q, k, v, k_cache, v_cache, page_table, kv_lens, inv_freq, cu_seqlens, positions,
+                  rope_axis, prefix_len):
     pages, hkv, size, d, page_stride = _cache(k_cache, v_cache)
+    n, max_pages = _sequences(page_table, kv_lens, cu_seqlens)
+    qs = _strides3(q, "q"), _strides3(k, "k"), _strides3(v, "v")
     tokens, hq = q.shape[0], q.shape[1]
-    n, max_pages = _sequences(q, page_table, kv_lens, cu_seqlens)
     if q.shape[2] != d or k.shape != (tokens, hkv, d) or v.shape != (tokens, hkv, d):
         raise ValueError("q, k, v and the caches must agree in tokens, kv heads and head_dim")
     axes = 1
@@ -159,60 +185,96 @@ def gdn_kv_append(q, k, v, k_cache, v_cache, page_table, kv_lens, inv_freq=None,
         rot = 2 * inv_freq.shape[0]
         if rope_axis is not None and rope_axis.shape != inv_freq.shape:
             raise ValueError("rope_axis must have one entry per frequency")
-    if q_out is None:
-        q_out = torch.empty((tokens, hq, d), dtype=torch.bfloat16, device=q.device)
-    elif q_out.shape != q.shape or not q_out.is_contiguous() or q_out.dtype != torch.bfloat16 \
-            or not q_out.is_cuda:
-        raise ValueError("q_out must be a contiguous bfloat16 CUDA tensor of q's shape")
-    _, ref = _shape(n, tokens, hq, hkv, d, size, pages, max_pages, prefix_len, rot, axes, None,
-                    page_stride, _strides3(q, "q"), _strides3(k, "k"), _strides3(v, "v"))
+    return _shape(n, tokens, hq, hkv, d, size, pages, max_pages, prefix_len, rot, axes, None,
+                  page_stride, *qs)
+
+
+def gdn_kv_append(q, k, v, k_cache, v_cache, page_table, kv_lens, inv_freq=None, cu_seqlens=None,
+                  positions=None, rope_axis=None, q_norm=None, k_norm=None, eps: float = 1e-6,
+                  q_out=None, prefix_len: int = 0, stream=None):
+    """Per-head RMS norm of q and k (with q_norm / k_norm [D] fp32), rotation of their first
+    2 * len(inv_freq) elements, q to q_out, k and v to their place in the paged cache.
+    q [T, Hq, D], k, v [T, Hkv, D] bf16, any token and head strides; caches
+    [pages, Hkv, page_size, D]; page_table [N, max_pages], kv_lens [N] (the call's tokens
+    included), cu_seqlens [N+1] int32 or None (one token per sequence); inv_freq [R/2] fp64
+    or None (no rotation); positions [T] or [axes, T] int32 (None: prefix_len + place) with
+    rope_axis [R/2] int32.  q_out None: a new tensor.  Returns q_out."""
+    device = q.get_device()
+    _bf16(device, "q, k, v and the caches", q, k, v, k_cache, v_cache)
+    key = (q.shape, q.stride(), k.shape, k.stride(), v.shape, v.stride(), k_cache.shape,
+           k_cache.stride(), v_cache.shape, v_cache.stride(), page_table.shape, kv_lens.shape,
+           None if inv_freq is None else inv_freq.shape,
+           None if cu_seqlens is None else cu_seqlens.shape,
+           None if positions is None else positions.shape,
+           None if rope_axis is None else rope_axis.shape, prefix_len)
+    made = _made.get(key) or _remember(key, _append_shape(
+        q, k, v, k_cache, v_cache, page_table, kv_lens, inv_freq, cu_seqlens, positions, rope_axis,
+        prefix_len))
+    d = k_cache.shape[3:]
+    q_out = torch.empty_like(q, memory_format=_DENSE) if q_out is None \
+        else _output(device, q_out, q, "q_out")
     st = lib().gdn_kv_append(
-        ref, q.data_ptr(), k.data_ptr(), v.data_ptr(),
-        None if q_norm is None else _float(q_norm, (d,), "q_norm"),
-        None if k_norm is None else _float(k_norm, (d,), "k_norm"), eps,
-        None if inv_freq is None else _index(inv_freq, "inv_freq", torch.float64),
-        None if rope_axis is None else _index(rope_axis, "rope_axis"),
-        None if positions is None else _index(positions, "positions"),
-        _index(page_table, "page_table"), _index(kv_lens, "kv_lens"),
-        None if cu_seqlens is None else _index(cu_seqlens, "cu_seqlens"),
-        q_out.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), _stream(stream, q))
+        made[1], q.data_ptr(), k.data_ptr(), v.data_ptr(),
+        None if q_norm is None else _float(device, q_norm, d, "q_norm"),
+        None if k_norm is None else _float(device, k_norm, d, "k_norm"), eps,
+        None if inv_freq is None else _index(device, inv_freq, "inv_freq", torch.float64),
+        None if rope_axis is None else _index(device, rope_axis, "rope_axis"),
+        None if positions is None else _index(device, positions, "positions"),
+        _index(device, page_table, "page_table"), _index(device, kv_lens, "kv_lens"),
+        None if cu_seqlens is None else _index(device, cu_seqlens, "cu_seqlens"),
+        q_out.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), _stream(stream, device))
     if st != GDN_OK:
         raise GdnError(st, "gdn_kv_append")
     return q_out
 
 
-def _attend(name, q, k_cache, v_cache, prefix_table, prefix_len, page_table, kv_lens, cu_seqlens,
-            gate, scale, o, lse, workspace, stream):
+def _attend_shape(q, k_cache, v_cache, prefix_table, prefix_len, page_table, kv_lens, cu_seqlens,
+                  gate, scale):
     pages, hkv, size, d, page_stride = _cache(k_cache, v_cache)
-    tokens, hq = q.shape[0], q.shape[1]
-    n, max_pages = _sequences(q, page_table, kv_lens, cu_seqlens)
+    n, max_pages = _sequences(page_table, kv_lens, cu_seqlens)
+    q_stride = _strides3(q, "q")
     if q.shape[2] != d:
         raise ValueError("q and the caches must agree in head_dim")
-    gate_stride = None
+    if gate is not None and gate.shape != q.shape:
+        raise ValueError("gate must have q's shape")
+    if prefix_table is not None and prefix_table.numel() * size < prefix_len:
+        raise ValueError("prefix_table must cover prefix_len keys")
+    return _shape(n, q.shape[0], q.shape[1], hkv, d, size, pages, max_pages, prefix_len, 0, 1,
+                  scale, page_stride, q_stride, None, None,
+                  None if gate is None else _strides3(gate, "gate"))
+
+
+def _attend(name, q, k_cache, v_cache, prefix_table, prefix_len, page_table, kv_lens, cu_seqlens,
+            gate, scale, o, lse, workspace, stream):
+    device = q.get_device()
+    _bf16(device, "q and the caches", q, k_cache, v_cache)
     if gate is not None:
-        if gate.shape != q.shape:
-            raise ValueError("gate must have q's shape")
-        gate_stride = _strides3(gate, "gate")
-    if o is None:
-        o = torch.empty((tokens, hq, d), dtype=torch.bfloat16, device=q.device)
-    elif o.shape != q.shape or not o.is_contiguous() or o.dtype != torch.bfloat16 or not o.is_cuda:
-        raise ValueError("o must be a contiguous bfloat16 CUDA tensor of q's shape")
-    s, ref = _shape(n, tokens, hq, hkv, d, size, pages, max_pages, prefix_len, 0, 1, scale,
-                    page_stride, _strides3(q, "q"), None, None, gate_stride)
+        _bf16(device, "gate", gate)
+    key = (q.shape, q.stride(), k_cache.shape, k_cache.stride(), v_cache.shape, v_cache.stride(),
+           page_table.shape, kv_lens.shape, None if cu_seqlens is None else cu_seqlens.shape,
+           None if gate is None else (gate.shape, gate.stride()), scale,
+           None if prefix_table is None else prefix_table.shape, prefix_len)
+    made = _made.get(key) or _remember(key, _attend_shape(
+        q, k_cache, v_cache, prefix_table, prefix_len, page_table, kv_lens, cu_seqlens, gate, scale))
+    o = torch.empty_like(q, memory_format=_DENSE) if o is None \
+        else _output(device, o, q, "o")
     if workspace is None:
-        workspace = torch.zeros(max(gdn_attn_workspace_size(s), 1), dtype=torch.uint8,
+        workspace = torch.zeros(max(gdn_attn_workspace_size(made[0]), 1), dtype=torch.uint8,
                                 device=q.device)
-    args = [ref, q.data_ptr(), None if gate is None else gate.data_ptr(), k_cache.data_ptr(),
-            v_cache.data_ptr()]
-    if prefix_table is not None:
-        if prefix_table.numel() * size < prefix_len:
-            raise ValueError("prefix_table must cover prefix_len keys")
-        args.append(_index(prefix_table, "prefix_table"))
-    st = getattr(lib(), name)(
-        *args, _index(page_table, "page_table"), _index(kv_lens, "kv_lens"),
-        None if cu_seqlens is None else _index(cu_seqlens, "cu_seqlens"), o.data_ptr(),
-        None if lse is None else _float(lse, (tokens, hq), "lse"), workspace.data_ptr(),
-        workspace.numel() * workspace.element_size(), _stream(stream, q))
+    elif workspace.get_device() != device or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous CUDA tensor on the queries' device")
+    ends = (_index(device, page_table, "page_table"), _index(device, kv_lens, "kv_lens"),
+            None if cu_seqlens is None else _index(device, cu_seqlens, "cu_seqlens"), o.data_ptr(),
+            None if lse is None else _float(device, lse, q.shape[:2], "lse"), workspace.data_ptr(),
+            workspace.nbytes, _stream(stream, device))
+    gate = None if gate is None else gate.data_ptr()
+    if prefix_table is None:
+        st = lib().gdn_paged_attention(made[1], q.data_ptr(), gate, k_cache.data_ptr(),
+                                       v_cache.data_ptr(), *ends)
+    else:
+        st = lib().gdn_shared_prefix_attention(made[1], q.data_ptr(), gate, k_cache.data_ptr(),
+                                               v_cache.data_ptr(),
+                                               _index(device, prefix_table, "prefix_table"), *ends)
     if st != GDN_OK:
         raise GdnError(st, name)
     return o
@@ -241,6 +303,30 @@ def gdn_shared_prefix_attention(q, k_cache, v_cache, prefix_table, prefix_len: i
                    page_table, kv_lens, cu_seqlens, gate, scale, o, lse, workspace, stream)
 
 
+def _norm_plan(x, out, group):
+    """(rows, columns, dtype code, output type, shape of the scales)."""
+    cols = x.shape[-1]
+    code = {torch.bfloat16: GDN_BF16, torch.float32: GDN_F32}.get(x.dtype)
+    if code is None:
+        raise TypeError("x must be bfloat16 or float32, got %s" % x.dtype)
+    if out not in ("same", "e4m3"):
+        raise ValueError("out must be 'same' or 'e4m3'")
+    if out == "same" and group:
+        raise ValueError("groups go with out='e4m3'")
+    if group and (group != 128 or cols % 128):
+        raise ValueError("group must be 0, or 128 and divide the columns")
+    scales = None if out == "same" else x.shape[:-1] + ((cols // group if group else 1),)
+    return (x.numel() // max(cols, 1), cols, code, x.dtype if out == "same" else torch.float8_e4m3fn,
+            scales)
+
+
+def _alike(device, x, t):
+    if t.dtype is not x.dtype or t.shape != x.shape or t.get_device() != device \
+            or not t.is_contiguous():
+        raise ValueError("x, residual and residual_out must be alike, contiguous CUDA tensors")
+    return t.data_ptr()
+
+
 def gdn_add_rmsnorm(x, residual, weight, eps: float = 1e-6, residual_out=None, y=None, scale=None,
                     out: str = "same", group: int = 0, stream=None):
     """h = x + residual (rounded to x's type; x itself with residual None) and its RMS norm
@@ -248,42 +334,32 @@ def gdn_add_rmsnorm(x, residual, weight, eps: float = 1e-6, residual_out=None, y
     type, returns (y, h); out "e4m3": y in float8_e4m3fn with fp32 scales per row (group 0) or
     per 128 columns (group 128), returns (y, scale, h).  x, residual bf16 or fp32; weight
     fp32.  residual_out may be residual or x."""
-    cols = x.shape[-1]
-    rows = x.numel() // max(cols, 1)
-    if x.dtype == torch.bfloat16:
-        code = GDN_BF16
-    elif x.dtype == torch.float32:
-        code = GDN_F32
-    else:
-        raise TypeError("x must be bfloat16 or float32, got %s" % x.dtype)
-    if out not in ("same", "e4m3"):
-        raise ValueError("out must be 'same' or 'e4m3'")
-    for t in (x, residual, residual_out):
-        if t is not None and (t.dtype != x.dtype or t.shape != x.shape or not t.is_cuda
-                              or not t.is_contiguous()):
-            raise ValueError("x, residual and residual_out must be alike, contiguous CUDA tensors")
+    device = x.get_device()
+    key = ("norm", x.shape, x.dtype, out, group)
+    rows, cols, code, kind, scales = _made.get(key) or _remember(key, _norm_plan(x, out, group))
+    if device < 0:
+        raise ValueError("x must be a CUDA tensor")
+    xp = _alike(device, x, x)
+    rp = None if residual is None else _alike(device, x, residual)
     if residual is not None and residual_out is None:
         residual_out = torch.empty_like(x)
-    kind = x.dtype if out == "same" else torch.float8_e4m3fn
+        hp = residual_out.data_ptr()
+    else:
+        hp = None if residual_out is None else _alike(device, x, residual_out)
     if y is None:
         y = torch.empty_like(x, dtype=kind)
-    elif y.dtype != kind or y.shape != x.shape or not y.is_cuda or not y.is_contiguous():
+    elif y.dtype is not kind or y.shape != x.shape or y.get_device() != device \
+            or not y.is_contiguous():
         raise ValueError("y must be a contiguous %s CUDA tensor of x's shape" % kind)
     sp = None
-    if out == "e4m3":
-        if group and (group != 128 or cols % 128):
-            raise ValueError("group must be 0, or 128 and divide the columns")
-        shape = x.shape[:-1] + ((cols // group if group else 1),)
+    if scales is not None:
         if scale is None:
-            scale = torch.empty(shape, dtype=torch.float32, device=x.device)
-        sp = _float(scale, shape, "scale")
-    elif group:
-        raise ValueError("groups go with out='e4m3'")
-    st = lib().gdn_add_rmsnorm(
-        rows, cols, code, x.data_ptr(), None if residual is None else residual.data_ptr(),
-        _float(weight, (cols,), "weight"), eps,
-        None if residual_out is None else residual_out.data_ptr(), y.data_ptr(), sp,
-        group, _stream(stream, x))
+            scale = torch.empty(scales, dtype=_F32, device=x.device)
+            sp = scale.data_ptr()
+        else:
+            sp = _float(device, scale, scales, "scale")
+    st = lib().gdn_add_rmsnorm(rows, cols, code, xp, rp, _float(device, weight, x.shape[-1:], "weight"),
+                               eps, hp, y.data_ptr(), sp, group, _stream(stream, device))
     if st != GDN_OK:
         raise GdnError(st, "gdn_add_rmsnorm")
     h = x if residual_out is None else residual_out

@@ -443,7 +443,8 @@ cudaError_t run(const AttnParams &p, char *ws, float *dense_ml, float *dense, un
   cudaError_t err = cache_maps(&k, &v, p, kTile);
   if (err != cudaSuccess) return err;
   const size_t smem = C::SMEM + 1024;
-  err = cudaFuncSetAttribute(step_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  static std::atomic<uint64_t> allowed{0};
+  err = allow_smem(step_kernel<D>, smem, allowed);
   if (err != cudaSuccess) return err;
   return launch_dependent(step_kernel<D>, C::CTAS, C::THREADS, smem, stream, 1, p, w, k, v);
 }

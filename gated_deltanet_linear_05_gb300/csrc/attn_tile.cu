@@ -1079,7 +1079,8 @@ cudaError_t run(const AttnParams &p, char *ws, unsigned int *errw, cudaStream_t 
   if (err == cudaSuccess) err = cache_maps(&k, &v, p, C::KROWS);
   if (err != cudaSuccess) return err;
   const size_t smem = C::SMEM + 1024;
-  err = cudaFuncSetAttribute(tile_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  static std::atomic<uint64_t> allowed{0};
+  err = allow_smem(tile_kernel<D>, smem, allowed);
   if (err != cudaSuccess) return err;
   if (p.prefix_len > 0) {
     err = launch_dependent(tile_kernel<D>, kSms, C::THREADS, smem, stream, C::GRP, p, pre, q, k, v);

@@ -6,6 +6,8 @@
 #include <math_constants.h>
 #include <string.h>
 
+#include <atomic>
+
 #include "attn.h"
 #include "common.cuh"
 
@@ -99,6 +101,19 @@ cudaError_t bf16_map(CUtensorMap *map, const void *x, int rank, const cuuint64_t
 // Maps of K and V, [page][head][row][column], for boxes of min(page_size, tile) rows; zero
 // (and never used) for a cache without pages.
 cudaError_t cache_maps(CUtensorMap *k, CUtensorMap *v, const AttnParams &p, int tile);
+
+// Allows `kernel` its dynamic shared memory, once per device (`done`: a bit per device).
+template <typename... Args>
+cudaError_t allow_smem(void (*kernel)(Args...), size_t smem, std::atomic<uint64_t> &done) {
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err != cudaSuccess) return err;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (err == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return err;
+}
 
 // Launch, in clusters of `cluster` CTAs, as a programmatic dependent of the work before it on
 // the stream.
