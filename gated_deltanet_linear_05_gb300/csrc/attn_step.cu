@@ -36,7 +36,8 @@ struct StepCfg {
   static constexpr int CH = D / 64;
   static constexpr int RP = 132;                       // padded row of the join buffers (floats)
   static constexpr int R_BYTES = HALVES * 2 * 16 * RP * 4;
-  static constexpr int SMEM = STAGES * UNIT + 16 * D * 2 + R_BYTES;
+  static constexpr int Q_BYTES = 16 * D * 2;           // a pair's query rows
+  static constexpr int SMEM = STAGES * UNIT + 2 * Q_BYTES + R_BYTES;
 };
 
 struct StepPlan {
@@ -58,106 +59,144 @@ __device__ __forceinline__ uint32_t sw_off(int row, int col) {
 
 template <int D>
 __global__ void __launch_bounds__(StepCfg<D>::THREADS, D == 128 ? 2 : 1)
-    step_kernel(AttnParams p, StepPlan w, const __grid_constant__ CUtensorMap kmap,
-                const __grid_constant__ CUtensorMap vmap) {
+    step_kernel(AttnParams p, StepPlan w, const __grid_constant__ CUtensorMap qmap,
+                const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
   using C = StepCfg<D>;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ uint64_t full[C::STAGES], empty[C::STAGES];
+  __shared__ uint64_t full[C::STAGES], empty[C::STAGES], q_full[2], q_empty[2];
   __shared__ int sh_dead, sh_last, sh_n, sh_scan[C::WARPS + 1];
-  __shared__ long long sh_base, sh_total;
-  __shared__ float sh_m[C::WARPS][16], sh_l[C::WARPS][16];
+  __shared__ long long sh_base;
+  __shared__ float sh_ms[2][C::WARPS][16], sh_l[C::WARPS][16];
   uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   uint8_t *sq = ring + C::STAGES * C::UNIT;
-  float *sr = reinterpret_cast<float *>(sq + 16 * D * 2);
+  float *sr = reinterpret_cast<float *>(sq + 2 * C::Q_BYTES);
   const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
   const int G = p.hq / p.hkv;
   volatile int *dead = &sh_dead;
   if (tid == 0) {
+    prefetch_map(&qmap);
+    prefetch_map(&kmap);
+    prefetch_map(&vmap);
     for (int i = 0; i < C::STAGES; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], C::WARPS);
+    for (int i = 0; i < 2; ++i) mbar_init(&q_full[i], 1), mbar_init(&q_empty[i], C::WARPS);
     mbar_fence_init();
     sh_dead = 0;
-    sh_total = 0;
   }
-  if (tid == 0) prefetch_map(&kmap), prefetch_map(&vmap);
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
-  __syncthreads();
-
-  // The run of this CTA: tiles [x0, x1) of all, and the sequence that x0 lies in.
-  long long mine = 0;
-  for (int n = tid; n < p.num_seqs; n += C::THREADS) mine += tiles_of(seq_len(p, n));
+  // The run of this CTA: tiles [x0, x1) of all, and the sequence that x0 lies in.  A scan of
+  // the sequences' tiles gives the total; with more sequences than threads a second one finds
+  // the place.
+  auto scan = [&](int n, int &tiles, long long &sum) {  // tiles before sequence n in the chunk, their sum
+    tiles = n < p.num_seqs ? tiles_of(seq_len(p, n)) : 0;
+    int s = tiles;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-  if (lane == 0) atomicAdd(reinterpret_cast<unsigned long long *>(&sh_total), (unsigned long long)mine);
-  __syncthreads();
-  const long long total = sh_total * p.hkv;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, s, o);
+      if (lane >= o) s += v;
+    }
+    __syncthreads();
+    if (lane == 31) sh_scan[warp] = s;
+    __syncthreads();
+    long long at = s - tiles;
+    sum = 0;
+#pragma unroll
+    for (int i = 0; i <= C::WARPS; ++i) {
+      at += i < warp ? sh_scan[i] : 0;
+      sum += sh_scan[i];
+    }
+    return at;
+  };
+  long long all = 0, sum, at;
+  int tiles;
+  for (int n0 = 0; n0 < p.num_seqs; n0 += C::THREADS) {
+    at = scan(n0 + tid, tiles, sum);
+    all += sum;
+  }
+  const long long total = all * p.hkv;
   const long long ctas = min((long long)gridDim.x, total);
   if (blockIdx.x >= ctas) return;
   const long long x0 = total * blockIdx.x / ctas, x1 = total * (blockIdx.x + 1) / ctas;
-  {
-    long long before = 0;  // tiles of one kv-head before the chunk of sequences
-    for (int n0 = 0; n0 < p.num_seqs; n0 += C::THREADS) {
-      const int n = n0 + tid;
-      const int t = n < p.num_seqs ? tiles_of(seq_len(p, n)) : 0;
-      int s = t;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, s, o);
-        if (lane >= o) s += v;
-      }
-      if (lane == 31) sh_scan[warp] = s;
-      __syncthreads();
-      long long at = before;
-      for (int i = 0; i < warp; ++i) at += sh_scan[i];
-      at += s - t;
-      if (t > 0 && at * p.hkv <= x0 && x0 < (at + t) * p.hkv) sh_n = n, sh_base = at * p.hkv;
-      for (int i = 0; i <= C::WARPS; ++i) before += sh_scan[i];
-      __syncthreads();
-      if (before * p.hkv > x0) break;
-    }
+  for (long long n0 = 0, before = 0; n0 < p.num_seqs && before * p.hkv <= x0; n0 += C::THREADS, before += sum) {
+    if (p.num_seqs > C::THREADS) at = scan((int)n0 + tid, tiles, sum);
+    const long long first = (before + at) * p.hkv;
+    if (tiles > 0 && first <= x0 && x0 < first + (long long)tiles * p.hkv) sh_n = (int)n0 + tid, sh_base = first;
   }
-  int n = sh_n;
-  long long base = sh_base;  // first tile of sequence n
+  __syncthreads();
+  // This CTA's pairs in order: sequence, head, first and last + 1 key tile.
+  struct Walk {
+    int n, h, len, tiles, j0, j1, ahead;
+    long long x;
+  };
+  auto start = [&]() {
+    Walk k;
+    k.n = sh_n;
+    k.x = x0;
+    k.len = seq_len(p, k.n);
+    k.tiles = tiles_of(k.len);
+    const long long rem = x0 - sh_base;
+    k.h = (int)(rem / k.tiles);
+    k.j0 = (int)(rem % k.tiles);
+    k.j1 = (int)min((long long)k.tiles, k.j0 + (x1 - x0));
+    k.ahead = k.n + 1 < p.num_seqs ? seq_len(p, k.n + 1) : 0;  // the next length is at hand when needed
+    return k;
+  };
+  auto step = [&](Walk &k) {
+    k.x += k.j1 - k.j0;
+    if (k.x >= x1) return;
+    if (++k.h == p.hkv) {
+      k.h = 0;
+      ++k.n;
+      k.len = k.ahead;
+      k.tiles = tiles_of(k.len);
+      k.ahead = k.n + 1 < p.num_seqs ? seq_len(p, k.n + 1) : 0;
+    }
+    k.j0 = 0;
+    k.j1 = (int)min((long long)k.tiles, x1 - k.x);
+  };
   const float asl = p.scale == 0.f ? 1.f : fabsf(p.scale) * 1.4426950408889634f;
   const float flip = p.scale == 0.f ? 0.f : p.scale < 0.f ? -1.f : 1.f;
-  uint32_t ld = 0;
+  uint32_t ld = 0, pairs = 0, turn = 0;  // tiles and pairs so far
 
   if (warp == C::WARPS) {
     // ---------------------------------------------------------------- loads
-    const int box = min(p.page_size, kTile), boxes = kTile / box;
+    const int box = min(p.page_size, kTile), boxes = kTile / box, lps = 31 - __clz(p.page_size);
     const int pi = lane / C::CH, ch = lane % C::CH;
-    for (long long x = x0; x < x1;) {
-      const int len = seq_len(p, n), tiles = tiles_of(len);
-      const long long rem = x - base;
-      const int h = (int)(rem / tiles), j0 = (int)(rem % tiles);
-      const int j1 = (int)min((long long)tiles, j0 + (x1 - x));
-      const int32_t *table = p.page_table + (long long)n * p.max_pages;
+    for (Walk k = start(); k.x < x1; step(k)) {
+      if (k.len == 0) continue;
+      const int32_t *table = p.page_table + (long long)k.n * p.max_pages;
       auto page_of = [&](int j) {
         const int key = j * kTile + pi * box;
-        if (pi >= boxes || j >= j1 || key >= len) return -1;
-        const int pg = table[key / p.page_size];
-        return (unsigned)pg < (unsigned)p.num_pages ? pg : p.num_pages;  // out of range: zeros
+        return pi < boxes && j < k.j1 && key < k.len ? table[key >> lps] : -1;
       };
-      if (len > 0) {
-        int next = page_of(j0);
-        for (int j = j0; j < j1; ++j) {
-          const int pg = next;
-          next = page_of(j + 1);
-          const int count = __popc(__ballot_sync(0xffffffffu, pg >= 0));
+      int next = page_of(k.j0);
+      const uint32_t qb = pairs & 1;
+      wait_bar(&q_empty[qb], ((pairs >> 1) & 1) ^ 1, dead, w.err);
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&q_full[qb], (uint32_t)G * D * 2);
+        for (int c = 0; c < C::CH; ++c)
+          tma_load_3d(sq + qb * C::Q_BYTES + c * 2048, &qmap, c * 64, k.h * G, k.n, &q_full[qb]);
+      }
+      __syncwarp();
+      ++pairs;
+      for (int j = k.j0; j < k.j1; ++j) {
+        const int key = j * kTile + pi * box;
+        const bool on = pi < boxes && key < k.len;
+        // (a page out of range reads as zeros)
+        const int pg = (unsigned)next < (unsigned)p.num_pages ? next : p.num_pages;
+        next = page_of(j + 1);
+        const int count = __popc(__ballot_sync(0xffffffffu, on));
 #pragma unroll
-          for (int kv = 0; kv < 2; ++kv, ++ld) {
-            const uint32_t st = ld % C::STAGES;
-            wait_bar(&empty[st], ((ld / C::STAGES) & 1) ^ 1, dead, w.err);
-            if (lane == 0) mbar_arrive_expect_tx(&full[st], (uint32_t)count * box * 128);
-            __syncwarp();
-            if (pg >= 0)
-              tma_4d(ring + st * C::UNIT + ch * (kTile * 128) + pi * box * 128, kv ? &vmap : &kmap, ch * 64,
-                     (j * kTile + pi * box) % p.page_size, h, pg, &full[st]);
-          }
+        for (int kv = 0; kv < 2; ++kv, ++ld) {
+          const uint32_t st = ld % C::STAGES;
+          wait_bar(&empty[st], ((ld / C::STAGES) & 1) ^ 1, dead, w.err);
+          if (lane == 0) mbar_arrive_expect_tx(&full[st], (uint32_t)count * box * 128);
+          __syncwarp();
+          if (on)
+            tma_4d(ring + st * C::UNIT + ch * (kTile * 128) + pi * box * 128, kv ? &vmap : &kmap, ch * 64,
+                   key & (p.page_size - 1), k.h, pg, &full[st]);
         }
       }
-      x += j1 - j0;
-      if (j1 == tiles && h == p.hkv - 1) base += (long long)tiles * p.hkv, ++n;
     }
     if (*dead) __nanosleep(1000000);  // copies in flight land before shared memory is given up
     return;
@@ -168,26 +207,17 @@ __global__ void __launch_bounds__(StepCfg<D>::THREADS, D == 128 ? 2 : 1)
   const int gid = lane >> 2, tig = lane & 3;
   const int kr = kg * 16;                                       // this warp's keys in a tile
   const int nthr = 32 * C::WARPS;
-  for (long long x = x0; x < x1;) {
-    const int len = seq_len(p, n), tiles = tiles_of(len);
-    const long long rem = x - base;
-    const int h = (int)(rem / tiles), j0 = (int)(rem % tiles);
-    const int j1 = (int)min((long long)tiles, j0 + (x1 - x));
-    const long long pair0 = base + (long long)h * tiles;  // first tile of the pair
-    // the pair's query rows, zero past G, in the layout that ldmatrix reads (the last pair's
-    // rows were done with before its join)
-    for (int i = tid; i < 16 * (D / 8); i += nthr) {
-      const int r = i / (D / 8), c = (i % (D / 8)) * 8;
-      uint4 u = make_uint4(0, 0, 0, 0);
-      if (r < G)
-        u = *reinterpret_cast<const uint4 *>((const __nv_bfloat16 *)p.q + n * p.qs[0] + (h * G + r) * p.qs[1] + c);
-      *reinterpret_cast<uint4 *>(sq + (c >> 6) * 2048 + r * 128 + ((((c >> 3) & 7) ^ (r & 7)) << 4)) = u;
-    }
-    bar_sync(1, nthr);
+  for (Walk k = start(); k.x < x1; step(k)) {
+    const int n = k.n, h = k.h, len = k.len, j0 = k.j0, j1 = k.j1;
+    const long long pair0 = k.x - j0;  // first tile of the pair
+    // the pair's G query rows; what lies in the rows after them reaches no result
+    const uint32_t qb = pairs & 1;
+    const uint8_t *qs = sq + qb * C::Q_BYTES;
+    if (len > 0) wait_bar(&q_full[qb], (pairs >> 1) & 1, dead, w.err);
     const int qrow = (lane & 7) + ((lane >> 3) & 1) * 8;
     auto q_frag = [&](uint32_t (&a)[4], int k) {
       const int c = k * 16 + (lane >> 4) * 8;
-      ldsm_x4(a, sq + (c >> 6) * 2048 + qrow * 128 + ((((c >> 3) & 7) ^ (qrow & 7)) << 4));
+      ldsm_x4(a, qs + (c >> 6) * 2048 + qrow * 128 + ((((c >> 3) & 7) ^ (qrow & 7)) << 4));
     };
     uint32_t qa[D == 128 ? 8 : 1][4];
     if (D == 128)
@@ -234,7 +264,7 @@ __global__ void __launch_bounds__(StepCfg<D>::THREADS, D == 128 ? 2 : 1)
         top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 2)) * asl;
       }
       // the reference moves when it would rise by more than 8 (2^8 is far from overflow)
-      if (__any_sync(0xffffffffu, top[0] > m[0] + 8.f || top[1] > m[1] + 8.f)) {
+      if (__any_sync(0xffffffffu, (gid < G && top[0] > m[0] + 8.f) || (gid + 8 < G && top[1] > m[1] + 8.f))) {
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
           const float m1 = fmaxf(m[r], top[r]);
@@ -284,7 +314,17 @@ __global__ void __launch_bounds__(StepCfg<D>::THREADS, D == 128 ? 2 : 1)
       ++ld;
     }
 
-    // join the warps: one maximum per row, then O in a tree over the four key groups
+    if (len > 0) {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&q_empty[qb]);
+      ++pairs;
+    }
+
+    // Join the warps: one maximum per row, then each half of the key groups sums O in a buffer.
+    // (The maxima are in two places by turns: a warp may be here while another still reads the
+    // last pair's; everything else is written after the first barrier.)
+    float (*sh_m)[16] = sh_ms[turn];
+    turn ^= 1;
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
@@ -292,45 +332,32 @@ __global__ void __launch_bounds__(StepCfg<D>::THREADS, D == 128 ? 2 : 1)
       if (tig == 0) sh_m[warp][gid + 8 * r] = m[r];
     }
     bar_sync(1, nthr);
-    float top[2];
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       const int row = gid + 8 * r;
-      top[r] = fmaxf(fmaxf(sh_m[hf * 4][row], sh_m[hf * 4 + 1][row]),
-                     fmaxf(sh_m[hf * 4 + 2][row], sh_m[hf * 4 + 3][row]));
-      const float a = top[r] == -CUDART_INF_F ? 0.f : ex2(m[r] - top[r]);
+      const float top = fmaxf(fmaxf(sh_m[hf * 4][row], sh_m[hf * 4 + 1][row]),
+                              fmaxf(sh_m[hf * 4 + 2][row], sh_m[hf * 4 + 3][row]));
+      const float a = top == -CUDART_INF_F ? 0.f : ex2(m[r] - top);
       if (tig == 0) sh_l[warp][row] = l[r] * a;
 #pragma unroll
       for (int t = 0; t < 16; ++t) o[t][2 * r] *= a, o[t][2 * r + 1] *= a;
     }
-    auto put = [&](float *buf) {
-#pragma unroll
-      for (int r = 0; r < 2; ++r)
-        if (gid + 8 * r < G)
-#pragma unroll
-          for (int t = 0; t < 16; ++t)
-            *reinterpret_cast<float2 *>(buf + (gid + 8 * r) * C::RP + 8 * t + 2 * tig) =
-                make_float2(o[t][2 * r], o[t][2 * r + 1]);
-    };
-    auto add = [&](const float *buf) {
+    float *buf = sr + (hf * 2 + (kg & 1)) * 16 * C::RP;
+    auto put = [&](bool add) {
 #pragma unroll
       for (int r = 0; r < 2; ++r)
         if (gid + 8 * r < G)
 #pragma unroll
           for (int t = 0; t < 16; ++t) {
-            const float2 v = *reinterpret_cast<const float2 *>(buf + (gid + 8 * r) * C::RP + 8 * t + 2 * tig);
-            o[t][2 * r] += v.x;
-            o[t][2 * r + 1] += v.y;
+            float2 *at = reinterpret_cast<float2 *>(buf + (gid + 8 * r) * C::RP + 8 * t + 2 * tig);
+            float2 v = make_float2(o[t][2 * r], o[t][2 * r + 1]);
+            if (add) v.x += at->x, v.y += at->y;
+            *at = v;
           }
     };
-    float *r0 = sr + hf * 2 * 16 * C::RP, *r1 = r0 + 16 * C::RP;
-    if (kg >= 2) put(kg == 2 ? r0 : r1);
+    if (kg >= 2) put(false);
     bar_sync(1, nthr);
-    if (kg < 2) add(kg == 0 ? r0 : r1);
-    bar_sync(1, nthr);
-    if (kg == 1) put(r1);
-    bar_sync(1, nthr);
-    if (kg == 0) add(r1), put(r0);
+    if (kg < 2) put(true);
     bar_sync(1, nthr);
 
     // a row of the pair to its place: final, or left for a join
@@ -346,16 +373,18 @@ __global__ void __launch_bounds__(StepCfg<D>::THREADS, D == 128 ? 2 : 1)
       }
       emit_row<D>(p, n, h * G + r, lane, mm, ll, v);
     };
-    const bool whole = j0 == 0 && j1 == tiles;
+    const bool whole = j0 == 0 && j1 == k.tiles;
     const long long slot = 2ll * blockIdx.x + (j0 == 0);
     for (int r = warp; r < G; r += C::WARPS) {
       const float mm = fmaxf(fmaxf(sh_m[0][r], sh_m[1][r]), fmaxf(sh_m[2][r], sh_m[3][r]));
       const float ll = (sh_l[0][r] + sh_l[1][r]) + (sh_l[2][r] + sh_l[3][r]);
       float v[D / 32];
 #pragma unroll
-      for (int k = 0; k < D / 128; ++k) {
-        const float4 u = *reinterpret_cast<const float4 *>(sr + k * 2 * 16 * C::RP + r * C::RP + 4 * lane);
-        v[4 * k] = u.x, v[4 * k + 1] = u.y, v[4 * k + 2] = u.z, v[4 * k + 3] = u.w;
+      for (int c = 0; c < D / 128; ++c) {
+        const float *at = sr + c * 2 * 16 * C::RP + r * C::RP + 4 * lane;
+        const float4 a = *reinterpret_cast<const float4 *>(at);
+        const float4 b = *reinterpret_cast<const float4 *>(at + 16 * C::RP);
+        v[4 * c] = a.x + b.x, v[4 * c + 1] = a.y + b.y, v[4 * c + 2] = a.z + b.z, v[4 * c + 3] = a.w + b.w;
       }
       if (whole) {
         emit(r, mm, ll, v);
@@ -369,7 +398,7 @@ __global__ void __launch_bounds__(StepCfg<D>::THREADS, D == 128 ? 2 : 1)
     }
     if (!whole) {
       // the runs that the pair lies in: c owns tile x iff total c / ctas <= x < total (c + 1) / ctas
-      const int c0 = (int)(((pair0 + 1) * ctas - 1) / total), c1 = (int)(((pair0 + tiles) * ctas - 1) / total);
+      const int c0 = (int)(((pair0 + 1) * ctas - 1) / total), c1 = (int)(((pair0 + k.tiles) * ctas - 1) / total);
       __threadfence();
       bar_sync(1, nthr);
       if (tid == 0) {
@@ -407,8 +436,6 @@ __global__ void __launch_bounds__(StepCfg<D>::THREADS, D == 128 ? 2 : 1)
         }
       }
     }
-    x += j1 - j0;
-    if (j1 == tiles && h == p.hkv - 1) base += (long long)tiles * p.hkv, ++n;
   }
 }
 
@@ -439,14 +466,15 @@ cudaError_t run(const AttnParams &p, char *ws, float *dense_ml, float *dense, un
   w.dense_ml = dense_ml;
   w.dense = dense;
   w.err = errw;
-  CUtensorMap k, v;
-  cudaError_t err = cache_maps(&k, &v, p, kTile);
+  CUtensorMap q, k, v;
+  cudaError_t err = q_map(&q, p, 1);
+  if (err == cudaSuccess) err = cache_maps(&k, &v, p, kTile);
   if (err != cudaSuccess) return err;
   const size_t smem = C::SMEM + 1024;
   static std::atomic<uint64_t> allowed{0};
   err = allow_smem(step_kernel<D>, smem, allowed);
   if (err != cudaSuccess) return err;
-  return launch_dependent(step_kernel<D>, C::CTAS, C::THREADS, smem, stream, 1, p, w, k, v);
+  return launch_dependent(step_kernel<D>, C::CTAS, C::THREADS, smem, stream, 1, p, w, q, k, v);
 }
 
 }  // namespace

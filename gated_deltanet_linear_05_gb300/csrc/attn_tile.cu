@@ -987,15 +987,6 @@ __global__ void __launch_bounds__(256) join_kernel(AttnParams p, TilePlan w, Til
 
 // ------------------------------------------------------------------ host
 
-// Tensor map of q for boxes of one sub-tile's rows: tpt tokens x G heads x 64 columns.
-cudaError_t q_map(CUtensorMap *map, const AttnParams &p) {
-  const int G = p.hq / p.hkv;
-  const cuuint64_t dims[3] = {(cuuint64_t)p.d, (cuuint64_t)p.hq, (cuuint64_t)p.tokens};
-  const cuuint64_t strides[2] = {(cuuint64_t)p.qs[1] * 2, (cuuint64_t)p.qs[0] * 2};
-  const cuuint32_t box[3] = {64, (cuuint32_t)G, (cuuint32_t)(128 / G)};
-  return bf16_map(map, p.q, 3, dims, strides, box);
-}
-
 // Tokens of a tile, tiles of a call at most, tiles of the shared prefix's pass.
 template <int D>
 struct Sizes {
@@ -1075,7 +1066,7 @@ cudaError_t run(const AttnParams &p, char *ws, unsigned int *errw, cudaStream_t 
   own.units = C::UNITS;
   own.slots = C::SLOTS;
   CUtensorMap q, k, v;
-  cudaError_t err = q_map(&q, p);
+  cudaError_t err = q_map(&q, p, z.tpt);
   if (err == cudaSuccess) err = cache_maps(&k, &v, p, C::KROWS);
   if (err != cudaSuccess) return err;
   const size_t smem = C::SMEM + 1024;
@@ -1138,6 +1129,13 @@ cudaError_t bf16_map(CUtensorMap *map, const void *x, int rank, const cuuint64_t
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
              ? cudaSuccess
              : cudaErrorInvalidValue;
+}
+
+cudaError_t q_map(CUtensorMap *map, const AttnParams &p, int tokens) {
+  const cuuint64_t dims[3] = {(cuuint64_t)p.d, (cuuint64_t)p.hq, (cuuint64_t)p.tokens};
+  const cuuint64_t strides[2] = {(cuuint64_t)p.qs[1] * 2, (cuuint64_t)p.qs[0] * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)(p.hq / p.hkv), (cuuint32_t)tokens};
+  return bf16_map(map, p.q, 3, dims, strides, box);
 }
 
 cudaError_t cache_maps(CUtensorMap *k, CUtensorMap *v, const AttnParams &p, int tile) {

@@ -98,6 +98,8 @@ __device__ __forceinline__ void emit_row(const AttnParams &p, int tok, int head,
 // Tensor map of a bf16 tensor with 128-byte swizzle (boxes of 64 columns).
 cudaError_t bf16_map(CUtensorMap *map, const void *x, int rank, const cuuint64_t *dims,
                      const cuuint64_t *strides, const cuuint32_t *box);
+// Map of q for boxes of `tokens` tokens x one kv-head's query heads x 64 columns.
+cudaError_t q_map(CUtensorMap *map, const AttnParams &p, int tokens);
 // Maps of K and V, [page][head][row][column], for boxes of min(page_size, tile) rows; zero
 // (and never used) for a cache without pages.
 cudaError_t cache_maps(CUtensorMap *k, CUtensorMap *v, const AttnParams &p, int tile);
