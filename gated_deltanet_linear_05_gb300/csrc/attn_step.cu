@@ -43,7 +43,7 @@ struct StepCfg {
 struct StepPlan {
   unsigned int *arrived;  // [CTAS] parts finished of the pair that begins in that CTA's run
   float *ml, *part;       // [2 CTAS][16] {m, l}, [2 CTAS][16][D]
-  float *dense_ml, *dense;  // rows' results left for a join (shared prefix), or NULL
+  PrefixParts pre;        // of a shared prefix
   unsigned int *err;
 };
 
@@ -360,17 +360,9 @@ __global__ void __launch_bounds__(StepCfg<D>::THREADS, D == 128 ? 2 : 1)
     if (kg < 2) put(true);
     bar_sync(1, nthr);
 
-    // a row of the pair to its place: final, or left for a join
-    auto emit = [&](int r, float mm, float ll, const float (&v)[D / 32]) {
-      const long long row = (long long)n * p.hq + h * G + r;
-      if (w.dense) {
-        if (lane == 0) *reinterpret_cast<float2 *>(w.dense_ml + 2 * row) = make_float2(mm, ll);
-#pragma unroll
-        for (int k = 0; k < D / 128; ++k)
-          *reinterpret_cast<float4 *>(w.dense + row * D + 128 * k + 4 * lane) =
-              make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
-        return;
-      }
+    // a finished row of the pair, with the shared prefix's parts
+    auto emit = [&](int r, float mm, float ll, float (&v)[D / 32]) {
+      add_prefix<D>(mm, ll, v, w.pre, n, h, r, G, p.hkv, lane);
       emit_row<D>(p, n, h * G + r, lane, mm, ll, v);
     };
     const bool whole = j0 == 0 && j1 == k.tiles;
@@ -409,29 +401,10 @@ __global__ void __launch_bounds__(StepCfg<D>::THREADS, D == 128 ? 2 : 1)
       if (sh_last) {
         __threadfence();
         for (int r = warp; r < G; r += C::WARPS) {
-          // parts c0 (which began the pair, slot 2 c0 + 1) to c1 (slots 2 c)
-          auto at = [&](int c) { return (2ll * c + (c == c0)) * 16 + r; };
-          float mm = -CUDART_INF_F;
-          for (int c = c0 + lane; c <= c1; c += 32) mm = fmaxf(mm, __ldcg(w.ml + 2 * at(c)));
-#pragma unroll
-          for (int k = 16; k > 0; k >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, k));
-          float ll = 0.f, v[D / 32] = {};
-          if (mm > -CUDART_INF_F) {
-#pragma unroll 4
-            for (int c = c0; c <= c1; ++c) {
-              const float2 q = __ldcg(reinterpret_cast<const float2 *>(w.ml + 2 * at(c)));
-              const float a = ex2(q.x - mm);
-              ll = fmaf(q.y, a, ll);
-#pragma unroll
-              for (int k = 0; k < D / 128; ++k) {
-                const float4 u = __ldcg(reinterpret_cast<const float4 *>(w.part + at(c) * D + 128 * k + 4 * lane));
-                v[4 * k] = fmaf(u.x, a, v[4 * k]);
-                v[4 * k + 1] = fmaf(u.y, a, v[4 * k + 1]);
-                v[4 * k + 2] = fmaf(u.z, a, v[4 * k + 2]);
-                v[4 * k + 3] = fmaf(u.w, a, v[4 * k + 3]);
-              }
-            }
-          }
+          // the run that began the pair has slot 2 c0 + 1, the others 2 c
+          float mm = -CUDART_INF_F, ll = 0.f, v[D / 32] = {};
+          add_parts<D>(mm, ll, v, w.ml, w.part, (2ll * c0 + 1) * 16 + r, 0, 1, lane);
+          add_parts<D>(mm, ll, v, w.ml, w.part, (2ll * c0 + 2) * 16 + r, 32, c1 - c0, lane);
           emit(r, mm, ll, v);
         }
       }
@@ -457,14 +430,12 @@ size_t layout(StepPlan *out, char *ws) {
 }
 
 template <int D>
-cudaError_t run(const AttnParams &p, char *ws, float *dense_ml, float *dense, unsigned int *errw,
-                cudaStream_t stream) {
+cudaError_t run(const AttnParams &p, char *ws, const PrefixParts &pre, unsigned int *errw, cudaStream_t stream) {
   using C = StepCfg<D>;
   static_assert(C::CTAS * sizeof(unsigned int) <= kArrivedBytes, "counters");
   StepPlan w;
   layout<D>(&w, ws);
-  w.dense_ml = dense_ml;
-  w.dense = dense;
+  w.pre = pre;
   w.err = errw;
   CUtensorMap q, k, v;
   cudaError_t err = q_map(&q, p, 1);
@@ -481,10 +452,10 @@ cudaError_t run(const AttnParams &p, char *ws, float *dense_ml, float *dense, un
 
 size_t attn_step_workspace(int d) { return d == 128 ? layout<128>(nullptr, nullptr) : layout<256>(nullptr, nullptr); }
 
-cudaError_t launch_attn_step(const AttnParams &p, void *ws, float *dense_ml, float *dense, unsigned int *err,
+cudaError_t launch_attn_step(const AttnParams &p, void *ws, const PrefixParts &pre, unsigned int *err,
                              cudaStream_t stream) {
-  return p.d == 128 ? run<128>(p, static_cast<char *>(ws), dense_ml, dense, err, stream)
-                    : run<256>(p, static_cast<char *>(ws), dense_ml, dense, err, stream);
+  return p.d == 128 ? run<128>(p, static_cast<char *>(ws), pre, err, stream)
+                    : run<256>(p, static_cast<char *>(ws), pre, err, stream);
 }
 
 }  // namespace gdn

@@ -35,7 +35,6 @@ namespace {
 
 constexpr int kBN = 128;        // keys per tile
 constexpr int kAhead = 2;       // 32-column chunks of the gate fetched ahead in the epilogue
-constexpr int kTileRows = 256;  // rows per tile: two sub-tiles
 
 template <int D_>
 struct Cfg {
@@ -268,7 +267,6 @@ struct TilePlan {
   Split *split;   // tiles to join
   float *ml;      // [slot][row] {m, l}
   float *part;    // [slot][row][D]
-  float *dense_ml, *dense;  // one result per row of the call instead (attn_step.cu), or NULL
   int max_tiles, max_entries, units, slots, all_slots;
   int uniform_parts, uniform_kt;  // > 0: no plan, equal parts of equal tiles (shared prefix)
   unsigned int *err;
@@ -927,60 +925,24 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
 
 // ------------------------------------------------------------------ join
 
-// One warp per row: the row's partial results (m_i, l_i, O_i) to
-//     M = max m_i,  o = sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i.
-// Rows: those of the split tiles in the plan's table, or with own results in `dense` (one
-// per row) all rows of the call; for each also the shared prefix's parts.
+// One warp per row of the split tiles in the plan's table: its parts, and the shared prefix's.
 template <int D>
-__global__ void __launch_bounds__(256) join_kernel(AttnParams p, TilePlan w, TilePlan pre, int tpt) {
-  constexpr int E = D / 32;
+__global__ void __launch_bounds__(256) join_kernel(AttnParams p, TilePlan w, PrefixParts pre, int tpt) {
   const int lane = threadIdx.x & 31;
-  const int G = p.hq / p.hkv, tt = tpt * 2;
+  const int G = p.hq / p.hkv, per_head = 2 * tpt * G;
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
-  const long long rows = w.dense ? (long long)p.tokens * p.hq : (long long)w.head[1] * p.hkv * (tt * G);
+  const long long rows = (long long)w.head[1] * p.hkv * per_head;
   const long long step = (long long)gridDim.x * 8;
   for (long long i = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); i < rows; i += step) {
-    int tok, h, g, dt = 0;
-    Split s{};
-    if (w.dense) {
-      tok = (int)(i / p.hq);
-      h = (int)(i % p.hq) / G;
-      g = (int)(i % p.hq) % G;
-    } else {
-      const int r = (int)(i % (tt * G));
-      h = (int)(i / (tt * G) % p.hkv);
-      s = w.split[i / (tt * G) / p.hkv];
-      dt = r / G;
-      g = r % G;
-      if (dt >= s.ntok) continue;
-      tok = s.tok0 + dt;
-    }
-    float acc[E] = {}, m = -CUDART_INF_F, l = 0.f;
-    auto take = [&](const float *ml_of, const float *part_of, long long at) {
-      const float2 ml = *reinterpret_cast<const float2 *>(ml_of + 2 * at);
-      if (!(ml.y > 0.f)) return;
-      const float m1 = fmaxf(m, ml.x), a = ex2(m - m1), b = ex2(ml.x - m1);
-      m = m1;
-      l = l * a + ml.y * b;
-      const float *o = part_of + at * D + lane * 4;
-#pragma unroll
-      for (int k = 0; k < E / 4; ++k) {
-        const float4 v = *reinterpret_cast<const float4 *>(o + 128 * k);
-        acc[4 * k] = acc[4 * k] * a + v.x * b;
-        acc[4 * k + 1] = acc[4 * k + 1] * a + v.y * b;
-        acc[4 * k + 2] = acc[4 * k + 2] * a + v.z * b;
-        acc[4 * k + 3] = acc[4 * k + 3] * a + v.w * b;
-      }
-    };
-    auto take_parts = [&](const TilePlan &src, int slot, int parts, int off) {
-      const int srow = off / tpt * 128 + (off % tpt) * G + g;
-      for (int q = 0; q < parts; ++q)
-        take(src.ml, src.part, (long long)(slot + q * p.hkv + h) * kTileRows + srow);
-    };
-    if (pre.uniform_parts > 0) take_parts(pre, tok / tt * pre.uniform_parts * p.hkv, pre.uniform_parts, tok % tt);
-    if (w.dense) take(w.dense_ml, w.dense, i);
-    else take_parts(w, s.slot, s.parts, dt);
+    const int r = (int)(i % per_head), h = (int)(i / per_head % p.hkv);
+    const Split s = w.split[i / per_head / p.hkv];
+    const int dt = r / G, g = r % G, tok = s.tok0 + dt;
+    if (dt >= s.ntok) continue;
+    float acc[D / 32] = {}, m = -CUDART_INF_F, l = 0.f;
+    add_prefix<D>(m, l, acc, pre, tok, h, g, G, p.hkv, lane);
+    add_parts<D>(m, l, acc, w.ml, w.part, (long long)(s.slot + h) * kTileRows + dt / tpt * 128 + dt % tpt * G + g,
+                 (long long)p.hkv * kTileRows, s.parts, lane);
     emit_row<D>(p, tok, h * G + g, lane, m, l, acc);
   }
 }
@@ -1011,8 +973,7 @@ int prefix_parts(int tiles, int hkv, int prefix_len) {
 }
 
 template <int D>
-size_t layout(TilePlan *own, TilePlan *pre, char *ws, int num_seqs, int tokens, int hq, int hkv, int prefix_len,
-              bool dense) {
+size_t layout(TilePlan *own, TilePlan *pre, char *ws, int num_seqs, int tokens, int hq, int hkv, int prefix_len) {
   const Sizes<D> z(tokens, num_seqs, hq, hkv);
   size_t at = 0;
   auto take = [&](size_t bytes) {
@@ -1025,11 +986,6 @@ size_t layout(TilePlan *own, TilePlan *pre, char *ws, int num_seqs, int tokens, 
   const size_t own_slots = prefix_len > 0 ? (size_t)z.max_tiles * hkv + split_slots : split_slots;
   const size_t slot = (size_t)kTileRows * sizeof(float);
   TilePlan a{}, b{};
-  if (dense) {
-    const size_t rows = (size_t)tokens * hq;
-    a.dense_ml = (float *)take(rows * 2 * sizeof(float));
-    a.dense = (float *)take(rows * D * sizeof(float));
-  }
   a.head = (int *)take(256);
   a.base = (int *)take(sizeof(int) * (size_t)(num_seqs + 1));
   a.rec = (Entry *)take(sizeof(Entry) * (size_t)z.max_tiles);
@@ -1059,9 +1015,9 @@ cudaError_t run(const AttnParams &p, char *ws, unsigned int *errw, cudaStream_t 
   char *tile_ws = ws + attn_step_workspace(D);
   using C = Cfg<D>;
   const Sizes<D> z(p.tokens, p.num_seqs, p.hq, p.hkv);
-  if (step && p.prefix_len == 0) return launch_attn_step(p, ws, nullptr, nullptr, errw, stream);
+  if (step && p.prefix_len == 0) return launch_attn_step(p, ws, PrefixParts{}, errw, stream);
   TilePlan own, pre;
-  layout<D>(&own, &pre, tile_ws, p.num_seqs, p.tokens, p.hq, p.hkv, p.prefix_len, step && p.prefix_len > 0);
+  layout<D>(&own, &pre, tile_ws, p.num_seqs, p.tokens, p.hq, p.hkv, p.prefix_len);
   own.err = pre.err = errw;
   own.units = C::UNITS;
   own.slots = C::SLOTS;
@@ -1077,27 +1033,21 @@ cudaError_t run(const AttnParams &p, char *ws, unsigned int *errw, cudaStream_t 
     err = launch_dependent(tile_kernel<D>, kSms, C::THREADS, smem, stream, C::GRP, p, pre, q, k, v);
     if (err != cudaSuccess) return err;
   }
-  if (step) {
-    err = launch_attn_step(p, ws, own.dense_ml, own.dense, errw, stream);
-  } else {
-    err = launch_dependent(plan_kernel, 1, kPlanThreads, 0, stream, 1, p, own, z.tt);
-    if (err != cudaSuccess) return err;
+  const PrefixParts parts{pre.ml, pre.part, pre.uniform_parts, z.tpt};
+  if (step) return launch_attn_step(p, ws, parts, errw, stream);
+  err = launch_dependent(plan_kernel, 1, kPlanThreads, 0, stream, 1, p, own, z.tt);
+  if (err == cudaSuccess)
     err = launch_dependent(tile_kernel<D>, kSms, C::THREADS, smem, stream, C::GRP, p, own, q, k, v);
-  }
   if (err != cudaSuccess) return err;
-  return launch_dependent(join_kernel<D>, 4 * kSms, 256, 0, stream, 1, p, own, pre, z.tpt);
+  return launch_dependent(join_kernel<D>, 4 * kSms, 256, 0, stream, 1, p, own, parts, z.tpt);
 }
 
 }  // namespace
 
 size_t attn_workspace(int num_seqs, int tokens, int hq, int hkv, int d, int prefix_len) {
-  // the decode kernel's part first (its counters stay in one place), then the larger of the
-  // layouts with and without cu_seqlens
-  const bool dense = prefix_len > 0;
-  return d == 128 ? attn_step_workspace(128) +
-                        layout<128>(nullptr, nullptr, nullptr, num_seqs, tokens, hq, hkv, prefix_len, dense)
-                  : attn_step_workspace(256) +
-                        layout<256>(nullptr, nullptr, nullptr, num_seqs, tokens, hq, hkv, prefix_len, dense);
+  // the decode kernel's part first: its counters stay in one place for all shapes
+  return attn_step_workspace(d) + (d == 128 ? layout<128>(nullptr, nullptr, nullptr, num_seqs, tokens, hq, hkv, prefix_len)
+                                            : layout<256>(nullptr, nullptr, nullptr, num_seqs, tokens, hq, hkv, prefix_len));
 }
 
 cudaError_t launch_attention(const AttnParams &p, void *ws, unsigned int *err, cudaStream_t stream) {

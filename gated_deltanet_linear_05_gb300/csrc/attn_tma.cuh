@@ -95,6 +95,61 @@ __device__ __forceinline__ void emit_row(const AttnParams &p, int tok, int head,
   if (p.lse && lane == 0) p.lse[row] = l > 0.f ? (m + log2f(l)) * kLn2 : -CUDART_INF_F;
 }
 
+// Partial results of a shared prefix, left by the tile kernel for every row of the call: tile t of
+// 2 tpt tokens has `parts` parts, part q of kv-head h in slot (t parts + q) Hkv + h, a slot 256
+// rows of {m, l} and D sums, row (token / tpt) 128 + (token % tpt) G + g of the tile's tokens.
+struct PrefixParts {
+  const float *ml, *part;
+  int parts, tpt;
+};
+constexpr int kTileRows = 256;
+
+// Adds `count` parts of a row, at `at`, `at` + pitch, ..., to (m, l, acc) by one warp:
+//     M = max(m, max m_q),  l = sum 2^(m_q - M) l_q,  acc = sum 2^(m_q - M) O_q.
+// The statistics first, a part a lane, so that the sums' loads do not wait for one another.
+template <int D>
+__device__ __forceinline__ void add_parts(float &m, float &l, float (&acc)[D / 32], const float *ml_of,
+                                          const float *part_of, long long at, long long pitch, int count, int lane) {
+  for (int q0 = 0; q0 < count; q0 += 32) {
+    float2 ml = make_float2(-CUDART_INF_F, 0.f);
+    if (q0 + lane < count) ml = __ldcg(reinterpret_cast<const float2 *>(ml_of + 2 * (at + (q0 + lane) * pitch)));
+    if (!(ml.y > 0.f)) ml = make_float2(-CUDART_INF_F, 0.f);
+    float top = ml.x;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (top == -CUDART_INF_F) continue;
+    const float m1 = fmaxf(m, top), a = ex2(m - m1), weight = ex2(ml.x - m1);
+    m = m1;
+    l = l * a + warp_sum(ml.y * weight);
+#pragma unroll
+    for (int k = 0; k < D / 32; ++k) acc[k] *= a;
+    const int some = min(32, count - q0);
+#pragma unroll 4
+    for (int q = 0; q < some; ++q) {  // (a part without keys holds zeros: its weight is 0)
+      const float b = __shfl_sync(0xffffffffu, weight, q);
+      const float *o = part_of + (at + (q0 + q) * pitch) * D + lane * 4;
+#pragma unroll
+      for (int k = 0; k < D / 128; ++k) {
+        const float4 v = __ldcg(reinterpret_cast<const float4 *>(o + 128 * k));
+        acc[4 * k] = fmaf(v.x, b, acc[4 * k]);
+        acc[4 * k + 1] = fmaf(v.y, b, acc[4 * k + 1]);
+        acc[4 * k + 2] = fmaf(v.z, b, acc[4 * k + 2]);
+        acc[4 * k + 3] = fmaf(v.w, b, acc[4 * k + 3]);
+      }
+    }
+  }
+}
+// The prefix's parts of (token, head h G + g).
+template <int D>
+__device__ __forceinline__ void add_prefix(float &m, float &l, float (&acc)[D / 32], const PrefixParts &pre,
+                                           int tok, int h, int g, int G, int hkv, int lane) {
+  if (pre.parts == 0) return;
+  const int tt = 2 * pre.tpt, off = tok % tt;
+  const long long at = ((long long)(tok / tt) * pre.parts * hkv + h) * kTileRows + off / pre.tpt * 128 +
+                       (off % pre.tpt) * G + g;
+  add_parts<D>(m, l, acc, pre.ml, pre.part, at, (long long)hkv * kTileRows, pre.parts, lane);
+}
+
 // Tensor map of a bf16 tensor with 128-byte swizzle (boxes of 64 columns).
 cudaError_t bf16_map(CUtensorMap *map, const void *x, int rank, const cuuint64_t *dims,
                      const cuuint64_t *strides, const cuuint32_t *box);
