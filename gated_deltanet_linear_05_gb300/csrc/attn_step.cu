@@ -43,7 +43,8 @@ struct StepCfg {
 struct StepPlan {
   unsigned int *arrived;  // [CTAS] parts finished of the pair that begins in that CTA's run
   float *ml, *part;       // [2 CTAS][16] {m, l}, [2 CTAS][16][D]
-  PrefixParts pre;        // of a shared prefix
+  PrefixParts pre;        // of a shared prefix, joined here
+  DenseRows dense;        // the results are left there instead of finished
   unsigned int *err;
 };
 
@@ -360,8 +361,17 @@ __global__ void __launch_bounds__(StepCfg<D>::THREADS, D == 128 ? 2 : 1)
     if (kg < 2) put(true);
     bar_sync(1, nthr);
 
-    // a finished row of the pair, with the shared prefix's parts
+    // a row of the pair: left for a join, or finished with the shared prefix's parts
     auto emit = [&](int r, float mm, float ll, float (&v)[D / 32]) {
+      if (w.dense.part) {
+        const long long row = (long long)n * p.hq + h * G + r;
+        if (lane == 0) *reinterpret_cast<float2 *>(w.dense.ml + 2 * row) = make_float2(mm, ll);
+#pragma unroll
+        for (int c = 0; c < D / 128; ++c)
+          *reinterpret_cast<float4 *>(w.dense.part + row * D + 128 * c + 4 * lane) =
+              make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+        return;
+      }
       add_prefix<D>(mm, ll, v, w.pre, n, h, r, G, p.hkv, lane);
       emit_row<D>(p, n, h * G + r, lane, mm, ll, v);
     };
@@ -430,12 +440,14 @@ size_t layout(StepPlan *out, char *ws) {
 }
 
 template <int D>
-cudaError_t run(const AttnParams &p, char *ws, const PrefixParts &pre, unsigned int *errw, cudaStream_t stream) {
+cudaError_t run(const AttnParams &p, char *ws, const PrefixParts &pre, const DenseRows &dense, unsigned int *errw,
+                cudaStream_t stream) {
   using C = StepCfg<D>;
   static_assert(C::CTAS * sizeof(unsigned int) <= kArrivedBytes, "counters");
   StepPlan w;
   layout<D>(&w, ws);
   w.pre = pre;
+  w.dense = dense;
   w.err = errw;
   CUtensorMap q, k, v;
   cudaError_t err = q_map(&q, p, 1);
@@ -452,10 +464,10 @@ cudaError_t run(const AttnParams &p, char *ws, const PrefixParts &pre, unsigned 
 
 size_t attn_step_workspace(int d) { return d == 128 ? layout<128>(nullptr, nullptr) : layout<256>(nullptr, nullptr); }
 
-cudaError_t launch_attn_step(const AttnParams &p, void *ws, const PrefixParts &pre, unsigned int *err,
-                             cudaStream_t stream) {
-  return p.d == 128 ? run<128>(p, static_cast<char *>(ws), pre, err, stream)
-                    : run<256>(p, static_cast<char *>(ws), pre, err, stream);
+cudaError_t launch_attn_step(const AttnParams &p, void *ws, const PrefixParts &pre, const DenseRows &dense,
+                             unsigned int *err, cudaStream_t stream) {
+  return p.d == 128 ? run<128>(p, static_cast<char *>(ws), pre, dense, err, stream)
+                    : run<256>(p, static_cast<char *>(ws), pre, dense, err, stream);
 }
 
 }  // namespace gdn

@@ -925,24 +925,35 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
 
 // ------------------------------------------------------------------ join
 
-// One warp per row of the split tiles in the plan's table: its parts, and the shared prefix's.
+// One warp per row: its parts and the shared prefix's.  Rows of the split tiles in the plan's table,
+// or with `dense` all rows of the call, whose own result the decode kernel left there.
 template <int D>
-__global__ void __launch_bounds__(256) join_kernel(AttnParams p, TilePlan w, PrefixParts pre, int tpt) {
+__global__ void __launch_bounds__(256) join_kernel(AttnParams p, TilePlan w, DenseRows dense, PrefixParts pre, int tpt) {
   const int lane = threadIdx.x & 31;
   const int G = p.hq / p.hkv, per_head = 2 * tpt * G;
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
-  const long long rows = (long long)w.head[1] * p.hkv * per_head;
+  const long long rows = dense.part ? (long long)p.tokens * p.hq : (long long)w.head[1] * p.hkv * per_head;
   const long long step = (long long)gridDim.x * 8;
   for (long long i = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); i < rows; i += step) {
-    const int r = (int)(i % per_head), h = (int)(i / per_head % p.hkv);
-    const Split s = w.split[i / per_head / p.hkv];
-    const int dt = r / G, g = r % G, tok = s.tok0 + dt;
-    if (dt >= s.ntok) continue;
     float acc[D / 32] = {}, m = -CUDART_INF_F, l = 0.f;
+    int tok, h, g;
+    if (dense.part) {
+      tok = (int)(i / p.hq);
+      h = (int)(i % p.hq) / G;
+      g = (int)(i % p.hq) % G;
+      add_parts<D>(m, l, acc, dense.ml, dense.part, i, 0, 1, lane);
+    } else {
+      const int r = (int)(i % per_head), dt = r / G;
+      const Split s = w.split[i / per_head / p.hkv];
+      if (dt >= s.ntok) continue;
+      h = (int)(i / per_head % p.hkv);
+      g = r % G;
+      tok = s.tok0 + dt;
+      add_parts<D>(m, l, acc, w.ml, w.part, (long long)(s.slot + h) * kTileRows + dt / tpt * 128 + dt % tpt * G + g,
+                   (long long)p.hkv * kTileRows, s.parts, lane);
+    }
     add_prefix<D>(m, l, acc, pre, tok, h, g, G, p.hkv, lane);
-    add_parts<D>(m, l, acc, w.ml, w.part, (long long)(s.slot + h) * kTileRows + dt / tpt * 128 + dt % tpt * G + g,
-                 (long long)p.hkv * kTileRows, s.parts, lane);
     emit_row<D>(p, tok, h * G + g, lane, m, l, acc);
   }
 }
@@ -973,7 +984,7 @@ int prefix_parts(int tiles, int hkv, int prefix_len) {
 }
 
 template <int D>
-size_t layout(TilePlan *own, TilePlan *pre, char *ws, int num_seqs, int tokens, int hq, int hkv, int prefix_len) {
+size_t layout(TilePlan *own, TilePlan *pre, DenseRows *dense, char *ws, int num_seqs, int tokens, int hq, int hkv, int prefix_len) {
   const Sizes<D> z(tokens, num_seqs, hq, hkv);
   size_t at = 0;
   auto take = [&](size_t bytes) {
@@ -986,6 +997,7 @@ size_t layout(TilePlan *own, TilePlan *pre, char *ws, int num_seqs, int tokens, 
   const size_t own_slots = prefix_len > 0 ? (size_t)z.max_tiles * hkv + split_slots : split_slots;
   const size_t slot = (size_t)kTileRows * sizeof(float);
   TilePlan a{}, b{};
+  DenseRows c{};
   a.head = (int *)take(256);
   a.base = (int *)take(sizeof(int) * (size_t)(num_seqs + 1));
   a.rec = (Entry *)take(sizeof(Entry) * (size_t)z.max_tiles);
@@ -1002,7 +1014,11 @@ size_t layout(TilePlan *own, TilePlan *pre, char *ws, int num_seqs, int tokens, 
     b.ml = (float *)take(slots * slot * 2);
     b.part = (float *)take(slots * slot * D);
     a.all_slots = 1;
+    const size_t rows = (size_t)tokens * hq;
+    c.ml = (float *)take(rows * 2 * sizeof(float));
+    c.part = (float *)take(rows * D * sizeof(float));
   }
+  if (dense) *dense = c;
   if (own) *own = a;
   if (pre) *pre = b;
   return at;
@@ -1015,9 +1031,10 @@ cudaError_t run(const AttnParams &p, char *ws, unsigned int *errw, cudaStream_t 
   char *tile_ws = ws + attn_step_workspace(D);
   using C = Cfg<D>;
   const Sizes<D> z(p.tokens, p.num_seqs, p.hq, p.hkv);
-  if (step && p.prefix_len == 0) return launch_attn_step(p, ws, PrefixParts{}, errw, stream);
+  if (step && p.prefix_len == 0) return launch_attn_step(p, ws, PrefixParts{}, DenseRows{}, errw, stream);
   TilePlan own, pre;
-  layout<D>(&own, &pre, tile_ws, p.num_seqs, p.tokens, p.hq, p.hkv, p.prefix_len);
+  DenseRows dense;
+  layout<D>(&own, &pre, &dense, tile_ws, p.num_seqs, p.tokens, p.hq, p.hkv, p.prefix_len);
   own.err = pre.err = errw;
   own.units = C::UNITS;
   own.slots = C::SLOTS;
@@ -1034,20 +1051,28 @@ cudaError_t run(const AttnParams &p, char *ws, unsigned int *errw, cudaStream_t 
     if (err != cudaSuccess) return err;
   }
   const PrefixParts parts{pre.ml, pre.part, pre.uniform_parts, z.tpt};
-  if (step) return launch_attn_step(p, ws, parts, errw, stream);
+  if (step) {
+    // The decode kernel joins the prefix's parts itself while every CTA has at most a pair of its
+    // own (five requests: 22 us with a join kernel, 19 without); with more pairs the join's reads
+    // hold up its stream of keys (128 requests: 105 us with a join kernel, 151 without).
+    if ((long long)p.num_seqs * p.hkv <= kSms) return launch_attn_step(p, ws, parts, DenseRows{}, errw, stream);
+    err = launch_attn_step(p, ws, PrefixParts{}, dense, errw, stream);
+    if (err != cudaSuccess) return err;
+    return launch_dependent(join_kernel<D>, 4 * kSms, 256, 0, stream, 1, p, own, dense, parts, z.tpt);
+  }
   err = launch_dependent(plan_kernel, 1, kPlanThreads, 0, stream, 1, p, own, z.tt);
   if (err == cudaSuccess)
     err = launch_dependent(tile_kernel<D>, kSms, C::THREADS, smem, stream, C::GRP, p, own, q, k, v);
   if (err != cudaSuccess) return err;
-  return launch_dependent(join_kernel<D>, 4 * kSms, 256, 0, stream, 1, p, own, parts, z.tpt);
+  return launch_dependent(join_kernel<D>, 4 * kSms, 256, 0, stream, 1, p, own, DenseRows{}, parts, z.tpt);
 }
 
 }  // namespace
 
 size_t attn_workspace(int num_seqs, int tokens, int hq, int hkv, int d, int prefix_len) {
   // the decode kernel's part first: its counters stay in one place for all shapes
-  return attn_step_workspace(d) + (d == 128 ? layout<128>(nullptr, nullptr, nullptr, num_seqs, tokens, hq, hkv, prefix_len)
-                                            : layout<256>(nullptr, nullptr, nullptr, num_seqs, tokens, hq, hkv, prefix_len));
+  return attn_step_workspace(d) + (d == 128 ? layout<128>(nullptr, nullptr, nullptr, nullptr, num_seqs, tokens, hq, hkv, prefix_len)
+                                            : layout<256>(nullptr, nullptr, nullptr, nullptr, num_seqs, tokens, hq, hkv, prefix_len));
 }
 
 cudaError_t launch_attention(const AttnParams &p, void *ws, unsigned int *err, cudaStream_t stream) {

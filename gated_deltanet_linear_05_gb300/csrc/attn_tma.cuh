@@ -103,6 +103,10 @@ struct PrefixParts {
   int parts, tpt;
 };
 constexpr int kTileRows = 256;
+// One result {m, l}, D sums per row of the call, left for a join.
+struct DenseRows {
+  float *ml, *part;
+};
 
 // Adds `count` parts of a row, at `at`, `at` + pitch, ..., to (m, l, acc) by one warp:
 //     M = max(m, max m_q),  l = sum 2^(m_q - M) l_q,  acc = sum 2^(m_q - M) O_q.
