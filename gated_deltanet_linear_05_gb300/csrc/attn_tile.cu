@@ -522,11 +522,12 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
 
   Entry e;
   int h;
-  // D = 128: 12 warps start with 168 registers each; the eight softmax warps take 224 and the
-  // other four keep 56 (8 x 224 + 4 x 56 = 12 x 168)
+  // D = 128: 12 warps start with 168 registers each; the eight softmax warps take 208 and the
+  // other four keep 88 (8 x 208 + 4 x 88 = 12 x 168).  With 224 and 56 the warps that load and
+  // issue ran short: packed prompts 949 us against 905.
   if (!C::PAIR) {
-    if (warp < 8) asm volatile("setmaxnreg.inc.sync.aligned.u32 224;\n");
-    else asm volatile("setmaxnreg.dec.sync.aligned.u32 56;\n");
+    if (warp < 8) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;\n");
+    else asm volatile("setmaxnreg.dec.sync.aligned.u32 88;\n");
   }
   if (warp < C::LOADER) {
     // ---------------------------------------------------------------- softmax, epilogue
