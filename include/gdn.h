@@ -49,8 +49,8 @@
  * synchronising.  The library allocates no memory; scratch memory, where an entry point
  * needs it, is the caller's `workspace` (query its size with gdn_workspace_size).  The
  * only state it keeps is one 32-bit status word per device (gdn_device_status), whose
- * address the first chunked call on a device looks up (make that call before any stream
- * capture).
+ * address the first chunked or attention call on a device looks up (make that call before
+ * any stream capture).
  *
  * Errors: arguments are validated on the host before anything is launched; a bad
  * argument returns its status and enqueues nothing.  A failed launch returns
