@@ -15,8 +15,10 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libgdn.so")
 SOURCES = ["gdn_api.cu", "decode.cu", "chunk_f32.cu", "chunk_bf16.cu", "chunk_fused.cu", "chunk_tc.cu",
            "gdn_noalloc.cu", "block_io.cu", "rollback.cu", "split.cu", "decode_block.cu",
-           "attn_api.cu", "attn_io.cu", "attn_tile.cu", "attn_step.cu"]
-HEADERS = ["common.cuh", "internal.h", "tc.cuh", "attn.h", "attn_tma.cuh"]
+           "attn_api.cu", "attn_io.cu", "attn_tile.cu", "attn_step.cu",
+           "attn_prefix.cu"]
+HEADERS = ["common.cuh", "internal.h", "tc.cuh", "attn.h", "attn_tma.cuh",
+           "attn_tile.cuh", "attn_step.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -47,12 +47,9 @@ constexpr int kStepRows = 16;      // query heads per kv-head that the decode ke
 // Either attention call: picks the kernels and lays out the workspace (attn_tile.cu).
 size_t attn_workspace(int num_seqs, int tokens, int hq, int hkv, int d, int prefix_len);
 cudaError_t launch_attention(const AttnParams &p, void *ws, unsigned int *err, cudaStream_t stream);
-// One token per sequence (attn_step.cu), joined with a shared prefix's parts or left in `dense`.
-struct PrefixParts;
-struct DenseRows;
+// One token per sequence (attn_step.cu).
 size_t attn_step_workspace(int d);
-cudaError_t launch_attn_step(const AttnParams &p, void *ws, const PrefixParts &pre, const DenseRows &dense,
-                             unsigned int *err, cudaStream_t stream);
+cudaError_t launch_attn_step(const AttnParams &p, void *ws, unsigned int *err, cudaStream_t stream);
 
 // The library's device status word on the current device (gdn_api.cu), or NULL.
 unsigned int *device_status_word();

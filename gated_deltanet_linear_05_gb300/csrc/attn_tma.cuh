@@ -100,6 +100,7 @@ __device__ __forceinline__ void emit_row(const AttnParams &p, int tok, int head,
 // rows of {m, l} and D sums, row (token / tpt) 128 + (token % tpt) G + g of the tile's tokens.
 struct PrefixParts {
   const float *ml, *part;
+  const int *head;  // not NULL: the number of parts is head[2], chosen on the device
   int parts, tpt;
 };
 constexpr int kTileRows = 256;
@@ -147,11 +148,12 @@ __device__ __forceinline__ void add_parts(float &m, float &l, float (&acc)[D / 3
 template <int D>
 __device__ __forceinline__ void add_prefix(float &m, float &l, float (&acc)[D / 32], const PrefixParts &pre,
                                            int tok, int h, int g, int G, int hkv, int lane) {
-  if (pre.parts == 0) return;
+  const int parts = pre.head ? pre.head[2] : pre.parts;
+  if (parts == 0) return;
   const int tt = 2 * pre.tpt, off = tok % tt;
-  const long long at = ((long long)(tok / tt) * pre.parts * hkv + h) * kTileRows + off / pre.tpt * 128 +
-                       (off % pre.tpt) * G + g;
-  add_parts<D>(m, l, acc, pre.ml, pre.part, at, (long long)hkv * kTileRows, pre.parts, lane);
+  const long long at =
+      ((long long)(tok / tt) * parts * hkv + h) * kTileRows + off / pre.tpt * 128 + (off % pre.tpt) * G + g;
+  add_parts<D>(m, l, acc, pre.ml, pre.part, at, (long long)hkv * kTileRows, parts, lane);
 }
 
 // Tensor map of a bf16 tensor with 128-byte swizzle (boxes of 64 columns).
