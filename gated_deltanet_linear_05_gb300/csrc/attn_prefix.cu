@@ -1,9 +1,11 @@
 // One token per sequence behind a shared prefix: the prefix's tiles, bound by the tensor cores,
 // and the sequences' own keys, bound by HBM, side by side in one launch.  Every CTA sees the lengths
 // and comes to the same division of the SMs, so that both kinds of work end about together:
-//     X : 152 - X  as  (row tiles x key tiles x cycles of a step) : (own bytes / 48 bytes a cycle),
-// 2450 cycles a step of a CTA (4154 of a pair's two) as measured in long prompts; 48 bytes a cycle is
-// what an SM streams when not all of them do.  A row tile is cut into as many parts as fill the X.
+//     X : 152 - X  as  (row tiles x key tiles x cycles of a step) : (own bytes / 36 bytes a cycle),
+// 2450 cycles a step of a CTA (4154 of a pair's two) as measured in long prompts; 36 bytes a cycle is
+// about what an SM streams when not all of them do (128 requests of up to 1000 own keys behind 16389:
+// 99 us with 48, 86 with 40 and 32, 89 with 26; 104 with the two one after the other).  A row tile is
+// cut into as many parts as fill the X.
 #include "attn_step.cuh"
 #include "attn_tile.cuh"
 
@@ -44,7 +46,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
   const int tt = 2 * (128 / (p.hq / p.hkv));
   const int items = (p.tokens + tt - 1) / tt * p.hkv;
   const float a = (float)items * pre.uniform_kt * (D == 128 ? 2450.f : 4154.f);
-  const float b = sum * p.hkv * (kTile * D * 4.f / 48.f);
+  const float b = sum * p.hkv * (kTile * D * 4.f / 36.f);
   const float want = C::UNITS * a / (a + b);
   int parts = min(pre.uniform_parts, max(1, (int)(want / items + 0.5f)));
   while (parts > 1 && items * parts > C::UNITS - 1) --parts;
