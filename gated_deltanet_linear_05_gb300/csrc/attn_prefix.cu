@@ -17,12 +17,12 @@ struct PrefixCfg {
   static constexpr int WORKERS = D == 128 ? 2 : 1;  // decode workers of a CTA
   static constexpr int WORKER_BYTES = (StepCfg<D>::SMEM + (int)sizeof(StepShared<D>) + 1023) / 1024 * 1024;
   static constexpr int SMEM = Cfg<D>::SMEM > WORKERS * WORKER_BYTES ? Cfg<D>::SMEM : WORKERS * WORKER_BYTES;
-  static_assert(WORKERS * StepCfg<D>::THREADS <= Cfg<D>::THREADS, "threads");
+  static_assert(WORKERS * StepCfg<D>::THREADS <= Cfg<D>::WIDE, "threads");
   static_assert(SMEM + 1024 + 1024 <= 232448, "shared memory");
 };
 
 template <int D>
-__global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
+__global__ void __launch_bounds__(Cfg<D>::WIDE, 1)
     prefix_kernel(AttnParams p, TilePlan pre, StepPlan w, const __grid_constant__ CUtensorMap tile_q,
                   const __grid_constant__ CUtensorMap tile_k, const __grid_constant__ CUtensorMap tile_v,
                   const __grid_constant__ CUtensorMap step_q, const __grid_constant__ CUtensorMap step_k,
@@ -31,18 +31,18 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
   using P = PrefixCfg<D>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ Barriers bars;
-  __shared__ float sh_sum[C::THREADS / 32];
+  __shared__ float sh_sum[C::WIDE / 32];
   const int tid = threadIdx.x;
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   float sum = 0.f;
-  for (int n = tid; n < p.num_seqs; n += C::THREADS) sum += tiles_of(seq_len(p, n));
+  for (int n = tid; n < p.num_seqs; n += C::WIDE) sum += tiles_of(seq_len(p, n));
   sum = warp_sum(sum);
   if ((tid & 31) == 0) sh_sum[tid >> 5] = sum;
   __syncthreads();
   sum = 0.f;
 #pragma unroll
-  for (int i = 0; i < C::THREADS / 32; ++i) sum += sh_sum[i];  // in the same order everywhere
+  for (int i = 0; i < C::WIDE / 32; ++i) sum += sh_sum[i];  // in the same order everywhere
   const int tt = 2 * (128 / (p.hq / p.hkv));
   const int items = (p.tokens + tt - 1) / tt * p.hkv;
   const float a = (float)items * pre.uniform_kt * (D == 128 ? 2450.f : 4154.f);
@@ -56,7 +56,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
   const int unit = (int)blockIdx.x / C::GRP;
   if (unit < units) {
     pre.uniform_parts = parts;
-    tile_role<D>(p, pre, tile_q, tile_k, tile_v, smem_raw, bars, unit, units, true);
+    tile_role<D, 8>(p, pre, tile_q, tile_k, tile_v, smem_raw, bars, unit, units, true);
     return;
   }
   const int v = tid / StepCfg<D>::THREADS;
@@ -86,7 +86,7 @@ cudaError_t run(const AttnParams &p, char *ws, const TilePlan &pre, const DenseR
   static std::atomic<uint64_t> allowed{0};
   err = allow_smem(prefix_kernel<D>, smem, allowed);
   if (err != cudaSuccess) return err;
-  return launch_dependent(prefix_kernel<D>, kSms, C::THREADS, smem, stream, C::GRP, p, pre, w, m[0], m[1], m[2], m[3],
+  return launch_dependent(prefix_kernel<D>, kSms, C::WIDE, smem, stream, C::GRP, p, pre, w, m[0], m[1], m[2], m[3],
                           m[4], m[5]);
 }
 

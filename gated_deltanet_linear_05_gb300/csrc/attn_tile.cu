@@ -149,7 +149,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
                 const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ Barriers bars;
-  tile_role<D>(p, w, qmap, kmap, vmap, smem_raw, bars, (int)blockIdx.x / Cfg<D>::GRP, Cfg<D>::UNITS, false);
+  tile_role<D, D == 128 ? 8 : 4>(p, w, qmap, kmap, vmap, smem_raw, bars, (int)blockIdx.x / Cfg<D>::GRP, Cfg<D>::UNITS, false);
 }
 
 // ------------------------------------------------------------------ join

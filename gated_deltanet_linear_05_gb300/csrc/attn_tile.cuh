@@ -49,8 +49,8 @@ struct Cfg {
   static constexpr int Q_BYTES = 128 * D * 2;       // one sub-tile
   static constexpr int KV_BYTES = 32768;            // a CTA's part of a K or V tile
   static constexpr int SMEM = SUBS * Q_BYTES + STAGES * KV_BYTES;
-  static constexpr int LOADER = 8;                  // warp that loads; the next issues products
-  static constexpr int THREADS = 384;               // 4 SUBS softmax warps; some of the 12 are idle
+  static constexpr int THREADS = PAIR ? 192 : 384;  // of the tile kernel (D = 128: two warps are idle)
+  static constexpr int WIDE = 384;                  // of the kernel that shares the SMs with decode workers
   static constexpr int UNITS = kSms / GRP;          // CTAs, or pairs of them
   static constexpr int SLOTS = 2 * UNITS;           // partial results of split tiles
 };
@@ -343,8 +343,9 @@ __device__ __forceinline__ int sub_tiles(const Entry &e, int i, int tpt) {
 }
 
 // The work of unit `unit` of `units` (a CTA, or a pair of them) by all of its threads.  `waited`: the
-// work before this kernel is known to be complete.
-template <int D>
+// work before this kernel is known to be complete.  The warps are 4 SUBS for the softmax, LOADER that
+// loads and the next that issues the products.
+template <int D, int LOADER>
 __device__ __forceinline__ void tile_role(const AttnParams &p, const TilePlan &w, const CUtensorMap &qmap,
                                           const CUtensorMap &kmap, const CUtensorMap &vmap, uint8_t *smem_raw,
                                           Barriers &bars, int unit, int units, bool waited) {
@@ -368,7 +369,7 @@ __device__ __forceinline__ void tile_role(const AttnParams &p, const TilePlan &w
     mbar_fence_init();
     bars.dead = 0;
   }
-  if (warp == C::LOADER) {
+  if (warp == LOADER) {
     if (lane == 0) {
       prefetch_map(&qmap);
       prefetch_map(&kmap);
@@ -389,14 +390,15 @@ __device__ __forceinline__ void tile_role(const AttnParams &p, const TilePlan &w
 
   Entry e;
   int h;
-  // The 12 warps start with 168 registers each.  D = 128: the eight softmax warps take 208, the
-  // other four keep 88 (with 224 and 56 the warps that load and issue ran short: packed prompts
-  // 949 us against 905).  D = 256: the four softmax warps take 232, four idle ones give theirs
-  // away.  8 x 208 + 4 x 88 = 4 x 232 + 4 x 24 + 4 x 248 = 12 x 168.
+  // 12 warps start with 168 registers each.  D = 128: the eight softmax warps take 208, the other
+  // four keep 88 (with 224 and 56 the warps that load and issue ran short: packed prompts 949 us
+  // against 905).  D = 256 in 12 warps: the four softmax warps take 232, four idle ones give theirs
+  // away; in 6 warps there are enough.  8 x 208 + 4 x 88 = 4 x 232 + 4 x 24 + 4 x 248 = 12 x 168.
+  constexpr bool kMove = LOADER == 8;
   if (warp < 4 * C::SUBS) {
     // ---------------------------------------------------------------- softmax, epilogue
-    if (C::PAIR) asm volatile("setmaxnreg.inc.sync.aligned.u32 232;\n");
-    else asm volatile("setmaxnreg.inc.sync.aligned.u32 208;\n");
+    if (kMove && C::PAIR) asm volatile("setmaxnreg.inc.sync.aligned.u32 232;\n");
+    else if (kMove) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;\n");
     const int sub = C::PAIR ? rank : warp >> 2;
     const int row = threadIdx.x & 127;
     const float asl = p.scale == 0.f ? 1.f : fabsf(p.scale) * 1.4426950408889634f;
@@ -589,12 +591,12 @@ __device__ __forceinline__ void tile_role(const AttnParams &p, const TilePlan &w
       }
       tc::fence_before();
     }
-  } else if (warp < C::LOADER) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 24;\n");
+  } else if (warp < LOADER) {
+    if (kMove) asm volatile("setmaxnreg.dec.sync.aligned.u32 24;\n");
   } else {
-   if (C::PAIR) asm volatile("setmaxnreg.inc.sync.aligned.u32 248;\n");
-   else asm volatile("setmaxnreg.dec.sync.aligned.u32 88;\n");
-   if (warp == C::LOADER) {
+   if (kMove && C::PAIR) asm volatile("setmaxnreg.inc.sync.aligned.u32 248;\n");
+   else if (kMove) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;\n");
+   if (warp == LOADER) {
     // ---------------------------------------------------------------- loads
     // A tile comes in boxes of box rows x 64 columns; lane b keeps the page of box b of the tile
     // after the present one, so that no load waits for the table.  In a pair, CTA r holds keys
@@ -685,7 +687,7 @@ __device__ __forceinline__ void tile_role(const AttnParams &p, const TilePlan &w
         if (++st == C::STAGES) st = 0, ph ^= 1;
       }
     }
-   } else if (warp == C::LOADER + 1 && rank == 0) {
+   } else if (warp == LOADER + 1 && rank == 0) {
     // ---------------------------------------------------------------- products
     // All values here are the same in every lane and known as such (uniform()): the
     // instruction takes its descriptors from uniform registers, and building them from
@@ -793,7 +795,7 @@ __device__ __forceinline__ void tile_role(const AttnParams &p, const TilePlan &w
   __syncthreads();
   if (C::PAIR) cluster_sync();  // no signal is on its way to a CTA that has gone
   tc::fence_after();
-  if (warp == C::LOADER) tmem_dealloc<C::GRP>(tmem);
+  if (warp == LOADER) tmem_dealloc<C::GRP>(tmem);
 }
 
 // A shared prefix beside the sequences' own keys, one token per sequence (attn_prefix.cu): the
