@@ -105,20 +105,25 @@ _BF16, _I32, _F32 = torch.bfloat16, torch.int32, torch.float32
 _DENSE = torch.contiguous_format
 
 
-def _bf16(device, what, *tensors):
-    for t in tensors:
+def _check(device, bf16, index):
+    """Types and places of a call's tensors.  (Written out in one expression where it passes: a call
+    for each tensor costs as much as the launch.)"""
+    for t in bf16:
+        if t.dtype is not _BF16 or t.get_device() != device:
+            break
+    else:
+        for t in index:
+            if t is not None and (t.dtype is not _I32 or t.get_device() != device
+                                  or not t.is_contiguous()):
+                break
+        else:
+            if device >= 0:
+                return
+    for t in bf16:
         if t.dtype is not _BF16:
-            raise TypeError("%s must be bfloat16, got %s" % (what, t.dtype))
-        if t.get_device() != device or device < 0:
-            raise ValueError("%s must be CUDA tensors of one device" % what)
-
-
-def _index(device, t, what, dtype=_I32):
-    """The address of a contiguous tensor of indices (or frequencies)."""
-    if t.dtype is not dtype or t.get_device() != device or not t.is_contiguous():
-        raise ValueError("%s must be a contiguous %s CUDA tensor on the queries' device"
-                         % (what, dtype))
-    return t.data_ptr()
+            raise TypeError("q, k, v, gate and the caches must be bfloat16, got %s" % t.dtype)
+    raise ValueError("the tensors must be CUDA tensors of one device, and those of indices contiguous "
+                     "int32")
 
 
 def _float(device, t, shape, what):
@@ -200,7 +205,11 @@ def gdn_kv_append(q, k, v, k_cache, v_cache, page_table, kv_lens, inv_freq=None,
     or None (no rotation); positions [T] or [axes, T] int32 (None: prefix_len + place) with
     rope_axis [R/2] int32.  q_out None: a new tensor.  Returns q_out."""
     device = q.get_device()
-    _bf16(device, "q, k, v and the caches", q, k, v, k_cache, v_cache)
+    _check(device, (q, k, v, k_cache, v_cache),
+           (page_table, kv_lens, cu_seqlens, positions, rope_axis))
+    if inv_freq is not None and (inv_freq.dtype is not torch.float64 or inv_freq.get_device() != device
+                                 or not inv_freq.is_contiguous()):
+        raise ValueError("inv_freq must be a contiguous float64 CUDA tensor")
     key = (q.shape, q.stride(), k.shape, k.stride(), v.shape, v.stride(), k_cache.shape,
            k_cache.stride(), v_cache.shape, v_cache.stride(), page_table.shape, kv_lens.shape,
            None if inv_freq is None else inv_freq.shape,
@@ -217,11 +226,11 @@ def gdn_kv_append(q, k, v, k_cache, v_cache, page_table, kv_lens, inv_freq=None,
         made[1], q.data_ptr(), k.data_ptr(), v.data_ptr(),
         None if q_norm is None else _float(device, q_norm, d, "q_norm"),
         None if k_norm is None else _float(device, k_norm, d, "k_norm"), eps,
-        None if inv_freq is None else _index(device, inv_freq, "inv_freq", torch.float64),
-        None if rope_axis is None else _index(device, rope_axis, "rope_axis"),
-        None if positions is None else _index(device, positions, "positions"),
-        _index(device, page_table, "page_table"), _index(device, kv_lens, "kv_lens"),
-        None if cu_seqlens is None else _index(device, cu_seqlens, "cu_seqlens"),
+        None if inv_freq is None else inv_freq.data_ptr(),
+        None if rope_axis is None else rope_axis.data_ptr(),
+        None if positions is None else positions.data_ptr(),
+        page_table.data_ptr(), kv_lens.data_ptr(),
+        None if cu_seqlens is None else cu_seqlens.data_ptr(),
         q_out.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), _stream(stream, device))
     if st != GDN_OK:
         raise GdnError(st, "gdn_kv_append")
@@ -247,9 +256,8 @@ def _attend_shape(q, k_cache, v_cache, prefix_table, prefix_len, page_table, kv_
 def _attend(name, q, k_cache, v_cache, prefix_table, prefix_len, page_table, kv_lens, cu_seqlens,
             gate, scale, o, lse, workspace, stream):
     device = q.get_device()
-    _bf16(device, "q and the caches", q, k_cache, v_cache)
-    if gate is not None:
-        _bf16(device, "gate", gate)
+    _check(device, (q, k_cache, v_cache) if gate is None else (q, k_cache, v_cache, gate),
+           (page_table, kv_lens, cu_seqlens, prefix_table))
     key = (q.shape, q.stride(), k_cache.shape, k_cache.stride(), v_cache.shape, v_cache.stride(),
            page_table.shape, kv_lens.shape, None if cu_seqlens is None else cu_seqlens.shape,
            None if gate is None else (gate.shape, gate.stride()), scale,
@@ -263,18 +271,16 @@ def _attend(name, q, k_cache, v_cache, prefix_table, prefix_len, page_table, kv_
                                 device=q.device)
     elif workspace.get_device() != device or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous CUDA tensor on the queries' device")
-    ends = (_index(device, page_table, "page_table"), _index(device, kv_lens, "kv_lens"),
-            None if cu_seqlens is None else _index(device, cu_seqlens, "cu_seqlens"), o.data_ptr(),
+    args = [made[1], q.data_ptr(), None if gate is None else gate.data_ptr(), k_cache.data_ptr(),
+            v_cache.data_ptr(), page_table.data_ptr(), kv_lens.data_ptr(),
+            None if cu_seqlens is None else cu_seqlens.data_ptr(), o.data_ptr(),
             None if lse is None else _float(device, lse, q.shape[:2], "lse"), workspace.data_ptr(),
-            workspace.nbytes, _stream(stream, device))
-    gate = None if gate is None else gate.data_ptr()
+            workspace.nbytes, _stream(stream, device)]
     if prefix_table is None:
-        st = lib().gdn_paged_attention(made[1], q.data_ptr(), gate, k_cache.data_ptr(),
-                                       v_cache.data_ptr(), *ends)
+        st = lib().gdn_paged_attention(*args)
     else:
-        st = lib().gdn_shared_prefix_attention(made[1], q.data_ptr(), gate, k_cache.data_ptr(),
-                                               v_cache.data_ptr(),
-                                               _index(device, prefix_table, "prefix_table"), *ends)
+        args.insert(5, prefix_table.data_ptr())
+        st = lib().gdn_shared_prefix_attention(*args)
     if st != GDN_OK:
         raise GdnError(st, name)
     return o
