@@ -12,6 +12,9 @@
 // at the end of a pair; with D = 256 a second set of warps takes the upper half of V's
 // columns (and repeats the scores: the shared memory they are read from has the bandwidth to spare).
 // One warp keeps a ring of K and V tiles full by TMA: 160 KB in flight per SM.
+//
+// 64 contexts of 255 to 8191 keys, 32 heads of 128 on 8: 169 us, 6.65 TB/s (98% of the copy rate).  Two
+// contexts of 90k to 131k keys, 16 heads of 256 on 2: 81 us, 5.5 TB/s with 8 us of start and join.
 #pragma once
 
 #include <cuda.h>

@@ -151,6 +151,42 @@ def test_prefix_rows(prefix, d):
     _check(b, *_run(b))
 
 
+@pytest.mark.parametrize("d", [128, 256])
+@pytest.mark.parametrize("lens,prefix", [([6000, 3500], 17), ([0, 0, 0], 9000), ([5000], 5000),
+                                         ([i * 7 % 401 for i in range(300)], 130), ([1], 1)])
+def test_prefix_divisions(lens, prefix, d):
+    """One kind of work far larger than the other, both alike, more sequences than CTAs."""
+    b = Batch([1] * len(lens), lens, 4, 2, d, 64, prefix=prefix, seed=24)
+    _check(b, *_run(b))
+
+
+@pytest.mark.parametrize("d", [128, 256])
+@pytest.mark.parametrize("hq,hkv", [(128, 1), (64, 1), (34, 2)])
+@pytest.mark.parametrize("prefix", [0, 70])
+def test_wide_groups(hq, hkv, prefix, d):
+    """More query heads a kv-head than the decode kernel takes, up to a tile of one token."""
+    for t, lens in (([1, 1, 1], [5, 130, 300]), ([3, 1, 20], [3, 130, 300])):
+        b = Batch(t, lens, hq, hkv, d, 32, prefix=prefix, gate=True, seed=25)
+        _check(b, *_run(b))
+
+
+@pytest.mark.parametrize("seed", range(12))
+def test_drawn_shapes(seed):
+    """Sizes drawn over the whole range of heads, pages, lengths and kinds of call."""
+    import random
+    r = random.Random(100 + seed)
+    hkv, group = r.choice([1, 2, 3]), r.choice([1, 2, 3, 5, 7, 8, 13, 16])
+    n = r.randint(1, 9)
+    step = r.random() < 0.4
+    t = [1] * n if step else [r.choice([0, 1, 2, 17, r.randint(1, 200)]) for _ in range(n)]
+    lens = [max(0, a + r.choice([-1, 0, 0, 1, r.randint(0, 700)])) for a in t]
+    b = Batch(t, lens, hkv * group, hkv, r.choice([128, 256]), r.choice([16, 32, 64, 128]),
+              prefix=r.choice([0, 0, 1, 63, 200]), gate=r.random() < 0.5, seed=seed, q_pad=r.choice([0, 8]),
+              page_pad=r.choice([0, 128]))
+    if sum(t):
+        _check(b, *_run(b, step=step))
+
+
 @pytest.mark.parametrize("step", [False, True])
 @pytest.mark.parametrize("prefix", [0, 100])
 def test_strides(step, prefix):
