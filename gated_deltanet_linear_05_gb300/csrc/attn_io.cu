@@ -45,7 +45,7 @@ __device__ __forceinline__ uint64_t turn_fraction(double f) {
   return (b >> 63) ? 0 - r : r;
 }
 
-constexpr int kAppendWarps = 8;
+constexpr int kAppendWarps = 4;
 constexpr int kAppendRows = 6;  // rows that a lane group has in flight (4: 83 us for packed prompts, 6: 78)
 
 // A warp takes one token's head rows (or, with few tokens, `share` warps a token), a row in D / 8
@@ -57,7 +57,7 @@ constexpr int kAppendRows = 6;  // rows that a lane group has in flight (4: 83 u
 // Bound by HBM: packed prompts of 33k tokens, 48 head rows of 128: 78 us, 5.5 TB/s (81% of the copy
 // rate); a decode step of 32 tokens by its chain of loads (length, page, row), about 4 us.
 template <int D, bool NORM>
-__global__ void __launch_bounds__(32 * kAppendWarps, 2) append_kernel(AppendParams p, int share) {
+__global__ void __launch_bounds__(32 * kAppendWarps, 4) append_kernel(AppendParams p, int share) {
   constexpr int LPR = D / 8, RPW = 32 / LPR, U = kAppendRows;
   const int lane = threadIdx.x & 31;
   const int part = (int)((blockIdx.x * kAppendWarps + (threadIdx.x >> 5)) % share);
@@ -321,9 +321,9 @@ cudaError_t launch_kv_append(const AppendParams &p, cudaStream_t stream) {
   const int rows = p.hq + 2 * p.hkv;
   // warps per token: enough to fill 152 SMs with 16 warps each, while each has rows to do
   int share = 1;
-  while (share < kAppendWarps && (long long)p.tokens * share < 152 * 16 && share * rpw < rows) share *= 2;
+  while (share < 8 && (long long)p.tokens * share < 152 * 16 && share * rpw < rows) share *= 2;
   const long long blocks = ((long long)p.tokens * share + kAppendWarps - 1) / kAppendWarps;
-  const unsigned grid = (unsigned)(blocks < 152 * 8 ? blocks : 152 * 8);
+  const unsigned grid = (unsigned)(blocks < 152 * 16 ? blocks : 152 * 16);
   const bool norm = p.q_norm || p.k_norm;
   auto *kernel = p.d == 128 ? (norm ? append_kernel<128, true> : append_kernel<128, false>)
                             : (norm ? append_kernel<256, true> : append_kernel<256, false>);
