@@ -3,7 +3,8 @@ append to the paged cache, attention over the cache, and the same behind a share
 
 Argument marshalling only, as in the package itself; include/gdn.h has the contract of each
 call.  The shape structs are kept by sizes and strides, so that a decode loop builds them
-once.
+once; a call whose combination has been seen goes through _marshal (csrc/marshal.c), which does
+the same checks in C and hands anything unusual back to the functions here.
 """
 from __future__ import annotations
 
@@ -13,7 +14,7 @@ from typing import Optional
 
 import torch
 
-from . import (GDN_BF16, GDN_ERR_INVALID_ARG, GDN_F32, GDN_OK, GdnError, lib)
+from . import (GDN_BF16, GDN_ERR_INVALID_ARG, GDN_F32, GDN_OK, GdnError, GdnUnavailable, lib)
 
 I64x2 = ctypes.c_int64 * 2
 
@@ -56,7 +57,7 @@ def _shape(n, tokens, hq, hkv, d, page_size, num_pages, max_pages, prefix_len, r
                       ("gate_stride", gate_stride)):
         if st is not None:
             getattr(s, field)[:] = st
-    return s, ctypes.byref(s)
+    return s, ctypes.byref(s), ctypes.addressof(s)
 
 
 def gdn_attn_workspace_size(shape: GdnAttnShape) -> int:
@@ -172,6 +173,27 @@ def _remember(key, value):
     return value
 
 
+_quick = None
+
+
+def _fast():
+    """The marshalling module, bound to torch and to the library's entry points."""
+    global _quick
+    if _quick is None:
+        L = lib()
+        try:
+            from . import _marshal
+        except ImportError as e:
+            raise GdnUnavailable("_marshal.so not built (run gated_deltanet_linear_05_gb300/build.py): "
+                                 "%s" % e)
+        _marshal.bind(_BF16, _F32, torch.float64, _I32, torch.empty, torch.empty_like, _raw_stream,
+                      _DENSE, *(ctypes.cast(getattr(L, f), ctypes.c_void_p).value for f in
+                                ("gdn_paged_attention", "gdn_shared_prefix_attention", "gdn_kv_append",
+                                 "gdn_add_rmsnorm")))
+        _quick = _marshal
+    return _quick
+
+
 def _append_shape(q, k, v, k_cache, v_cache, page_table, kv_lens, inv_freq, cu_seqlens, positions,
                   rope_axis, prefix_len):
     pages, hkv, size, d, page_stride = _cache(k_cache, v_cache)
@@ -204,6 +226,14 @@ def gdn_kv_append(q, k, v, k_cache, v_cache, page_table, kv_lens, inv_freq=None,
     included), cu_seqlens [N+1] int32 or None (one token per sequence); inv_freq [R/2] fp64
     or None (no rotation); positions [T] or [axes, T] int32 (None: prefix_len + place) with
     rope_axis [R/2] int32.  q_out None: a new tensor.  Returns q_out."""
+    if stream is None:
+        r = (_quick or _fast()).append(_made, q, k, v, k_cache, v_cache, page_table, kv_lens, inv_freq,
+                                       cu_seqlens, positions, rope_axis, q_norm, k_norm, eps, q_out,
+                                       prefix_len)
+        if type(r) is int:
+            raise GdnError(r, "gdn_kv_append")
+        if r is not None:
+            return r
     device = q.get_device()
     _check(device, (q, k, v, k_cache, v_cache),
            (page_table, kv_lens, cu_seqlens, positions, rope_axis))
@@ -255,6 +285,13 @@ def _attend_shape(q, k_cache, v_cache, prefix_table, prefix_len, page_table, kv_
 
 def _attend(name, q, k_cache, v_cache, prefix_table, prefix_len, page_table, kv_lens, cu_seqlens,
             gate, scale, o, lse, workspace, stream):
+    if stream is None and lse is None:
+        r = (_quick or _fast()).attend(_made, q, k_cache, v_cache, prefix_table, prefix_len, page_table,
+                                       kv_lens, cu_seqlens, gate, scale, o, workspace)
+        if type(r) is int:
+            raise GdnError(r, name)
+        if r is not None:
+            return r
     device = q.get_device()
     _check(device, (q, k_cache, v_cache) if gate is None else (q, k_cache, v_cache, gate),
            (page_table, kv_lens, cu_seqlens, prefix_table))
@@ -340,6 +377,12 @@ def gdn_add_rmsnorm(x, residual, weight, eps: float = 1e-6, residual_out=None, y
     type, returns (y, h); out "e4m3": y in float8_e4m3fn with fp32 scales per row (group 0) or
     per 128 columns (group 128), returns (y, scale, h).  x, residual bf16 or fp32; weight
     fp32.  residual_out may be residual or x."""
+    if residual_out is None and y is None and scale is None and stream is None:
+        r = (_quick or _fast()).norm(_made, x, residual, weight, eps, out, group)
+        if type(r) is int:
+            raise GdnError(r, "gdn_add_rmsnorm")
+        if r is not None:
+            return r
     device = x.get_device()
     key = ("norm", x.shape, x.dtype, out, group)
     rows, cols, code, kind, scales = _made.get(key) or _remember(key, _norm_plan(x, out, group))

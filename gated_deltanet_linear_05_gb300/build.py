@@ -1,5 +1,6 @@
 """Build libgdn.so in-tree for sm_103a with nvcc (one translation unit per kernel file,
-compiled in parallel, then linked).  No torch, no cmake."""
+compiled in parallel, then linked), and the attention calls' marshalling module with gcc.
+No torch, no cmake."""
 from __future__ import annotations
 
 import concurrent.futures
@@ -7,12 +8,14 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libgdn.so")
+MARSHAL = os.path.join(HERE, "_marshal.so")  # the attention calls' argument marshalling (CPython)
 SOURCES = ["gdn_api.cu", "decode.cu", "chunk_f32.cu", "chunk_bf16.cu", "chunk_fused.cu", "chunk_tc.cu",
            "gdn_noalloc.cu", "block_io.cu", "rollback.cu", "split.cu", "decode_block.cu",
            "attn_api.cu", "attn_io.cu", "attn_tile.cu", "attn_step.cu",
@@ -70,6 +73,12 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
         tmp = LIB + ".tmp%d" % os.getpid()
         run([nvcc()] + ARCH + ["-shared", "-o", tmp] + objs + ["-lcudart"])
         os.replace(tmp, LIB)
+    src = os.path.join(CSRC, "marshal.c")
+    if force or _stale(MARSHAL, [src, os.path.join(ROOT, "include", "gdn.h")]):
+        tmp = MARSHAL + ".tmp%d" % os.getpid()
+        run(["gcc", "-O2", "-Wall", "-Wextra", "-fPIC", "-shared", "-I", sysconfig.get_paths()["include"],
+             "-I", os.path.join(ROOT, "include"), src, "-o", tmp])
+        os.replace(tmp, MARSHAL)
     return LIB
 
 
