@@ -25,7 +25,7 @@
 //
 // Bound by the tensor cores for prompts: 8192 tokens, 32 heads of 128 take 338 us (1625 TFLOP/s, 85%
 // of cuBLAS's rate; a step of 128 keys 2450 cycles against the products' 2048); 4096 tokens, 16
-// heads of 256 take 91 us (1510), with a gate 108 (the epilogue's sigmoids).  Drafts of 16 tokens on
+// heads of 256 take 89 us (1540), with a gate 109 (the epilogue's sigmoids).  Drafts of 16 tokens on
 // contexts of 200 to 4000 are bound by HBM: 108 us, 5.1 TB/s with the plan.
 #pragma once
 
@@ -48,10 +48,6 @@ struct Cfg {
   static constexpr int SUBS = PAIR ? 1 : 2;         // sub-tiles of 128 rows in a CTA
   static constexpr int NBUF = PAIR ? 2 : 1;         // S buffers of a sub-tile
   static constexpr int STAGES = 5;
-  // 32-column chunks that the epilogue takes at a time: a pair has no other sub-tile whose products
-  // hide it, and two cost it fewer waits (4096 gated tokens, 16 heads: 108 us, one at a time 115);
-  // with another sub-tile one is enough (drafts of 16 tokens: 108 us, two at a time 109).
-  static constexpr int CHUNKS = PAIR ? 2 : 1;
   static constexpr int CH = D / 64;                 // 128-byte column chunks of a row of q or K
   static constexpr int KROWS = PAIR ? 64 : kBN;     // keys of a K tile in this CTA
   static constexpr int Q_BYTES = 128 * D * 2;       // one sub-tile
@@ -550,8 +546,7 @@ __device__ __forceinline__ void tile_role(const AttnParams &p, const TilePlan &w
         if (live && p.lse) p.lse[orow] = l > 0.f ? (m + log2f(l)) * kLn2 : -CUDART_INF_F;
         const float inv = l > 0.f ? 1.f / l : 0.f;
         const __nv_bfloat16 *gk[4];
-        constexpr int W = C::CHUNKS;
-        uint4 gate[W][4];
+        uint4 gate[4];
         if (p.gate) {
           const long long off = live ? tok * p.gs[0] + head * p.gs[1] : 0;
 #pragma unroll
@@ -565,46 +560,32 @@ __device__ __forceinline__ void tile_role(const AttnParams &p, const TilePlan &w
             if (rowk[k] >= 0) to[k] = load_now(gk[k] + c);
           }
         };
-        if (p.gate) {
-#pragma unroll
-          for (int b = 0; b < W; ++b) fetch(gate[b], 32 * b);
-        }
+        if (p.gate) fetch(gate, 0);
         if (n > 0) settle();
-        // (A pair's loop is not unrolled: 115 us again if it is; the other's by 2: 914 us for eight
-        // prompts of 256 to 8192 tokens, 927 without and with 4.)
+        // A pair's loop stays rolled (16 heads of 256, 4096 tokens: 89 us, by two 91); the other is
+        // unrolled by two (8192 tokens, 32 heads of 128: 338 us, rolled 346).
         constexpr int kUnroll = C::PAIR ? 1 : 2;
 #pragma unroll (kUnroll)
-        for (int c = 0; c < D; c += 32 * W) {
-          uint32_t o[W][32];
-          uint4 u[W][4];
+        for (int c = 0; c < D; c += 32) {
+          uint32_t o[32];
+          uint4 u[4];
+          read_o(o, o_base + c, n > 0);
+          if (p.gate) transpose4(gate, lane);
 #pragma unroll
-          for (int b = 0; b < W; ++b) read_o(o[b], o_base + c + 32 * b, n > 0);
+          for (int k = 0; k < 4; ++k) {
+            float x[8];
 #pragma unroll
-          for (int b = 0; b < W; ++b) {
-            if (p.gate) transpose4(gate[b], lane);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              float x[8];
-#pragma unroll
-              for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(o[b][8 * k + i]) * inv;
-              if (p.gate) gate8(x, gate[b][k]);
-              u[b][k] = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]),
-                                   pack_bf16(x[6], x[7]));
-            }
+            for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(o[8 * k + i]) * inv;
+            if (p.gate) gate8(x, gate[k]);
+            u[k] = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]),
+                              pack_bf16(x[6], x[7]));
           }
-          if (p.gate && c + 32 * W < D) {
-#pragma unroll
-            for (int b = 0; b < W; ++b) fetch(gate[b], c + 32 * (W + b));
-          }
-#pragma unroll
-          for (int b = 0; b < W; ++b) transpose4(u[b], lane);
+          if (p.gate && c + 32 < D) fetch(gate, c + 32);
+          transpose4(u, lane);
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            if (rowk[k] >= 0) {
-              __nv_bfloat16 *at = (__nv_bfloat16 *)p.o + (long long)rowk[k] * D + c + 8 * unit4;
-#pragma unroll
-              for (int b = 0; b < W; ++b) *reinterpret_cast<uint4 *>(at + 32 * b) = u[b][k];
-            }
+            if (rowk[k] >= 0)
+              *reinterpret_cast<uint4 *>((__nv_bfloat16 *)p.o + (long long)rowk[k] * D + c + 8 * unit4) = u[k];
         }
       }
       tc::fence_before();
