@@ -46,7 +46,7 @@ __device__ __forceinline__ uint64_t turn_fraction(double f) {
 }
 
 constexpr int kAppendWarps = 4;
-constexpr int kAppendRows = 6;  // rows that a lane group has in flight (4: 83 us for packed prompts, 6: 78)
+constexpr int kAppendRows = 6;  // rows that a lane group has in flight (4: 83 us for packed prompts, 6: 76)
 
 // A warp takes one token's head rows (or, with few tokens, `share` warps a token), a row in D / 8
 // lanes of 8 elements.  The turns per position of a lane's frequencies are kept over the warp's
@@ -54,7 +54,7 @@ constexpr int kAppendRows = 6;  // rows that a lane group has in flight (4: 83 u
 // loads are in flight while the ones before are rotated.  The rotation's other half reaches a
 // lane as the raw bf16 words of the lane that has it.  Sine and cosine by the fast
 // instructions on an angle already reduced to half a turn: 2^-21 absolute, against 2^-9 of bf16.
-// Bound by HBM: packed prompts of 33k tokens, 48 head rows of 128: 78 us, 5.5 TB/s (81% of the copy
+// Bound by HBM: packed prompts of 33k tokens, 48 head rows of 128: 75 us, 5.7 TB/s (84% of the copy
 // rate); a decode step of 32 tokens by its chain of loads (length, page, row), about 4 us.
 template <int D, bool NORM>
 __global__ void __launch_bounds__(32 * kAppendWarps, 4) append_kernel(AppendParams p, int share) {
