@@ -56,7 +56,7 @@ __global__ void __launch_bounds__(Cfg<D>::WIDE, 1)
   const int unit = (int)blockIdx.x / C::GRP;
   if (unit < units) {
     pre.uniform_parts = parts;
-    tile_role<D, 8>(p, pre, tile_q, tile_k, tile_v, smem_raw, bars, unit, units, true);
+    tile_role<C, 8>(p, pre, tile_q, tile_k, tile_v, smem_raw, bars, unit, units, true);
     return;
   }
   const int v = tid / StepCfg<D>::THREADS;

@@ -16,8 +16,10 @@ constexpr int kPlanTiles = 4096;  // tiles whose lengths are kept in shared memo
 
 // Cuts the batch into entries, one block.  Tiles with many key tiles are split so that the
 // SMs get even shares: of kCand chunk lengths the one with the smallest
-//     max(chunk, ceil(entries / units) * mean entry) + 3 ceil(entries / units)
-// (in key tiles; 3 is about what starting and ending an entry costs).  Entries are ordered by
+//     max(chunk, ceil(entries / units) * mean entry) + 3 ceil(entries / units) + join
+// (in key tiles; 3 is about what starting and ending an entry costs), where the join costs 0.12 a part of
+// the longest tile and 2.4e-6 a float of partial sums (one prompt of 1200 tokens, 12 gated heads of 256:
+// 54 us if it is taken to be free, 30 so; any factor from 0.6e-6 to 5e-6 does within 3 us).  Entries are ordered by
 // length, longest first, in 64 classes, for the kernel's back-and-forth assignment.  All of it
 // is latency: the lengths stay in shared memory and a warp tries each chunk length.
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(AttnParams p, TilePlan w, int tt) {
@@ -95,7 +97,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(AttnParams p, TilePl
       const float items = (float)cnt * p.hkv, rounds = ceilf(items / w.units);
       sh_cost[c] = c > 0 && (long long)spl * p.hkv > w.slots
                        ? CUDART_INF_F
-                       : fmaxf((float)chunk, rounds * (work * p.hkv / fmaxf(items, 1.f))) + 3.f * rounds;
+                       : fmaxf((float)chunk, rounds * (work * p.hkv / fmaxf(items, 1.f))) + 3.f * rounds +
+                             (spl > 0 ? 0.12f * parts_in(kvmax, chunk, inv) + 2.4e-6f * spl * ((float)p.tokens * p.hq * p.d / tiles) : 0.f);
     }
   }
   __syncthreads();
@@ -143,13 +146,13 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(AttnParams p, TilePl
   if (tid == 0) w.head[1] = sh_nsplit;
 }
 
-template <int D>
-__global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
+template <class C>
+__global__ void __launch_bounds__(C::THREADS, C::CTAS)
     tile_kernel(AttnParams p, TilePlan w, const __grid_constant__ CUtensorMap qmap,
                 const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ Barriers bars;
-  tile_role<D, D == 128 ? 8 : 4>(p, w, qmap, kmap, vmap, smem_raw, bars, (int)blockIdx.x / Cfg<D>::GRP, Cfg<D>::UNITS, false);
+  tile_role<C, C::SUBS == 2 ? 8 : 4>(p, w, qmap, kmap, vmap, smem_raw, bars, (int)blockIdx.x / C::GRP, C::UNITS, false);
 }
 
 // ------------------------------------------------------------------ join
@@ -157,9 +160,9 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
 // One warp per row: its parts and the shared prefix's.  Rows of the split tiles in the plan's table,
 // or with `dense` all rows of the call, whose own result the decode kernel left there.
 template <int D>
-__global__ void __launch_bounds__(256) join_kernel(AttnParams p, TilePlan w, DenseRows dense, PrefixParts pre, int tpt) {
+__global__ void __launch_bounds__(256) join_kernel(AttnParams p, TilePlan w, DenseRows dense, PrefixParts pre, int tpt, int tile_rows) {
   const int lane = threadIdx.x & 31;
-  const int G = p.hq / p.hkv, per_head = 2 * tpt * G;
+  const int G = p.hq / p.hkv, per_head = tile_rows / 128 * tpt * G;
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   const long long rows = dense.part ? (long long)p.tokens * p.hq : (long long)w.head[1] * p.hkv * per_head;
@@ -179,8 +182,8 @@ __global__ void __launch_bounds__(256) join_kernel(AttnParams p, TilePlan w, Den
       h = (int)(i / per_head % p.hkv);
       g = r % G;
       tok = s.tok0 + dt;
-      add_parts<D>(m, l, acc, w.ml, w.part, (long long)(s.slot + h) * kTileRows + dt / tpt * 128 + dt % tpt * G + g,
-                   (long long)p.hkv * kTileRows, s.parts, lane);
+      add_parts<D>(m, l, acc, w.ml, w.part, (long long)(s.slot + h) * tile_rows + dt / tpt * 128 + dt % tpt * G + g,
+                   (long long)p.hkv * tile_rows, s.parts, lane);
     }
     add_prefix<D>(m, l, acc, pre, tok, h, g, G, p.hkv, lane);
     emit_row<D>(p, tok, h * G + g, lane, m, l, acc);
@@ -221,20 +224,21 @@ size_t layout(TilePlan *own, TilePlan *pre, DenseRows *dense, char *ws, int num_
     at += up256(bytes);
     return r;
   };
-  constexpr int split_slots = Cfg<D>::SLOTS;
-  const int entries = z.max_tiles + split_slots;
-  const size_t own_slots = prefix_len > 0 ? (size_t)z.max_tiles * hkv + split_slots : split_slots;
+  // Tables for the narrow tiles, which are more; partial rows for the wide ones, which have no fewer.
+  constexpr int split_slots = Cfg<D, true>::SLOTS;
+  static_assert(split_slots * Cfg<D, true>::ROWS == Cfg<D>::SLOTS * Cfg<D>::ROWS, "rows");
+  const int narrow_tiles = tokens / z.tpt + num_seqs, entries = narrow_tiles + split_slots;
+  const size_t own_slots = prefix_len > 0 ? (size_t)z.max_tiles * hkv + Cfg<D>::SLOTS : Cfg<D>::SLOTS;
   const size_t slot = (size_t)kTileRows * sizeof(float);
   TilePlan a{}, b{};
   DenseRows c{};
   a.head = (int *)take(256);
   a.base = (int *)take(sizeof(int) * (size_t)(num_seqs + 1));
-  a.rec = (Entry *)take(sizeof(Entry) * (size_t)z.max_tiles);
+  a.rec = (Entry *)take(sizeof(Entry) * (size_t)narrow_tiles);
   a.entry = (Entry *)take(sizeof(Entry) * (size_t)entries);
-  a.split = (Split *)take(sizeof(Split) * (size_t)(prefix_len > 0 ? z.max_tiles : split_slots));
+  a.split = (Split *)take(sizeof(Split) * (size_t)(prefix_len > 0 ? narrow_tiles : split_slots));
   a.ml = (float *)take(own_slots * slot * 2);
   a.part = (float *)take(own_slots * slot * D);
-  a.max_tiles = z.max_tiles;
   a.max_entries = entries;
   if (prefix_len > 0) {
     b.uniform_parts = prefix_parts<D>(z.prefix_tiles, hkv, prefix_len);
@@ -254,6 +258,29 @@ size_t layout(TilePlan *own, TilePlan *pre, DenseRows *dense, char *ws, int num_
   return at;
 }
 
+// The sequences' own keys in tiles of configuration C: plan, tiles, join.
+template <class C>
+cudaError_t run_tiles(const AttnParams &p, TilePlan own, const PrefixParts &parts, int tpt, const CUtensorMap &q,
+                      unsigned int *errw, cudaStream_t stream) {
+  const int tt = tpt * (C::ROWS / 128);
+  own.err = errw;
+  own.max_tiles = p.tokens / tt + p.num_seqs;
+  own.units = C::UNITS;
+  own.slots = C::SLOTS;
+  CUtensorMap k, v;
+  cudaError_t err = cache_maps(&k, &v, p, C::KROWS);
+  if (err != cudaSuccess) return err;
+  const size_t smem = C::SMEM + 1024;
+  static std::atomic<uint64_t> allowed{0};
+  err = allow_smem(tile_kernel<C>, smem, allowed);
+  if (err == cudaSuccess)
+    err = launch_dependent(plan_kernel, 1, kPlanThreads, 0, stream, 1, p, own, tt);
+  if (err == cudaSuccess)
+    err = launch_dependent(tile_kernel<C>, C::UNITS * C::GRP, C::THREADS, smem, stream, C::GRP, p, own, q, k, v);
+  if (err != cudaSuccess) return err;
+  return launch_dependent(join_kernel<C::D>, 4 * kSms, 256, 0, stream, 1, p, own, DenseRows{}, parts, tpt, C::ROWS);
+}
+
 template <int D>
 cudaError_t run(const AttnParams &p, char *ws, unsigned int *errw, cudaStream_t stream) {
   // one token per sequence: the decode kernel does the sequences' own keys
@@ -265,34 +292,36 @@ cudaError_t run(const AttnParams &p, char *ws, unsigned int *errw, cudaStream_t 
   TilePlan own, pre;
   DenseRows dense;
   layout<D>(&own, &pre, &dense, tile_ws, p.num_seqs, p.tokens, p.hq, p.hkv, p.prefix_len);
-  own.err = pre.err = errw;
-  own.units = C::UNITS;
-  own.slots = C::SLOTS;
+  pre.err = errw;
   if (step) {  // the prefix and the sequences' own keys side by side, then their join
     pre.head = own.head;
     cudaError_t err = launch_attn_prefix(p, ws, pre, dense, errw, stream);
     if (err != cudaSuccess) return err;
     const PrefixParts parts{pre.ml, pre.part, pre.head, 0, z.tpt};
-    return launch_dependent(join_kernel<D>, 4 * kSms, 256, 0, stream, 1, p, own, dense, parts, z.tpt);
+    return launch_dependent(join_kernel<D>, 4 * kSms, 256, 0, stream, 1, p, own, dense, parts, z.tpt, C::ROWS);
   }
-  CUtensorMap q, k, v;
+  CUtensorMap q;
   cudaError_t err = q_map(&q, p, z.tpt);
-  if (err == cudaSuccess) err = cache_maps(&k, &v, p, C::KROWS);
-  if (err != cudaSuccess) return err;
-  const size_t smem = C::SMEM + 1024;
-  static std::atomic<uint64_t> allowed{0};
-  err = allow_smem(tile_kernel<D>, smem, allowed);
   if (err != cudaSuccess) return err;
   if (p.prefix_len > 0) {
-    err = launch_dependent(tile_kernel<D>, kSms, C::THREADS, smem, stream, C::GRP, p, pre, q, k, v);
+    CUtensorMap k, v;
+    err = cache_maps(&k, &v, p, C::KROWS);
+    const size_t smem = C::SMEM + 1024;
+    static std::atomic<uint64_t> allowed{0};
+    if (err == cudaSuccess) err = allow_smem(tile_kernel<C>, smem, allowed);
+    if (err == cudaSuccess)
+      err = launch_dependent(tile_kernel<C>, kSms, C::THREADS, smem, stream, C::GRP, p, pre, q, k, v);
     if (err != cudaSuccess) return err;
   }
-  PrefixParts parts{pre.ml, pre.part, nullptr, pre.uniform_parts, z.tpt};
-  err = launch_dependent(plan_kernel, 1, kPlanThreads, 0, stream, 1, p, own, z.tt);
-  if (err == cudaSuccess)
-    err = launch_dependent(tile_kernel<D>, kSms, C::THREADS, smem, stream, C::GRP, p, own, q, k, v);
-  if (err != cudaSuccess) return err;
-  return launch_dependent(join_kernel<D>, 4 * kSms, 256, 0, stream, 1, p, own, DenseRows{}, parts, z.tpt);
+  const PrefixParts parts{pre.ml, pre.part, nullptr, pre.uniform_parts, z.tpt};
+  // Narrow tiles where a sequence's rows fill half a wide one at most, as drafts' do: twice the tiles are
+  // under way, and starts and ends overlap (105 drafts of 9 to 18 tokens after 34, 32 heads of 128: 26 us,
+  // wide 40; 128 of 16 after 200 to 4000: 103 and 107).  At D = 256 two stages of 64 KB hold long contexts
+  // back (28 drafts after 367 to 1469 keys: 74 us, wide 63; 54 after 480: 58 and 66, after 900: 83 and 85).
+  if ((long long)p.tokens <= (long long)p.num_seqs * z.tpt &&
+      (D == 128 || (long long)p.max_pages * p.page_size <= 1024))
+    return run_tiles<Cfg<D, true>>(p, own, parts, z.tpt, q, errw, stream);
+  return run_tiles<C>(p, own, parts, z.tpt, q, errw, stream);
 }
 
 }  // namespace

@@ -20,13 +20,15 @@
 // alone had 64-key tiles, whose score products are bound by shared memory: 48 cycles for 32).
 // Two S buffers: the next tile's scores are computed while this one's softmax runs.
 // Both: 64 KB of Q and a ring of five 32 KB tiles in shared memory, loaded by TMA page by page.
+// Narrow tiles have one sub-tile and one CTA: D = 128 two CTAs to an SM, with half its tensor memory and
+// two 32 KB stages each; D = 256 two 64 KB stages and two S buffers.
 //
 // Warps: 4 per sub-tile for the softmax and the epilogue, one for the loads, one for the products.
 //
 // Bound by the tensor cores for prompts: 8192 tokens, 32 heads of 128 take 338 us (1625 TFLOP/s, 85%
 // of cuBLAS's rate; a step of 128 keys 2450 cycles against the products' 2048); 4096 tokens, 16
 // heads of 256 take 89 us (1540), with a gate 109 (the epilogue's sigmoids).  Drafts of 16 tokens on
-// contexts of 200 to 4000 are bound by HBM: 108 us, 5.1 TB/s with the plan.
+// contexts of 200 to 4000 are bound by HBM: 103 us, 5.3 TB/s with the plan.
 #pragma once
 
 #include <cuda.h>
@@ -40,22 +42,27 @@ namespace gdn {
 
 constexpr int kBN = 128;        // keys per tile
 
-template <int D_>
+template <int D_, bool NARROW = false>
 struct Cfg {
   static constexpr int D = D_;
-  static constexpr bool PAIR = D == 256;            // two CTAs share a tile, one sub-tile each
+  static constexpr bool PAIR = D == 256 && !NARROW;  // two CTAs share a tile, one sub-tile each
   static constexpr int GRP = PAIR ? 2 : 1;          // tcgen05 cta_group
-  static constexpr int SUBS = PAIR ? 1 : 2;         // sub-tiles of 128 rows in a CTA
-  static constexpr int NBUF = PAIR ? 2 : 1;         // S buffers of a sub-tile
-  static constexpr int STAGES = 5;
+  static constexpr int SUBS = PAIR || NARROW ? 1 : 2;  // sub-tiles of 128 rows in a CTA
+  static constexpr int ROWS = 128 * SUBS * GRP;     // of a tile
+  static constexpr int CTAS = NARROW && D == 128 ? 2 : 1;  // on an SM
+  static constexpr int NBUF = D == 256 ? 2 : 1;     // S buffers of a sub-tile
+  static constexpr int STAGES = NARROW ? 2 : 5;
   static constexpr int CH = D / 64;                 // 128-byte column chunks of a row of q or K
   static constexpr int KROWS = PAIR ? 64 : kBN;     // keys of a K tile in this CTA
   static constexpr int Q_BYTES = 128 * D * 2;       // one sub-tile
-  static constexpr int KV_BYTES = 32768;            // a CTA's part of a K or V tile
+  static constexpr int VCH = PAIR ? 2 : D / 64;     // 64-column chunks of a V tile in this CTA
+  static constexpr int KV_BYTES = VCH * 16384;      // a CTA's part of a K or V tile
+  static constexpr int O_COL = CTAS == 2 ? 128 : 256;  // tensor memory: S from column 0, O from here
+  static constexpr int COLS = CTAS == 2 ? 256 : 512;
   static constexpr int SMEM = SUBS * Q_BYTES + STAGES * KV_BYTES;
-  static constexpr int THREADS = PAIR ? 192 : 384;  // of the tile kernel (D = 128: two warps are idle)
+  static constexpr int THREADS = SUBS == 1 ? 192 : 384;  // of the tile kernel (384: two warps are idle)
   static constexpr int WIDE = 384;                  // of the kernel that shares the SMs with decode workers
-  static constexpr int UNITS = kSms / GRP;          // CTAs, or pairs of them
+  static constexpr int UNITS = kSms * CTAS / GRP;   // CTAs, or pairs of them
   static constexpr int SLOTS = 2 * UNITS;           // partial results of split tiles
 };
 
@@ -111,18 +118,18 @@ __device__ __forceinline__ void commit(uint64_t *bar) {
         : "memory");
   }
 }
-template <int GRP>
+template <int GRP, int COLS>
 __device__ __forceinline__ void tmem_alloc(uint32_t *slot) {
   if (GRP == 1) {
-    tc::alloc<512>(slot);
+    tc::alloc<COLS>(slot);
   } else {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;\n" ::"r"(smem_u32(slot)) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;\n" ::: "memory");
   }
 }
-template <int GRP>
+template <int GRP, int COLS>
 __device__ __forceinline__ void tmem_dealloc(uint32_t base) {
-  if (GRP == 1) tc::dealloc<512>(base);
+  if (GRP == 1) tc::dealloc<COLS>(base);
   else asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;\n" ::"r"(base) : "memory");
 }
 __device__ __forceinline__ void cluster_sync() {
@@ -191,11 +198,12 @@ __device__ __forceinline__ void transpose4(uint4 (&u)[4], int lane) {
   swap_units(u[1], u[3], lane & 2, 2);
 }
 
-// Rows of a V tile (two 64-column chunks of 128 rows) from `valid` on to zero, by one warp:
+// Rows of a V tile (CHUNKS chunks of 64 columns, 128 rows) from `valid` on to zero, by one warp:
 // they lie past the last key, and 0 * NaN is not 0.
+template <int CHUNKS>
 __device__ __forceinline__ void clear_rows(uint8_t *tile, int valid, int lane) {
-  for (int x = lane; x < (128 - valid) * 16; x += 32) {
-    const int r = valid + (x >> 4), y = x & 15;
+  for (int x = lane; x < (128 - valid) * (8 * CHUNKS); x += 32) {
+    const int r = valid + x / (8 * CHUNKS), y = x % (8 * CHUNKS);
     *reinterpret_cast<uint4 *>(tile + (y >> 3) * 16384 + r * 128 + (y & 7) * 16) = make_uint4(0, 0, 0, 0);
   }
   tc::fence_proxy_async();
@@ -349,16 +357,16 @@ __device__ __forceinline__ int sub_tiles(const Entry &e, int i, int tpt) {
 // The work of unit `unit` of `units` (a CTA, or a pair of them) by all of its threads.  `waited`: the
 // work before this kernel is known to be complete.  The warps are 4 SUBS for the softmax, LOADER that
 // loads and the next that issues the products.
-template <int D, int LOADER>
+template <class C, int LOADER>
 __device__ __forceinline__ void tile_role(const AttnParams &p, const TilePlan &w, const CUtensorMap &qmap,
                                           const CUtensorMap &kmap, const CUtensorMap &vmap, uint8_t *smem_raw,
                                           Barriers &bars, int unit, int units, bool waited) {
-  using C = Cfg<D>;
+  constexpr int D = C::D;
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   uint8_t *sq = smem, *skv = smem + C::SUBS * C::Q_BYTES;
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   volatile int *dead = &bars.dead;
-  const int G = p.hq / p.hkv, tpt = 128 / G, tt = tpt * 2;
+  const int G = p.hq / p.hkv, tpt = 128 / G, tt = tpt * (C::ROWS / 128);
   const int rank = C::PAIR ? (int)(blockIdx.x & 1) : 0;  // CTA of the pair
 
   if (threadIdx.x == 0) {
@@ -380,7 +388,7 @@ __device__ __forceinline__ void tile_role(const AttnParams &p, const TilePlan &w
       prefetch_map(&vmap);
     }
     __syncwarp();
-    tmem_alloc<C::GRP>(&bars.tmem);
+    tmem_alloc<C::GRP, C::COLS>(&bars.tmem);
   }
   tc::fence_before();
   __syncthreads();
@@ -407,7 +415,7 @@ __device__ __forceinline__ void tile_role(const AttnParams &p, const TilePlan &w
     const int row = threadIdx.x & 127;
     const float asl = p.scale == 0.f ? 1.f : fabsf(p.scale) * 1.4426950408889634f;
     const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
-    const uint32_t o_base = lanes + 256 + (C::PAIR ? 0 : sub * 128);
+    const uint32_t o_base = lanes + C::O_COL + (C::PAIR ? 0 : sub * 128);
     uint32_t cnt = 0;  // tiles of this sub-tile so far, over all items
     for (int round = 0; item_at(p, w, unit, units, round, tt, e, h); ++round) {
       // (a pair's sub-tiles run through the same tiles: one product is for both)
@@ -522,7 +530,7 @@ __device__ __forceinline__ void tile_role(const AttnParams &p, const TilePlan &w
 #pragma unroll
       for (int k = 0; k < 4; ++k) rowk[k] = __shfl_sync(0xffffffffu, orow, (lane & 28) + k);
       if (e.slot >= 0) {
-        const long long at = (long long)(e.slot + h) * kTileRows + sub * 128 + row;
+        const long long at = (long long)(e.slot + h) * C::ROWS + sub * 128 + row;
         if (live) *reinterpret_cast<float2 *>(w.ml + 2 * at) = make_float2(m, l);
         float *part = w.part + (at - unit4) * D + 4 * unit4;
         if (n > 0) settle();
@@ -668,7 +676,7 @@ __device__ __forceinline__ void tile_role(const AttnParams &p, const TilePlan &w
           const int pg = page_in(b), row = (key0 + b * box) & (p.page_size - 1);
           if (elect_one()) {
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
+            for (int c = 0; c < C::VCH; ++c) {
               const int x = (C::PAIR ? rank * 128 : 0) + c * 64;
               uint8_t *at = dst + c * (kBN * 128) + b * box * 128;
               if (tail) tma_4d(at, &vmap, x, row, head, pg, &bars.v_tail);
@@ -680,7 +688,7 @@ __device__ __forceinline__ void tile_role(const AttnParams &p, const TilePlan &w
         if (tail) {  // both CTAs clear their columns past the last key, then the products may start
           wait_bar(&bars.v_tail, tails & 1, dead, w.err);
           ++tails;
-          clear_rows(dst, left, lane);
+          clear_rows<C::VCH>(dst, left, lane);
           if (lane == 0) release_first(&bars.tail_ok[st]);
         }
         if (++st == C::STAGES) st = 0, ph ^= 1;
@@ -755,10 +763,10 @@ __device__ __forceinline__ void tile_role(const AttnParams &p, const TilePlan &w
             wait_bar(&bars.tail_ok[sv], tails >> sv & 1, dead, w.err);
             tails ^= 1u << sv;  // parity of each stage's own
           } else {
-            clear_rows(skv + sv * C::KV_BYTES, valid, lane);
+            clear_rows<C::VCH>(skv + sv * C::KV_BYTES, valid, lane);
           }
         }
-        if (C::NBUF == 1 && more) wait_bar(&bars.kv_full[sk], pk, dead, w.err);
+        if (C::SUBS == 2 && more) wait_bar(&bars.kv_full[sk], pk, dead, w.err);
 #pragma unroll
         for (int i = 0; i < C::SUBS; ++i) {
           if (j >= n[i]) continue;
@@ -773,12 +781,18 @@ __device__ __forceinline__ void tile_role(const AttnParams &p, const TilePlan &w
             if (elect_one()) {
 #pragma unroll
               for (int k = 4 * part; k < 4 * part + 4; ++k)
-                mma_ts<C::GRP>(tm + 256 + i * 128, pa + k * 8, b + (k * 2048 >> 4), id_pv, j > 0 || k > 0);
+                mma_ts<C::GRP>(tm + C::O_COL + i * 128, pa + k * 8, b + (k * 2048 >> 4), id_pv, j > 0 || k > 0);
               if (part) commit<C::GRP>(&bars.pv_done[buf]);
             }
             __syncwarp();
           }
-          if (C::NBUF == 1 && j + 1 < n[i]) qk(i, sk, c + 1);
+          if (C::NBUF == 1 && j + 1 < n[i]) {
+            if (C::SUBS == 1) {
+              wait_bar(&bars.kv_full[sk], pk, dead, w.err);
+              tc::fence_after();
+            }
+            qk(i, sk, c + 1);
+          }
         }
         done(&bars.kv_empty[sv]);
         if (C::NBUF == 1 && more) {
@@ -794,7 +808,7 @@ __device__ __forceinline__ void tile_role(const AttnParams &p, const TilePlan &w
   __syncthreads();
   if (C::PAIR) cluster_sync();  // no signal is on its way to a CTA that has gone
   tc::fence_after();
-  if (warp == LOADER) tmem_dealloc<C::GRP>(tmem);
+  if (warp == LOADER) tmem_dealloc<C::GRP, C::COLS>(tmem);
 }
 
 // A shared prefix beside the sequences' own keys, one token per sequence (attn_prefix.cu): the

@@ -170,6 +170,43 @@ def test_wide_groups(hq, hkv, prefix, d):
         _check(b, *_run(b))
 
 
+@pytest.mark.parametrize("gate", [False, True])
+@pytest.mark.parametrize("lens", [[5, 17, 128, 129, 700], [1024, 90], [1025, 90, 300]])
+@pytest.mark.parametrize("d", [128, 256])
+def test_drafts_around_the_narrow_bound(d, lens, gate):
+    """A few rows a sequence, contexts to both sides of what chooses the tiles' width."""
+    b = Batch([3, 5, 1, 8, 2][:len(lens)], lens, 12, 4, d, 16, gate=gate, seed=51)
+    _check(b, *_run(b))
+
+
+@pytest.mark.parametrize("t", [31, 32, 33, 65])
+@pytest.mark.parametrize("d", [128, 256])
+def test_rows_around_a_narrow_tile(t, d):
+    """Rows of one, and just more than one, sub-tile: mean rows a sequence of 124 to 260."""
+    b = Batch([t, t, t], [t, t + 1, t + 200], 8, 2, d, 32, gate=True, seed=52)
+    _check(b, *_run(b))
+
+
+@pytest.mark.parametrize("d,length", [(128, 9000), (256, 1000), (256, 9000)])
+def test_one_draft_split(d, length):
+    b = Batch([6], [length], 8, 2, d, 64, seed=53)
+    _check(b, *_run(b))
+
+
+@pytest.mark.parametrize("prefix", [70, 1500])
+@pytest.mark.parametrize("d", [128, 256])
+def test_prefix_drafts(prefix, d):
+    b = Batch([2, 9, 1, 4], [2, 40, 333, 129], 12, 4, d, 16, prefix=prefix, gate=True, seed=54)
+    _check(b, *_run(b))
+
+
+@pytest.mark.parametrize("d", [128, 256])
+def test_prompt_of_uneven_tiles(d):
+    """One prompt whose tiles would fill the machine unevenly, split or not."""
+    b = Batch([700], [703], 12, 4, d, 128, gate=True, seed=55)
+    _check(b, *_run(b))
+
+
 @pytest.mark.parametrize("seed", range(12))
 def test_drawn_shapes(seed):
     """Sizes drawn over the whole range of heads, pages, lengths and kinds of call."""
