@@ -410,23 +410,50 @@ __device__ __forceinline__ void step_role(const AttnParams &p, const StepPlan &w
       }
     }
     if (!whole) {
-      // the runs that the pair lies in: c owns tile x iff total c / ctas <= x < total (c + 1) / ctas
+      // The runs c0 .. c1 that the pair lies in (c owns tile x iff total c / ctas <= x < total (c + 1) / ctas).
+      // Many parts are joined in two levels, groups of `size` runs (the last takes the rest) and then the
+      // groups, whose sums replace their first run's: a part costs a row's join about 0.2 us, and one
+      // sequence of 66k keys with one kv-head has 304.  A counter per group, of a run that lies inside the
+      // pair, so that no other pair has it (a group has `size` runs at least); the pair's is c0's.
       const int c0 = (int)(((pair0 + 1) * ctas - 1) / total), c1 = (int)(((pair0 + k.tiles) * ctas - 1) / total);
-      __threadfence();
-      bar_sync(bar, nthr);
-      if (tid == 0) {
-        sh.last = atomicAdd(&w.arrived[c0], 1u) == (unsigned)(c1 - c0);
-        if (sh.last) w.arrived[c0] = 0;  // ready for the next call
-      }
-      bar_sync(bar, nthr);
-      if (sh.last) {
+      const int count = c1 - c0 + 1, size = count < 64 ? 8 : 16, groups = count < 16 ? 1 : count / size;
+      const int g = min((worker - c0) / size, groups - 1), first = c0 + g * size;
+      const int runs = g == groups - 1 ? count - g * size : size;
+      auto last_of = [&](unsigned int *arrived, int all) {  // all threads, after their writes
         __threadfence();
+        bar_sync(bar, nthr);
+        if (tid == 0) {
+          sh.last = atomicAdd(arrived, 1u) == (unsigned)(all - 1);
+          if (sh.last) *arrived = 0;  // ready for the next call
+        }
+        bar_sync(bar, nthr);
+        if (sh.last) __threadfence();
+        return sh.last != 0;
+      };
+      // (the run that began the pair has slot 2 c0 + 1, the others 2 c)
+      if (last_of(&w.arrived[groups > 1 ? first + 1 : c0], runs)) {
         for (int r = warp; r < G; r += C::WARPS) {
-          // the run that began the pair has slot 2 c0 + 1, the others 2 c
           float mm = -CUDART_INF_F, ll = 0.f, v[D / 32] = {};
-          add_parts<D>(mm, ll, v, w.ml, w.part, (2ll * c0 + 1) * 16 + r, 0, 1, lane);
-          add_parts<D>(mm, ll, v, w.ml, w.part, (2ll * c0 + 2) * 16 + r, 32, c1 - c0, lane);
-          emit(r, mm, ll, v);
+          const long long own = (2ll * first + (g == 0)) * 16 + r;
+          add_parts<D>(mm, ll, v, w.ml, w.part, own, 0, 1, lane);
+          add_parts<D>(mm, ll, v, w.ml, w.part, (2ll * first + 2) * 16 + r, 32, runs - 1, lane);
+          if (groups == 1) {
+            emit(r, mm, ll, v);
+          } else {
+            if (lane == 0) *reinterpret_cast<float2 *>(w.ml + 2 * own) = make_float2(mm, ll);
+#pragma unroll
+            for (int c = 0; c < D / 128; ++c)
+              *reinterpret_cast<float4 *>(w.part + own * D + 128 * c + 4 * lane) =
+                  make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+          }
+        }
+        if (groups > 1 && last_of(&w.arrived[c0], groups)) {
+          for (int r = warp; r < G; r += C::WARPS) {
+            float mm = -CUDART_INF_F, ll = 0.f, v[D / 32] = {};
+            add_parts<D>(mm, ll, v, w.ml, w.part, (2ll * c0 + 1) * 16 + r, 0, 1, lane);
+            add_parts<D>(mm, ll, v, w.ml, w.part, 2ll * (c0 + size) * 16 + r, 32 * size, groups - 1, lane);
+            emit(r, mm, ll, v);
+          }
         }
       }
     }
