@@ -13,8 +13,9 @@
 // columns (and repeats the scores: the shared memory they are read from has the bandwidth to spare).
 // One warp keeps a ring of K and V tiles full by TMA: 160 KB in flight per SM.
 //
-// 64 contexts of 255 to 8191 keys, 32 heads of 128 on 8: 169 us, 6.65 TB/s (98% of the copy rate).  Two
-// contexts of 90k to 131k keys, 16 heads of 256 on 2: 81 us, 5.5 TB/s with 8 us of start and join.
+// 64 contexts of 255 to 8191 keys, 32 heads of 128 on 8: 170 us, 6.65 TB/s (98% of the copy rate).  Two
+// contexts of 90k to 131k keys, 16 heads of 256 on 2: 79 us, 5.6 TB/s with 7 us of start and join.  One of
+// 66k, 4 heads of 128 on 1: 20 us (its floor is 5).
 #pragma once
 
 #include <cuda.h>
@@ -435,8 +436,8 @@ __device__ __forceinline__ void step_role(const AttnParams &p, const StepPlan &w
         for (int r = warp; r < G; r += C::WARPS) {
           float mm = -CUDART_INF_F, ll = 0.f, v[D / 32] = {};
           const long long own = (2ll * first + (g == 0)) * 16 + r;
-          add_parts<D>(mm, ll, v, w.ml, w.part, own, 0, 1, lane);
-          add_parts<D>(mm, ll, v, w.ml, w.part, (2ll * first + 2) * 16 + r, 32, runs - 1, lane);
+          add_parts<D, 8>(mm, ll, v, w.ml, w.part, own, 0, 1, lane);
+          add_parts<D, 8>(mm, ll, v, w.ml, w.part, (2ll * first + 2) * 16 + r, 32, runs - 1, lane);
           if (groups == 1) {
             emit(r, mm, ll, v);
           } else {
@@ -450,8 +451,8 @@ __device__ __forceinline__ void step_role(const AttnParams &p, const StepPlan &w
         if (groups > 1 && last_of(&w.arrived[c0], groups)) {
           for (int r = warp; r < G; r += C::WARPS) {
             float mm = -CUDART_INF_F, ll = 0.f, v[D / 32] = {};
-            add_parts<D>(mm, ll, v, w.ml, w.part, (2ll * c0 + 1) * 16 + r, 0, 1, lane);
-            add_parts<D>(mm, ll, v, w.ml, w.part, 2ll * (c0 + size) * 16 + r, 32 * size, groups - 1, lane);
+            add_parts<D, 8>(mm, ll, v, w.ml, w.part, (2ll * c0 + 1) * 16 + r, 0, 1, lane);
+            add_parts<D, 8>(mm, ll, v, w.ml, w.part, 2ll * (c0 + size) * 16 + r, 32 * size, groups - 1, lane);
             emit(r, mm, ll, v);
           }
         }

@@ -111,8 +111,10 @@ struct DenseRows {
 
 // Adds `count` parts of a row, at `at`, `at` + pitch, ..., to (m, l, acc) by one warp:
 //     M = max(m, max m_q),  l = sum 2^(m_q - M) l_q,  acc = sum 2^(m_q - M) O_q.
-// The statistics first, a part a lane, so that the sums' loads do not wait for one another.
-template <int D>
+// The statistics first, a part a lane, so that the sums' loads do not wait for one another
+// (AHEAD of them at a time; 8 for the decode kernel's one CTA, 30 us for 32, two contexts of 30k; the
+// join's many warps are slower with 8).
+template <int D, int AHEAD = 4>
 __device__ __forceinline__ void add_parts(float &m, float &l, float (&acc)[D / 32], const float *ml_of,
                                           const float *part_of, long long at, long long pitch, int count, int lane) {
   for (int q0 = 0; q0 < count; q0 += 32) {
@@ -129,7 +131,7 @@ __device__ __forceinline__ void add_parts(float &m, float &l, float (&acc)[D / 3
 #pragma unroll
     for (int k = 0; k < D / 32; ++k) acc[k] *= a;
     const int some = min(32, count - q0);
-#pragma unroll 4
+#pragma unroll (AHEAD)
     for (int q = 0; q < some; ++q) {  // (a part without keys holds zeros: its weight is 0)
       const float b = __shfl_sync(0xffffffffu, weight, q);
       const float *o = part_of + (at + (q0 + q) * pitch) * D + lane * 4;
