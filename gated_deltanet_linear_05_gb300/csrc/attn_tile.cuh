@@ -27,7 +27,7 @@
 //
 // Bound by the tensor cores for prompts: 8192 tokens, 32 heads of 128 take 338 us (1625 TFLOP/s, 85%
 // of cuBLAS's rate; a step of 128 keys 2450 cycles against the products' 2048); 4096 tokens, 16
-// heads of 256 take 89 us (1540), with a gate 109 (the epilogue's sigmoids).  Drafts of 16 tokens on
+// heads of 256 take 89 us (1540), with a gate 104 (the epilogue's sigmoids).  Drafts of 16 tokens on
 // contexts of 200 to 4000 are bound by HBM: 103 us, 5.3 TB/s with the plan.
 #pragma once
 
@@ -425,6 +425,11 @@ __device__ __forceinline__ void tile_role(const AttnParams &p, const TilePlan &w
       // keys this row sees, counted from the entry's first
       const int limit = (live ? visible(e.place0, dt + 1, e.kvlen) : 0) - e.kt0 * kBN;
       float m = -CUDART_INF_F, l = 0.f;
+      if (p.gate && live && e.slot < 0) {  // the epilogue's gate, into L2 meanwhile (4096 tokens: 112 -> 107 us)
+        const char *at = (const char *)((const __nv_bfloat16 *)p.gate + (e.tok0 + dt) * p.gs[0] + (h * G + row % G) * p.gs[1]);
+#pragma unroll
+        for (int c = 0; c < 2 * D; c += 128) asm volatile("prefetch.global.L2 [%0];\n" ::"l"(at + c));
+      }
       for (int j = 0; j < n; ++j, ++cnt) {
         const int b = C::NBUF == 2 ? (cnt & 1) : sub;
         const uint32_t s_addr = lanes + b * 128;
@@ -572,11 +577,16 @@ __device__ __forceinline__ void tile_role(const AttnParams &p, const TilePlan &w
         if (n > 0) settle();
         // A pair's loop stays rolled (16 heads of 256, 4096 tokens: 89 us, by two 91); the other is
         // unrolled by two (8192 tokens, 32 heads of 128: 338 us, rolled 346).
+        // With the registers for it (D = 256) the next columns' gate is fetched before these ones' sigmoids
+        // and not after (107 -> 104 us; D = 128: 353 -> 369).
         constexpr int kUnroll = C::PAIR ? 1 : 2;
+        constexpr bool kEarly = D == 256;
 #pragma unroll (kUnroll)
         for (int c = 0; c < D; c += 32) {
           uint32_t o[32];
           uint4 u[4];
+          uint4 next[4];
+          if (kEarly && p.gate && c + 32 < D) fetch(next, c + 32);
           read_o(o, o_base + c, n > 0);
           if (p.gate) transpose4(gate, lane);
 #pragma unroll
@@ -588,7 +598,9 @@ __device__ __forceinline__ void tile_role(const AttnParams &p, const TilePlan &w
             u[k] = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]),
                               pack_bf16(x[6], x[7]));
           }
-          if (p.gate && c + 32 < D) fetch(gate, c + 32);
+          if (!kEarly && p.gate && c + 32 < D) fetch(gate, c + 32);
+#pragma unroll
+          for (int k = 0; kEarly && k < 4; ++k) gate[k] = next[k];
           transpose4(u, lane);
 #pragma unroll
           for (int k = 0; k < 4; ++k)
