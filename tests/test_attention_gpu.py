@@ -75,6 +75,18 @@ def test_step_long_split(d):
     _check(b, *_run(b))
 
 
+@pytest.mark.parametrize("lens", [[20000], [3100], [1300], [900, 15000, 5], [7000, 7000]])
+@pytest.mark.parametrize("hq,d", [(4, 128), (16, 128), (5, 256)])
+def test_step_joins_of_many_parts(hq, d, lens):
+    """One kv-head: a context lies in up to all runs; the second call finds the counters ready."""
+    b = Batch([1] * len(lens), lens, hq, 1, d, 64, gate=True, seed=41)
+    ws = _workspace(b)
+    out, l = _run(b, workspace=ws)
+    _check(b, out, l)
+    again, l2 = _run(b, workspace=ws)
+    assert torch.equal(out, again) and torch.equal(l, l2)
+
+
 def test_step_many_sequences():
     """More sequences than CTAs, empty ones among them."""
     g = torch.Generator().manual_seed(4)
