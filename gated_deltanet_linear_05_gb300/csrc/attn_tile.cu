@@ -95,10 +95,11 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(AttnParams p, TilePl
     work = warp_sum(work);
     if (lane == 0) {
       const float items = (float)cnt * p.hkv, rounds = ceilf(items / w.units);
+      const float floats = (float)spl * p.tokens * p.hq * p.d / max(tiles, 1);  // of partial sums
+      const float join = spl > 0 ? 0.12f * parts_in(kvmax, chunk, inv) + 2.4e-6f * floats : 0.f;
       sh_cost[c] = c > 0 && (long long)spl * p.hkv > w.slots
                        ? CUDART_INF_F
-                       : fmaxf((float)chunk, rounds * (work * p.hkv / fmaxf(items, 1.f))) + 3.f * rounds +
-                             (spl > 0 ? 0.12f * parts_in(kvmax, chunk, inv) + 2.4e-6f * spl * ((float)p.tokens * p.hq * p.d / tiles) : 0.f);
+                       : fmaxf((float)chunk, rounds * (work * p.hkv / fmaxf(items, 1.f))) + 3.f * rounds + join;
     }
   }
   __syncthreads();
@@ -160,7 +161,8 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
 // One warp per row: its parts and the shared prefix's.  Rows of the split tiles in the plan's table,
 // or with `dense` all rows of the call, whose own result the decode kernel left there.
 template <int D>
-__global__ void __launch_bounds__(256) join_kernel(AttnParams p, TilePlan w, DenseRows dense, PrefixParts pre, int tpt, int tile_rows) {
+__global__ void __launch_bounds__(256)
+    join_kernel(AttnParams p, TilePlan w, DenseRows dense, PrefixParts pre, int tpt, int tile_rows) {
   const int lane = threadIdx.x & 31;
   const int G = p.hq / p.hkv, per_head = tile_rows / 128 * tpt * G;
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
