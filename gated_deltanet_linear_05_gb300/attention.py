@@ -2,9 +2,12 @@
 append to the paged cache, attention over the cache, and the same behind a shared prefix.
 
 Argument marshalling only, as in the package itself; include/gdn.h has the contract of each
-call.  The shape structs are kept by sizes and strides, so that a decode loop builds them
-once; a call whose combination has been seen goes through _marshal (csrc/marshal.c), which does
-the same checks in C and hands anything unusual back to the functions here.
+call.  A call that is given a stream runs with that stream current, so that what it allocates
+belongs to it: outputs come as if made under torch.cuda.stream(stream).
+
+The shape structs are kept by sizes and strides, so that a decode loop builds them once; a call
+whose combination has been seen goes through _marshal (csrc/marshal.c), which does the same
+checks in C and hands anything unusual back to the functions here.
 """
 from __future__ import annotations
 
@@ -141,12 +144,8 @@ def _output(device, t, like, what):
     return t
 
 
-def _stream(stream, device):
-    """The stream's handle: the current one of the device (a raw handle, as making a Stream
-    object costs as much as the rest of the marshalling), or the given Stream's."""
-    return _raw_stream(device) if stream is None else stream.cuda_stream
-
-
+# The device's current stream as a raw handle: making a Stream object costs as much as the rest of
+# the marshalling.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                       lambda device: torch.cuda.current_stream(device).cuda_stream)
 
@@ -226,14 +225,17 @@ def gdn_kv_append(q, k, v, k_cache, v_cache, page_table, kv_lens, inv_freq=None,
     included), cu_seqlens [N+1] int32 or None (one token per sequence); inv_freq [R/2] fp64
     or None (no rotation); positions [T] or [axes, T] int32 (None: prefix_len + place) with
     rope_axis [R/2] int32.  q_out None: a new tensor.  Returns q_out."""
-    if stream is None:
-        r = (_quick or _fast()).append(_made, q, k, v, k_cache, v_cache, page_table, kv_lens, inv_freq,
-                                       cu_seqlens, positions, rope_axis, q_norm, k_norm, eps, q_out,
-                                       prefix_len)
-        if type(r) is int:
-            raise GdnError(r, "gdn_kv_append")
-        if r is not None:
-            return r
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return gdn_kv_append(q, k, v, k_cache, v_cache, page_table, kv_lens, inv_freq, cu_seqlens,
+                                 positions, rope_axis, q_norm, k_norm, eps, q_out, prefix_len)
+    r = (_quick or _fast()).append(_made, q, k, v, k_cache, v_cache, page_table, kv_lens, inv_freq,
+                                   cu_seqlens, positions, rope_axis, q_norm, k_norm, eps, q_out,
+                                   prefix_len)
+    if type(r) is int:
+        raise GdnError(r, "gdn_kv_append")
+    if r is not None:
+        return r
     device = q.get_device()
     _check(device, (q, k, v, k_cache, v_cache),
            (page_table, kv_lens, cu_seqlens, positions, rope_axis))
@@ -261,7 +263,7 @@ def gdn_kv_append(q, k, v, k_cache, v_cache, page_table, kv_lens, inv_freq=None,
         None if positions is None else positions.data_ptr(),
         page_table.data_ptr(), kv_lens.data_ptr(),
         None if cu_seqlens is None else cu_seqlens.data_ptr(),
-        q_out.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), _stream(stream, device))
+        q_out.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), _raw_stream(device))
     if st != GDN_OK:
         raise GdnError(st, "gdn_kv_append")
     return q_out
@@ -285,7 +287,11 @@ def _attend_shape(q, k_cache, v_cache, prefix_table, prefix_len, page_table, kv_
 
 def _attend(name, q, k_cache, v_cache, prefix_table, prefix_len, page_table, kv_lens, cu_seqlens,
             gate, scale, o, lse, workspace, stream):
-    if stream is None and lse is None:
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return _attend(name, q, k_cache, v_cache, prefix_table, prefix_len, page_table, kv_lens,
+                           cu_seqlens, gate, scale, o, lse, workspace, None)
+    if lse is None:
         r = (_quick or _fast()).attend(_made, q, k_cache, v_cache, prefix_table, prefix_len, page_table,
                                        kv_lens, cu_seqlens, gate, scale, o, workspace)
         if type(r) is int:
@@ -312,7 +318,7 @@ def _attend(name, q, k_cache, v_cache, prefix_table, prefix_len, page_table, kv_
             v_cache.data_ptr(), page_table.data_ptr(), kv_lens.data_ptr(),
             None if cu_seqlens is None else cu_seqlens.data_ptr(), o.data_ptr(),
             None if lse is None else _float(device, lse, q.shape[:2], "lse"), workspace.data_ptr(),
-            workspace.nbytes, _stream(stream, device)]
+            workspace.nbytes, _raw_stream(device)]
     if prefix_table is None:
         st = lib().gdn_paged_attention(*args)
     else:
@@ -377,7 +383,10 @@ def gdn_add_rmsnorm(x, residual, weight, eps: float = 1e-6, residual_out=None, y
     type, returns (y, h); out "e4m3": y in float8_e4m3fn with fp32 scales per row (group 0) or
     per 128 columns (group 128), returns (y, scale, h).  x, residual bf16 or fp32; weight
     fp32.  residual_out may be residual or x."""
-    if residual_out is None and y is None and scale is None and stream is None:
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return gdn_add_rmsnorm(x, residual, weight, eps, residual_out, y, scale, out, group)
+    if residual_out is None and y is None and scale is None:
         r = (_quick or _fast()).norm(_made, x, residual, weight, eps, out, group)
         if type(r) is int:
             raise GdnError(r, "gdn_add_rmsnorm")
@@ -408,7 +417,7 @@ def gdn_add_rmsnorm(x, residual, weight, eps: float = 1e-6, residual_out=None, y
         else:
             sp = _float(device, scale, scales, "scale")
     st = lib().gdn_add_rmsnorm(rows, cols, code, xp, rp, _float(device, weight, x.shape[-1:], "weight"),
-                               eps, hp, y.data_ptr(), sp, group, _stream(stream, device))
+                               eps, hp, y.data_ptr(), sp, group, _raw_stream(device))
     if st != GDN_OK:
         raise GdnError(st, "gdn_add_rmsnorm")
     h = x if residual_out is None else residual_out

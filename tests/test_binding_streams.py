@@ -1,0 +1,92 @@
+"""What the torch binding allocates when a call is given a stream of its own, without a GPU: outputs
+and workspaces have to belong to that stream, or the allocator hands them to work that is not
+ordered with it, and the zeroes of a fresh workspace race the kernels."""
+import pytest
+import torch
+
+import gated_deltanet_linear_05_gb300 as gdn
+from gated_deltanet_linear_05_gb300 import build as gdn_build
+from pretend import Library, Stream, World, on
+
+SIDE = 777
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    gdn_build.build()
+
+
+@pytest.fixture
+def attention(monkeypatch):
+    """(attention.py over a recording library, the pretended machine)."""
+    import ctypes
+    from gated_deltanet_linear_05_gb300 import attention as A
+    real = gdn.lib()
+    world = World(monkeypatch, ctypes.sizeof(gdn.GdnAttnShape))
+    library = Library(world, real)
+    monkeypatch.setattr(A, "lib", lambda: library)
+    monkeypatch.setattr(A, "_raw_stream", lambda device: world.handle)
+    monkeypatch.setattr(A, "_quick", None)  # bound anew to the recording entry points
+    A._made.clear()
+    yield A, world
+    A._made.clear()
+
+
+def _batch(n=3, hq=4, hkv=2, d=128):
+    q = on(torch.zeros(n, hq, d, dtype=torch.bfloat16))
+    k, v = (on(torch.zeros(n, hkv, d, dtype=torch.bfloat16)) for _ in range(2))
+    kc, vc = (on(torch.zeros(8, hkv, 16, d, dtype=torch.bfloat16)) for _ in range(2))
+    table, lens = on(torch.zeros(n, 2, dtype=torch.int32)), on(torch.ones(n, dtype=torch.int32))
+    return q, k, v, kc, vc, table, lens
+
+
+@pytest.mark.parametrize("turn", [1, 2])  # unseen sizes, then seen ones
+@pytest.mark.parametrize("prefix", [False, True])
+def test_attention_on_a_stream(attention, prefix, turn):
+    A, world = attention
+    q, _, _, kc, vc, table, lens = _batch()
+    for _ in range(turn):
+        if prefix:
+            o = A.gdn_shared_prefix_attention(q, kc, vc, table[0].contiguous(), 20, table, lens, stream=Stream(SIDE))
+        else:
+            o = A.gdn_paged_attention(q, kc, vc, table, lens, stream=Stream(SIDE))
+    name, args = world.calls[-1]
+    assert args[-1] == SIDE and args[-5] == o.data_ptr()
+    assert world.made_at(o.data_ptr())[2] == SIDE
+    assert world.made_at(args[-3])[2] == SIDE  # the workspace
+
+
+@pytest.mark.parametrize("turn", [1, 2])
+def test_append_on_a_stream(attention, turn):
+    A, world = attention
+    q, k, v, kc, vc, table, lens = _batch()
+    for _ in range(turn):
+        out = A.gdn_kv_append(q, k, v, kc, vc, table, lens, stream=Stream(SIDE))
+    assert world.calls[-1][1][-1] == SIDE
+    assert world.made_at(out.data_ptr())[2] == SIDE
+
+
+@pytest.mark.parametrize("turn", [1, 2])
+@pytest.mark.parametrize("out,group", [("same", 0), ("e4m3", 128)])
+def test_norm_on_a_stream(attention, out, group, turn):
+    A, world = attention
+    x, w = on(torch.ones(3, 256)), on(torch.ones(256))
+    for _ in range(turn):
+        outputs = A.gdn_add_rmsnorm(x, x, w, out=out, group=group, stream=Stream(SIDE))
+    assert world.calls[-1][1][-1] == SIDE
+    for t in outputs:
+        assert world.made_at(t.data_ptr())[2] == SIDE
+
+
+def test_given_tensors_are_used(attention):
+    """With everything given nothing is allocated, on a stream of its own or not."""
+    A, world = attention
+    q, _, _, kc, vc, table, lens = _batch()
+    ws = A.gdn_attn_workspace(3, 3, 4, 2, 128)
+    o = on(torch.empty_like(q))
+    world.made.clear()
+    for stream in (Stream(SIDE), None):
+        assert A.gdn_paged_attention(q, kc, vc, table, lens, o=o, workspace=ws, stream=stream) is o
+        assert world.calls[-1][1][-1] == (SIDE if stream else 100)
+        assert world.calls[-1][1][-3] == ws.data_ptr()
+    assert not world.made
