@@ -13,6 +13,8 @@ S <- S + k_t (x) ((v_t - kv) beta_t); o_t = S^T q_t.
 from __future__ import annotations
 
 import ctypes
+import functools
+import inspect
 import os
 from typing import Optional
 
@@ -210,6 +212,21 @@ def _stream(stream) -> int:
     return s.cuda_stream
 
 
+def _on_its_stream(call):
+    """For calls that allocate: given a stream, the call runs with that stream current, so that
+    what it allocates belongs to it (outputs come as if made under torch.cuda.stream(stream))."""
+    at = list(inspect.signature(call).parameters).index("stream")
+
+    @functools.wraps(call)
+    def f(*args, **kw):
+        stream = args[at] if len(args) > at else kw.get("stream")
+        if stream is None:
+            return call(*args, **kw)
+        with _torch().cuda.stream(stream):
+            return call(*args, **kw)
+    return f
+
+
 def _workspace(shape: GdnShape, op: int, device, workspace):
     need = gdn_workspace_size(shape, op)
     if need == 0:
@@ -235,6 +252,7 @@ def _call(name, op, q, k, v, g, beta, state_in, state_out, cu_seqlens, o, chunk,
     return o, state_out
 
 
+@_on_its_stream
 def gdn_prefill_chunked(q, k, v, g, beta, state_in, state_out, cu_seqlens, o=None,
                         chunk: int = 64, workspace=None, stream=None, algo: int = GDN_ALGO_AUTO):
     """Chunkwise-parallel prompt pass.  Tensors as in include/gdn.h:
@@ -260,6 +278,7 @@ def split_segment_len(num_seqs: int, num_v_heads: int, tokens_per_seq: int, chun
     return -(-seg // chunk) * chunk
 
 
+@_on_its_stream
 def gdn_prefill_split(q, k, v, g, beta, state_in, state_out, cu_seqlens, o=None,
                       segment_len=None, chunk: int = 64, workspace=None, stream=None,
                       algo: int = GDN_ALGO_AUTO):
@@ -295,6 +314,7 @@ def gdn_prefill_split(q, k, v, g, beta, state_in, state_out, cu_seqlens, o=None,
     return o, state_out
 
 
+@_on_its_stream
 def gdn_verify_block(q, k, v, g, beta, state_in, state_out, cu_seqlens, o=None,
                      chunk: int = 16, workspace=None, stream=None, algo: int = GDN_ALGO_AUTO):
     """Draft-verify block from the snapshot state_in (left unchanged)."""
@@ -304,6 +324,7 @@ def gdn_verify_block(q, k, v, g, beta, state_in, state_out, cu_seqlens, o=None,
                  cu_seqlens, o, chunk, workspace, stream, algo)
 
 
+@_on_its_stream
 def gdn_decode_step(q, k, v, g, beta, state_in, state_out, cu_seqlens=None, o=None,
                     stream=None):
     """Token-by-token recurrence (cu_seqlens None: one token per sequence)."""
@@ -313,6 +334,7 @@ def gdn_decode_step(q, k, v, g, beta, state_in, state_out, cu_seqlens=None, o=No
                  cu_seqlens, o, 64, None, stream)
 
 
+@_on_its_stream
 def gdn_input_prologue(q_raw, k_raw, v_raw, a, b, conv_w, A_log, dt_bias, conv_state_in,
                        conv_state_out, cu_seqlens=None, eps: float = 1e-6, q=None, k=None, v=None,
                        g=None, beta=None, stream=None):
@@ -348,6 +370,7 @@ def gdn_input_prologue(q_raw, k_raw, v_raw, a, b, conv_w, A_log, dt_bias, conv_s
     return q, k, v, g, beta
 
 
+@_on_its_stream
 def gdn_gated_rmsnorm(o, z, weight, eps: float = 1e-6, y=None, stream=None):
     """Gated RMSNorm of each (token, v-head) row: o / sqrt(mean(o^2) + eps) * weight * SiLU(z).
     o [T, Hv, 128] (z's dtype, or fp32 with bf16 z); z [T, Hv, 128]; weight [128] fp32.
@@ -367,6 +390,7 @@ def gdn_gated_rmsnorm(o, z, weight, eps: float = 1e-6, y=None, stream=None):
     return y
 
 
+@_on_its_stream
 def gdn_decode_block_step(q_raw, k_raw, v_raw, a, b, conv_w, A_log, dt_bias, conv_state_in,
                           conv_state_out, state_in, state_out, z, norm_w, eps_qk: float = 1e-6,
                           eps_norm: float = 1e-6, y=None, o=None, workspace=None, stream=None):
@@ -401,6 +425,7 @@ def gdn_decode_block_step(q_raw, k_raw, v_raw, a, b, conv_w, A_log, dt_bias, con
     return y, state_out
 
 
+@_on_its_stream
 def gdn_verify_block_capture(q, k, v, g, beta, state_in, state_out, cu_seqlens, o=None,
                              delta=None, chunk: int = 16, stream=None, algo: int = GDN_ALGO_AUTO):
     """Draft-verify block (state_in left unchanged) that also writes each token's delta

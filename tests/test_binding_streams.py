@@ -90,3 +90,64 @@ def test_given_tensors_are_used(attention):
         assert world.calls[-1][1][-1] == (SIDE if stream else 100)
         assert world.calls[-1][1][-3] == ws.data_ptr()
     assert not world.made
+
+
+# ------------------------------------------------------------------ the delta-rule calls
+
+class Recorder:
+    """Entry points that record (name, arguments); the size queries are the real library's."""
+
+    def __init__(self, real):
+        self.real, self.calls = real, []
+
+    def __getattr__(self, name):
+        if "size" in name:
+            return getattr(self.real, name)
+        return lambda *args: self.calls.append((name, args)) or 0
+
+
+@pytest.fixture
+def layer(monkeypatch):
+    """(the recorder in the library's place, the pretended machine)."""
+    rec = Recorder(gdn.lib())
+    world = World(monkeypatch, 0)
+    monkeypatch.setattr(gdn, "lib", lambda: rec)
+    return rec, world
+
+
+def _layer_tensors(n=2, t=2, hk=2, hv=4):
+    bf, f = torch.bfloat16, torch.float32
+    z = lambda dtype, *shape: on(torch.zeros(*shape, dtype=dtype))  # noqa: E731
+    c = 128 * (2 * hk + hv)
+    return dict(q=z(bf, t, hk, 128), k=z(bf, t, hk, 128), v=z(bf, t, hv, 128), g=z(f, t, hv), beta=z(f, t, hv),
+                s=z(f, n, hv, 128, 128), cu=z(torch.int32, n + 1), conv_w=z(f, c, 4), A=z(f, hv), dt=z(f, hv),
+                conv=z(bf, n, 3, c), w=z(f, 128))
+
+
+LAYER = {
+    "prefill": lambda x, st: gdn.gdn_prefill_chunked(x["q"], x["k"], x["v"], x["g"], x["beta"], None, x["s"], x["cu"], stream=st),
+    "prefill, by position": lambda x, st: gdn.gdn_prefill_chunked(x["q"], x["k"], x["v"], x["g"], x["beta"], None, x["s"],
+                                                                  x["cu"], None, 64, None, st),
+    "split": lambda x, st: gdn.gdn_prefill_split(x["q"], x["k"], x["v"], x["g"], x["beta"], None, x["s"], x["cu"],
+                                                 segment_len=64, stream=st),
+    "verify": lambda x, st: gdn.gdn_verify_block(x["q"], x["k"], x["v"], x["g"], x["beta"], None, x["s"], x["cu"], stream=st),
+    "decode": lambda x, st: gdn.gdn_decode_step(x["q"], x["k"], x["v"], x["g"], x["beta"], None, x["s"], stream=st),
+    "prologue": lambda x, st: gdn.gdn_input_prologue(x["q"], x["k"], x["v"], x["g"], x["beta"], x["conv_w"], x["A"], x["dt"],
+                                                     None, x["conv"], stream=st),
+    "norm": lambda x, st: gdn.gdn_gated_rmsnorm(x["v"], x["v"], x["w"], stream=st),
+    "block step": lambda x, st: gdn.gdn_decode_block_step(x["q"], x["k"], x["v"], x["g"], x["beta"], x["conv_w"], x["A"],
+                                                          x["dt"], x["conv"], x["conv"], x["s"], x["s"], x["v"], x["w"], stream=st),
+    "capture": lambda x, st: gdn.gdn_verify_block_capture(x["q"], x["k"], x["v"], x["g"], x["beta"], None, x["s"], x["cu"], stream=st),
+}
+
+
+@pytest.mark.parametrize("call", LAYER)
+def test_delta_rule_calls_on_a_stream(layer, call):
+    rec, world = layer
+    x = _layer_tensors()
+    world.made.clear()
+    LAYER[call](x, Stream(SIDE))
+    assert rec.calls[-1][1][-1] == SIDE
+    assert world.made and all(handle == SIDE for _, _, _, handle in world.made), world.made
+    LAYER[call](x, None)
+    assert rec.calls[-1][1][-1] == 100

@@ -65,3 +65,25 @@ def test_append_and_norm_beside_a_busy_stream():
         assert torch.equal(_beside_a_busy_stream(append, [b.q.nbytes]), q)
         y2, scale2, h2 = _beside_a_busy_stream(norm, [x.nbytes, y.nbytes, scale.nbytes])
         assert torch.equal(y2.float(), y.float()) and torch.equal(scale2, scale) and torch.equal(h2, h)
+
+
+def test_decode_block_step_beside_a_busy_stream():
+    """The fused decode step without a workspace: its counters are zeroed on the call's own stream."""
+    import gated_deltanet_linear_05_gb300 as gdn
+    g = torch.Generator().manual_seed(63)
+    n, hk, hv = 6, 4, 8
+    c = 128 * (2 * hk + hv)
+    r = lambda dtype, *shape: torch.randn(*shape, generator=g).to(dtype).cuda()  # noqa: E731
+    bf, f = torch.bfloat16, torch.float32
+    q, k, v, z = (r(bf, n, h, 128) for h in (hk, hk, hv, hv))
+    a, b, w, conv = r(f, n, hv), r(f, n, hv), r(f, c, 4), r(bf, n, 3, c)
+    A, dt, state, norm = r(f, hv), r(f, hv), r(f, n, hv, 128, 128), r(f, 128)
+    conv_out, state_out = torch.empty_like(conv), torch.empty_like(state)
+    step = lambda stream: gdn.gdn_decode_block_step(  # noqa: E731
+        q, k, v, a, b, w, A, dt, conv, conv_out, state, state_out, z, norm, stream=stream)[0]
+    want = step(None).clone()
+    want_state = state_out.clone()
+    size = gdn.gdn_workspace_size(gdn.make_shape(n, n, hk, hv), gdn.GDN_OP_DECODE_BLOCK) + 256
+    for _ in range(3):
+        assert torch.equal(_beside_a_busy_stream(step, [size, z.nbytes]), want)
+        assert torch.equal(state_out, want_state)
