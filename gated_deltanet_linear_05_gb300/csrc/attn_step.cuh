@@ -390,7 +390,7 @@ __device__ __forceinline__ void step_role(const AttnParams &p, const StepPlan &w
     const bool whole = j0 == 0 && j1 == k.tiles;
     const long long slot = 2ll * worker + (j0 == 0);
     for (int r = warp; r < G; r += C::WARPS) {
-      const float mm = fmaxf(fmaxf(sh_m[0][r], sh_m[1][r]), fmaxf(sh_m[2][r], sh_m[3][r]));
+      const float mm = seen_max(fmaxf(fmaxf(sh_m[0][r], sh_m[1][r]), fmaxf(sh_m[2][r], sh_m[3][r])), len > 0);
       const float ll = (sh.l[0][r] + sh.l[1][r]) + (sh.l[2][r] + sh.l[3][r]);
       float v[D / 32];
 #pragma unroll

@@ -516,6 +516,7 @@ __device__ __forceinline__ void tile_role(const AttnParams &p, const TilePlan &w
         const float2 su = unpack2(add2(sum[0], sum[1]));
         l += su.x + su.y;
       }
+      m = seen_max(m, limit > 0);
       // epilogue
       auto settle = [&]() {  // the last P V
         if (C::NBUF == 2) {
@@ -556,8 +557,8 @@ __device__ __forceinline__ void tile_role(const AttnParams &p, const TilePlan &w
           }
         }
       } else {
-        if (live && p.lse) p.lse[orow] = l > 0.f ? (m + log2f(l)) * kLn2 : -CUDART_INF_F;
-        const float inv = l > 0.f ? 1.f / l : 0.f;
+        if (live && p.lse) p.lse[orow] = row_lse(m, l);
+        const float inv = row_inverse(m, l);
         const __nv_bfloat16 *gk[4];
         uint4 gate[4];
         if (p.gate) {

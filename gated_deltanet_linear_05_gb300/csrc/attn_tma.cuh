@@ -74,13 +74,27 @@ __device__ __forceinline__ float ex2(float x) {
   return r;
 }
 
+// A row's maximum m (base 2) and sum of powers l.  m is -inf only while the row has seen no key: one
+// that has, of scores that are all -inf (l = 0) or NaN (l = NaN), gets the lowest finite m.  So
+// "no key" (0, as the contract says) and 0 / 0 or NaN (which must not pass for it) stay apart, and a
+// row's result does not depend on how its keys were cut.
+__device__ __forceinline__ float seen_max(float m, bool saw_key) {
+  return m == -CUDART_INF_F && saw_key ? -3.402823466e38f : m;
+}
+__device__ __forceinline__ float row_inverse(float m, float l) {
+  return l != 0.f ? 1.f / l : m == -CUDART_INF_F ? 0.f : CUDART_NAN_F;
+}
+__device__ __forceinline__ float row_lse(float m, float l) {
+  return l == 0.f ? -CUDART_INF_F : (m + log2f(l)) * kLn2;
+}
+
 // A row (token, head) of the output by one warp: lane l has columns 128 k + 4 l .. + 3 of the
 // sum O (v[4 k ..]) with the maximum m (base 2) and the sum l.
 template <int D>
 __device__ __forceinline__ void emit_row(const AttnParams &p, int tok, int head, int lane, float m, float l,
                                          const float (&v)[D / 32]) {
   const long long row = (long long)tok * p.hq + head;
-  const float inv = l > 0.f ? 1.f / l : 0.f;
+  const float inv = row_inverse(m, l);
 #pragma unroll
   for (int k = 0; k < D / 128; ++k) {
     float x[4];
@@ -92,7 +106,7 @@ __device__ __forceinline__ void emit_row(const AttnParams &p, int tok, int head,
     *reinterpret_cast<uint2 *>((__nv_bfloat16 *)p.o + row * D + lane * 4 + 128 * k) =
         make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
   }
-  if (p.lse && lane == 0) p.lse[row] = l > 0.f ? (m + log2f(l)) * kLn2 : -CUDART_INF_F;
+  if (p.lse && lane == 0) p.lse[row] = row_lse(m, l);
 }
 
 // Partial results of a shared prefix, left by the tile kernel for every row of the call: tile t of
@@ -110,7 +124,8 @@ struct DenseRows {
 };
 
 // Adds `count` parts of a row, at `at`, `at` + pitch, ..., to (m, l, acc) by one warp:
-//     M = max(m, max m_q),  l = sum 2^(m_q - M) l_q,  acc = sum 2^(m_q - M) O_q.
+//     M = max(m, max m_q),  l = sum 2^(m_q - M) l_q,  acc = sum 2^(m_q - M) O_q
+// (m_q = -inf: no key, weight 0; a NaN in l_q reaches l whatever its weight).
 // The statistics first, a part a lane, so that the sums' loads do not wait for one another
 // (AHEAD of them at a time; 8 for the decode kernel's one CTA, 30 us for 32, two contexts of 30k; the
 // join's many warps are slower with 8).
@@ -120,7 +135,6 @@ __device__ __forceinline__ void add_parts(float &m, float &l, float (&acc)[D / 3
   for (int q0 = 0; q0 < count; q0 += 32) {
     float2 ml = make_float2(-CUDART_INF_F, 0.f);
     if (q0 + lane < count) ml = __ldcg(reinterpret_cast<const float2 *>(ml_of + 2 * (at + (q0 + lane) * pitch)));
-    if (!(ml.y > 0.f)) ml = make_float2(-CUDART_INF_F, 0.f);
     float top = ml.x;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));

@@ -445,7 +445,8 @@ size_t gdn_prefill_split_workspace_size(const gdn_shape *shape, int32_t segment_
  *     gate         [total_tokens, Hq, D]   bf16, with the strides of the shape
  *     o            [total_tokens, Hq, D]   bf16, contiguous
  *     lse          [total_tokens, Hq]      float32 or NULL: ln of each row's sum of
- *                                          exp(scores), -inf for a row that sees no key
+ *                                          exp(scores), -inf for a row that sees no key (NaN
+ *                                          for one with a score of NaN or +inf)
  *     k_cache, v_cache [num_pages, Hkv, page_size, D] bf16, page_stride elements from page
  *                                          to page (a page's heads contiguous)
  *     page_table   [num_seqs, max_pages]   int32: the pages of each sequence in order
@@ -511,7 +512,8 @@ gdn_status gdn_kv_append(const gdn_attn_shape *shape, const void *q, const void 
  * Attention of every token over its sequence's keys up to its own place:
  *     o = softmax(scale q K^T) V, and o <- o * sigmoid(gate) with a gate (not NULL).
  * Scores, softmax statistics and sums in float32, the probabilities rounded to bf16 for
- * their product with V (as V is held), o rounded once.  A row that sees no key is 0.
+ * their product with V (as V is held), o rounded once.  A row that sees no key is 0; one
+ * with a score of NaN or +inf, or whose scores are all -inf, is NaN.
  * o must not overlap q or gate (GDN_ERR_ALIAS).  shape->prefix_len must be 0.
  * workspace: gdn_attn_workspace_size(shape) bytes, 256-byte aligned, zero before the first
  * call that uses it; every call leaves it ready for the next.  Calls sharing a workspace must
