@@ -201,9 +201,18 @@ def _shape_of(q, v, o, state_out, cu_seqlens, chunk: int, algo: int = 0) -> GdnS
 
 
 def _check_tensors(*ts):
+    """Contiguous CUDA tensors of the current device: the library launches there."""
+    current = None
     for t in ts:
-        if t is not None and (not t.is_cuda or not t.is_contiguous()):
+        if t is None:
+            continue
+        if not t.is_cuda or not t.is_contiguous():
             raise ValueError("libgdn takes contiguous CUDA tensors")
+        if current is None:
+            current = _torch().cuda.current_device()
+        if t.get_device() != current:
+            raise ValueError("libgdn takes tensors of the current device (cuda:%d), got one of cuda:%d"
+                             % (current, t.get_device()))
 
 
 def _stream(stream) -> int:

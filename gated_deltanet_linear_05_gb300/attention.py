@@ -121,13 +121,22 @@ def _check(device, bf16, index):
                                   or not t.is_contiguous()):
                 break
         else:
-            if device >= 0:
+            if device >= 0 and device == _current_device():
                 return
     for t in bf16:
         if t.dtype is not _BF16:
             raise TypeError("q, k, v, gate and the caches must be bfloat16, got %s" % t.dtype)
+    if device >= 0:
+        _check_device(device)
     raise ValueError("the tensors must be CUDA tensors of one device, and those of indices contiguous "
                      "int32")
+
+
+def _check_device(device):
+    """The library launches on the current device."""
+    if device != _current_device():
+        raise ValueError("the tensors must be of the current device (cuda:%d), got cuda:%d"
+                         % (_current_device(), device))
 
 
 def _float(device, t, shape, what):
@@ -144,6 +153,7 @@ def _output(device, t, like, what):
     return t
 
 
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 # The device's current stream as a raw handle: making a Stream object costs as much as the rest of
 # the marshalling.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
@@ -186,7 +196,7 @@ def _fast():
             raise GdnUnavailable("_marshal.so not built (run gated_deltanet_linear_05_gb300/build.py): "
                                  "%s" % e)
         _marshal.bind(_BF16, _F32, torch.float64, _I32, torch.empty, torch.empty_like, _raw_stream,
-                      _DENSE, *(ctypes.cast(getattr(L, f), ctypes.c_void_p).value for f in
+                      _DENSE, _current_device, *(ctypes.cast(getattr(L, f), ctypes.c_void_p).value for f in
                                 ("gdn_paged_attention", "gdn_shared_prefix_attention", "gdn_kv_append",
                                  "gdn_add_rmsnorm")))
         _quick = _marshal
@@ -397,6 +407,7 @@ def gdn_add_rmsnorm(x, residual, weight, eps: float = 1e-6, residual_out=None, y
     rows, cols, code, kind, scales = _made.get(key) or _remember(key, _norm_plan(x, out, group))
     if device < 0:
         raise ValueError("x must be a CUDA tensor")
+    _check_device(device)
     xp = _alike(device, x, x)
     rp = None if residual is None else _alike(device, x, residual)
     if residual is not None and residual_out is None:

@@ -16,7 +16,7 @@
 
 static PyObject *n_shape, *n_stride, *n_dtype, *n_device, *n_get_device, *n_data_ptr, *n_is_contiguous, *n_nbytes;
 /* set by bind() */
-static PyObject *t_bf16, *t_f32, *t_f64, *t_i32, *f_empty, *f_empty_like, *f_stream, *dense_format;
+static PyObject *t_bf16, *t_f32, *t_f64, *t_i32, *f_empty, *f_empty_like, *f_stream, *dense_format, *f_current;
 static PyObject *kw_format, *kw_dtype, *kw_dtype_device;
 static gdn_status (*c_paged)(const gdn_attn_shape *, const void *, const void *, const void *, const void *,
                              const int32_t *, const int32_t *, const int32_t *, void *, float *, void *, size_t, void *);
@@ -69,12 +69,18 @@ static uintptr_t address(PyObject *t) {
   Py_DECREF(p);
   return (uintptr_t)v;
 }
+/* The tensor's device, which has to be the current one: the library launches there. */
 static int device_of(PyObject *t, long *device) {
   PyObject *d = PyObject_CallMethodNoArgs(t, n_get_device);
   if (!d) return -1;
   *device = PyLong_AsLong(d);
   Py_DECREF(d);
-  return PyErr_Occurred() ? -1 : *device >= 0;
+  if (PyErr_Occurred()) return -1;
+  if (*device < 0) return 0;
+  if (!(d = PyObject_CallNoArgs(f_current))) return -1;
+  const long current = PyLong_AsLong(d);
+  Py_DECREF(d);
+  return PyErr_Occurred() ? -1 : current == *device;
 }
 static int stream_of(long device, void **stream) {
   PyObject *n = PyLong_FromLong(device), *s = n ? PyObject_CallOneArg(f_stream, n) : NULL;
@@ -365,14 +371,14 @@ end:
 }
 
 /* bind(bfloat16, float32, float64, int32, empty, empty_like, raw_stream, contiguous_format,
- *      gdn_paged_attention, gdn_shared_prefix_attention, gdn_kv_append, gdn_add_rmsnorm) */
+ *      current_device, gdn_paged_attention, gdn_shared_prefix_attention, gdn_kv_append, gdn_add_rmsnorm) */
 static PyObject *bind(PyObject *self, PyObject *const *a, Py_ssize_t count) {
   (void)self;
-  if (count != 12) return PyErr_Format(PyExc_TypeError, "bind takes 12 arguments");
-  PyObject **to[8] = {&t_bf16, &t_f32, &t_f64, &t_i32, &f_empty, &f_empty_like, &f_stream, &dense_format};
-  for (int i = 0; i < 8; ++i) Py_XSETREF(*to[i], Py_NewRef(a[i]));
+  if (count != 13) return PyErr_Format(PyExc_TypeError, "bind takes 13 arguments");
+  PyObject **to[9] = {&t_bf16, &t_f32, &t_f64, &t_i32, &f_empty, &f_empty_like, &f_stream, &dense_format, &f_current};
+  for (int i = 0; i < 9; ++i) Py_XSETREF(*to[i], Py_NewRef(a[i]));
   uintptr_t f[4];
-  for (int i = 0; i < 4; ++i) f[i] = (uintptr_t)PyLong_AsUnsignedLongLong(a[8 + i]);
+  for (int i = 0; i < 4; ++i) f[i] = (uintptr_t)PyLong_AsUnsignedLongLong(a[9 + i]);
   if (PyErr_Occurred()) return NULL;
   *(uintptr_t *)&c_paged = f[0];
   *(uintptr_t *)&c_prefix = f[1];

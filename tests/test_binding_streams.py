@@ -1,6 +1,7 @@
-"""What the torch binding allocates when a call is given a stream of its own, without a GPU: outputs
-and workspaces have to belong to that stream, or the allocator hands them to work that is not
-ordered with it, and the zeroes of a fresh workspace race the kernels."""
+"""Streams and devices of the torch binding's calls, without a GPU.  What a call allocates when it is
+given a stream of its own has to belong to that stream, or the allocator hands it to work that is
+not ordered with it, and the zeroes of a fresh workspace race the kernels.  Tensors of another
+device than the current one are refused: the library launches on the current one."""
 import pytest
 import torch
 
@@ -26,6 +27,7 @@ def attention(monkeypatch):
     library = Library(world, real)
     monkeypatch.setattr(A, "lib", lambda: library)
     monkeypatch.setattr(A, "_raw_stream", lambda device: world.handle)
+    monkeypatch.setattr(A, "_current_device", lambda: world.device, raising=False)
     monkeypatch.setattr(A, "_quick", None)  # bound anew to the recording entry points
     A._made.clear()
     yield A, world
@@ -151,3 +153,61 @@ def test_delta_rule_calls_on_a_stream(layer, call):
     assert world.made and all(handle == SIDE for _, _, _, handle in world.made), world.made
     LAYER[call](x, None)
     assert rec.calls[-1][1][-1] == 100
+
+
+# ------------------------------------------------------------------ devices
+
+def _moved(tensors, index):
+    return [on(t, index) for t in tensors]
+
+
+def _calls(A, q, k, v, kc, vc, table, lens, x, w):
+    ws = on(torch.zeros(1 << 22, dtype=torch.uint8), q.get_device())
+    prefix = table[0].contiguous()
+    return {
+        "attention": lambda st: A.gdn_paged_attention(q, kc, vc, table, lens, workspace=ws, stream=st),
+        "prefix": lambda st: A.gdn_shared_prefix_attention(q, kc, vc, prefix, 20, table, lens, workspace=ws, stream=st),
+        "append": lambda st: A.gdn_kv_append(q, k, v, kc, vc, table, lens, stream=st),
+        "norm": lambda st: A.gdn_add_rmsnorm(x, x, w, out="e4m3", stream=st),
+    }
+
+
+@pytest.mark.parametrize("seen", [False, True])
+@pytest.mark.parametrize("call", ["attention", "prefix", "append", "norm"])
+def test_tensors_of_another_device(attention, call, seen):
+    """Refused, whether or not their sizes have been seen; a stream of their device makes it current."""
+    A, world = attention
+    tensors = _batch() + (on(torch.ones(3, 256)), on(torch.ones(256)))
+    here, there = _calls(A, *tensors), _calls(A, *_moved(tensors, 1))
+    if seen:
+        for _ in range(2):
+            here[call](None)
+    before = len(world.calls)
+    with pytest.raises(ValueError):
+        there[call](None)
+    with pytest.raises(ValueError):
+        here[call](Stream(SIDE, 1))
+    assert len(world.calls) == before
+    there[call](Stream(SIDE, 1))
+    assert len(world.calls) == before + 1 and world.calls[-1][1][-1] == SIDE
+    world.device = 1
+    there[call](None)
+    with pytest.raises(ValueError):
+        here[call](None)
+    assert len(world.calls) == before + 2
+
+
+@pytest.mark.parametrize("call", LAYER)
+def test_delta_rule_tensors_of_another_device(layer, call):
+    rec, world = layer
+    x = _layer_tensors()
+    there = {k: on(t, 1) for k, t in x.items()}
+    with pytest.raises(ValueError):
+        LAYER[call](there, None)
+    with pytest.raises(ValueError):
+        LAYER[call]({**x, "v": there["v"]}, None)
+    with pytest.raises(ValueError):
+        LAYER[call](x, Stream(SIDE, 1))
+    assert not rec.calls
+    LAYER[call](there, Stream(SIDE, 1))
+    assert rec.calls[-1][1][-1] == SIDE
