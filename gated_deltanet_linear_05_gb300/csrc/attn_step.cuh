@@ -87,8 +87,10 @@ __device__ __forceinline__ void step_role(const AttnParams &p, const StepPlan &w
   volatile int *dead = &sh.dead;
   if (tid == 0) {
     prefetch_map(&qmap);
-    prefetch_map(&kmap);
-    prefetch_map(&vmap);
+    if (p.num_pages > 0) {  // else there are no such maps
+      prefetch_map(&kmap);
+      prefetch_map(&vmap);
+    }
     for (int i = 0; i < C::STAGES; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], C::WARPS);
     for (int i = 0; i < 2; ++i) mbar_init(&q_full[i], 1), mbar_init(&q_empty[i], C::WARPS);
     mbar_fence_init();

@@ -384,8 +384,10 @@ __device__ __forceinline__ void tile_role(const AttnParams &p, const TilePlan &w
   if (warp == LOADER) {
     if (lane == 0) {
       prefetch_map(&qmap);
-      prefetch_map(&kmap);
-      prefetch_map(&vmap);
+      if (p.num_pages > 0) {  // else there are no such maps
+        prefetch_map(&kmap);
+        prefetch_map(&vmap);
+      }
     }
     __syncwarp();
     tmem_alloc<C::GRP, C::COLS>(&bars.tmem);

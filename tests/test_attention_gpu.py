@@ -325,6 +325,22 @@ def test_graph_and_stream(kind):
     _check(b, out, l)
 
 
+@pytest.mark.parametrize("d", [128, 256])
+@pytest.mark.parametrize("t", [[1, 1, 1], [4, 130, 1], [2, 2, 2]])
+def test_cache_without_pages(t, d):
+    """No page, so no key, whatever the lengths say: zeros and -inf; the append stores nothing."""
+    import gated_deltanet_linear_05_gb300 as gdn
+    b = Batch(t, [5, 200, 3], 4, 2, d, 16, gate=True, seed=28)
+    b.k_cache, b.v_cache = (torch.empty(0, 2, 16, d, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    k, v = (torch.ones(sum(t), 2, d, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    q = gdn.gdn_kv_append(b.q, k, v, b.k_cache, b.v_cache, b.page_table, b.kv_lens, cu_seqlens=b.cu)
+    for step in ([True, False] if t == [1, 1, 1] else [False]):
+        out, l = _run(b, step=step)
+        torch.cuda.synchronize()
+        assert torch.equal(q, b.q) and (out == 0).all() and (l == -float("inf")).all()
+    assert gdn.gdn_device_status() == 0
+
+
 def test_bad_pages_stay_with_their_sequence():
     """A table entry out of range spoils its own sequence only."""
     import gated_deltanet_linear_05_gb300 as gdn
