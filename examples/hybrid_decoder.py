@@ -102,7 +102,9 @@ class Model:
     def workspace(self, kind, batch, tokens, layer):
         """Kept from call to call; zeroed once, as the calls ask for."""
         n = batch.lens.numel()
-        key = (kind, n, tokens)
+        # what decides the size; a batch behind a prefix needs more than a plain one
+        key = (kind, n, tokens) + ((layer.hq, layer.hkv, layer.d, batch.shared > 0) if kind == "attention"
+                                   else (layer.hk, layer.hv))
         if key not in self.workspaces:
             if kind == "attention":
                 self.workspaces[key] = gdn.gdn_attn_workspace(n, tokens, layer.hq, layer.hkv, layer.d,

@@ -32,3 +32,11 @@ def test_served_batch_equals_whole_sequences(example, prompts, system):
     torch.cuda.synchronize()
     assert error < 0.1
     assert gdn.gdn_device_status() == 0
+
+
+def test_prompt_as_long_as_the_shared_prefix(example):
+    """Plain and prefixed batches of one size in turn: each with a workspace of its own."""
+    import torch
+    error = example.main(requests=1, system=33, prompts=(33,), steps=3)
+    torch.cuda.synchronize()
+    assert error < 0.1
