@@ -72,7 +72,7 @@ gdn_status attention(const gdn_attn_shape *s, const void *q, const void *gate, c
                      void *workspace, size_t workspace_bytes, void *stream) {
   gdn_status st = check_cache(s);
   if (st != GDN_OK) return st;
-  if (!isfinite(s->scale)) return GDN_ERR_INVALID_ARG;
+  if (!isfinite(s->scale * 1.4426950408889634f)) return GDN_ERR_INVALID_ARG;
   if ((st = check_stride(s->q_stride, s->head_dim)) != GDN_OK) return st;
   if (gate && (st = check_stride(s->gate_stride, s->head_dim)) != GDN_OK) return st;
   if ((st = check_tables(s, k_cache, v_cache, page_table, kv_lens, cu_seqlens)) != GDN_OK) return st;
@@ -99,7 +99,9 @@ gdn_status attention(const gdn_attn_shape *s, const void *q, const void *gate, c
   p.num_pages = s->num_pages;
   p.max_pages = s->num_pages > 0 ? s->max_pages : 0;  // no page: no key
   p.prefix_len = s->prefix_len;
-  p.scale = s->scale;
+  // The kernels multiply by scale * log2(e) with subnormals flushed: one would turn a masked -inf into
+  // NaN.  Below the normal range a scale counts as 0 (it would take a score of 2^100 to see it).
+  p.scale = fabsf(s->scale) < 1.17549435e-38f ? 0.f : s->scale;
   for (int i = 0; i < 2; ++i) p.qs[i] = s->q_stride[i], p.gs[i] = s->gate_stride[i];
   p.page_stride = s->page_stride;
   p.q = q;

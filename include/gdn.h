@@ -477,7 +477,8 @@ typedef struct {
                         /* 0 <= R <= D (gdn_kv_append)                                   */
   int32_t num_axes;     /* rows of positions, 1..8 (gdn_kv_append)                       */
   gdn_dtype dtype;      /* GDN_BF16                                                      */
-  float scale;          /* scores are scale * q.k (the attention calls); finite          */
+  float scale;          /* scores are scale * q.k (the attention calls); scale * log2(e) */
+                        /* finite in float32, a subnormal scale counts as 0              */
   /* element strides {token, head}; multiples of 8, each >= D                             */
   int64_t q_stride[2], k_stride[2], v_stride[2], gate_stride[2];
   int64_t page_stride;  /* >= Hkv * page_size * D, a multiple of 8                       */

@@ -115,6 +115,15 @@ def test_attention_other_refusals(L):
     assert _attend(L, _shape(n=2, tokens=0)) == OK
 
 
+def test_scale_past_float32(L):
+    """The kernels take scale * log2(e) in float32: its overflow is refused, not turned into NaN."""
+    for scale in (3e38, -3e38, 2.4e38):
+        assert _attend(L, _shape(scale=scale)) == INVALID
+        assert _attend(L, _shape(scale=scale, prefix_len=16), prefix=10 * A) == INVALID
+    for scale in (2.3e38, -2.3e38, 1e-44, 0.0):
+        assert _attend(L, _shape(scale=scale)) == OK
+
+
 @pytest.mark.parametrize("change,status", [
     (dict(q=None), INVALID), (dict(k=None), INVALID), (dict(v=None), INVALID), (dict(out=None), INVALID),
     (dict(kc=None), INVALID), (dict(vc=None), INVALID), (dict(freq=None), INVALID), (dict(freq=20 * A + 4), INVALID),

@@ -264,6 +264,15 @@ def test_scale_and_extreme_scores(step):
         assert ((l.cpu().double() - lse).abs() <= 2.0 ** -15 * (1 + lse.abs()) + err).all()
 
 
+@pytest.mark.parametrize("scale", [1e-39, -1e-39, 1e-44, 2.0 ** -126, -2.0 ** -126])
+@pytest.mark.parametrize("kind", ["step", "rows", "prefix"])
+def test_scales_at_the_end_of_float32(kind, scale):
+    """At and below the smallest normal number: the mean of the visible values."""
+    t = [7, 30, 1] if kind == "rows" else [1, 1, 1]
+    b = Batch(t, [9, 300, 130], 4, 2, 128, 16, prefix=50 if kind == "prefix" else 0, seed=26)
+    _check(b, *_run(b, step=kind != "rows", scale=scale), scale)
+
+
 def test_far_pages():
     """A cache whose pages lie past 2^31 elements."""
     import gated_deltanet_linear_05_gb300 as gdn
