@@ -212,7 +212,8 @@ template <int D>
 int prefix_parts(int tiles, int hkv, int prefix_len) {
   constexpr int units = Cfg<D>::UNITS;
   const int kt = (prefix_len + kBN - 1) / kBN;
-  const int fill = units / (int)(((long long)tiles * hkv < units) ? tiles * hkv : units);
+  const long long items = (long long)tiles * hkv;
+  const int fill = units / (int)(items < 1 ? 1 : items < units ? items : units);  // (no tokens: no tiles)
   const int most = (kt + 1) / 2;
   return fill < 1 ? 1 : fill < most ? fill : most;
 }

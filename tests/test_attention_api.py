@@ -115,6 +115,16 @@ def test_attention_other_refusals(L):
     assert _attend(L, _shape(n=2, tokens=0)) == OK
 
 
+def test_no_tokens_behind_a_prefix(L):
+    """Nothing to do, and a size all the same (tiles of the prefix's pass are divided by their number)."""
+    for n in (0, 2):
+        for d in (128, 256):
+            shape = _shape(n=n, tokens=0, d=d, prefix_len=40)
+            assert 0 < gdn.gdn_attn_workspace_size(shape) <= gdn.gdn_attn_workspace_size(
+                _shape(n=max(n, 1), tokens=1, d=d, prefix_len=40))
+            assert _attend(L, shape, prefix=10 * A) == OK
+
+
 def test_scale_past_float32(L):
     """The kernels take scale * log2(e) in float32: its overflow is refused, not turned into NaN."""
     for scale in (3e38, -3e38, 2.4e38):
