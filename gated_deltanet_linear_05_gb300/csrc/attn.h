@@ -43,6 +43,7 @@ struct AttnParams {
 };
 
 constexpr int kSms = 152;          // persistent CTAs, and the shares that work is cut into
+constexpr int kMostKeys = 0x7fffe000;  // that a row of an attention call may see
 constexpr int kStepRows = 16;      // query heads per kv-head that the decode kernel takes
 // Either attention call: picks the kernels and lays out the workspace (attn_tile.cu).
 size_t attn_workspace(int num_seqs, int tokens, int hq, int hkv, int d, int prefix_len);

@@ -72,6 +72,8 @@ gdn_status attention(const gdn_attn_shape *s, const void *q, const void *gate, c
                      void *workspace, size_t workspace_bytes, void *stream) {
   gdn_status st = check_cache(s);
   if (st != GDN_OK) return st;
+  // key tiles are counted, and boxes of them addressed, up to some thousand keys past the last in 32 bits
+  if ((long long)s->max_pages * s->page_size + s->prefix_len > gdn::kMostKeys) return GDN_ERR_UNSUPPORTED;
   if (!isfinite(s->scale * 1.4426950408889634f)) return GDN_ERR_INVALID_ARG;
   if ((st = check_stride(s->q_stride, s->head_dim)) != GDN_OK) return st;
   if (gate && (st = check_stride(s->gate_stride, s->head_dim)) != GDN_OK) return st;

@@ -263,7 +263,7 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 // One piece of work of a kv-head: tokens tok0 .. tok0 + ntok - 1 of a sequence against its
 // key tiles kt0 .. kt1 - 1.
 struct Entry {
-  int tok0, ntok, seq, place0;  // place0: place of tok0 (INT_MAX / 2: every key is seen)
+  int tok0, ntok, seq, place0;  // place0: place of tok0 (kMostKeys: every key is seen)
   int kt0, kt1, slot, kvlen;    // slot: partial result's (of kv-head 0, then Hkv apart), -1: final
 };
 struct Split {  // a tile whose parts are joined afterwards
@@ -330,7 +330,7 @@ __device__ __forceinline__ bool item_at(const AttnParams &p, const TilePlan &w, 
     e.tok0 = tile * tt;
     e.ntok = min(tt, p.tokens - e.tok0);
     e.seq = 0;
-    e.place0 = 0x3fffffff;
+    e.place0 = kMostKeys;
     e.kt0 = (int)((long long)kvt * q / w.uniform_parts);
     e.kt1 = (int)((long long)kvt * (q + 1) / w.uniform_parts);
     e.slot = at * p.hkv;

@@ -472,7 +472,8 @@ typedef struct {
   int32_t page_size;    /* tokens per page: 16, 32, 64 or 128                            */
   int32_t num_pages;    /* pages in the cache                                            */
   int32_t max_pages;    /* entries in a row of page_table                                */
-  int32_t prefix_len;   /* keys of the shared prefix; 0 without one                      */
+  int32_t prefix_len;   /* keys of the shared prefix; 0 without one.  For the attention  */
+                        /* calls max_pages * page_size + prefix_len <= 2^31 - 2^13       */
   int32_t rotary_dim;   /* R: the first R of D elements are rotated; a multiple of 16,   */
                         /* 0 <= R <= D (gdn_kv_append)                                   */
   int32_t num_axes;     /* rows of positions, 1..8 (gdn_kv_append)                       */

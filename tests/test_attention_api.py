@@ -125,6 +125,20 @@ def test_no_tokens_behind_a_prefix(L):
             assert _attend(L, shape, prefix=10 * A) == OK
 
 
+@pytest.mark.parametrize("page", [16, 32, 64, 128])
+def test_contexts_next_to_the_end_of_32_bits(L, page):
+    """Key tiles are counted in whole tiles past the last key: the last few thousand are refused."""
+    most, room = 0x7fffffff // page, 0x7fffe000 // page
+    assert _attend(L, _shape(page_size=page, max_pages=most)) == UNSUPPORTED
+    assert _attend(L, _shape(page_size=page, max_pages=room + 1)) == UNSUPPORTED
+    assert _attend(L, _shape(page_size=page, max_pages=room)) == OK
+    assert _attend(L, _shape(page_size=page, max_pages=room // 2, prefix_len=0x7fffe000 - room // 2 * page),
+                   prefix=10 * A) == OK
+    assert _attend(L, _shape(page_size=page, max_pages=room // 2, prefix_len=0x7fffe001 - room // 2 * page),
+                   prefix=10 * A) == UNSUPPORTED
+    assert _append(L, _shape(page_size=page, max_pages=most)) == OK
+
+
 def test_scale_past_float32(L):
     """The kernels take scale * log2(e) in float32: its overflow is refused, not turned into NaN."""
     for scale in (3e38, -3e38, 2.4e38):

@@ -273,6 +273,32 @@ def test_scales_at_the_end_of_float32(kind, scale):
     _check(b, *_run(b, step=kind != "rows", scale=scale), scale)
 
 
+@pytest.mark.parametrize("kind", ["step", "rows", "prefix step", "prefix rows"])
+def test_more_than_2_to_the_30_keys(kind):
+    """One page over and over, its scores 0, and at the end of the context 40 times one whose scores
+    are 60: the mean of that page's values."""
+    import gated_deltanet_linear_05_gb300 as gdn
+    g = torch.Generator().manual_seed(29)
+    keys = (1 << 30) + 128 * 50
+    k, v = torch.zeros(2, 1, 128, 128), torch.randn(2, 1, 128, 128, generator=g)
+    k[1] = 60 / 128 ** 0.5
+    k, v = k.bfloat16().cuda(), v.bfloat16().cuda()
+    far = torch.zeros(1, keys // 128, dtype=torch.int32, device="cuda")
+    far[:, -40:] = 1
+    q = torch.ones(1, 1, 128, dtype=torch.bfloat16, device="cuda")
+    cu = torch.tensor([0, 1], dtype=torch.int32, device="cuda") if "rows" in kind else None
+    lens = torch.tensor([0 if "prefix" in kind else keys], dtype=torch.int32, device="cuda")
+    if "prefix" in kind:
+        o = gdn.gdn_shared_prefix_attention(q, k, v, far[0], keys, far[:, :1].contiguous(), lens, cu)
+    else:
+        o = gdn.gdn_paged_attention(q, k, v, far, lens, cu)
+    torch.cuda.synchronize()
+    x = v[1, 0].double()
+    want, mean = x.mean(0), x.abs().mean(0)
+    assert ((o[0, 0].double() - want).abs() <= 2.0 ** -8 * (mean + want.abs()) + 2.0 ** -14 * mean).all()
+    assert gdn.gdn_device_status() == 0
+
+
 def test_far_pages():
     """A cache whose pages lie past 2^31 elements."""
     import gated_deltanet_linear_05_gb300 as gdn
