@@ -36,7 +36,9 @@ gdn_status check_shape(const gdn_attn_shape *s) {
   if (s->head_dim != 128 && s->head_dim != 256) return GDN_ERR_UNSUPPORTED;
   if (s->dtype != GDN_BF16) return GDN_ERR_UNSUPPORTED;
   if (s->num_q_heads / s->num_kv_heads > 128 || s->num_q_heads > 65535) return GDN_ERR_UNSUPPORTED;
+  // tables of tiles, at most one a token and one a sequence with some hundred parts beside them, and
   // rows and (sequence, head) pairs are counted in 32 bits
+  if ((long long)s->num_seqs + s->total_tokens > 0x7fffffffLL - 4096) return GDN_ERR_UNSUPPORTED;
   if ((long long)s->total_tokens * s->num_q_heads > 0x7fffffffLL ||
       (long long)s->num_seqs * s->num_q_heads > 0x7fffffffLL)
     return GDN_ERR_UNSUPPORTED;

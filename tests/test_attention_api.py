@@ -206,6 +206,16 @@ def test_workspace_size(L):
         gdn.gdn_attn_workspace_size(_shape(d=64))
 
 
+@pytest.mark.parametrize("n,tokens", [(0x7fffffff, 0), (0x7fffffff - 600, 0), (0x7ffffff0, 0x7ffffff0), (1 << 30, 1 << 30)])
+@pytest.mark.parametrize("prefix", [0, 5])
+def test_tables_past_32_bits(L, n, tokens, prefix):
+    """Tiles are counted in 32 bits: more sequences and tokens are refused, not given a short workspace."""
+    shape = _shape(n=n, tokens=tokens, hq=1, hkv=1, prefix_len=prefix)
+    assert L.gdn_attn_workspace_size(ctypes.byref(shape)) == ctypes.c_size_t(-1).value
+    assert _attend(L, shape, prefix=10 * A if prefix else None) == UNSUPPORTED
+    assert gdn.gdn_attn_workspace_size(_shape(n=1 << 30, tokens=0, hq=1, hkv=1, prefix_len=prefix)) > 36 << 30
+
+
 # ------------------------------------------------------------------ the binding's own checks
 
 def test_binding_refuses_before_the_library():
