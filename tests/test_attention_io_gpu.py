@@ -240,6 +240,27 @@ def test_norm_zero_rows_and_nan(group):
     assert torch.isfinite(y[3]).all() and (y[3] == 448).all()
 
 
+@pytest.mark.parametrize("group", [0, 128])
+def test_norm_codes_at_ties(group):
+    """y = the weights exactly (a row of ones, eps 0), over a scale of 3, 5 and 7: quotients that lie on a
+    tie between two codes go to the even one, and every other to the nearest."""
+    import gated_deltanet_linear_05_gb300 as gdn
+    ties = [17.0, 19.0, 21.0, 27.0, 34.0, 38.0, 46.0, 68.0, 92.0, 232.0, 424.0, 1.0625, 0.5625 + 2.0 ** -5]
+    for s in (3.0, 5.0, 7.0):
+        w = torch.zeros(512)
+        for at in range(0, 512, 128):
+            w[at] = 448 * s
+            w[at + 1:at + 14] = torch.tensor(ties) * s
+            w[at + 14:at + 27] = -torch.tensor(ties) * s
+            w[at + 27:at + 100] = torch.linspace(-400, 400, 73) * s
+        x = torch.ones(5, 512, dtype=torch.float32, device="cuda")
+        y8, scale, _ = gdn.gdn_add_rmsnorm(x, None, w.cuda(), 0.0, out="e4m3", group=group)
+        torch.cuda.synchronize()
+        assert (scale == s).all()
+        want = (w / s).to(torch.float8_e4m3fn).float()  # one float32 quotient, exact where it is a tie
+        assert torch.equal(y8.cpu().float(), want.expand(5, -1))
+
+
 def test_norm_rows_past_32_bits():
     """Rows whose elements lie past 2^31."""
     import gated_deltanet_linear_05_gb300 as gdn
