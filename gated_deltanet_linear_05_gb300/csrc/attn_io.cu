@@ -290,7 +290,7 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_kernel(AddNormParams p) {
         p.scale[(long long)blockIdx.x * (p.cols >> 7) + (c >> 7)] = scale;
     }
     if (c < p.cols) {
-      // y / scale by the reciprocal in two floats, q + less = (1 / scale)within 2^-46: rounded once, and exact
+      // y / scale by the reciprocal in two floats, q + less = 1 / scale within 2^-46: rounded once, and exact
       // where the quotient is, so that a tie between two codes stays one.  (q alone put codes next to a
       // tie off by one; by division the prompts' norm took 85 us for 76.  Of an infinite scale q is 0.)
       const float q = 1.f / scale, less = scale == CUDART_INF_F ? 0.f : fmaf(-scale, q, 1.f) * q;
