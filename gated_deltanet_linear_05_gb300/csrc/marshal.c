@@ -6,6 +6,8 @@
  * attention.py then checks again and says what is wrong.  Tensors are seen through their Python
  * attributes only.
  *
+ * The interpreter lock is let go around the library's call: a launch blocks while the stream's queue is full.
+ *
  * Results: None, an int (a libgdn status that is not GDN_OK), or what the call returns.
  */
 #define PY_SSIZE_T_CLEAN
@@ -201,9 +203,11 @@ static PyObject *attend(PyObject *self, PyObject *const *a, Py_ssize_t count) {
     Py_DECREF(out);
     return NULL;
   }
-  const gdn_status st = prefix == Py_None
-                            ? c_paged(&s, pq, pg, pk, pv, pt, pl, pc, po, NULL, pw, ws_bytes, stream)
-                            : c_prefix(&s, pq, pg, pk, pv, pp, pt, pl, pc, po, NULL, pw, ws_bytes, stream);
+  gdn_status st;
+  Py_BEGIN_ALLOW_THREADS
+  st = prefix == Py_None ? c_paged(&s, pq, pg, pk, pv, pt, pl, pc, po, NULL, pw, ws_bytes, stream)
+                         : c_prefix(&s, pq, pg, pk, pv, pp, pt, pl, pc, po, NULL, pw, ws_bytes, stream);
+  Py_END_ALLOW_THREADS
   if (st == GDN_OK) return out;
   Py_DECREF(out);
   return PyLong_FromLong(st);
@@ -276,7 +280,10 @@ static PyObject *append(PyObject *self, PyObject *const *a, Py_ssize_t count) {
     Py_DECREF(out);
     return NULL;
   }
-  const gdn_status st = c_append(&s, pq, pk, pv, pqn, pkn, (float)eps, pf, pa, pp, pt, pl, pc, po, pkc, pvc, stream);
+  gdn_status st;
+  Py_BEGIN_ALLOW_THREADS
+  st = c_append(&s, pq, pk, pv, pqn, pkn, (float)eps, pf, pa, pp, pt, pl, pc, po, pkc, pvc, stream);
+  Py_END_ALLOW_THREADS
   if (st == GDN_OK) return out;
   Py_DECREF(out);
   return PyLong_FromLong(st);
@@ -356,7 +363,10 @@ static PyObject *norm(PyObject *self, PyObject *const *a, Py_ssize_t count) {
     void *ph = h ? (void *)address(h) : NULL, *py = (void *)address(y);
     float *ps = scale ? (float *)address(scale) : NULL;
     if (PyErr_Occurred()) goto end;
-    const gdn_status st = c_norm(rows, cols, code, px, pr, pw, (float)eps, ph, py, ps, group, stream);
+    gdn_status st;
+    Py_BEGIN_ALLOW_THREADS
+    st = c_norm(rows, cols, code, px, pr, pw, (float)eps, ph, py, ps, group, stream);
+    Py_END_ALLOW_THREADS
     if (st != GDN_OK) result = PyLong_FromLong(st);
     else if (scale) result = PyTuple_Pack(3, y, scale, h ? h : x);
     else result = PyTuple_Pack(2, y, h ? h : x);

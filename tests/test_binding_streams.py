@@ -211,3 +211,57 @@ def test_delta_rule_tensors_of_another_device(layer, call):
     assert not rec.calls
     LAYER[call](there, Stream(SIDE, 1))
     assert rec.calls[-1][1][-1] == SIDE
+
+
+# ------------------------------------------------------------------ the interpreter lock
+
+@pytest.mark.parametrize("call", ["attention", "append", "norm"])
+def test_other_threads_run_while_a_launch_waits(attention, call):
+    """A launch blocks while the stream's queue is full: the interpreter lock is not held meanwhile (a
+    host function on the stream may need it).  The launch here is 0.4 s of sleep."""
+    import threading
+    import time
+    A, world = attention
+    tensors = _batch() + (on(torch.ones(3, 256)), on(torch.ones(256)))
+    calls = _calls(A, *tensors)
+    calls[call](None)  # sizes seen
+    # as the entry point: a C function that sleeps, whatever its arguments
+    sleep = _sleeper()
+    library = A.lib()
+    for name in ("gdn_paged_attention", "gdn_kv_append", "gdn_add_rmsnorm"):
+        setattr(library, name, getattr(sleep, name))
+    A._quick = None
+    count, stop = [0], threading.Event()
+
+    def work():
+        while not stop.is_set():
+            count[0] += 1
+            time.sleep(0.01)
+
+    t = threading.Thread(target=work)
+    t.start()
+    try:
+        time.sleep(0.05)
+        before = count[0]
+        calls[call](None)
+        after = count[0]
+    finally:
+        stop.set()
+        t.join()
+    assert after - before >= 5  # of about 40
+
+
+def _sleeper():
+    """A library whose entry points sleep 0.4 s and return GDN_OK."""
+    import ctypes
+    import os
+    import subprocess
+    import tempfile
+    with tempfile.TemporaryDirectory() as d:
+        src, so = os.path.join(d, "s.c"), os.path.join(d, "s.so")
+        with open(src, "w") as f:
+            f.write("#include <unistd.h>\n" + "".join(
+                "int %s() { usleep(400000); return 0; }\n" % n
+                for n in ("gdn_paged_attention", "gdn_kv_append", "gdn_add_rmsnorm")))
+        subprocess.run(["gcc", "-std=gnu11", "-shared", "-fPIC", src, "-o", so], check=True)
+        return ctypes.CDLL(so)
