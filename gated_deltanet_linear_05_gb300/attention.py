@@ -17,7 +17,7 @@ from typing import Optional
 
 import torch
 
-from . import (GDN_BF16, GDN_ERR_INVALID_ARG, GDN_F32, GDN_OK, GdnError, GdnUnavailable, lib)
+from . import GDN_BF16, GDN_ERR_INVALID_ARG, GDN_F32, GDN_OK, GdnError, lib
 
 I64x2 = ctypes.c_int64 * 2
 
@@ -185,16 +185,26 @@ def _remember(key, value):
 _quick = None
 
 
+class _Unbuilt:
+    """In _marshal's place: every call is left to the functions here."""
+    @staticmethod
+    def attend(*args):
+        return None
+
+    append = norm = attend
+
+
 def _fast():
-    """The marshalling module, bound to torch and to the library's entry points."""
+    """The marshalling module, bound to torch and to the library's entry points; where it has not
+    been built, a stand-in that has seen no call."""
     global _quick
     if _quick is None:
         L = lib()
         try:
             from . import _marshal
-        except ImportError as e:
-            raise GdnUnavailable("_marshal.so not built (run gated_deltanet_linear_05_gb300/build.py): "
-                                 "%s" % e)
+        except ImportError:
+            _quick = _Unbuilt
+            return _quick
         _marshal.bind(_BF16, _F32, torch.float64, _I32, torch.empty, torch.empty_like, _raw_stream,
                       _DENSE, _current_device, *(ctypes.cast(getattr(L, f), ctypes.c_void_p).value for f in
                                 ("gdn_paged_attention", "gdn_shared_prefix_attention", "gdn_kv_append",

@@ -1,5 +1,6 @@
 """Build libgdn.so in-tree for sm_103a with nvcc (one translation unit per kernel file,
-compiled in parallel, then linked), and the attention calls' marshalling module with gcc.
+compiled in parallel, then linked), and the attention calls' marshalling module with gcc
+(left out where Python's C headers are missing; attention.py does without it).
 No torch, no cmake."""
 from __future__ import annotations
 
@@ -74,9 +75,12 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
         run([nvcc()] + ARCH + ["-shared", "-o", tmp] + objs + ["-lcudart"])
         os.replace(tmp, LIB)
     src = os.path.join(CSRC, "marshal.c")
-    if force or _stale(MARSHAL, [src, os.path.join(ROOT, "include", "gdn.h")]):
+    python = sysconfig.get_paths()["include"]
+    if not os.path.exists(os.path.join(python, "Python.h")):
+        sys.stderr.write("no Python.h in %s: the attention calls' marshalling stays in Python\n" % python)
+    elif force or _stale(MARSHAL, [src, os.path.join(ROOT, "include", "gdn.h")]):
         tmp = MARSHAL + ".tmp%d" % os.getpid()
-        run(["gcc", "-O2", "-Wall", "-Wextra", "-fPIC", "-shared", "-I", sysconfig.get_paths()["include"],
+        run(["gcc", "-O2", "-Wall", "-Wextra", "-fPIC", "-shared", "-I", python,
              "-I", os.path.join(ROOT, "include"), src, "-o", tmp])
         os.replace(tmp, MARSHAL)
     return LIB

@@ -132,3 +132,40 @@ def test_references_stay():
     after = [sys.getrefcount(t) for t in held]
     assert all(abs(a - c) <= 2 for a, c in zip(before, after)), (before, after)
     assert torch.cuda.memory_allocated() <= memory + (1 << 16)
+
+
+# ------------------------------------------------------------------ without the module
+
+def test_calls_without_the_module(monkeypatch):
+    """The Python side does all that the module does: without it the calls work, a little slower."""
+    import ctypes
+    import torch
+    from pretend import Library, World, on
+    A = _attention()
+    world = World(monkeypatch, ctypes.sizeof(gdn.GdnAttnShape))
+    library = Library(world, gdn.lib())
+    for name, value in (("lib", lambda: library), ("_raw_stream", lambda d: world.handle), ("_current_device", lambda: 0),
+                        ("_quick", None)):
+        monkeypatch.setattr(A, name, value)
+    monkeypatch.setitem(sys.modules, "gated_deltanet_linear_05_gb300._marshal", None)
+    monkeypatch.delattr(gdn, "_marshal", raising=False)
+    x, w = on(torch.ones(3, 256)), on(torch.ones(256))
+    for _ in range(2):
+        y, scale, h = A.gdn_add_rmsnorm(x, x, w, out="e4m3")
+        assert world.calls[-1][1][7:10] == [h.data_ptr(), y.data_ptr(), scale.data_ptr()]
+    q = on(torch.zeros(2, 2, 128, dtype=torch.bfloat16))
+    c = on(torch.zeros(1, 2, 16, 128, dtype=torch.bfloat16))
+    i = on(torch.zeros(2, 1, dtype=torch.int32))
+    for _ in range(2):
+        assert A.gdn_kv_append(q, q, q, c, c, i, i[:, 0].contiguous()).data_ptr() == world.calls[-1][1][-4]
+        assert A.gdn_paged_attention(q, c, c, i, i[:, 0].contiguous()).data_ptr() == world.calls[-1][1][-5]
+    assert len(world.calls) == 6
+    A._made.clear()
+
+
+def test_build_without_python_headers(monkeypatch, tmp_path):
+    """The library is what a build has to make; the module is left out where Python.h is not there."""
+    monkeypatch.setattr(gdn_build.sysconfig, "get_paths", lambda: {"include": str(tmp_path)})
+    monkeypatch.setattr(gdn_build, "MARSHAL", str(tmp_path / "_marshal.so"))
+    assert gdn_build.build() == gdn_build.LIB
+    assert not (tmp_path / "_marshal.so").exists()
