@@ -20,6 +20,7 @@ import torch
 from . import GDN_BF16, GDN_ERR_INVALID_ARG, GDN_F32, GDN_OK, GdnError, lib
 
 I64x2 = ctypes.c_int64 * 2
+_COUNTER_BYTES = 2048  # GDN_ATTN_COUNTER_BYTES (include/gdn.h)
 
 
 class GdnAttnShape(ctypes.Structure):
@@ -72,12 +73,19 @@ def gdn_attn_workspace_size(shape: GdnAttnShape) -> int:
 
 def gdn_attn_workspace(num_seqs: int, total_tokens: int, num_q_heads: int, num_kv_heads: int,
                        head_dim: int, prefix_len: int = 0, device="cuda"):
-    """A zeroed workspace for the attention calls up to these sizes, to be kept and given to
-    every call (one per stream)."""
+    """A workspace for the attention calls up to these sizes, ready for the first, to be kept and
+    given to every call (one per stream)."""
     shape = make_attn_shape(num_seqs, total_tokens, num_q_heads, num_kv_heads, head_dim,
                             prefix_len=prefix_len)
-    # the caching allocator's blocks start on 512-byte boundaries
-    return torch.zeros(max(gdn_attn_workspace_size(shape), 1), dtype=torch.uint8, device=device)
+    return _new_workspace(shape, device)
+
+
+def _new_workspace(shape, device):
+    """Its counters zeroed; the rest may hold anything.  (The caching allocator's blocks start on
+    512-byte boundaries.)"""
+    ws = torch.empty(max(gdn_attn_workspace_size(shape), 1), dtype=torch.uint8, device=device)
+    ws[:_COUNTER_BYTES].zero_()
+    return ws
 
 
 def _strides3(t, what):
@@ -330,8 +338,7 @@ def _attend(name, q, k_cache, v_cache, prefix_table, prefix_len, page_table, kv_
     o = torch.empty_like(q, memory_format=_DENSE) if o is None \
         else _output(device, o, q, "o")
     if workspace is None:
-        workspace = torch.zeros(max(gdn_attn_workspace_size(made[0]), 1), dtype=torch.uint8,
-                                device=q.device)
+        workspace = _new_workspace(made[0], q.device)
     elif workspace.get_device() != device or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous CUDA tensor on the queries' device")
     args = [made[1], q.data_ptr(), None if gate is None else gate.data_ptr(), k_cache.data_ptr(),
@@ -355,8 +362,7 @@ def gdn_paged_attention(q, k_cache, v_cache, page_table, kv_lens, cu_seqlens=Non
     """Causal attention of q [T, Hq, D] over each sequence's keys in the paged cache, times
     sigmoid(gate) with a gate.  cu_seqlens None: one token per sequence.  scale None:
     1 / sqrt(D).  lse (fp32 [T, Hq], optional) receives ln of each row's sum of exp(scores).
-    workspace: from gdn_attn_workspace, kept by the caller (None: a fresh zeroed one per
-    call).  Returns o."""
+    workspace: from gdn_attn_workspace, kept by the caller (None: a fresh one per call).  Returns o."""
     return _attend("gdn_paged_attention", q, k_cache, v_cache, None, 0, page_table, kv_lens,
                    cu_seqlens, gate, scale, o, lse, workspace, stream)
 

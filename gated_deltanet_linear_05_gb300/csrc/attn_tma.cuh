@@ -16,7 +16,7 @@ namespace gdn {
 constexpr float kLn2 = 0.6931471805599453f;
 // Counters at the start of an attention workspace: zero before the first call and after
 // every one, at the same place for all shapes.
-constexpr size_t kArrivedBytes = 2048;
+constexpr size_t kArrivedBytes = GDN_ATTN_COUNTER_BYTES;
 
 __host__ __device__ inline size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 

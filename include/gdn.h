@@ -510,6 +510,8 @@ gdn_status gdn_kv_append(const gdn_attn_shape *shape, const void *q, const void 
                          const int32_t *kv_lens, const int32_t *cu_seqlens, void *q_out,
                          void *k_cache, void *v_cache, void *stream);
 
+#define GDN_ATTN_COUNTER_BYTES 2048 /* at the start of an attention workspace */
+
 /*
  * Attention of every token over its sequence's keys up to its own place:
  *     o = softmax(scale q K^T) V, and o <- o * sigmoid(gate) with a gate (not NULL).
@@ -517,8 +519,9 @@ gdn_status gdn_kv_append(const gdn_attn_shape *shape, const void *q, const void 
  * their product with V (as V is held), o rounded once.  A row that sees no key is 0; one
  * with a score of NaN or +inf, or whose scores are all -inf, is NaN.
  * o must not overlap q or gate (GDN_ERR_ALIAS).  shape->prefix_len must be 0.
- * workspace: gdn_attn_workspace_size(shape) bytes, 256-byte aligned, zero before the first
- * call that uses it; every call leaves it ready for the next.  Calls sharing a workspace must
+ * workspace: gdn_attn_workspace_size(shape) bytes, 256-byte aligned, the first
+ * GDN_ATTN_COUNTER_BYTES of them zero before the first call that uses it (the rest may hold
+ * anything); every call leaves it ready for the next.  Calls sharing a workspace must
  * not overlap on the GPU.  The results do not depend on the order of execution.
  */
 gdn_status gdn_paged_attention(const gdn_attn_shape *shape, const void *q, const void *gate,

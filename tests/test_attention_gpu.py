@@ -336,6 +336,17 @@ def test_workspace_is_left_ready_and_results_repeat():
             assert torch.equal(o, o2) and torch.equal(l, l2)
 
 
+@pytest.mark.parametrize("t,lens,prefix", [([1, 1, 1], [9000, 70, 0], 0), ([20, 3, 1], [6000, 70, 9], 0),
+                                           ([1, 1, 1], [50, 7, 900], 2000), ([20, 3, 1], [60, 7, 900], 2000)])
+@pytest.mark.parametrize("d", [128, 256])
+def test_workspace_beyond_its_counters_may_hold_anything(d, t, lens, prefix):
+    b = Batch(t, lens, 8, 2, d, 64, prefix=prefix, gate=True, seed=30)
+    ws = _workspace(b)
+    for poison in (0, 255, 127):
+        ws[2048:] = poison
+        _check(b, *_run(b, workspace=ws))
+
+
 @pytest.mark.parametrize("kind", ["step", "rows", "prefix"])
 def test_graph_and_stream(kind):
     """Captured on a side stream and replayed on new values of the same tensors."""

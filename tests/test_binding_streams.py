@@ -94,6 +94,26 @@ def test_given_tensors_are_used(attention):
     assert not world.made
 
 
+@pytest.mark.parametrize("prefix", [False, True])
+def test_fresh_workspaces_zero_their_counters_alone(attention, prefix):
+    """A gigabyte of partial results need not be zeroed at every call that brings no workspace."""
+    A, world = attention
+    n = 1024
+    q = on(torch.zeros(n, 32, 128, dtype=torch.bfloat16))
+    kc, vc = (on(torch.zeros(2, 8, 16, 128, dtype=torch.bfloat16)) for _ in range(2))
+    table, lens = on(torch.zeros(n, 1, dtype=torch.int32)), on(torch.ones(n, dtype=torch.int32))
+    world.made.clear()
+    if prefix:
+        A.gdn_shared_prefix_attention(q, kc, vc, table[0].contiguous(), 5, table, lens)
+    else:
+        A.gdn_paged_attention(q, kc, vc, table, lens)
+    ws = A.gdn_attn_workspace(n, n, 32, 8, 128, prefix_len=5 if prefix else 0)
+    assert (ws[:2048] == 0).all()
+    name, size, _ = world.made_at(world.calls[-1][1][-3])
+    assert size == ws.nbytes
+    assert all(name != "zeros" or size <= 2048 for name, _, size, _ in world.made)
+
+
 # ------------------------------------------------------------------ the delta-rule calls
 
 class Recorder:
