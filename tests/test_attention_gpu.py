@@ -246,6 +246,46 @@ def test_strides(step, prefix):
     _check(b, *_run(b, step=step))
 
 
+def _head_major(x):
+    return None if x is None else x.transpose(0, 1).contiguous().transpose(0, 1)
+
+
+@pytest.mark.parametrize("d", [128, 256])
+@pytest.mark.parametrize("step", [False, True])
+@pytest.mark.parametrize("prefix", [0, 100])
+def test_head_major(prefix, step, d):
+    """A token stride below the head stride, in q and gate together or in one of them."""
+    t = [1] * 5 if step else [3, 20, 1, 140]
+    b = Batch(t, [30, 64, 1, 299, 7][:len(t)], 6, 2, d, 16, prefix=prefix, gate=True, seed=31)
+    q, gate = b.q, b.gate
+    for both in ((_head_major(q), gate), (q, _head_major(gate)), (_head_major(q), _head_major(gate))):
+        b.q, b.gate = both
+        _check(b, *_run(b, step=step))
+
+
+@pytest.mark.parametrize("d", [128, 256])
+@pytest.mark.parametrize("prefix", [0, 70])
+@pytest.mark.parametrize("kind", ["step", "drafts", "prompts"])
+@pytest.mark.parametrize("gate", [False, True])
+def test_calls_as_users_make_them(gate, kind, prefix, d):
+    """No log-sum-exp, a new output, sizes that have been seen: the way through the marshalling module,
+    with other values of the same sizes each time."""
+    import gated_deltanet_linear_05_gb300 as gdn
+    t = {"step": [1] * 4, "drafts": [3, 7, 1, 5], "prompts": [200, 1, 90]}[kind]
+    lens = [200, 64, 99, 300][:len(t)]
+    ws = None
+    for seed in (32, 33, 34):
+        b = Batch(t, lens, 8, 2, d, 32, prefix=prefix, gate=gate, seed=seed)
+        ws = _workspace(b) if ws is None else ws
+        args = (b.page_table, b.kv_lens, None if kind == "step" else b.cu)
+        if prefix:
+            out = gdn.gdn_shared_prefix_attention(b.q, b.k_cache, b.v_cache, b.prefix_table, prefix, *args,
+                                                  gate=b.gate, workspace=ws)
+        else:
+            out = gdn.gdn_paged_attention(b.q, b.k_cache, b.v_cache, *args, gate=b.gate, workspace=ws)
+        _check(b, out)
+
+
 @pytest.mark.parametrize("step", [False, True])
 def test_scale_and_extreme_scores(step):
     """Scores of +-1000: the running maximum carries them; a negative and a zero scale."""

@@ -130,6 +130,34 @@ def test_append_step(n):
                          contiguous=True))
 
 
+@pytest.mark.parametrize("d", [128, 256])
+def test_append_head_major(d):
+    """Token strides below the head strides give the bits of contiguous rows."""
+    import gated_deltanet_linear_05_gb300 as gdn
+    g = torch.Generator().manual_seed(81)
+    q, k, v = (_bf16(46, h, d, g=g).cuda() for h in (6, 2, 2))
+    table = torch.arange(24, dtype=torch.int32).view(4, 6).cuda()
+    lens, cu = (torch.tensor(x, dtype=torch.int32).cuda() for x in ([5, 17, 3, 90], [0, 5, 6, 6, 46]))
+    freq, w = torch.linspace(1e-4, 1, 32, dtype=torch.float64).cuda(), 1 + 0.1 * torch.arange(d).cuda() / d
+    got = []
+    for rows in ((q, k, v), [x.transpose(0, 1).contiguous().transpose(0, 1) for x in (q, k, v)]):
+        kc, vc = (torch.zeros(24, 2, 16, d, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        got.append((gdn.gdn_kv_append(*rows, kc, vc, table, lens, freq, cu, q_norm=w, k_norm=w), kc, vc))
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(*got)) and got[0][1].any()
+
+
+@pytest.mark.parametrize("axes", [0, 3])
+@pytest.mark.parametrize("norm", [False, True])
+@pytest.mark.parametrize("step", [False, True])
+def test_append_of_seen_sizes(step, norm, axes):
+    """Other values of the same sizes each time: the way through the marshalling module."""
+    t, lens = ([1] * 4, [5, 17, 3, 90]) if step else ([5, 1, 3, 40], [5, 17, 3, 90])
+    for seed in (82, 83, 84):
+        _within(_append_case(t, lens, 6, 2, 128, 16, 64, axes, norm, fused=True, seed=seed, prefix=9,
+                             contiguous=step))
+
+
 def test_append_rows_without_a_place():
     """More tokens than keys: the first tokens are rotated for q but not stored; a sequence of
     no keys stores nothing."""
