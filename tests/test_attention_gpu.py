@@ -142,6 +142,31 @@ def test_rows_many_sequences():
     _check(b, *_run(b, step=False))
 
 
+def _check_many(b, out, l):
+    """_check with the caches brought over once, not once a sequence."""
+    b.k_cache, b.v_cache = (c.cpu().double() for c in (b.k_cache, b.v_cache))
+    _check(b, out, l)
+
+
+@pytest.mark.parametrize("prefix", [0, 20])
+def test_rows_more_tiles_than_the_plan_keeps(prefix):
+    """Several chunks of sequences in the plan and tiles past those whose lengths it keeps at hand;
+    long sequences, whose tiles all threads write, in the first chunk and after it."""
+    g = torch.Generator().manual_seed(35)
+    t = torch.randint(0, 4, (4600,), generator=g).tolist()
+    t[7], t[1300], t[4599] = 700, 400, 333
+    lens = [x + int(torch.randint(0, 9, (1,), generator=g)) for x in t]
+    b = Batch(t, lens, 4, 2, 128, 16, prefix=prefix, seed=35)
+    _check_many(b, *_run(b, step=False))
+
+
+@pytest.mark.parametrize("d,n", [(128, 5000), (256, 2700)])
+def test_prefix_more_row_tiles_than_units(d, n):
+    """One query head a kv-head: more (row tile, kv-head) pairs of the prefix than units, so one part each."""
+    b = Batch([1] * n, [i % 5 for i in range(n)], 8, 8, d, 16, prefix=130, gate=True, seed=36)
+    _check_many(b, *_run(b))
+
+
 @pytest.mark.parametrize("d", [128, 256])
 @pytest.mark.parametrize("hq,hkv", [(1, 1), (4, 4), (6, 2), (16, 1), (24, 1)])
 @pytest.mark.parametrize("prefix", [1, 64, 300])
