@@ -518,7 +518,6 @@ __device__ __forceinline__ void tile_role(const AttnParams &p, const TilePlan &w
         const float2 su = unpack2(add2(sum[0], sum[1]));
         l += su.x + su.y;
       }
-      m = seen_max(m, limit > 0);
       // epilogue
       auto settle = [&]() {  // the last P V
         if (C::NBUF == 2) {
@@ -539,7 +538,7 @@ __device__ __forceinline__ void tile_role(const AttnParams &p, const TilePlan &w
       for (int k = 0; k < 4; ++k) rowk[k] = __shfl_sync(0xffffffffu, orow, (lane & 28) + k);
       if (e.slot >= 0) {
         const long long at = (long long)(e.slot + h) * C::ROWS + sub * 128 + row;
-        if (live) *reinterpret_cast<float2 *>(w.ml + 2 * at) = make_float2(m, l);
+        if (live) *reinterpret_cast<float2 *>(w.ml + 2 * at) = make_float2(seen_max(m, limit > 0), l);
         float *part = w.part + (at - unit4) * D + 4 * unit4;
         if (n > 0) settle();
 #pragma unroll 1
@@ -560,7 +559,9 @@ __device__ __forceinline__ void tile_role(const AttnParams &p, const TilePlan &w
         }
       } else {
         if (live && p.lse) p.lse[orow] = row_lse(m, l);
-        const float inv = row_inverse(m, l);
+        // as row_inverse, which took 0.5% longer here (a NaN in l is in every column of O too)
+        float inv = l > 0.f ? 1.f / l : 0.f;
+        if (l == 0.f && limit > 0) inv = CUDART_NAN_F;
         const __nv_bfloat16 *gk[4];
         uint4 gate[4];
         if (p.gate) {
