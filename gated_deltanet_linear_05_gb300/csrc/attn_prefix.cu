@@ -3,7 +3,7 @@
 // and comes to the same division of the SMs, so that both kinds of work end about together:
 //     X : 152 - X  as  (row tiles x key tiles x cycles of a step) : (own bytes / 36 bytes a cycle),
 // 2450 cycles a step of a CTA (4154 of a pair's two) as measured in long prompts; 36 bytes a cycle is
-// about what an SM streams when not all of them do (128 requests of up to 1000 own keys behind 16389:
+// about what an SM streams when not all of them do (from one shape, 128 requests of up to 1000 own keys behind 16389:
 // 99 us with 48, 86 with 40 and 32, 89 with 26; 104 with the two one after the other).  A row tile is
 // cut into as many parts as fill the X.
 #include "attn_step.cuh"

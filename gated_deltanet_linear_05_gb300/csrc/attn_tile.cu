@@ -321,6 +321,9 @@ cudaError_t run(const AttnParams &p, char *ws, unsigned int *errw, cudaStream_t 
   // under way, and starts and ends overlap (105 drafts of 9 to 18 tokens after 34, 32 heads of 128: 26 us,
   // wide 40; 128 of 16 after 200 to 4000: 103 and 107).  At D = 256 two stages of 64 KB hold long contexts
   // back (28 drafts after 367 to 1469 keys: 74 us, wide 63; 54 after 480: 58 and 66, after 900: 83 and 85).
+  // The host knows neither lengths nor rows of a sequence: the rule takes the mean rows, so that a prompt
+  // among many single tokens gets narrow tiles, and at D = 256 the most keys that the page table can hold,
+  // so that behind a table of more than 1024 keys drafts get wide ones whatever their contexts.
   if ((long long)p.tokens <= (long long)p.num_seqs * z.tpt &&
       (D == 128 || (long long)p.max_pages * p.page_size <= 1024))
     return run_tiles<Cfg<D, true>>(p, own, parts, z.tpt, q, errw, stream);

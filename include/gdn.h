@@ -521,8 +521,9 @@ gdn_status gdn_kv_append(const gdn_attn_shape *shape, const void *q, const void 
  * o must not overlap q or gate (GDN_ERR_ALIAS).  shape->prefix_len must be 0.
  * workspace: gdn_attn_workspace_size(shape) bytes, 256-byte aligned, the first
  * GDN_ATTN_COUNTER_BYTES of them zero before the first call that uses it (the rest may hold
- * anything); every call leaves it ready for the next.  Calls sharing a workspace must
- * not overlap on the GPU.  The results do not depend on the order of execution.
+ * anything); every call leaves it ready for the next (after GDN_STATUS_WAIT_TIMEOUT zero them
+ * again).  Calls sharing a workspace must not overlap on the GPU.  The results do not depend on
+ * the order of execution.
  */
 gdn_status gdn_paged_attention(const gdn_attn_shape *shape, const void *q, const void *gate,
                                const void *k_cache, const void *v_cache,
