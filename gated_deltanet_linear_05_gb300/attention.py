@@ -1,5 +1,6 @@
 """Binding of the attention-layer operators: residual + RMS norm, rotary positions and the
-append to the paged cache, attention over the cache, and the same behind a shared prefix.
+append to the paged cache, attention over the cache, the same behind a shared prefix, and for
+trees of drafts.
 
 Argument marshalling only, as in the package itself; include/gdn.h has the contract of each
 call.  A call that is given a stream runs with that stream current, so that what it allocates
@@ -183,10 +184,10 @@ def _sequences(page_table, kv_lens, cu_seqlens):
 _made = {}
 
 
-def _remember(key, value):
-    if len(_made) >= 4096:
-        _made.clear()
-    _made[key] = value
+def _remember(key, value, made=_made):
+    if len(made) >= 4096:
+        made.clear()
+    made[key] = value
     return value
 
 
@@ -314,12 +315,12 @@ def _attend_shape(q, k_cache, v_cache, prefix_table, prefix_len, page_table, kv_
 
 
 def _attend(name, q, k_cache, v_cache, prefix_table, prefix_len, page_table, kv_lens, cu_seqlens,
-            gate, scale, o, lse, workspace, stream):
+            gate, scale, o, lse, workspace, stream, parents=None):
     if stream is not None:
         with torch.cuda.stream(stream):
             return _attend(name, q, k_cache, v_cache, prefix_table, prefix_len, page_table, kv_lens,
-                           cu_seqlens, gate, scale, o, lse, workspace, None)
-    if lse is None:
+                           cu_seqlens, gate, scale, o, lse, workspace, None, parents)
+    if lse is None and parents is None:
         r = (_quick or _fast()).attend(_made, q, k_cache, v_cache, prefix_table, prefix_len, page_table,
                                        kv_lens, cu_seqlens, gate, scale, o, workspace)
         if type(r) is int:
@@ -328,7 +329,7 @@ def _attend(name, q, k_cache, v_cache, prefix_table, prefix_len, page_table, kv_
             return r
     device = q.get_device()
     _check(device, (q, k_cache, v_cache) if gate is None else (q, k_cache, v_cache, gate),
-           (page_table, kv_lens, cu_seqlens, prefix_table))
+           (page_table, kv_lens, cu_seqlens, prefix_table, parents))
     key = (q.shape, q.stride(), k_cache.shape, k_cache.stride(), v_cache.shape, v_cache.stride(),
            page_table.shape, kv_lens.shape, None if cu_seqlens is None else cu_seqlens.shape,
            None if gate is None else (gate.shape, gate.stride()), scale,
@@ -346,7 +347,11 @@ def _attend(name, q, k_cache, v_cache, prefix_table, prefix_len, page_table, kv_
             None if cu_seqlens is None else cu_seqlens.data_ptr(), o.data_ptr(),
             None if lse is None else _float(device, lse, q.shape[:2], "lse"), workspace.data_ptr(),
             workspace.nbytes, _raw_stream(device)]
-    if prefix_table is None:
+    if parents is not None:
+        args[5:5] = [None if prefix_table is None else prefix_table.data_ptr()]
+        args[9:9] = [parents.data_ptr()]
+        st = lib().gdn_tree_attention(*args)
+    elif prefix_table is None:
         st = lib().gdn_paged_attention(*args)
     else:
         args.insert(5, prefix_table.data_ptr())
@@ -376,6 +381,20 @@ def gdn_shared_prefix_attention(q, k_cache, v_cache, prefix_table, prefix_len: i
     keys alone.  Returns o."""
     return _attend("gdn_shared_prefix_attention", q, k_cache, v_cache, prefix_table, prefix_len,
                    page_table, kv_lens, cu_seqlens, gate, scale, o, lse, workspace, stream)
+
+
+def gdn_tree_attention(q, k_cache, v_cache, page_table, kv_lens, cu_seqlens, parents, gate=None,
+                       scale: Optional[float] = None, o=None, lse=None, prefix_table=None,
+                       prefix_len: int = 0, workspace=None, stream=None):
+    """The attention of trees of drafts: each sequence's tokens are the nodes of a tree of at most
+    GDN_TREE_NODES, and a node sees the keys before the tree, its ancestors and itself.
+    parents [T] int32: each node's parent as an index into its own sequence's nodes, which stands
+    before it; -1: the node hangs on the keys before the tree.  With prefix_len > 0 every node
+    also sees the shared prefix in prefix_table.  Returns o."""
+    if cu_seqlens is None or parents.shape != q.shape[:1]:
+        raise ValueError("trees need cu_seqlens and parents [tokens]")
+    return _attend("gdn_tree_attention", q, k_cache, v_cache, prefix_table, prefix_len, page_table,
+                   kv_lens, cu_seqlens, gate, scale, o, lse, workspace, stream, parents)
 
 
 def _norm_plan(x, out, group):

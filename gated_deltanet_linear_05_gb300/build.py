@@ -20,9 +20,9 @@ MARSHAL = os.path.join(HERE, "_marshal.so")  # the attention calls' argument mar
 SOURCES = ["gdn_api.cu", "decode.cu", "chunk_f32.cu", "chunk_bf16.cu", "chunk_fused.cu", "chunk_tc.cu",
            "gdn_noalloc.cu", "block_io.cu", "rollback.cu", "split.cu", "decode_block.cu",
            "attn_api.cu", "attn_io.cu", "attn_tile.cu", "attn_step.cu",
-           "attn_prefix.cu"]
+           "attn_prefix.cu", "verify_tree.cu", "beam.cu", "beam_api.cu"]
 HEADERS = ["common.cuh", "internal.h", "tc.cuh", "attn.h", "attn_tma.cuh",
-           "attn_tile.cuh", "attn_step.cuh"]
+           "attn_tile.cuh", "attn_step.cuh", "beam.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -38,6 +38,8 @@ struct AttnParams {
   int64_t qs[2], gs[2], page_stride;
   const void *q, *gate, *k_cache, *v_cache;
   const int32_t *prefix_table, *page_table, *kv_lens, *cu_seqlens;
+  const int32_t *parents;  // not NULL: the sequences' tokens are trees
+  uint64_t *above;         // of each node, with parents: bit j: node j is its ancestor or itself
   void *o;
   float *lse;
 };

@@ -70,8 +70,8 @@ gdn_status check_tables(const gdn_attn_shape *s, const void *k_cache, const void
 
 gdn_status attention(const gdn_attn_shape *s, const void *q, const void *gate, const void *k_cache,
                      const void *v_cache, const int32_t *prefix_table, const int32_t *page_table,
-                     const int32_t *kv_lens, const int32_t *cu_seqlens, void *o, float *lse,
-                     void *workspace, size_t workspace_bytes, void *stream) {
+                     const int32_t *kv_lens, const int32_t *cu_seqlens, const int32_t *parents, void *o,
+                     float *lse, void *workspace, size_t workspace_bytes, void *stream) {
   gdn_status st = check_cache(s);
   if (st != GDN_OK) return st;
   // key tiles are counted, and boxes of them addressed, up to some thousand keys past the last in 32 bits
@@ -116,6 +116,7 @@ gdn_status attention(const gdn_attn_shape *s, const void *q, const void *gate, c
   p.page_table = page_table;
   p.kv_lens = kv_lens;
   p.cu_seqlens = cu_seqlens;
+  p.parents = parents;
   p.o = o;
   p.lse = lse;
   return cuda_status(gdn::launch_attention(p, workspace, gdn::device_status_word(),
@@ -140,8 +141,8 @@ gdn_status gdn_paged_attention(const gdn_attn_shape *shape, const void *q, const
   const gdn_status st = check_shape(shape);
   if (st != GDN_OK) return st;
   if (shape->prefix_len != 0) return GDN_ERR_INVALID_ARG;
-  return attention(shape, q, gate, k_cache, v_cache, nullptr, page_table, kv_lens, cu_seqlens, o, lse,
-                   workspace, workspace_bytes, stream);
+  return attention(shape, q, gate, k_cache, v_cache, nullptr, page_table, kv_lens, cu_seqlens, nullptr, o,
+                   lse, workspace, workspace_bytes, stream);
 }
 
 gdn_status gdn_shared_prefix_attention(const gdn_attn_shape *shape, const void *q,
@@ -153,8 +154,21 @@ gdn_status gdn_shared_prefix_attention(const gdn_attn_shape *shape, const void *
   const gdn_status st = check_shape(shape);
   if (st != GDN_OK) return st;
   if (shape->prefix_len == 0) return GDN_ERR_INVALID_ARG;
-  return attention(shape, q, gate, k_cache, v_cache, prefix_table, page_table, kv_lens, cu_seqlens, o,
-                   lse, workspace, workspace_bytes, stream);
+  return attention(shape, q, gate, k_cache, v_cache, prefix_table, page_table, kv_lens, cu_seqlens, nullptr,
+                   o, lse, workspace, workspace_bytes, stream);
+}
+
+gdn_status gdn_tree_attention(const gdn_attn_shape *shape, const void *q, const void *gate,
+                              const void *k_cache, const void *v_cache,
+                              const int32_t *prefix_table, const int32_t *page_table,
+                              const int32_t *kv_lens, const int32_t *cu_seqlens,
+                              const int32_t *parents, void *o, float *lse, void *workspace,
+                              size_t workspace_bytes, void *stream) {
+  const gdn_status st = check_shape(shape);
+  if (st != GDN_OK) return st;
+  if (!cu_seqlens || !aligned(parents, 4) || (shape->total_tokens > 0 && !parents)) return GDN_ERR_INVALID_ARG;
+  return attention(shape, q, gate, k_cache, v_cache, prefix_table, page_table, kv_lens, cu_seqlens, parents,
+                   o, lse, workspace, workspace_bytes, stream);
 }
 
 gdn_status gdn_kv_append(const gdn_attn_shape *s, const void *q, const void *k, const void *v,

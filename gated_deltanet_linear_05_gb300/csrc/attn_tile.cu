@@ -3,6 +3,8 @@
 // tiles, and the choice of kernels for a call.
 #include <string.h>
 
+#include <algorithm>
+
 #include "attn_tile.cuh"
 
 namespace gdn {
@@ -13,6 +15,32 @@ namespace {
 constexpr int kPlanThreads = 512;
 constexpr int kCand = 16;
 constexpr int kPlanTiles = 4096;  // tiles whose lengths are kept in shared memory
+
+// The nodes that each node of the trees sees, by the blocks beside the planning one: 64 threads to a
+// sequence walk up from a node each, through parents in shared memory (a chain of 64: 2 us of the plan's 6).
+constexpr int kTreesABlock = kPlanThreads / GDN_TREE_NODES;
+__device__ __forceinline__ void ancestors(const AttnParams &p, int block, int blocks, int (*up)[GDN_TREE_NODES]) {
+  const int i = threadIdx.x % GDN_TREE_NODES, mine = threadIdx.x / GDN_TREE_NODES;
+  for (int n0 = block * kTreesABlock; n0 < p.num_seqs; n0 += blocks * kTreesABlock) {
+    const int n = n0 + mine;
+    int bos = 0, eos = 0;
+    if (n < p.num_seqs) seq_range(p.cu_seqlens, n, p.tokens, bos, eos);
+    const int t = min(eos - bos, GDN_TREE_NODES);
+    if (i < t) up[mine][i] = p.parents[bos + i];
+    __syncthreads();
+    if (i < t) {
+      uint64_t above = 0;
+      for (int j = i, next; ; j = next) {  // (goes down at every step)
+        above |= 1ull << j;
+        next = up[mine][j];
+        if (next < 0 || next >= j) break;
+      }
+      p.above[bos + i] = above;
+    }
+    for (int j = bos + GDN_TREE_NODES + i; j < eos; j += GDN_TREE_NODES) p.above[j] = 0;  // too many: no bit left
+    __syncthreads();
+  }
+}
 
 // Cuts the batch into entries, one block.  Tiles with many key tiles are split so that the
 // SMs get even shares: of kCand chunk lengths the one with the smallest
@@ -29,14 +57,19 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(AttnParams p, TilePl
   __shared__ float sh_cost[kCand];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
+  if (blockIdx.x > 0) {
+    ancestors(p, (int)blockIdx.x - 1, (int)gridDim.x - 1, reinterpret_cast<int (*)[GDN_TREE_NODES]>(sh_kvt));
+    return;
+  }
   if (tid == 0) sh_total = sh_kvmax = sh_slot = sh_nsplit = sh_nbig = 0;
   if (tid < 64) sh_hist[tid] = 0;
   int kvmax = 1;
   auto put = [&](int at, int n, int bos, int t, int len, int i) {
     if (at >= w.max_tiles) return;  // only with a malformed cu_seqlens
     const int tok0 = i * tt, ntok = min(tt, t - tok0);
-    const int kvt = (visible(len - t + tok0, ntok, len) + kBN - 1) / kBN;
-    w.rec[at] = Entry{bos + tok0, ntok, n, len - t + tok0, 0, kvt, 0, len};
+    const int place0 = p.parents ? kMostKeys : len - t + tok0;  // (a tree's nodes may see any key)
+    const int kvt = (visible(place0, ntok, len) + kBN - 1) / kBN;
+    w.rec[at] = Entry{bos + tok0, ntok, n, place0, 0, kvt, 0, len};
     if (at < kPlanTiles) sh_kvt[at] = kvt;
     kvmax = max(kvmax, kvt);
   };
@@ -219,7 +252,8 @@ int prefix_parts(int tiles, int hkv, int prefix_len) {
 }
 
 template <int D>
-size_t layout(TilePlan *own, TilePlan *pre, DenseRows *dense, char *ws, int num_seqs, int tokens, int hq, int hkv, int prefix_len) {
+size_t layout(TilePlan *own, TilePlan *pre, DenseRows *dense, uint64_t **above, char *ws, int num_seqs, int tokens, int hq,
+              int hkv, int prefix_len) {
   const Sizes<D> z(tokens, num_seqs, hq, hkv);
   size_t at = 0;
   auto take = [&](size_t bytes) {
@@ -255,6 +289,8 @@ size_t layout(TilePlan *own, TilePlan *pre, DenseRows *dense, char *ws, int num_
     c.ml = (float *)take(rows * 2 * sizeof(float));
     c.part = (float *)take(rows * D * sizeof(float));
   }
+  uint64_t *nodes = (uint64_t *)take(sizeof(uint64_t) * (size_t)tokens);
+  if (above) *above = nodes;
   if (dense) *dense = c;
   if (own) *own = a;
   if (pre) *pre = b;
@@ -276,8 +312,10 @@ cudaError_t run_tiles(const AttnParams &p, TilePlan own, const PrefixParts &part
   const size_t smem = C::SMEM + 1024;
   static std::atomic<uint64_t> allowed{0};
   err = allow_smem(tile_kernel<C>, smem, allowed);
+  // (152 blocks of 8 trees beside the plan's)
+  const int trees = C::TREE ? std::min((p.num_seqs + kTreesABlock - 1) / kTreesABlock, kSms - 1) : 0;
   if (err == cudaSuccess)
-    err = launch_dependent(plan_kernel, 1, kPlanThreads, 0, stream, 1, p, own, tt);
+    err = launch_dependent(plan_kernel, 1 + trees, kPlanThreads, 0, stream, 1, p, own, tt);
   if (err == cudaSuccess)
     err = launch_dependent(tile_kernel<C>, C::UNITS * C::GRP, C::THREADS, smem, stream, C::GRP, p, own, q, k, v);
   if (err != cudaSuccess) return err;
@@ -285,16 +323,17 @@ cudaError_t run_tiles(const AttnParams &p, TilePlan own, const PrefixParts &part
 }
 
 template <int D>
-cudaError_t run(const AttnParams &p, char *ws, unsigned int *errw, cudaStream_t stream) {
+cudaError_t run(const AttnParams &call, char *ws, unsigned int *errw, cudaStream_t stream) {
   // one token per sequence: the decode kernel does the sequences' own keys
-  const bool step = !p.cu_seqlens && p.hq / p.hkv <= kStepRows;
+  const bool step = !call.cu_seqlens && call.hq / call.hkv <= kStepRows;
   char *tile_ws = ws + attn_step_workspace(D);
   using C = Cfg<D>;
-  const Sizes<D> z(p.tokens, p.num_seqs, p.hq, p.hkv);
-  if (step && p.prefix_len == 0) return launch_attn_step(p, ws, errw, stream);
+  const Sizes<D> z(call.tokens, call.num_seqs, call.hq, call.hkv);
+  if (step && call.prefix_len == 0) return launch_attn_step(call, ws, errw, stream);
   TilePlan own, pre;
   DenseRows dense;
-  layout<D>(&own, &pre, &dense, tile_ws, p.num_seqs, p.tokens, p.hq, p.hkv, p.prefix_len);
+  AttnParams p = call;
+  layout<D>(&own, &pre, &dense, &p.above, tile_ws, p.num_seqs, p.tokens, p.hq, p.hkv, p.prefix_len);
   pre.err = errw;
   if (step) {  // the prefix and the sequences' own keys side by side, then their join
     pre.head = own.head;
@@ -324,18 +363,21 @@ cudaError_t run(const AttnParams &p, char *ws, unsigned int *errw, cudaStream_t 
   // The host knows neither lengths nor rows of a sequence: the rule takes the mean rows, so that a prompt
   // among many single tokens gets narrow tiles, and at D = 256 the most keys that the page table can hold,
   // so that behind a table of more than 1024 keys drafts get wide ones whatever their contexts.
-  if ((long long)p.tokens <= (long long)p.num_seqs * z.tpt &&
-      (D == 128 || (long long)p.max_pages * p.page_size <= 1024))
-    return run_tiles<Cfg<D, true>>(p, own, parts, z.tpt, q, errw, stream);
-  return run_tiles<C>(p, own, parts, z.tpt, q, errw, stream);
+  const bool narrow = (long long)p.tokens <= (long long)p.num_seqs * z.tpt &&
+                      (D == 128 || (long long)p.max_pages * p.page_size <= 1024);
+  if (p.parents)
+    return narrow ? run_tiles<Cfg<D, true, true>>(p, own, parts, z.tpt, q, errw, stream)
+                  : run_tiles<Cfg<D, false, true>>(p, own, parts, z.tpt, q, errw, stream);
+  return narrow ? run_tiles<Cfg<D, true>>(p, own, parts, z.tpt, q, errw, stream)
+                : run_tiles<C>(p, own, parts, z.tpt, q, errw, stream);
 }
 
 }  // namespace
 
 size_t attn_workspace(int num_seqs, int tokens, int hq, int hkv, int d, int prefix_len) {
   // the decode kernel's part first: its counters stay in one place for all shapes
-  return attn_step_workspace(d) + (d == 128 ? layout<128>(nullptr, nullptr, nullptr, nullptr, num_seqs, tokens, hq, hkv, prefix_len)
-                                            : layout<256>(nullptr, nullptr, nullptr, nullptr, num_seqs, tokens, hq, hkv, prefix_len));
+  return attn_step_workspace(d) + (d == 128 ? layout<128>(nullptr, nullptr, nullptr, nullptr, nullptr, num_seqs, tokens, hq, hkv, prefix_len)
+                                            : layout<256>(nullptr, nullptr, nullptr, nullptr, nullptr, num_seqs, tokens, hq, hkv, prefix_len));
 }
 
 cudaError_t launch_attention(const AttnParams &p, void *ws, unsigned int *err, cudaStream_t stream) {

@@ -42,9 +42,10 @@ namespace gdn {
 
 constexpr int kBN = 128;        // keys per tile
 
-template <int D_, bool NARROW = false>
+template <int D_, bool NARROW = false, bool TREE_ = false>
 struct Cfg {
   static constexpr int D = D_;
+  static constexpr bool TREE = TREE_;               // the tokens are trees' nodes
   static constexpr bool PAIR = D == 256 && !NARROW;  // two CTAs share a tile, one sub-tile each
   static constexpr int GRP = PAIR ? 2 : 1;          // tcgen05 cta_group
   static constexpr int SUBS = PAIR || NARROW ? 1 : 2;  // sub-tiles of 128 rows in a CTA
@@ -315,6 +316,14 @@ struct Barriers {
   int dead;
 };
 
+// Columns of a key tile that a tree's node sees, 32 to a word: the keys before the tree, which starts
+// `before` columns past the first of them (or before it, if negative), and the nodes in `above`.
+__device__ __forceinline__ uint32_t seen_columns(uint64_t above, int before) {
+  if (before >= 32) return ~0u;
+  if (before > 0) return ((1u << before) - 1) | (uint32_t)(above << before);
+  return before > -64 ? (uint32_t)(above >> -before) : 0u;
+}
+
 // Work item of this round: the entry and its kv-head.
 __device__ __forceinline__ bool item_at(const AttnParams &p, const TilePlan &w, int unit, int units, int round,
                                         int tt, Entry &e, int &h) {
@@ -425,7 +434,18 @@ __device__ __forceinline__ void tile_role(const AttnParams &p, const TilePlan &w
       const int dt = sub * tpt + row / G;
       const bool live = row < tpt * G && dt < e.ntok;
       // keys this row sees, counted from the entry's first
-      const int limit = (live ? visible(e.place0, dt + 1, e.kvlen) : 0) - e.kt0 * kBN;
+      int limit = (live ? visible(e.place0, dt + 1, e.kvlen) : 0) - e.kt0 * kBN;
+      // of a tree's node: the nodes it sees, and the tree's first key, counted alike
+      uint64_t above = 0;
+      int tree0 = 0;
+      if (C::TREE && live) {
+        int bos, t, len;
+        seq_info(p, e.seq, bos, t, len);
+        above = p.above[e.tok0 + dt];
+        tree0 = len - t - e.kt0 * kBN;
+        // whether it sees any key in these tiles (128 columns or more: the tree ends in them)
+        limit = tree0 > 0 || (tree0 > -64 && above >> -tree0 != 0);
+      }
       float m = -CUDART_INF_F, l = 0.f;
       if (p.gate && live && e.slot < 0) {  // the epilogue's gate, into L2 meanwhile (4096 tokens: 112 -> 107 us)
         const char *at = (const char *)((const __nv_bfloat16 *)p.gate + (e.tok0 + dt) * p.gs[0] + (h * G + row % G) * p.gs[1]);
@@ -454,11 +474,21 @@ __device__ __forceinline__ void tile_role(const AttnParams &p, const TilePlan &w
             s[c / 32][c % 32] = __float_as_uint(p.scale == 0.f ? 0.f : -x);
           }
         }
-        const int lim = limit - j * kBN;
+        const int lim = (C::TREE ? tree0 : limit) - j * kBN;
         if (__any_sync(0xffffffffu, lim < kBN)) {
+          if (C::TREE) {
 #pragma unroll
-          for (int c = 0; c < kBN; ++c)
-            if (c >= lim) s[c / 32][c % 32] = 0xff800000u;
+            for (int w = 0; w < 4; ++w) {
+              const uint32_t seen = seen_columns(above, lim - 32 * w);
+#pragma unroll
+              for (int c = 0; c < 32; ++c)
+                if (!(seen >> c & 1)) s[w][c] = 0xff800000u;
+            }
+          } else {
+#pragma unroll
+            for (int c = 0; c < kBN; ++c)
+              if (c >= lim) s[c / 32][c % 32] = 0xff800000u;
+          }
         }
         float mx[4];
 #pragma unroll

@@ -75,6 +75,11 @@ bool partial_overlap(const void *a, const void *b, size_t n) {
   return x < y + n && y < x + n;
 }
 
+bool overlap(const void *a, size_t na, const void *b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a && b && na && nb && x < y + nb && y < x + na;
+}
+
 struct Common {
   const gdn_shape *s;
   const void *q, *k, *v;
@@ -615,6 +620,53 @@ gdn_status gdn_verify_block_capture(const gdn_shape *shape, const void *q, const
   const uintptr_t a = reinterpret_cast<uintptr_t>(state_in), b = reinterpret_cast<uintptr_t>(state_out);
   if (a < b + n && b < a + n) return GDN_ERR_ALIAS;
   return run_chunked(c, nullptr, 0, stream, delta);
+}
+
+gdn_status gdn_verify_tree(const gdn_shape *shape, const void *q, const void *k, const void *v,
+                           const float *g, const float *beta, const float *state_in,
+                           const int32_t *cu_seqlens, const int32_t *parents, void *o,
+                           float *delta, void *stream) {
+  const gdn_status st = check_shape(shape, true);
+  if (st != GDN_OK) return st;
+  const gdn_shape *s = shape;
+  if (s->algo != GDN_ALGO_AUTO) return GDN_ERR_UNSUPPORTED;
+  if (s->total_tokens > 0 && (!q || !k || !v || !g || !beta || !parents || !o || !delta)) return GDN_ERR_INVALID_ARG;
+  if (s->num_seqs > 0 && !cu_seqlens) return GDN_ERR_INVALID_ARG;
+  for (const void *p : {q, k, v, (const void *)g, (const void *)beta, (const void *)state_in, (const void *)o,
+                        (const void *)delta})
+    if (!aligned16(p)) return GDN_ERR_INVALID_ARG;
+  for (const void *p : {cu_seqlens, parents})
+    if (reinterpret_cast<uintptr_t>(p) & 3u) return GDN_ERR_INVALID_ARG;
+  const size_t rows = (size_t)s->total_tokens * s->num_v_heads, es = s->qkv_dtype == GDN_BF16 ? 2 : 4;
+  const size_t qb = (size_t)s->total_tokens * s->num_k_heads * s->dk * es, vb = rows * s->dv * es, gb = rows * 4;
+  const size_t ob = rows * s->dv * (s->o_fp32 ? 4 : es), db = rows * s->dv * 4;
+  const struct { const void *p; size_t bytes; } in[] = {
+      {q, qb}, {k, qb}, {v, vb}, {g, gb}, {beta, gb}, {state_in, state_bytes(s)},
+      {cu_seqlens, (size_t)(s->num_seqs + 1) * 4}, {parents, (size_t)s->total_tokens * 4}};
+  for (const auto &x : in)
+    if (overlap(o, ob, x.p, x.bytes) || overlap(delta, db, x.p, x.bytes)) return GDN_ERR_ALIAS;
+  if (overlap(o, ob, delta, db)) return GDN_ERR_ALIAS;
+  if (s->total_tokens == 0 || s->num_seqs == 0) return GDN_OK;
+  gdn::TreeParams p{};
+  p.num_seqs = s->num_seqs;
+  p.total_tokens = s->total_tokens;
+  p.hk = s->num_k_heads;
+  p.hv = s->num_v_heads;
+  p.chunk = s->chunk;
+  p.dtype = s->qkv_dtype;
+  p.o_fp32 = s->o_fp32;
+  p.q = q;
+  p.k = k;
+  p.v = v;
+  p.g = g;
+  p.beta = beta;
+  p.state_in = state_in;
+  p.cu_seqlens = cu_seqlens;
+  p.parents = parents;
+  p.o = o;
+  p.delta = delta;
+  p.err = status_word();
+  return cuda_status(gdn::launch_verify_tree(p, static_cast<cudaStream_t>(stream)));
 }
 
 gdn_status gdn_state_rollback(const gdn_shape *shape, const void *k, const float *g,

@@ -108,6 +108,20 @@ struct RollbackParams {
 cudaError_t launch_rollback(const RollbackParams &p, cudaStream_t stream);
 cudaError_t launch_conv_state(const PrologueParams &p, cudaStream_t stream);
 
+// The delta rule over trees of drafts (verify_tree.cu).
+struct TreeParams {
+  int num_seqs, total_tokens, hk, hv, chunk;
+  gdn_dtype dtype;
+  int o_fp32;  // o is float32 regardless of dtype
+  const void *q, *k, *v;
+  const float *g, *beta, *state_in;
+  const int32_t *cu_seqlens, *parents;
+  void *o;
+  float *delta;
+  unsigned int *err;  // the library's device status word, or NULL
+};
+cudaError_t launch_verify_tree(const TreeParams &p, cudaStream_t stream);
+
 // Gated RMSNorm of rows of 128: y = o / sqrt(mean o^2 + eps) * w * SiLU(z).
 struct NormParams {
   long long rows;

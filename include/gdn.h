@@ -232,6 +232,28 @@ gdn_status gdn_state_rollback(const gdn_shape *shape, const void *k, const float
                               const int32_t *cu_seqlens, void *stream);
 
 /*
+ * Draft-verify block whose drafts form a tree ("New in v2", prompt lookup decoding, with more
+ * than one continuation; the per-token rule of "How it works" along every path): node i starts from
+ * its parent's state, or from the snapshot state_in[n] if it hangs on it:
+ *     S_i = S' + k_i delta_i^T,  S' = e^{g_i} S_parent(i),
+ *     delta_i = beta_i (v_i - S'^T k_i),  o_i = S_i^T q_i.
+ *     parents    [total_tokens]          int32, 4-byte aligned: as for gdn_tree_attention
+ *     state_in   [num_seqs, Hv, dk, dv]  float32, left unchanged; NULL: zero
+ *     o          [total_tokens, Hv, dv]  qkv_dtype, or float32 when shape->o_fp32
+ *     delta      [total_tokens, Hv, dv]  float32
+ * o and delta must not overlap each other or an input (GDN_ERR_ALIAS).  shape->chunk (16, 32 or
+ * 64) is the most nodes of a tree; a sequence with more gives unspecified results for itself alone.
+ * shape->algo must be GDN_ALGO_AUTO.  No state is written: the one after an accepted path follows
+ * from gdn_state_rollback on the path's rows of k, g and delta.
+ * q, k and v are taken exactly and the state to 24 bits on the tensor cores, sums in float32 (bf16
+ * and f32 alike).  One launch, no workspace.
+ */
+gdn_status gdn_verify_tree(const gdn_shape *shape, const void *q, const void *k, const void *v,
+                           const float *g, const float *beta, const float *state_in,
+                           const int32_t *cu_seqlens, const int32_t *parents, void *o,
+                           float *delta, void *stream);
+
+/*
  * Conv FIFO after the accepted prefix of each sequence's draft: conv_state_out[n][j] is
  * the raw input at position a - (W-1) + j of sequence n (a = prefix_len[n], clamped to
  * the sequence's length; positions before the draft come from conv_state_in, the FIFO
@@ -437,6 +459,7 @@ size_t gdn_prefill_split_workspace_size(const gdn_shape *shape, int32_t segment_
  *   gdn_kv_append                q/k head norms, rotary positions, scatter into the cache
  *   gdn_paged_attention          attention over the paged cache
  *   gdn_shared_prefix_attention  the same behind a prefix that the whole batch shares
+ *   gdn_tree_attention           the same for trees of drafted tokens
  *
  * Device pointers; 16-byte aligned unless said otherwise (page_table, prefix_table, kv_lens,
  * cu_seqlens, positions, rope_axis and lse: 4 bytes; inv_freq: 8 bytes).
@@ -545,7 +568,29 @@ gdn_status gdn_shared_prefix_attention(const gdn_attn_shape *shape, const void *
                                        const int32_t *cu_seqlens, void *o, float *lse,
                                        void *workspace, size_t workspace_bytes, void *stream);
 
-/* Workspace bytes that either attention call needs for `shape`, with or without cu_seqlens
+#define GDN_TREE_NODES 64 /* most nodes of a tree of drafts */
+
+/*
+ * The same for trees of drafted tokens: the T_n tokens of sequence n (its last T_n keys, as ever)
+ * are the nodes of a tree that hangs on the keys before them, and a node sees those keys, its
+ * ancestors and itself, but no other node:
+ *     parents      [total_tokens] int32, 4-byte aligned: node i's parent as an index into its own
+ *                  sequence's nodes; it stands before its child, and any value outside [0, i)
+ *                  (-1) says that the node hangs on the keys before the tree
+ * A chain (parents i - 1) is gdn_paged_attention's causal order.  With shape->prefix_len > 0 every
+ * node sees the shared prefix (prefix_table as above), without it prefix_table is not read.
+ * cu_seqlens must not be NULL.  T_n is at most GDN_TREE_NODES: a sequence with more gives
+ * unspecified results for itself alone.  Everything else is as for the calls above, the
+ * workspace and its size too.
+ */
+gdn_status gdn_tree_attention(const gdn_attn_shape *shape, const void *q, const void *gate,
+                              const void *k_cache, const void *v_cache,
+                              const int32_t *prefix_table, const int32_t *page_table,
+                              const int32_t *kv_lens, const int32_t *cu_seqlens,
+                              const int32_t *parents, void *o, float *lse, void *workspace,
+                              size_t workspace_bytes, void *stream);
+
+/* Workspace bytes that any of the attention calls needs for `shape`, with or without cu_seqlens
  * (num_seqs, total_tokens, the heads, head_dim and prefix_len decide; larger values of any
  * of the first two never need less); (size_t)-1 for an invalid shape. */
 size_t gdn_attn_workspace_size(const gdn_attn_shape *shape);
@@ -569,6 +614,63 @@ gdn_status gdn_add_rmsnorm(int64_t rows, int32_t cols, gdn_dtype dtype, const vo
                            const void *residual, const float *weight, float eps,
                            void *residual_out, void *y, float *scale, int32_t group,
                            void *stream);
+
+/* ------------------------------------------------------------------------------------
+ * Several beams
+ * ------------------------------------------------------------------------------------ */
+typedef struct {
+  int32_t num_groups; /* requests, >= 0                                                  */
+  int32_t beams;      /* W: beams of a request, 1..64                                    */
+  int32_t vocab;      /* V: 1..2^24                                                      */
+  int32_t top;        /* continuations to select, 1..64, at most V                       */
+  gdn_dtype dtype;    /* of the logits: float32 or bf16                                  */
+  int32_t pad_token;  /* the token that a finished beam goes on with, 0..V-1             */
+  int64_t row_stride; /* elements from beam to beam in logits, >= V                      */
+} gdn_beam_shape;
+
+/*
+ * Selection over beams and vocabulary: of the W V continuations (w, x) of a request's beams the
+ * `top` best by
+ *     s(w, x) = scores[w] + logits[w][x] - ln sum_y exp(logits[w][y]),
+ * best first, equal ones in order of the beam and then of the token.  A finished beam has one
+ * continuation, pad_token, that keeps its score.
+ *     logits     [num_groups, W, V]  dtype, row_stride elements from row to row; any address that
+ *                                    is a multiple of the element
+ *     scores     [num_groups, W]     float32: the beams' scores so far
+ *     finished   [num_groups, W]     bytes, not 0: finished; or NULL
+ *     scores_out [num_groups, top]   float32
+ *     parents    [num_groups, top]   int32: the beam that each goes on from
+ *     tokens     [num_groups, top]   int32
+ * float32 and int32 tensors 4-byte aligned.  No output may overlap another buffer (GDN_ERR_ALIAS).
+ * A continuation of probability 0 (a logit of -inf), all of a beam whose score is -inf or NaN or
+ * +inf, or whose logits hold NaN or +inf or nothing but -inf, and all but one of a finished beam's
+ * count as -inf: they come after the others, in order of beam and token.
+ * Scores are compared in float64; the powers are summed in float32 (a few hundred at a time) and
+ * then in float64.  A request's results do not depend on the others.  A level of a tree of drafts
+ * is grown the same way (W = 1 at its root).
+ * workspace: gdn_beam_workspace_size(shape) bytes, 256-byte aligned; it may hold anything.  Calls
+ * sharing a workspace must not overlap on the GPU.  Two launches.
+ */
+gdn_status gdn_beam_select(const gdn_beam_shape *shape, const void *logits, const float *scores,
+                           const uint8_t *finished, float *scores_out, int32_t *parents,
+                           int32_t *tokens, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Workspace bytes for gdn_beam_select; (size_t)-1 for an invalid shape. */
+size_t gdn_beam_workspace_size(const gdn_beam_shape *shape);
+
+/*
+ * Reordering of the beams' rows, in place: with the rows [num_layers, num_groups, W, row_bytes]
+ *     row (l, g, w) <- the row (l, g, parents[g][w]) from before the call.
+ * Any state that has a row for each beam: delta-rule states, convolution inputs, page tables, lengths
+ * (a partly filled page of the cache that several beams go on writing to is the caller's to copy).
+ *     parents    [num_groups, W]  int32, 4-byte aligned; a row whose entry lies outside [0, W)
+ *                                 stays as it is
+ *     rows       4-byte aligned, row_bytes a multiple of 4 (multiples of 16 are faster)
+ * W at most 64.  Only rows that change are written, and only rows that they come from are read.
+ * One launch, no workspace.
+ */
+gdn_status gdn_beam_reorder(int32_t num_layers, int32_t num_groups, int32_t beams,
+                            int64_t row_bytes, const int32_t *parents, void *rows, void *stream);
 
 /* Bits of the device status word. */
 #define GDN_STATUS_WAIT_TIMEOUT 1u /* a kernel gave up a bounded wait on a barrier */
