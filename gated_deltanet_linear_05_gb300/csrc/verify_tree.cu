@@ -3,23 +3,27 @@
 //
 // With G_i the sum of g over node i's path (itself included), j < i for "j is an ancestor of i", and S
 // the snapshot, the per-token rule of "How it works" along the path gives, as in its chunkwise form,
-//     delta_i = beta_i (v_i - e^(G_i) S^T k_i - sum_{j < i} e^(G_i - G_j) (k_i.k_j) delta_j)
+//     delta_i = beta_i (r_i - sum_{j < i} e^(G_i - G_j) (k_i.k_j) delta_j),   r_i = v_i - e^(G_i) S^T k_i
 //     o_i     = e^(G_i) S^T q_i + sum_{j <= i} e^(G_i - G_j) (q_i.k_j) delta_j,
 // so a tree is one block whose triangular mask is the ancestors', and all paths share the two products
-// with S and the Gram matrix.
+// with S and the Gram matrix.  The recursion is linear in r: with T its matrix, found by running it on the unit
+// vectors (C columns, not the 128 of r), and W = (decays . Q K^T) T, both zero but for ancestors,
+//     delta = T r,   o = diag(e^G) Q S + W r.
 //
-// A CTA of 128 threads takes a (sequence, v-head); thread c owns value column c.
+// A CTA takes a (sequence, v-head).  Threads 0..127 own a value column each, C / 32 warps more the tree.
 //   products  [Q; K] (2 C rows) S on the tcgen05 tensor cores as D^T = S^T [Q; K]^T: S^T is the operand
 //             with 128 rows, in tensor memory, where thread c writes its column of S straight from
 //             coalesced loads, 32 keys at a time; S never passes through shared memory.  Each value of S is
 //             split in three bf16 terms (24 bits, all that float32 has); q and k are bf16 as they
 //             are, or three terms too (f32), of whose products the six above 2^-24 are taken.
 //             Accumulation is float32, so both types come out as float32 arithmetic would.
-//   Gram      [Q; K] K^T the same way into the columns that S^T takes later; the thread of each row
-//             multiplies the entries of its node's ancestors by their decays and appends them to the
-//             node's list in shared memory.  The exponents are differences of G in two floats.
-//   solve     each thread walks the nodes in order down its own column: the deltas it needs are its own, so
-//             there is no barrier, and the work is the sum of the depths, not the square of the nodes.
+//   tree      meanwhile: the Gram products K [Q; K]^T come the same way into D^T's columns before S needs
+//             them; the thread of key j multiplies those of its descendants by the decays (exponents:
+//             differences of G in two floats).  Then thread j runs the recursion on unit vector j, 16 nodes
+//             at a time in registers.  (Down lists of the ancestors alone it took 90 cycles for each four of
+//             them, one after another: 24 trees of 40 to 64 nodes, some of them chains, in f32 237 us.)
+//   results   r, in three terms over S^T's columns, times [W; T]^T in three terms, added to
+//             diag(e^G) D^T in place.
 //
 // Bound by HBM: the 64 KB of S per head are read once.
 #include "attn_tma.cuh"
@@ -29,22 +33,30 @@
 namespace gdn {
 namespace {
 
-constexpr int kTreeThreads = 128;
-constexpr int kKeys = 32;  // keys of S to a step
+constexpr int kColumns = 128;  // threads with a value column
+constexpr int kKeys = 32;      // keys of S to a step
 
-// Bytes of shared memory: operand tiles, v, deltas and a row of zeros, coefficients, their nodes.
+// Shared memory: operand tiles, whose place [W; T] in three terms takes; N and A, whose place W and T
+// take; v.
 template <typename T, int C>
 struct TreeCfg {
   static constexpr int TERMS = sizeof(T) == 2 ? 1 : 3;  // bf16 terms of a value of q or k
   static constexpr int CHUNK = 2 * C * 128;             // 64 columns of [Q; K]
   static constexpr int QK = TERMS * 2 * CHUNK;
-  static constexpr int V = C * kD * (int)sizeof(T);
-  static constexpr int DELTA = (C + 1) * kD * 4;
-  static constexpr int PAIRS = C * (C - 1) / 2 + 3 * C;  // every list a multiple of 4 long
-  static constexpr int SMEM = 1024 + QK + V + DELTA + PAIRS * 9;
-  // Gram rows past 2 C are read from whatever follows the tiles; all of it is the CTA's own
-  static_assert(QK - CHUNK + 16384 <= SMEM - 1024, "the Gram product's 128 rows");
-  static constexpr int COLS = 2 * C + 64 <= 128 ? 128 : 256;  // tensor memory
+  static constexpr int WT_TERM = 2 * C * C * 2;         // a term of [W; T]
+  static constexpr int N_AT = QK > 3 * WT_TERM ? QK : 3 * WT_TERM;
+  static constexpr int ROW = C + 4;                     // floats: 16-byte accesses of a column of rows spread over the banks
+  static constexpr int A_AT = N_AT + C * ROW * 4;
+  static constexpr int V_AT = A_AT + C * ROW * 4;
+  static constexpr int USED = V_AT + C * kD * (int)sizeof(T);
+  // the Gram product reads 128 rows from K's first; past the tiles they are whatever follows
+  static constexpr int GRAM = QK - CHUNK + C * 128 + 16384;
+  static constexpr int SMEM = 1024 + (USED > GRAM ? USED : GRAM);
+  static constexpr int A_COL = 2 * C, A_COLS = 3 * C / 2 > 48 ? 3 * C / 2 : 48;  // tensor memory: after D^T
+  static constexpr int COLS = A_COL + A_COLS <= 128 ? 128 : 256;
+  static constexpr int TREE_WARPS = C == 64 ? 2 : 1;
+  static constexpr int THREADS = kColumns + 32 * TREE_WARPS;
+  static constexpr int CTAS = C == 64 ? 2 : 4;
 };
 
 // 64 columns x 2 C rows of bf16, 128-byte swizzle, K-major.
@@ -81,36 +93,73 @@ __device__ __forceinline__ uint32_t take_bf16(float &a, float &b) {
   return p;
 }
 
-// beta, e^G, q.k of a node itself, its list: first entry << 8 | entries
-struct Node {
-  float beta, from_state, own;
-  int list;
-};
+__device__ __forceinline__ void st8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("{\n .reg .b64 x, y, z;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n mov.b64 z, {%6, %7};\n"
+      " fma.rn.f32x2 z, x, y, z;\n mov.b64 {%0, %1}, z;\n}\n"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return r;
+}
+// acc[i] += row[i] x for the entries FIRST and up of 16, in pairs.
+template <int FIRST>
+__device__ __forceinline__ void add_row(float2 (&acc)[8], const float *row, float x) {
+#pragma unroll
+  for (int i = FIRST / 4; i < 4; ++i) {
+    const float4 c = *reinterpret_cast<const float4 *>(row + 4 * i);
+    if (2 * (2 * i + 1) > FIRST) acc[2 * i] = fma2(make_float2(c.x, c.y), make_float2(x, x), acc[2 * i]);
+    acc[2 * i + 1] = fma2(make_float2(c.z, c.w), make_float2(x, x), acc[2 * i + 1]);
+  }
+}
+template <int I>
+__device__ __forceinline__ float entry(const float2 (&x)[8]) {
+  return I & 1 ? x[I / 2].y : x[I / 2].x;
+}
+// Nodes I and up of 16: r and w hold what the nodes before them add; d takes their column of T.
+template <int I>
+__device__ __forceinline__ void solve(float2 (&r)[8], float2 (&w)[8], float (&d)[16], const float *sn, const float *sa,
+                                      int pitch, const float *beta, int unit) {
+  d[I] = beta[I] * ((unit == I ? 1.f : 0.f) - entry<I>(r));
+  if constexpr (I < 15) add_row<I + 1>(r, sn + I * pitch, d[I]);
+  add_row<I>(w, sa + I * pitch, d[I]);
+  if constexpr (I < 15) solve<I + 1>(r, w, d, sn, sa, pitch, beta, unit);
+}
+
+// Products of three-term operands whose order is at most 2^-16 (2^-24 is left of their sum), small first.
+constexpr int kProducts = 6;
+__device__ constexpr int kTermA[kProducts] = {2, 1, 0, 1, 0, 0}, kTermB[kProducts] = {0, 1, 2, 0, 1, 0};
 
 template <typename T, typename TO, int C>
-__global__ void __launch_bounds__(kTreeThreads, C == 64 ? 2 : 4) verify_tree_kernel(TreeParams p) {
+__global__ void __launch_bounds__(TreeCfg<T, C>::THREADS, TreeCfg<T, C>::CTAS) verify_tree_kernel(TreeParams p) {
   using F = TreeCfg<T, C>;
+  constexpr int kTree = 32 * F::TREE_WARPS;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(16) Node nodes[C];
-  __shared__ uint64_t above[C];
-  __shared__ float2 path[C];  // G in two floats
-  __shared__ int up[C], sum0;
-  __shared__ float gates[C];
-  __shared__ uint64_t bar;
+  __shared__ uint64_t above[C];    // a node's ancestors, itself among them
+  __shared__ float2 path[C];       // G in two floats
+  __shared__ float from_state[C];  // e^G
+  __shared__ float gates[C], beta[C];
+  __shared__ int up[C];
+  __shared__ uint64_t bar_gram, bar_s, bar_out;
   __shared__ uint32_t tmem_slot;
   __shared__ int dead_flag;
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-  uint8_t *qk = smem;
-  T *sv = reinterpret_cast<T *>(smem + F::QK);
-  float *sd = reinterpret_cast<float *>(smem + F::QK + F::V);
-  float2 *coef = reinterpret_cast<float2 *>(smem + F::QK + F::V + F::DELTA);
-  uint8_t *which = reinterpret_cast<uint8_t *>(coef + F::PAIRS);
-  const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
+  // of key m and node t, at m ROW + t: the factors of delta_m in delta_t and in o_t; then W and T
+  float *sn = reinterpret_cast<float *>(smem + F::N_AT), *sa = reinterpret_cast<float *>(smem + F::A_AT);
+  T *sv = reinterpret_cast<T *>(smem + F::V_AT);
+  const int tid = threadIdx.x, warp = uniform(tid >> 5);
   volatile int *dead = &dead_flag;
 
   if (warp == 0) tc::alloc<F::COLS>(&tmem_slot);
   if (tid == 32) {
-    mbar_init(&bar, 1);
+    mbar_init(&bar_gram, 1);
+    mbar_init(&bar_s, 1);
+    mbar_init(&bar_out, 1);
     mbar_fence_init();
     dead_flag = 0;
   }
@@ -122,9 +171,9 @@ __global__ void __launch_bounds__(kTreeThreads, C == 64 ? 2 : 4) verify_tree_ker
   const int t_n = min(eos - bos, C);
 
   // the state's first 64 keys, then the rows of q, k and v
-  const float *state = p.state_in ? p.state_in + ((size_t)n * p.hv + h) * kD * kD + tid : nullptr;
+  const float *state = p.state_in ? p.state_in + ((size_t)n * p.hv + h) * kD * kD + (tid & 127) : nullptr;
   float s[2][kKeys];
-  if (state && t_n > 0) {
+  if (state && t_n > 0 && warp < 4) {
 #pragma unroll
     for (int c = 0; c < 2; ++c)
 #pragma unroll
@@ -132,20 +181,20 @@ __global__ void __launch_bounds__(kTreeThreads, C == 64 ? 2 : 4) verify_tree_ker
   }
   const T *q = static_cast<const T *>(p.q), *k = static_cast<const T *>(p.k), *v = static_cast<const T *>(p.v);
   if (F::TERMS == 1) {
-#pragma unroll 4
-    for (int e = tid; e < 2 * C * 16; e += kTreeThreads) {
+#pragma unroll 2
+    for (int e = tid; e < 2 * C * 16; e += F::THREADS) {
       const int row = e >> 4, unit = e & 15, t = row & (C - 1);
       const T *src = (row < C ? q : k) + ((size_t)(bos + (t < t_n ? t : 0)) * p.hk + kh) * kD + unit * 8;
-      cp_async16(qk + (unit >> 3) * F::CHUNK + tile_off(row, unit & 7), src, t < t_n ? 16 : 0);
+      cp_async16(smem + (unit >> 3) * F::CHUNK + tile_off(row, unit & 7), src, t < t_n ? 16 : 0);
     }
   } else {
-#pragma unroll 4
-    for (int e = tid; e < 2 * C * 32; e += kTreeThreads) {
+#pragma unroll 2
+    for (int e = tid; e < 2 * C * 32; e += F::THREADS) {
       const int row = e >> 5, quad = e & 31, t = row & (C - 1);
       float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
       if (t < t_n)
         x = *reinterpret_cast<const float4 *>((row < C ? q : k) + ((size_t)(bos + t) * p.hk + kh) * kD + quad * 4);
-      uint8_t *at = qk + (quad >> 4) * F::CHUNK + tile_off(row, (quad & 15) >> 1) + (quad & 1) * 8;
+      uint8_t *at = smem + (quad >> 4) * F::CHUNK + tile_off(row, (quad & 15) >> 1) + (quad & 1) * 8;
 #pragma unroll
       for (int term = 0; term < 3; ++term) {
         uint2 w;
@@ -156,7 +205,7 @@ __global__ void __launch_bounds__(kTreeThreads, C == 64 ? 2 : 4) verify_tree_ker
     }
   }
   constexpr int kUnits = kD * (int)sizeof(T) / 16;  // of a row of v
-  for (int e = tid; e < t_n * kUnits; e += kTreeThreads) {
+  for (int e = tid; e < t_n * kUnits; e += F::THREADS) {
     const int t = e / kUnits, unit = e % kUnits;
     cp_async16(reinterpret_cast<uint8_t *>(sv) + e * 16,
                reinterpret_cast<const uint8_t *>(v + ((size_t)(bos + t) * p.hv + h) * kD) + unit * 16, 16);
@@ -164,40 +213,33 @@ __global__ void __launch_bounds__(kTreeThreads, C == 64 ? 2 : 4) verify_tree_ker
   cp_async_commit();
 
   // ancestors, path sums, and the places of the lists
-  float beta = 0.f;
-  if (tid < t_n) {
-    up[tid] = p.parents[bos + tid];
-    gates[tid] = p.g[(size_t)(bos + tid) * p.hv + h];
-    beta = p.beta[(size_t)(bos + tid) * p.hv + h];
-  }
-  sd[C * kD + tid] = 0.f;
-  __syncthreads();
-  int entries = 0, list = 0;
-  uint64_t mine = 0;
-  if (tid < C) {
+  const int j = tid - kColumns;  // of a thread of the tree: its node, and its key
+  if (warp >= 4) {
+    const bool node = j < t_n;
+    if (node) {
+      up[j] = p.parents[bos + j];
+      gates[j] = p.g[(size_t)(bos + j) * p.hv + h];
+    }
+    bar_sync(3, kTree);
+    uint64_t mine = 0;
     float hi = 0.f, lo = 0.f;
-    if (tid < t_n) {
-      for (int j = tid, next; ; j = next) {  // (goes down at every step)
-        mine |= 1ull << j;
-        const float x = gates[j], y = hi + x, z = y - hi;  // two-sum: y + (what it lost) = hi + x
+    if (node) {
+      for (int i = j, next; ; i = next) {  // (goes down at every step)
+        mine |= 1ull << i;
+        const float x = gates[i], y = hi + x, z = y - hi;  // two-sum: y + (what it lost) = hi + x
         lo += (hi - (y - z)) + (x - z);
         hi = y;
-        next = up[j];
-        if (next < 0 || next >= j) break;
+        next = up[i];
+        if (next < 0 || next >= i) break;
       }
-      mine &= ~(1ull << tid);
-      above[tid] = mine;
-      path[tid] = make_float2(hi, lo);
     }
-    entries = (__popcll(mine) + 3) & ~3;
-    list = entries;
-#pragma unroll
-    for (int o = 1; o < (C < 32 ? C : 32); o <<= 1) {
-      const int x = __shfl_up_sync(C < 32 ? 0xffffu : 0xffffffffu, list, o);
-      if (lane >= o) list += x;
+    __syncwarp();
+    if (j < C) {
+      above[j] = mine;
+      path[j] = make_float2(hi, lo);
+      from_state[j] = expf(hi + lo);
+      beta[j] = node ? p.beta[(size_t)(bos + j) * p.hv + h] : 0.f;
     }
-    if (tid == 31) sum0 = list;
-    nodes[tid] = Node{beta, expf(hi + lo), 0.f, 0};
   }
   cp_async_wait<0>();
   tc::fence_proxy_async();
@@ -205,154 +247,228 @@ __global__ void __launch_bounds__(kTreeThreads, C == 64 ? 2 : 4) verify_tree_ker
   __syncthreads();
   tc::fence_after();
   const uint32_t tmem = tmem_slot;
-  constexpr uint32_t kA = 2 * C;  // columns: D^T from 0, Gram and then S^T from here
-  const uint64_t tiles = tile_desc(uniform(smem_u32(qk)));
+  const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+  const uint64_t tiles = tile_desc(uniform(smem_u32(smem)));
   constexpr uint32_t kChunk = F::CHUNK >> 4;
-  // terms of a product whose order is at most 2^-16 (2^-24 is left of their sum), small ones first
-  constexpr int kTermA[6] = {2, 1, 0, 1, 0, 0}, kTermB[6] = {0, 1, 2, 0, 1, 0};
-  if (warp == 0 && t_n > 0) {
-    if (elect_one()) {
-      constexpr uint32_t id = tc::idesc(128, C, 1, 0, 0);
-      const uint64_t keys = tiles + (C * 128 >> 4);
-      bool some = false;
+  constexpr uint32_t id_s = tc::idesc(128, 2 * C, 1, 0, 0);
+  if (t_n > 0 && warp >= 4) {
+    // ---------------------------------------------------------------- the tree
+    if (warp == 4) {
+      if (elect_one()) {
+        const uint64_t keys = tiles + (C * 128 >> 4);
+        bool some = false;
 #pragma unroll
-      for (int x = F::TERMS == 1 ? 5 : 0; x < 6; ++x)
+        for (int x = F::TERMS == 1 ? kProducts - 1 : 0; x < kProducts; ++x)
 #pragma unroll
-        for (int i = 0; i < kD / 16; ++i, some = true)
-          tc::mma_ss(tmem + kA, tiles + (kTermA[x] * 2 + i / 4) * kChunk + (i % 4) * 2,
-                     keys + (kTermB[x] * 2 + i / 4) * kChunk + (i % 4) * 2, id, some);
-      tc::commit(&bar);
+          for (int i = 0; i < kD / 16; ++i, some = true)
+            tc::mma_ss(tmem, keys + (kTermA[x] * 2 + i / 4) * kChunk + (i % 4) * 2,
+                       tiles + (kTermB[x] * 2 + i / 4) * kChunk + (i % 4) * 2, id_s, some);
+        tc::commit(&bar_gram);
+      }
+      __syncwarp();
     }
-    __syncwarp();
-  }
-  if (tid < t_n) {
-    if (tid >= 32) list += sum0;
-    nodes[tid].list = (list - entries) << 8 | entries;
-    for (int i = __popcll(mine); i < entries; ++i) {
-      coef[list - entries + i] = make_float2(0.f, 0.f);
-      which[list - entries + i] = C;  // the row of zeros
-    }
-  }
-  __syncthreads();
-  uint32_t phase = 0;
-  const uint32_t lanes = tmem + ((uint32_t)(32 * warp) << 16);
-  if (t_n > 0) {
-    wait_bar(&bar, phase, dead, p.err);
+    wait_bar(&bar_gram, 0, dead, p.err);
     tc::fence_after();
-    if (32 * warp < 2 * C) {  // rows of the Gram matrix: of Q, then of K
-      const int t = tid & (C - 1);
-      const bool of_k = tid >= C, row = tid < 2 * C && t < t_n;
-      const uint64_t bits = row ? above[t] : 0;
-      const float2 mine2 = row ? path[t] : make_float2(0.f, 0.f);
-      int at = row ? nodes[t].list >> 8 : 0;
+    const float2 own = path[j & (C - 1)];
 #pragma unroll 1
-      for (int j0 = 0; j0 < t_n; j0 += 16) {
-        uint32_t x[16];
-        ld16(lanes + kA + j0, x);
-        tc::wait_ld();
-        tie(x);
+    for (int t0 = 0; t0 < (t_n + 15) / 16 * 16; t0 += 8) {
+      uint32_t x[8], y[8];
+      ld8(lanes + t0, x);  // (by whole warps: at C = 16 half of the lanes have no key)
+      ld8(lanes + C + t0, y);
+      tc::wait_ld();
+      tie(x);
+      tie(y);
+      float a[8], b[8];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int j = j0 + i;
-          if (bits >> j & 1) {
-            const float2 g = path[j];
-            const float y = __uint_as_float(x[i]) * expf((mine2.x - g.x) + (mine2.y - g.y));
-            if (of_k) coef[at].x = y;
-            else coef[at].y = y, which[at] = j;
-            ++at;
-          }
-          if (row && !of_k && j == t) nodes[t].own = __uint_as_float(x[i]);
+      for (int i = 0; i < 8; ++i) {
+        const int t = t0 + i;
+        const float2 g = path[t];
+        const float decay = expf((g.x - own.x) + (g.y - own.y));
+        const bool on = above[t] >> j & 1;  // (its own: decay 1, and no factor of delta)
+        a[i] = on ? __uint_as_float(x[i]) * decay : 0.f;
+        b[i] = on && t != j ? __uint_as_float(y[i]) * decay : 0.f;
+      }
+      if (j < C) {
+#pragma unroll
+        for (int i = 0; i < 8; i += 4) {
+          *reinterpret_cast<float4 *>(sa + j * F::ROW + t0 + i) = make_float4(a[i], a[i + 1], a[i + 2], a[i + 3]);
+          *reinterpret_cast<float4 *>(sn + j * F::ROW + t0 + i) = make_float4(b[i], b[i + 1], b[i + 2], b[i + 3]);
         }
       }
     }
-    phase ^= 1;
+    tc::fence_before();
+    bar_arrive(1, kTree + 32);  // D^T's columns are free
+    bar_sync(3, kTree);
+    // column j of T and W, 16 nodes at a time; they take the place of the factors that have been used
+#pragma unroll 1
+    for (int t0 = 0; t0 < t_n; t0 += 16) {
+      float2 r[8] = {}, w[8] = {};
+      float d[16];
+      if (j < C) {
+#pragma unroll 1
+        for (int m = 0; m < t0; m += 4) {
+          const float4 x = *reinterpret_cast<const float4 *>(sa + j * F::ROW + m);
+          const float xs[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            add_row<0>(r, sn + (m + i) * F::ROW + t0, xs[i]);
+            add_row<0>(w, sa + (m + i) * F::ROW + t0, xs[i]);
+          }
+        }
+        solve<0>(r, w, d, sn + t0 * F::ROW + t0, sa + t0 * F::ROW + t0, F::ROW, beta + t0, j - t0);
+      }
+      bar_sync(3, kTree);
+      if (j < C) {
+#pragma unroll
+        for (int i = 0; i < 16; i += 4) {
+          *reinterpret_cast<float4 *>(sa + j * F::ROW + t0 + i) = make_float4(d[i], d[i + 1], d[i + 2], d[i + 3]);
+          *reinterpret_cast<float4 *>(sn + j * F::ROW + t0 + i) =
+              make_float4(w[i / 2].x, w[i / 2].y, w[i / 2 + 1].x, w[i / 2 + 1].y);
+        }
+      }
+    }
+    bar_sync(3, kTree);
+    // [W; T] in three terms over the tiles, which the products with S have read by then: 8-row x 16-byte
+    // core matrices, rows of a key column contiguous
+    if (state) wait_bar(&bar_s, 0, dead, p.err);
+    const int keys16 = (t_n + 15) / 16 * 16;
+#pragma unroll 2
+    for (int e = j; e < keys16 * (C / 2); e += kTree) {
+      const int t = e & (C - 1), c = 2 * (e / C);
+      const float *a = sn + c * F::ROW + t, *b = sa + c * F::ROW + t;
+      float a0 = a[0], a1 = a[F::ROW], b0 = b[0], b1 = b[F::ROW];
+      uint8_t *at = smem + (c >> 3) * (2 * C * 16) + t * 16 + (c & 7) * 2;
+#pragma unroll
+      for (int term = 0; term < 3; ++term) {
+        *reinterpret_cast<uint32_t *>(at + term * F::WT_TERM) = take_bf16(a0, a1);
+        *reinterpret_cast<uint32_t *>(at + term * F::WT_TERM + C * 16) = take_bf16(b0, b1);
+      }
+    }
+    tc::fence_proxy_async();
+  } else if (t_n > 0) {
+    // ---------------------------------------------------------------- D^T = S^T [Q; K]^T
+    if (state) {
+#pragma unroll 1
+      for (int c0 = 0; c0 < kD / kKeys; c0 += 2) {
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const int c = c0 + half;
+          float(&x)[kKeys] = s[half];
+#pragma unroll
+          for (int term = 0; term < 3; ++term) {
+            uint32_t w[kKeys / 2];
+#pragma unroll
+            for (int i = 0; i < kKeys / 2; ++i) w[i] = take_bf16(x[2 * i], x[2 * i + 1]);
+            if (term == 0 && c > 0) {  // the products of the step before have read their operand
+              wait_bar(&bar_out, (c - 1) & 1, dead, p.err);
+              tc::fence_after();
+            }
+            tc::st16(lanes + F::A_COL + 16 * term, w);
+          }
+          if (c0 == 0) {
+#pragma unroll
+            for (int i = 0; i < kKeys; ++i) x[i] = __ldcs(state + ((c + 2) * kKeys + i) * kD);
+          }
+          tc::wait_st();
+          tc::fence_before();
+          bar_sync(2, kColumns);
+          if (warp == 0) {
+            if (c == 0) bar_sync(1, kTree + 32);  // the Gram products have been read
+            tc::fence_after();
+            if (elect_one()) {
+              uint32_t some = c > 0;
+#pragma unroll
+              for (int y = 0; y < kProducts; ++y) {
+                if (F::TERMS == 1 && kTermB[y] > 0) continue;
+#pragma unroll
+                for (int i = 0; i < kKeys / 16; ++i, some = 1)
+                  tc::mma_ts(tmem, tmem + F::A_COL + 16 * kTermA[y] + 8 * i,
+                             tiles + (kTermB[y] * 2 + (c0 >> 1)) * kChunk + (half * 2 + i) * 2, id_s, some);
+              }
+              tc::commit(c + 1 < kD / kKeys ? &bar_out : &bar_s);
+            }
+            __syncwarp();
+          }
+        }
+      }
+      wait_bar(&bar_s, 0, dead, p.err);
+      tc::fence_after();
+    } else {
+      if (warp == 0) bar_sync(1, kTree + 32);
+      bar_sync(2, kColumns);
+      tc::fence_after();
+    }
+    // r, and what it will be added to
+#pragma unroll 1
+    for (int t0 = 0; t0 < t_n; t0 += 16) {
+      uint32_t x[16], y[16];
+      if (state) {
+        ld16(lanes + t0, x);
+        ld16(lanes + C + t0, y);
+        tc::wait_ld();
+        tie(x);
+        tie(y);
+      }
+      float r[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int t = t0 + i;
+        const bool node = t < t_n;
+        const float scale = node && state ? from_state[t] : 0.f;
+        r[i] = node ? Elem<T>::load(sv + t * kD + tid) : 0.f;
+        if (state) r[i] = fmaf(-scale, __uint_as_float(y[i]), r[i]);
+        x[i] = state ? __float_as_uint(scale * __uint_as_float(x[i])) : 0u;
+        y[i] = 0u;
+      }
+      tc::st16(lanes + t0, x);
+      tc::st16(lanes + C + t0, y);
+#pragma unroll
+      for (int term = 0; term < 3; ++term) {
+        uint32_t w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = take_bf16(r[2 * i], r[2 * i + 1]);
+        st8(lanes + F::A_COL + term * (C / 2) + t0 / 2, w);
+      }
+    }
+    tc::wait_st();
   }
   tc::fence_before();
   __syncthreads();
-  tc::fence_after();
-
-  // D^T = S^T [Q; K]^T
-  if (state && t_n > 0) {
-    constexpr uint32_t id = tc::idesc(128, 2 * C, 1, 0, 0);
+  if (t_n > 0 && warp < 4) {
+    if (warp == 0) {
+      tc::fence_after();
+      const uint64_t wt = tc::sdesc(uniform(smem_u32(smem)), 2 * C * 16, 128);
+      const int steps = (t_n + 15) / 16;
+      if (elect_one()) {
 #pragma unroll
-    for (int c = 0; c < kD / kKeys; ++c) {
-      float(&x)[kKeys] = s[c & 1];
-#pragma unroll
-      for (int term = 0; term < 3; ++term) {
-        uint32_t w[kKeys / 2];
-#pragma unroll
-        for (int i = 0; i < kKeys / 2; ++i) w[i] = take_bf16(x[2 * i], x[2 * i + 1]);
-        if (term == 0 && c > 0) {  // the products of the step before have read their operand
-          wait_bar(&bar, phase, dead, p.err);
-          phase ^= 1;
-          tc::fence_after();
-        }
-        tc::st16(lanes + kA + 16 * term, w);
-      }
-      if (c + 2 < kD / kKeys) {
-#pragma unroll
-        for (int i = 0; i < kKeys; ++i) x[i] = __ldcs(state + ((c + 2) * kKeys + i) * kD);
-      }
-      tc::wait_st();
-      tc::fence_before();
-      __syncthreads();
-      if (warp == 0) {
-        tc::fence_after();
-        if (elect_one()) {
-          bool some = c > 0;
-#pragma unroll
-          for (int y = 0; y < 6; ++y) {
-            if (F::TERMS == 1 && kTermB[y] > 0) continue;
-#pragma unroll
-            for (int i = 0; i < kKeys / 16; ++i, some = true)
-              tc::mma_ts(tmem, tmem + kA + 16 * kTermA[y] + 8 * i,
-                         tiles + (kTermB[y] * 2 + c / 2) * kChunk + ((c % 2) * 2 + i) * 2, id, some);
-          }
-          tc::commit(&bar);
-        }
-        __syncwarp();
-      }
-    }
-    wait_bar(&bar, phase, dead, p.err);
-    tc::fence_after();
-  }
-
-  // the nodes in order, each thread down its column
-  TO *o = static_cast<TO *>(p.o);
+        for (int y = 0; y < kProducts; ++y)
 #pragma unroll 1
-  for (int t0 = 0; t0 < t_n; t0 += 8) {
-    uint32_t qs[8] = {}, ks[8] = {};
-    if (state) {
-      ld8(lanes + t0, qs);
-      ld8(lanes + C + t0, ks);
-      tc::wait_ld();
-      tie(qs);
-      tie(ks);
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int t = t0 + i;
-      if (t < t_n) {
-        const Node node = nodes[t];
-        float below = 0.f, out = 0.f;
-        const int first = node.list >> 8, last = first + (node.list & 255);
-        for (int e = first; e < last; e += 4) {
-          const uint32_t w = *reinterpret_cast<const uint32_t *>(which + e);
-          const float4 c0 = *reinterpret_cast<const float4 *>(coef + e), c1 = *reinterpret_cast<const float4 *>(coef + e + 2);
-          const float d0 = sd[(w & 255) * kD + tid], d1 = sd[(w >> 8 & 255) * kD + tid],
-                      d2 = sd[(w >> 16 & 255) * kD + tid], d3 = sd[(w >> 24) * kD + tid];
-          below = fmaf(c0.x, d0, below), out = fmaf(c0.y, d0, out);
-          below = fmaf(c0.z, d1, below), out = fmaf(c0.w, d1, out);
-          below = fmaf(c1.x, d2, below), out = fmaf(c1.y, d2, out);
-          below = fmaf(c1.z, d3, below), out = fmaf(c1.w, d3, out);
-        }
-        const float d =
-            node.beta * (Elem<T>::load(sv + t * kD + tid) - fmaf(node.from_state, __uint_as_float(ks[i]), below));
-        sd[t * kD + tid] = d;
-        const size_t at = ((size_t)(bos + t) * p.hv + h) * kD + tid;
-        p.delta[at] = d;
-        Elem<TO>::store(o + at, fmaf(node.own, d, fmaf(node.from_state, __uint_as_float(qs[i]), out)));
+          for (int i = 0; i < steps; ++i)
+            tc::mma_ts(tmem, tmem + F::A_COL + kTermA[y] * (C / 2) + 8 * i,
+                       wt + ((kTermB[y] * F::WT_TERM + i * 2 * (2 * C * 16)) >> 4), id_s, 1);
+        tc::commit(&bar_out);
       }
+      __syncwarp();
+    }
+    wait_bar(&bar_out, state ? 1 : 0, dead, p.err);
+    tc::fence_after();
+    TO *o = static_cast<TO *>(p.o) + ((size_t)bos * p.hv + h) * kD + tid;
+    float *delta = p.delta + ((size_t)bos * p.hv + h) * kD + tid;
+    const size_t row = (size_t)p.hv * kD;
+#pragma unroll 1
+    for (int t0 = 0; t0 < t_n; t0 += 16) {
+      uint32_t x[16], y[16];
+      ld16(lanes + t0, x);
+      ld16(lanes + C + t0, y);
+      tc::wait_ld();
+      tie(x);
+      tie(y);
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (t0 + i < t_n) {
+          Elem<TO>::store(o + (t0 + i) * row, __uint_as_float(x[i]));
+          delta[(t0 + i) * row] = __uint_as_float(y[i]);
+        }
     }
   }
   if (*dead) __nanosleep(1000000);  // products in flight end before tensor memory is given up
@@ -368,7 +484,7 @@ cudaError_t launch(const TreeParams &p, cudaStream_t stream) {
   static std::atomic<uint64_t> allowed{0};
   const cudaError_t err = allow_smem(verify_tree_kernel<T, TO, C>, smem, allowed);
   if (err != cudaSuccess) return err;
-  return launch_dependent(verify_tree_kernel<T, TO, C>, (unsigned)(p.num_seqs * p.hv), kTreeThreads, smem, stream, 1, p);
+  return launch_dependent(verify_tree_kernel<T, TO, C>, (unsigned)(p.num_seqs * p.hv), TreeCfg<T, C>::THREADS, smem, stream, 1, p);
 }
 template <typename T, typename TO>
 cudaError_t by_size(const TreeParams &p, cudaStream_t stream) {
