@@ -14,19 +14,21 @@ namespace {
 // row finds its maximum, its sum of powers and its `top` best logits without the sum being known; the
 // second kernel puts the beams together.
 //
-// Pass 1: a CTA takes a part of a row, in steps of 256 threads x 32 values.  A thread keeps its own m and l
-// with one rescaling a step.  What may still be among the best is told by a threshold: k lists whose best
-// reach it hold k values that do, so the k-th largest of the lists' maxima (a list: what some threads
-// have seen in this step, or what has been kept so far) is one, and no more than k lists have
-// values above it.  Values that pass are appended to a buffer in shared memory, and the k best of it are found by
-// counting how many are better.  Equal logits go by index: the keys are (value, index) in 64 bits, all
-// different, so however the values lie the buffer holds what comes.
+// Pass 1: a CTA takes a part of a row, in steps of 256 threads x MOST values, the next step's loads under way
+// while this one's are looked at.  A thread keeps its own m and l with one rescaling a step.  What may still be
+// among the best is told by a limit: once `top` are kept the last of them, and where more threads than that
+// reach it, a value that at least `top` threads' largest reach, found by halving the range of their largest
+// (a barrier that counts for each halving; some 8 of them in a part's first step, seldom any later).  Values that
+// pass are appended to a buffer in shared memory, and the k best of it found by counting how many are better.
+// Equal logits go by index: the keys there are (value, index) in 64 bits, all different.  Where equal values
+// pass in numbers that the buffer does not hold, the limit is the top-th largest of the threads' largest keys, which
+// no more than `top` threads have values above.
 //
 // Bound by HBM (the logits are read once) where rows are many; by latency where they are few.
 
 constexpr int kThreads = 256;
-constexpr int kVec = 4;                   // 16-byte loads of a thread and step
 constexpr unsigned kAll = 0xffffffffu;
+constexpr float kLog2e = 1.4426950408889634f;
 
 // Order-preserving images of floats (larger float, larger image; NaN as -inf, -0 as 0).
 __device__ __forceinline__ uint32_t image(float x) {
@@ -47,22 +49,46 @@ __device__ __forceinline__ double value_of(uint64_t u) {
   return __longlong_as_double((long long)(u >> 63 ? u & ~(1ull << 63) : ~u));
 }
 
-template <typename T>
-struct Logits;
-template <>
-struct Logits<float> {
-  static constexpr int PER = 4;
-  static __device__ __forceinline__ void unpack(const uint4 &v, float *x) {
-    x[0] = __uint_as_float(v.x), x[1] = __uint_as_float(v.y), x[2] = __uint_as_float(v.z), x[3] = __uint_as_float(v.w);
+// A thread's values of a step: 16-byte units as loaded, where every row starts on a 16-byte boundary; else single
+// values, coalesced over the threads.  Which thread has which value is the same for all rows of a call, so that
+// equal rows give equal sums.
+template <typename T, bool ALIGNED, int VEC>
+struct Values {
+  static constexpr int PER = 16 / (int)sizeof(T);
+  static constexpr int MOST = VEC * PER, UNIT = ALIGNED ? PER : 1;  // values, consecutive ones
+  uint32_t w[ALIGNED ? VEC * 4 : MOST];
+
+  static __device__ __forceinline__ int index(int base, int i) {
+    return base + ((i / UNIT) * kThreads + (int)threadIdx.x) * UNIT + i % UNIT;
   }
-};
-template <>
-struct Logits<__nv_bfloat16> {
-  static constexpr int PER = 8;
-  static __device__ __forceinline__ void unpack(const uint4 &v, float *x) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  // those from `base` on of x[0 .. end), -inf beyond
+  __device__ __forceinline__ void load(const T *x, int base, int end) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) x[2 * i] = __uint_as_float(w[i] << 16), x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    for (int i = 0; i < MOST; i += UNIT) {
+      const int at = index(base, i);
+      if (ALIGNED && at + UNIT <= end) {
+        const uint4 v = __ldcs(reinterpret_cast<const uint4 *>(x + at));
+        uint32_t *to = w + i / UNIT * 4;
+        to[0] = v.x, to[1] = v.y, to[2] = v.z, to[3] = v.w;
+      } else if (!ALIGNED) {
+        w[i] = __float_as_uint(at < end ? Elem<T>::load(x + at) : -CUDART_INF_F);
+      } else if (sizeof(T) == 4) {
+#pragma unroll
+        for (int e = 0; e < UNIT; ++e)
+          w[i + e] = __float_as_uint(at + e < end ? Elem<T>::load(x + at + e) : -CUDART_INF_F);
+      } else {
+#pragma unroll
+        for (int e = 0; e < UNIT; e += 2) {
+          const float lo = at + e < end ? Elem<T>::load(x + at + e) : -CUDART_INF_F;
+          const float hi = at + e + 1 < end ? Elem<T>::load(x + at + e + 1) : -CUDART_INF_F;
+          w[(i + e) / 2] = __float_as_uint(lo) >> 16 | (__float_as_uint(hi) & 0xffff0000u);
+        }
+      }
+    }
+  }
+  __device__ __forceinline__ float operator[](int i) const {
+    if (!ALIGNED || sizeof(T) == 4) return __uint_as_float(w[i]);
+    return __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
   }
 };
 
@@ -71,53 +97,61 @@ __device__ __forceinline__ void rank_keys(const uint64_t *keys, int count, uint6
   for (int i = threadIdx.x; i < count; i += kThreads) {
     const uint64_t mine = keys[i];
     int better = 0;
+#pragma unroll 4
     for (int j = 0; j < count; ++j) better += keys[j] > mine;
     if (better < top) out[better] = mine;
   }
 }
 
-constexpr float kLog2e = 1.4426950408889634f;
+// A value that at least `top` threads' reach, and not many more if it can be helped: `mine` of the threads that take
+// part (0 for the others), of which there are `top` at least.
+__device__ __forceinline__ uint32_t common_limit(uint32_t mine, int top, uint32_t (&sh)[2][kThreads / 32]) {
+  const uint32_t big = __reduce_max_sync(kAll, mine), small = __reduce_min_sync(kAll, mine == 0 ? ~0u : mine);
+  if ((threadIdx.x & 31) == 0) sh[0][threadIdx.x >> 5] = big, sh[1][threadIdx.x >> 5] = small;
+  __syncthreads();
+  uint32_t lo = ~0u, hi = 0;
+#pragma unroll
+  for (int i = 0; i < kThreads / 32; ++i) hi = max(hi, sh[0][i]), lo = min(lo, sh[1][i]);
+  while (lo < hi) {
+    const uint32_t mid = lo + (hi - lo + 1) / 2;
+    const int count = __syncthreads_count(mine >= mid);
+    if (count >= top) lo = mid;
+    else hi = mid - 1;
+    if (count >= top && count <= top + top / 2 + 8) break;
+  }
+  return lo;
+}
 
-// ALIGNED: every row starts on a 16-byte boundary, and a thread's loads are 16 bytes; else they are single
-// values, coalesced over the threads.  Which thread has which value is the same for all rows of a
-// call, so that equal rows give equal sums.
-template <typename T, bool ALIGNED>
-__global__ void __launch_bounds__(kThreads, 3) beam_rows_kernel(BeamParams p) {
-  constexpr int MOST = kVec * Logits<T>::PER;           // values of a thread and step
-  constexpr int UNIT = ALIGNED ? Logits<T>::PER : 1;    // consecutive ones
-  __shared__ uint64_t best[64];  // the best so far, largest first (0: none)
+template <typename T, bool ALIGNED, int VEC>
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && ALIGNED && VEC == 4 ? 3 : 4) beam_rows_kernel(BeamParams p) {
+  using V = Values<T, ALIGNED, VEC>;
+  constexpr int MOST = V::MOST, STEP = MOST * kThreads;
+  __shared__ uint64_t best[64];  // the best so far, largest first
   __shared__ uint64_t heads[kThreads], sh_limit;
+  __shared__ uint32_t sh_range[2][kThreads / 32];
   __shared__ int sh_count;
   __shared__ float2 sums[kThreads / 32];
   extern __shared__ uint64_t buffer[];  // what may count: `kept` from before, then new ones
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int row = blockIdx.x / p.parts, part = blockIdx.x - row * p.parts, top = p.top;
+  const int row = blockIdx.x / p.parts, part = blockIdx.x - row * p.parts, top = p.top, room = top * MOST;
   if (tid < 64) best[tid] = 0;
   if (tid == 0) sh_count = 0;
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   if ((p.finished && p.finished[row]) || !isfinite(p.scores[row])) return;  // (its logits do not count)
   const T *x = static_cast<const T *>(p.logits) + (long long)row * p.row_stride;
-  const int units = (p.vocab + UNIT - 1) / UNIT;
-  const int u0 = (int)((long long)units * part / p.parts), u1 = (int)((long long)units * (part + 1) / p.parts);
-  const int lists = top <= 16 ? 32 : kThreads, per_list = kThreads / lists;  // (32 lists are enough for few)
-  const int end = min(u1 * UNIT, p.vocab);
+  const int units = (p.vocab + V::UNIT - 1) / V::UNIT;
+  const int from = (int)((long long)units * part / p.parts) * V::UNIT;
+  const int end = min((int)((long long)units * (part + 1) / p.parts) * V::UNIT, p.vocab);
   float m = -CUDART_INF_F, l = 0.f;
   int kept = 0;
+  V y, ahead;
+  ahead.load(x, from, end);
   __syncthreads();
-  for (int base = u0; base < u1; base += kThreads * (MOST / UNIT)) {
-    auto index = [&](int i) { return (base + (i / UNIT) * kThreads + tid) * UNIT + i % UNIT; };
-    float y[MOST];
-#pragma unroll
-    for (int i = 0; i < MOST; i += UNIT) {
-      const int at = index(i);
-      if (ALIGNED && at + UNIT <= end) {
-        Logits<T>::unpack(__ldcs(reinterpret_cast<const uint4 *>(x + at)), y + i);
-      } else {
-#pragma unroll
-        for (int e = 0; e < UNIT; ++e) y[i + e] = at + e < end ? Elem<T>::load(x + at + e) : -CUDART_INF_F;
-      }
-    }
+#pragma unroll 1
+  for (int base = from; base < end; base += STEP) {
+    y = ahead;
+    if (base + STEP < end) ahead.load(x, base + STEP, end);
     float big = y[0];
 #pragma unroll
     for (int i = 1; i < MOST; ++i) big = fmaxf(big, y[i]);
@@ -133,41 +167,56 @@ __global__ void __launch_bounds__(kThreads, 3) beam_rows_kernel(BeamParams p) {
     l = l * ex2((m - ref) * kLog2e) + (sum + sum2);
     m = m1;
 
-    // threads with a value that may count; with few of them all such values are taken
-    const uint64_t last = best[top - 1];  // 0 while there are fewer
-    const bool some = last == 0 || big >= value_of((uint32_t)(last >> 32));
+    // Threads with a value that may count.  Equal ones from here on come after those that are kept.
+    const float last = kept == top ? value_of((uint32_t)(best[top - 1] >> 32)) : 0.f;
+    const bool some = kept < top ? V::index(base, 0) < end : big > last;
     const int busy = __syncthreads_count(some);
     if (busy == 0) continue;
-    uint64_t limit = last;
-    if (busy > top) {
-      uint64_t head = 0;
-      if (some) {
-#pragma unroll
-        for (int i = 0; i < MOST; ++i)
-          if (index(i) < end) head = max(head, key_of(y[i], index(i)));
-      }
-      for (int o = 1; o < per_list; o <<= 1) head = max(head, __shfl_xor_sync(kAll, head, o));
-      if (tid % per_list == 0) heads[tid / per_list] = head;
-      __syncthreads();
-      if (tid < lists) {  // the top-th largest; 0 where fewer lists have a value
-        const uint64_t mine = heads[tid];
-        int better = 0;
-        for (int j = 0; j < lists; ++j) better += heads[j] > mine;
-        if (better < top && (better == top - 1 || mine == 0)) sh_limit = mine;
-      }
-      __syncthreads();
-      limit = max(limit, sh_limit);
-    }
-    if (some) {
+    float limit = -CUDART_INF_F;
+    if (busy > top) limit = value_of(common_limit(some ? image(big) : 0u, top, sh_range));
+    if (some && big >= limit) {
 #pragma unroll
       for (int i = 0; i < MOST; ++i) {
-        const uint64_t key = key_of(y[i], index(i));
-        if (index(i) < end && key >= limit) buffer[kept + atomicAdd(&sh_count, 1)] = key;
+        const int at = V::index(base, i);
+        if (y[i] >= limit && at < end && (kept < top || y[i] > last)) {
+          const int to = atomicAdd(&sh_count, 1);
+          if (to < room) buffer[kept + to] = key_of(y[i], at);
+        }
       }
     }
     __syncthreads();
-    const int total = kept + sh_count;
-    if (total > kept) {
+    int fresh = sh_count;
+    if (fresh > room) {  // (by so many equal values)
+      __syncthreads();
+      uint64_t head = 0;
+      if (some) {
+#pragma unroll 1
+        for (int i = 0; i < MOST; ++i) {
+          const int at = V::index(base, i);
+          if (at < end) head = max(head, key_of(Elem<T>::load(x + at), at));
+        }
+      }
+      heads[tid] = head;
+      if (tid == 0) sh_count = 0;
+      __syncthreads();
+      int better = 0;
+      for (int j = 0; j < kThreads; ++j) better += heads[j] > head;
+      // the top-th largest; 0 where fewer threads have a value
+      if (better < top && (better == top - 1 || head == 0)) sh_limit = head;
+      __syncthreads();
+      if (some && head >= sh_limit) {
+#pragma unroll 1
+        for (int i = 0; i < MOST; ++i) {
+          const int at = V::index(base, i);
+          const uint64_t key = at < end ? key_of(Elem<T>::load(x + at), at) : 0;
+          if (key >= sh_limit && key > (kept == top ? best[top - 1] : 0)) buffer[kept + atomicAdd(&sh_count, 1)] = key;
+        }
+      }
+      __syncthreads();
+      fresh = sh_count;
+    }
+    if (fresh > 0) {
+      const int total = kept + fresh;
       rank_keys(buffer, total, best, top);
       kept = min(top, total);
       __syncthreads();
@@ -204,37 +253,40 @@ __device__ __forceinline__ bool better(const Cand &a, const Cand &b) {
   return a.score > b.score || (a.score == b.score && a.place < b.place);
 }
 
-// Pass 2: a request.  Each (beam, part) list is in order, so the top-th best of the lists' heads bounds what
-// counts, and the lists are walked down to it.
-constexpr int kHeads = 4096;  // lists whose heads are kept
+// Pass 2: a request.  Each (beam, part) list is in order, so a score that `top` of the lists' heads reach bounds what
+// counts, and the lists are walked down to it, four entries at a time.  Sums in float64 are few: a warp's take 16
+// cycles on this GPU.
+constexpr int kLists = 4096;  // lists of a request at most
+constexpr int kPool = 1024;   // what may count, but for equal scores
 __global__ void __launch_bounds__(kThreads) beam_join_kernel(BeamParams p) {
-  __shared__ double shift[64];     // score_w - lse_w: what a logit's score adds; NaN: see kind
-  __shared__ int kind[64];         // 0: as the logits say; 1: every continuation -inf; 2: finished
-  __shared__ Cand bound;
-  __shared__ int count;
+  __shared__ double shift[64];  // score_w - lse_w: what a logit's score adds
+  __shared__ int kind[64];      // 0: as the logits say; 1: every continuation -inf; 2: finished
+  __shared__ uint32_t sh_range[2][kThreads / 32];
+  __shared__ Cand sh_bound;
+  __shared__ int sh_count;
   extern __shared__ uint64_t raw[];
   const int tid = threadIdx.x, group = blockIdx.x, w_n = p.beams, parts = p.parts, top = p.top;
-  const int lists = w_n * parts;
-  Cand *heads = reinterpret_cast<Cand *>(raw);        // [lists]
-  Cand *pool = heads + lists;                         // [top * top]
+  const int lists = w_n * parts, room = max(kPool, top * top);
+  Cand *heads = reinterpret_cast<Cand *>(raw);  // [lists]
+  Cand *pool = heads + lists;                   // [room]
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
-  if (tid == 0) count = 0;
-  for (int w = tid >> 5; w < w_n; w += kThreads / 32) {  // a warp a beam
-    const int row = group * w_n + w, lane = tid & 31;
+  if (tid == 0) sh_count = 0;
+  {  // four threads a beam
+    const int w = tid >> 2, row = group * w_n + w;
+    const bool here = w < w_n;
     float m = -CUDART_INF_F;
-    for (int i = lane; i < parts; i += 32) m = fmaxf(m, p.sums[(long long)row * parts + i].x);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, o));
-    const float r = m == -CUDART_INF_F ? 0.f : m;
+    for (int i = tid & 3; here && i < parts; i += 4) m = fmaxf(m, p.sums[(long long)row * parts + i].x);
+    m = fmaxf(m, __shfl_xor_sync(kAll, m, 1));
+    m = fmaxf(m, __shfl_xor_sync(kAll, m, 2));
     double l = 0.0;
-    for (int i = lane; i < parts; i += 32) {
+    for (int i = tid & 3; here && i < parts; i += 4) {
       const float2 s = p.sums[(long long)row * parts + i];
-      l += (double)s.y * exp((double)s.x - (double)r);
+      l += (double)(s.y * expf(s.x - (m == -CUDART_INF_F ? 0.f : m)));
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(kAll, l, o);
-    if (lane == 0) {
+    l += __shfl_xor_sync(kAll, l, 1);
+    l += __shfl_xor_sync(kAll, l, 2);
+    if (here && (tid & 3) == 0) {
       const float score = p.scores[row];
       const bool done = p.finished && p.finished[row];
       shift[w] = done ? (double)score : (double)score - ((double)m + log(l));
@@ -259,36 +311,64 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(BeamParams p) {
         return true;
       }
       i = i - 1 < p.pad_token ? i - 1 : i;
-      if (i >= p.vocab) return false;
     }
+    if (i >= p.vocab) return false;
     c = Cand{image(-CUDART_INF), base + (uint32_t)i};
     return true;
   };
-  for (int i = tid; i < lists; i += kThreads)
-    if (!entry(i, 0, heads[i])) heads[i] = Cand{0, ~0u};
-  if (tid == 0) bound = Cand{0, ~0u};
-  __syncthreads();
-  if (lists > top) {
+  uint32_t most = 0;  // of this thread's heads (the images' upper halves)
+  for (int i = tid; i < lists; i += kThreads) {
+    Cand c;
+    if (!entry(i, 0, c)) c = Cand{0, ~0u};
+    heads[i] = c;
+    most = max(most, (uint32_t)(c.score >> 32));
+  }
+  Cand bound{0, ~0u};
+  const int busy = __syncthreads_count(most != 0);
+  if (busy > top) bound.score = (uint64_t)common_limit(most, top, sh_range) << 32;
+  // what is no worse than the bound; a list's head tells whether it has any
+  auto gather = [&]() {
+    for (int i = tid; i < lists; i += kThreads) {
+      Cand c = heads[i];
+      if (c.score == 0 || better(bound, c)) continue;
+      for (int e = 0; e < top; e += 4) {
+        Cand some[4];
+        bool good[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) good[u] = e + u < top && entry(i, e + u, some[u]);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          good[u] = good[u] && !better(bound, some[u]);
+          if (good[u]) {
+            const int to = atomicAdd(&sh_count, 1);
+            if (to < room) pool[to] = some[u];
+          }
+        }
+        if (!good[3]) break;
+      }
+    }
+    __syncthreads();
+    return sh_count;
+  };
+  int n = gather();
+  if (n > room) {  // equal scores: the top-th best head itself
+    __syncthreads();
+    if (tid == 0) sh_count = 0, sh_bound = Cand{0, ~0u};
+    __syncthreads();
     for (int i = tid; i < lists; i += kThreads) {
       const Cand mine = heads[i];
       int b = 0;
       for (int j = 0; j < lists; ++j) b += better(heads[j], mine);
-      if (b == top - 1 && mine.score != 0) bound = mine;
+      if (b == top - 1 && mine.score != 0) sh_bound = mine;
     }
     __syncthreads();
+    bound = sh_bound;
+    n = gather();
   }
-  for (int i = tid; i < lists; i += kThreads) {
-    Cand c = heads[i];
-    for (int e = 0; c.score != 0 && !better(bound, c);) {
-      pool[atomicAdd(&count, 1)] = c;
-      if (++e == top || !entry(i, e, c)) break;
-    }
-  }
-  __syncthreads();
-  const int n = count;
   for (int i = tid; i < n; i += kThreads) {
     const Cand mine = pool[i];
     int b = 0;
+#pragma unroll 4
     for (int j = 0; j < n; ++j) b += better(pool[j], mine);
     if (b < top) {
       const long long at = (long long)group * top + b;
@@ -299,11 +379,15 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(BeamParams p) {
   }
 }
 
+// Values of a thread and step, in 16-byte units: four; one where the rows are few, so that more CTAs share
+// them (2 requests of 4 beams over 32000: see below).
+int vec_of(int rows, int vocab, int per) { return (long long)rows * (vocab / (kThreads * 4 * per)) < 2 * kSms ? 1 : 4; }
+
 // Parts of a row: enough CTAs to fill the GPU three times over, of a step at least, and no more lists
-// a request than the join keeps.
+// a request than the join takes.
 int parts_of(int rows, int beams, int vocab, int step) {
-  const int most = std::max(1, std::min(vocab / step, kHeads / beams));
-  const int fill = (int)((3LL * 3 * kSms + rows - 1) / std::max(rows, 1));
+  const int most = std::max(1, std::min(vocab / step, kLists / beams));
+  const int fill = (int)((3LL * 4 * kSms + rows - 1) / std::max(rows, 1));
   return std::max(1, std::min(most, fill));
 }
 
@@ -346,29 +430,32 @@ __global__ void __launch_bounds__(128) reorder_kernel(ReorderParams p) {
     if (from[w] != w) rows[w * per_row + col] = stage[from[w] * 128 + tid];
 }
 
-template <typename T, bool ALIGNED>
+template <typename T, bool ALIGNED, int VEC>
 cudaError_t select(const BeamParams &p, cudaStream_t stream) {
-  const size_t lists = (size_t)p.top * (p.top <= 16 ? kThreads / 32 : 1);  // threads whose values may all count
-  const size_t rows = sizeof(uint64_t) * (lists * kVec * Logits<T>::PER + p.top);
-  const size_t join = sizeof(Cand) * ((size_t)p.beams * p.parts + (size_t)p.top * p.top);
-  static std::atomic<uint64_t> allowed{0}, allowed2{0};
-  cudaError_t err = allow_smem(beam_rows_kernel<T, ALIGNED>, 64 * 1024, allowed);
-  if (err == cudaSuccess) err = allow_smem(beam_join_kernel, 160 * 1024, allowed2);
+  const size_t rows = sizeof(uint64_t) * (size_t)p.top * (Values<T, ALIGNED, VEC>::MOST + 1);
+  const size_t join = sizeof(Cand) * ((size_t)p.beams * p.parts + std::max(kPool, p.top * p.top));
+  static std::atomic<uint64_t> allowed{0};
+  cudaError_t err = allow_smem(beam_join_kernel, 160 * 1024, allowed);
   if (err == cudaSuccess)
-    err = launch_dependent(beam_rows_kernel<T, ALIGNED>, (unsigned)(p.groups * p.beams * p.parts), kThreads, rows, stream, 1, p);
+    err = launch_dependent(beam_rows_kernel<T, ALIGNED, VEC>, (unsigned)(p.groups * p.beams * p.parts), kThreads, rows, stream, 1, p);
   if (err != cudaSuccess) return err;
   return launch_dependent(beam_join_kernel, (unsigned)p.groups, kThreads, join, stream, 1, p);
 }
 template <typename T>
 cudaError_t by_alignment(const BeamParams &p, cudaStream_t stream) {
-  const bool aligned = reinterpret_cast<uintptr_t>(p.logits) % 16 == 0 && p.row_stride % (16 / (int)sizeof(T)) == 0;
-  return aligned ? select<T, true>(p, stream) : select<T, false>(p, stream);
+  constexpr int per = 16 / (int)sizeof(T);
+  const bool aligned = reinterpret_cast<uintptr_t>(p.logits) % 16 == 0 && p.row_stride % per == 0;
+  if (vec_of(p.groups * p.beams, p.vocab, per) == 1)
+    return aligned ? select<T, true, 1>(p, stream) : select<T, false, 1>(p, stream);
+  // (single values of 16 bits take a register each: half as many)
+  return aligned ? select<T, true, 4>(p, stream) : select<T, false, sizeof(T) == 2 ? 2 : 4>(p, stream);
 }
 
 }  // namespace
 
 int beam_parts(int groups, int beams, int vocab, bool bf16) {
-  return parts_of(groups * beams, beams, vocab, kThreads * kVec * (bf16 ? 8 : 4));
+  const int rows = groups * beams, per = bf16 ? 8 : 4;
+  return parts_of(rows, beams, vocab, kThreads * vec_of(rows, vocab, per) * per);
 }
 
 cudaError_t launch_beam_select(const BeamParams &p, gdn_dtype dtype, cudaStream_t stream) {
