@@ -63,6 +63,20 @@ struct Values {
   }
   // those from `base` on of x[0 .. end), -inf beyond
   __device__ __forceinline__ void load(const T *x, int base, int end) {
+    if (base + MOST * kThreads <= end) {
+      const T *mine = x + base + threadIdx.x * UNIT;
+#pragma unroll
+      for (int i = 0; i < MOST; i += UNIT) {
+        if (ALIGNED) {
+          const uint4 v = __ldcs(reinterpret_cast<const uint4 *>(mine + i * kThreads));
+          uint32_t *to = w + i / UNIT * 4;
+          to[0] = v.x, to[1] = v.y, to[2] = v.z, to[3] = v.w;
+        } else {
+          w[i] = __float_as_uint(Elem<T>::load(mine + i * kThreads));
+        }
+      }
+      return;
+    }
 #pragma unroll
     for (int i = 0; i < MOST; i += UNIT) {
       const int at = index(base, i);
@@ -140,11 +154,24 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && ALIGNED && VEC == 
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   if ((p.finished && p.finished[row]) || !isfinite(p.scores[row])) return;  // (its logits do not count)
   const T *x = static_cast<const T *>(p.logits) + (long long)row * p.row_stride;
-  const int units = (p.vocab + V::UNIT - 1) / V::UNIT;
-  const int from = (int)((long long)units * part / p.parts) * V::UNIT;
-  const int end = min((int)((long long)units * (part + 1) / p.parts) * V::UNIT, p.vocab);
+  const int steps = (p.vocab + STEP - 1) / STEP;  // of the row: parts take whole ones
+  const int from = (int)((long long)steps * part / p.parts) * STEP;
+  const int end = (int)min((long long)((long long)steps * (part + 1) / p.parts) * STEP, (long long)p.vocab);
   float m = -CUDART_INF_F, l = 0.f;
-  int kept = 0;
+  int kept = 0, late = 0;  // kept: in order; late: threads (at most) that have appended since
+  float last = 0.f;        // of the `top` that are kept
+  // The best of what is kept and what has been appended; after a barrier, and ends with one.
+  auto settle = [&]() {
+    const int total = kept + sh_count;
+    if (total > kept) rank_keys(buffer, total, best, top);
+    kept = min(top, total);
+    late = 0;
+    __syncthreads();
+    if (tid < kept) buffer[tid] = best[tid];
+    if (tid == 0) sh_count = 0;
+    last = kept == top ? value_of((uint32_t)(best[top - 1] >> 32)) : 0.f;
+    __syncthreads();
+  };
   V y, ahead;
   ahead.load(x, from, end);
   __syncthreads();
@@ -168,10 +195,15 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && ALIGNED && VEC == 
     m = m1;
 
     // Threads with a value that may count.  Equal ones from here on come after those that are kept.
-    const float last = kept == top ? value_of((uint32_t)(best[top - 1] >> 32)) : 0.f;
-    const bool some = kept < top ? V::index(base, 0) < end : big > last;
-    const int busy = __syncthreads_count(some);
+    auto may = [&]() { return kept < top ? V::index(base, 0) < end : big > last; };
+    int busy = __syncthreads_count(may());
     if (busy == 0) continue;
+    if (late > 0 && late + busy > top) {  // (the buffer holds all values of `top` threads)
+      settle();
+      busy = __syncthreads_count(may());
+      if (busy == 0) continue;
+    }
+    const bool some = may();
     float limit = -CUDART_INF_F;
     if (busy > top) limit = value_of(common_limit(some ? image(big) : 0u, top, sh_range));
     if (some && big >= limit) {
@@ -184,9 +216,10 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && ALIGNED && VEC == 
         }
       }
     }
+    late += busy;
+    if (busy <= top) continue;
     __syncthreads();
-    int fresh = sh_count;
-    if (fresh > room) {  // (by so many equal values)
+    if (sh_count > room) {  // (by so many equal values)
       __syncthreads();
       uint64_t head = 0;
       if (some) {
@@ -213,17 +246,11 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && ALIGNED && VEC == 
         }
       }
       __syncthreads();
-      fresh = sh_count;
     }
-    if (fresh > 0) {
-      const int total = kept + fresh;
-      rank_keys(buffer, total, best, top);
-      kept = min(top, total);
-      __syncthreads();
-      if (tid < kept) buffer[tid] = best[tid];
-      if (tid == 0) sh_count = 0;
-    }
+    settle();
   }
+  __syncthreads();
+  if (late > 0) settle();
   // the part's maximum, sum of powers and best
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
@@ -254,95 +281,143 @@ __device__ __forceinline__ bool better(const Cand &a, const Cand &b) {
 }
 
 // Pass 2: a request.  Each (beam, part) list is in order, so a score that `top` of the lists' heads reach bounds what
-// counts, and the lists are walked down to it, four entries at a time.  Sums in float64 are few: a warp's take 16
-// cycles on this GPU.
+// counts, and the lists are walked down to it, four entries at a time.  Where that leaves many (few lists, one
+// of them far better than the rest), a second bound is found among them by halving.  The bounds are taken on scores
+// in float32, less what their rounding may make of them; only what passes them gets its score in float64
+// (slow on this GPU).
 constexpr int kLists = 4096;  // lists of a request at most
-constexpr int kPool = 1024;   // what may count, but for equal scores
+__host__ __device__ constexpr int room_of(int top) { return (top + top / 2 + 8) * top; }  // what may count, but for equal scores
+
+// ln(a + b), b small beside a > 0, to 2^-28: a = 2^e f with f in [1/sqrt 2, sqrt 2), ln f = 2 artanh(s) with
+// s = (f - 1) / (f + 1), |s| < 0.172; s in two floats, its series from s^3 on (to s^11) in one.
+__device__ __forceinline__ double log_of(float a, float b) {
+  const int e = (__float_as_int(a) - 0x3f3504f3) >> 23;
+  const float scale = __int_as_float((127 - e) << 23), f = a * scale, g = b * scale;
+  const float x = f - 1.f, y = f + 1.f, y_low = f - (y - 1.f);  // (x is exact; y + y_low = f + 1)
+  const float s = x / y;
+  const float low = (fmaf(-s, y, x) + (g - s * (g + y_low))) / y;
+  const float q = s * s;
+  const float tail = s * q * fmaf(q, fmaf(q, fmaf(q, fmaf(q, 1.f / 11, 1.f / 9), 1.f / 7), 1.f / 5), 1.f / 3);
+  return (double)e * 0.693147180559945309 + 2.0 * ((double)s + (double)(low + tail));
+}
+
 __global__ void __launch_bounds__(kThreads) beam_join_kernel(BeamParams p) {
-  __shared__ double shift[64];  // score_w - lse_w: what a logit's score adds
+  __shared__ double lse[64];    // of a beam (dead or finished: 0)
+  __shared__ float score_of[64];  // (dead: 0)
+  __shared__ float shift[64];     // score less lse, for the bound
   __shared__ int kind[64];      // 0: as the logits say; 1: every continuation -inf; 2: finished
   __shared__ uint32_t sh_range[2][kThreads / 32];
   __shared__ Cand sh_bound;
-  __shared__ int sh_count;
+  __shared__ int sh_count, sh_sum[2], sh_widest;  // widest: the largest |score| + |lse|, as its float's bits
   extern __shared__ uint64_t raw[];
   const int tid = threadIdx.x, group = blockIdx.x, w_n = p.beams, parts = p.parts, top = p.top;
-  const int lists = w_n * parts, room = max(kPool, top * top);
-  Cand *heads = reinterpret_cast<Cand *>(raw);  // [lists]
-  Cand *pool = heads + lists;                   // [room]
+  const int lists = w_n * parts, room = room_of(top);
+  Cand *exact = reinterpret_cast<Cand *>(raw);                               // [max(lists, room)]
+  uint64_t *pool = reinterpret_cast<uint64_t *>(exact + max(lists, room));   // [room] image of the score, list, entry
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
-  if (tid == 0) sh_count = 0;
+  if (tid == 0) sh_count = sh_widest = 0;
+  __syncthreads();
   {  // four threads a beam
     const int w = tid >> 2, row = group * w_n + w;
     const bool here = w < w_n;
+    const float score = here ? p.scores[row] : 0.f;
+    const bool done = here && isfinite(score) && p.finished && p.finished[row];
     float m = -CUDART_INF_F;
+#pragma unroll 4
     for (int i = tid & 3; here && i < parts; i += 4) m = fmaxf(m, p.sums[(long long)row * parts + i].x);
     m = fmaxf(m, __shfl_xor_sync(kAll, m, 1));
     m = fmaxf(m, __shfl_xor_sync(kAll, m, 2));
-    double l = 0.0;
+    const float ref = m == -CUDART_INF_F ? 0.f : m;
+    float l = 0.f, low = 0.f;  // the sum in two floats
+    auto add = [&](float x) {
+      const float y = l + x, z = y - l;
+      low += (l - (y - z)) + (x - z);
+      l = y;
+    };
+#pragma unroll 4
     for (int i = tid & 3; here && i < parts; i += 4) {
       const float2 s = p.sums[(long long)row * parts + i];
-      l += (double)(s.y * expf(s.x - (m == -CUDART_INF_F ? 0.f : m)));
+      add(s.y * expf(s.x - ref));
     }
-    l += __shfl_xor_sync(kAll, l, 1);
-    l += __shfl_xor_sync(kAll, l, 2);
+#pragma unroll
+    for (int o = 1; o < 4; o <<= 1) {
+      const float x = __shfl_xor_sync(kAll, l, o), y = __shfl_xor_sync(kAll, low, o);
+      // (both sides add the same two in the same order)
+      const bool first = (tid & o) == 0;
+      const float a = first ? l : x, b = first ? x : l, sum = a + b, z = sum - a;
+      low = low + y + ((a - (sum - z)) + (b - z));
+      l = sum;
+    }
     if (here && (tid & 3) == 0) {
-      const float score = p.scores[row];
-      const bool done = p.finished && p.finished[row];
-      shift[w] = done ? (double)score : (double)score - ((double)m + log(l));
-      kind[w] = done ? 2 : isfinite(score) && l > 0.0 && isfinite(l) && isfinite(m) ? 0 : 1;
+      const bool alive = isfinite(score) && l > 0.f && isfinite(l) && isfinite(m);
+      const double sum = alive && !done ? (double)m + log_of(l, low) : 0.0;
+      lse[w] = sum;
+      score_of[w] = done || alive ? score : 0.f;
+      shift[w] = score_of[w] - (float)sum;
+      kind[w] = done ? 2 : alive ? 0 : 1;
+      atomicMax(&sh_widest, __float_as_int(fabsf(score_of[w]) + fabsf((float)sum)));
     }
   }
   __syncthreads();
-  // entry i of list (w, part)
-  auto entry = [&](int list, int i, Cand &c) {
+  // entry i of list (w, part): its logit (a finished or dead beam's: 0 or -inf) and its place
+  auto entry = [&](int list, int i, float &logit, uint32_t &place) {
     const int w = list / parts, part = list - w * parts;
     const uint32_t base = (uint32_t)w * (uint32_t)p.vocab;
     if (kind[w] == 0) {
       const uint64_t key = p.keys[((long long)group * lists + list) * top + i];
-      if (key == 0) return false;
-      c = Cand{image(shift[w] + (double)value_of((uint32_t)(key >> 32))), base + ~(uint32_t)key};
-      return true;
+      logit = value_of((uint32_t)(key >> 32));
+      place = base + ~(uint32_t)key;
+      return key != 0;
     }
     if (part > 0) return false;  // in order of the token, a finished beam's own before them
+    logit = -CUDART_INF_F;
     if (kind[w] == 2) {
       if (i == 0) {
-        c = Cand{image(shift[w]), base + (uint32_t)p.pad_token};
+        logit = 0.f;
+        place = base + (uint32_t)p.pad_token;
         return true;
       }
       i = i - 1 < p.pad_token ? i - 1 : i;
     }
-    if (i >= p.vocab) return false;
-    c = Cand{image(-CUDART_INF), base + (uint32_t)i};
-    return true;
+    place = base + (uint32_t)i;
+    return i < p.vocab;
   };
-  uint32_t most = 0;  // of this thread's heads (the images' upper halves)
+  // (the first sum is exact but for far exponents, so that beams of equal rows tie where score and logit do)
+  auto exactly = [&](float logit, uint32_t place) {
+    const int w = place / (uint32_t)p.vocab;
+    return Cand{image(((double)score_of[w] + (double)logit) - lse[w]), place};
+  };
+  auto about = [&](int list, float logit) { return shift[list / parts] + logit; };
+  uint32_t most = 0;  // of this thread's heads
   for (int i = tid; i < lists; i += kThreads) {
-    Cand c;
-    if (!entry(i, 0, c)) c = Cand{0, ~0u};
-    heads[i] = c;
-    most = max(most, (uint32_t)(c.score >> 32));
+    float logit;
+    uint32_t place;
+    if (entry(i, 0, logit, place)) most = max(most, image(about(i, logit)));
   }
-  Cand bound{0, ~0u};
+  // (a score in float32 is off by three roundings of 2^-24)
+  auto loosened = [&](float x) {
+    return x > -CUDART_INF_F ? x - (3.6e-7f * (fabsf(x) + __int_as_float(sh_widest)) + 1e-30f) : x;
+  };
+  float bound = -CUDART_INF_F;
   const int busy = __syncthreads_count(most != 0);
-  if (busy > top) bound.score = (uint64_t)common_limit(most, top, sh_range) << 32;
-  // what is no worse than the bound; a list's head tells whether it has any
-  auto gather = [&]() {
+  if (busy > top) bound = loosened(value_of(common_limit(most, top, sh_range)));
+  // Puts what reaches the bound, and is no worse than `least`, into the pool; lists are in order.
+  auto gather = [&](const Cand *least) {
     for (int i = tid; i < lists; i += kThreads) {
-      Cand c = heads[i];
-      if (c.score == 0 || better(bound, c)) continue;
       for (int e = 0; e < top; e += 4) {
-        Cand some[4];
+        float logit[4];
+        uint32_t place[4];
         bool good[4];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) good[u] = e + u < top && entry(i, e + u, some[u]);
+        for (int u = 0; u < 4; ++u) good[u] = e + u < top && entry(i, e + u, logit[u], place[u]);
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-          good[u] = good[u] && !better(bound, some[u]);
-          if (good[u]) {
-            const int to = atomicAdd(&sh_count, 1);
-            if (to < room) pool[to] = some[u];
-          }
+          const float about_it = about(i, logit[u]);
+          good[u] = good[u] && about_it >= bound && !(least && better(*least, exactly(logit[u], place[u])));
+          if (!good[u]) continue;
+          const int to = atomicAdd(&sh_count, 1);
+          if (to < room) pool[to] = (uint64_t)image(about_it) << 32 | (uint32_t)(i << 6 | (e + u));
         }
         if (!good[3]) break;
       }
@@ -350,26 +425,67 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(BeamParams p) {
     __syncthreads();
     return sh_count;
   };
-  int n = gather();
-  if (n > room) {  // equal scores: the top-th best head itself
+  int n = gather(nullptr);
+  if (n > room) {  // equal scores: bounded by the top-th best head itself
     __syncthreads();
     if (tid == 0) sh_count = 0, sh_bound = Cand{0, ~0u};
+    for (int i = tid; i < lists; i += kThreads) {
+      float logit;
+      uint32_t place;
+      exact[i] = entry(i, 0, logit, place) ? exactly(logit, place) : Cand{0, ~0u};
+    }
     __syncthreads();
     for (int i = tid; i < lists; i += kThreads) {
-      const Cand mine = heads[i];
+      const Cand mine = exact[i];
       int b = 0;
-      for (int j = 0; j < lists; ++j) b += better(heads[j], mine);
+      for (int j = 0; j < lists; ++j) b += better(exact[j], mine);
       if (b == top - 1 && mine.score != 0) sh_bound = mine;
     }
     __syncthreads();
-    bound = sh_bound;
-    n = gather();
+    n = gather(&sh_bound);
   }
+  if (n > 2 * top + 32) {  // a bound among them
+    uint32_t lo = image(bound), hi = 0;
+    for (int i = tid; i < n; i += kThreads) hi = max(hi, (uint32_t)(pool[i] >> 32));
+    hi = __reduce_max_sync(kAll, hi);
+    if ((tid & 31) == 0) sh_range[0][tid >> 5] = hi;
+    if (tid < 2) sh_sum[tid] = 0;
+    __syncthreads();
+    for (int i = 0; i < kThreads / 32; ++i) hi = max(hi, sh_range[0][i]);
+    for (int turn = 0; lo < hi; turn ^= 1) {
+      const uint32_t mid = lo + (hi - lo + 1) / 2;
+      int count = 0;
+      for (int i = tid; i < n; i += kThreads) count += (uint32_t)(pool[i] >> 32) >= mid;
+      count = __reduce_add_sync(kAll, count);
+      if ((tid & 31) == 0 && count) atomicAdd(&sh_sum[turn], count);
+      __syncthreads();
+      count = sh_sum[turn];
+      __syncthreads();
+      if (tid == 0) sh_sum[turn] = 0;
+      if (count >= top) lo = mid;
+      else hi = mid - 1;
+      if (count >= top && count <= top + top / 2 + 8) break;
+    }
+    bound = fmaxf(bound, loosened(value_of(lo)));
+  }
+  // their scores
+  __syncthreads();
+  if (tid == 0) sh_count = 0;
+  __syncthreads();
   for (int i = tid; i < n; i += kThreads) {
-    const Cand mine = pool[i];
+    const uint64_t it = pool[i];
+    float logit;
+    uint32_t place;
+    if (value_of((uint32_t)(it >> 32)) >= bound && entry((int)((uint32_t)it >> 6), (int)(it & 63), logit, place))
+      exact[atomicAdd(&sh_count, 1)] = exactly(logit, place);
+  }
+  __syncthreads();
+  n = sh_count;
+  for (int i = tid; i < n; i += kThreads) {
+    const Cand mine = exact[i];
     int b = 0;
 #pragma unroll 4
-    for (int j = 0; j < n; ++j) b += better(pool[j], mine);
+    for (int j = 0; j < n; ++j) b += better(exact[j], mine);
     if (b < top) {
       const long long at = (long long)group * top + b;
       p.scores_out[at] = (float)value_of(mine.score);
@@ -383,12 +499,18 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(BeamParams p) {
 // them (2 requests of 4 beams over 32000: see below).
 int vec_of(int rows, int vocab, int per) { return (long long)rows * (vocab / (kThreads * 4 * per)) < 2 * kSms ? 1 : 4; }
 
-// Parts of a row: enough CTAs to fill the GPU three times over, of a step at least, and no more lists
-// a request than the join takes.
-int parts_of(int rows, int beams, int vocab, int step) {
-  const int most = std::max(1, std::min(vocab / step, kLists / beams));
-  const int fill = (int)((3LL * 4 * kSms + rows - 1) / std::max(rows, 1));
-  return std::max(1, std::min(most, fill));
+// Parts of a row, each of whole steps: the number that ends first if the CTAs come in waves of `slots` and a
+// CTA's start and end take as long as three steps; no more lists a request than the join takes.
+int parts_of(int rows, int beams, int vocab, int step, int slots) {
+  const int steps = (vocab + step - 1) / step, most = std::min(steps, kLists / beams);
+  int best = 1;
+  long long least = 0;
+  for (int parts = 1; parts <= most; ++parts) {
+    const long long waves = ((long long)rows * parts + slots - 1) / slots;
+    const long long cost = waves * ((steps + parts - 1) / parts + 3);
+    if (parts == 1 || cost < least) best = parts, least = cost;
+  }
+  return best;
 }
 
 // ------------------------------------------------------------------ reordering
@@ -433,9 +555,9 @@ __global__ void __launch_bounds__(128) reorder_kernel(ReorderParams p) {
 template <typename T, bool ALIGNED, int VEC>
 cudaError_t select(const BeamParams &p, cudaStream_t stream) {
   const size_t rows = sizeof(uint64_t) * (size_t)p.top * (Values<T, ALIGNED, VEC>::MOST + 1);
-  const size_t join = sizeof(Cand) * ((size_t)p.beams * p.parts + std::max(kPool, p.top * p.top));
+  const size_t join = sizeof(Cand) * std::max(p.beams * p.parts, room_of(p.top)) + sizeof(uint64_t) * room_of(p.top);
   static std::atomic<uint64_t> allowed{0};
-  cudaError_t err = allow_smem(beam_join_kernel, 160 * 1024, allowed);
+  cudaError_t err = allow_smem(beam_join_kernel, 164 * 1024, allowed);
   if (err == cudaSuccess)
     err = launch_dependent(beam_rows_kernel<T, ALIGNED, VEC>, (unsigned)(p.groups * p.beams * p.parts), kThreads, rows, stream, 1, p);
   if (err != cudaSuccess) return err;
@@ -454,8 +576,8 @@ cudaError_t by_alignment(const BeamParams &p, cudaStream_t stream) {
 }  // namespace
 
 int beam_parts(int groups, int beams, int vocab, bool bf16) {
-  const int rows = groups * beams, per = bf16 ? 8 : 4;
-  return parts_of(rows, beams, vocab, kThreads * vec_of(rows, vocab, per) * per);
+  const int rows = groups * beams, per = bf16 ? 8 : 4, vec = vec_of(rows, vocab, per);
+  return parts_of(rows, beams, vocab, kThreads * vec * per, kSms * (bf16 && vec == 4 ? 3 : 4));
 }
 
 cudaError_t launch_beam_select(const BeamParams &p, gdn_dtype dtype, cudaStream_t stream) {

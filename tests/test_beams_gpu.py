@@ -25,7 +25,8 @@ def definition(logits, scores, finished, pad):
         f = finished.cpu()
         x[f] = -math.inf
         for g, w in torch.nonzero(f).tolist():
-            x[g, w, pad] = scores[g, w].double().item()
+            if math.isfinite(scores[g, w]):
+                x[g, w, pad] = scores[g, w].double().item()
     return x.flatten(1)
 
 
@@ -113,6 +114,16 @@ def test_select_nothing_left(dtype):
         for pad in (0, 2, 2999):
             check(x, s, top, fin, pad)
     check(x[3:4], s[3:4], 8, torch.ones(1, 4, dtype=torch.bool, device="cuda"), 5)
+    for score in (-math.inf, math.nan, math.inf):  # finished, and dead all the same
+        check(x[4:5], torch.full((1, 4), score, device="cuda"), 8, torch.ones(1, 4, dtype=torch.bool, device="cuda"), 2999)
+
+
+def test_select_far_scores():
+    """Logits and scores far from 0 that cancel: the comparison in 64 bits decides."""
+    g = torch.Generator(device="cuda").manual_seed(9)
+    x = torch.randn(2, 64, 3001, generator=g, device="cuda") * 0.01
+    x += torch.linspace(-3e4, 3e4, 64, device="cuda")[None, :, None]
+    check(x, -1e3 * torch.rand(2, 64, generator=g, device="cuda"), 33)
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
