@@ -207,13 +207,15 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && ALIGNED && VEC == 
     float limit = -CUDART_INF_F;
     if (busy > top) limit = value_of(common_limit(some ? image(big) : 0u, top, sh_range));
     if (some && big >= limit) {
+      uint32_t bits = 0;
 #pragma unroll
-      for (int i = 0; i < MOST; ++i) {
-        const int at = V::index(base, i);
-        if (y[i] >= limit && at < end && (kept < top || y[i] > last)) {
-          const int to = atomicAdd(&sh_count, 1);
-          if (to < room) buffer[kept + to] = key_of(y[i], at);
-        }
+      for (int i = 0; i < MOST; ++i) bits |= y[i] >= limit && (kept < top || y[i] > last) ? 1u << i : 0u;
+      const bool alone = (bits & (bits - 1)) == 0;  // (then it is the largest; else they are read again)
+      for (; bits; bits &= bits - 1) {
+        const int at = V::index(base, __ffs(bits) - 1);
+        if (at >= end) break;
+        const int to = atomicAdd(&sh_count, 1);
+        if (to < room) buffer[kept + to] = key_of(alone ? big : Elem<T>::load(x + at), at);
       }
     }
     late += busy;
@@ -280,13 +282,13 @@ __device__ __forceinline__ bool better(const Cand &a, const Cand &b) {
   return a.score > b.score || (a.score == b.score && a.place < b.place);
 }
 
-// Pass 2: a request.  Each (beam, part) list is in order, so a score that `top` of the lists' heads reach bounds what
-// counts, and the lists are walked down to it, four entries at a time.  Where that leaves many (few lists, one
-// of them far better than the rest), a second bound is found among them by halving.  The bounds are taken on scores
-// in float32, less what their rounding may make of them; only what passes them gets its score in float64
-// (slow on this GPU).
-constexpr int kLists = 4096;  // lists of a request at most
-__host__ __device__ constexpr int room_of(int top) { return (top + top / 2 + 8) * top; }  // what may count, but for equal scores
+// Pass 2: a request.  The (beam, part) lists are in order.  Their first entries, up to kSample of them, tell a score that at least `top` reach and not many more, found by halving: first by threads'
+// largest, then by all.  What reaches it, and what follows in lists whose sampled entries all do, is ranked by
+// counting.  The halving is done on scores in float32, less what their rounding may make of them; only what passes
+// gets its score in float64 (slow on this GPU).
+constexpr int kLists = 4096;           // lists of a request at most
+constexpr int kSample = 4096;
+constexpr int kRoom = kLists;          // what may pass, but for equal scores: no less than 64 entries of 64 lists
 
 // ln(a + b), b small beside a > 0, to 2^-28: a = 2^e f with f in [1/sqrt 2, sqrt 2), ln f = 2 artanh(s) with
 // s = (f - 1) / (f + 1), |s| < 0.172; s in two floats, its series from s^3 on (to s^11) in one.
@@ -301,6 +303,13 @@ __device__ __forceinline__ double log_of(float a, float b) {
   return (double)e * 0.693147180559945309 + 2.0 * ((double)s + (double)(low + tail));
 }
 
+__device__ __forceinline__ uint64_t pick(const uint64_t (&x)[8], int i) {
+  uint64_t r = x[0];
+#pragma unroll
+  for (int k = 1; k < 8; ++k) r = i == k ? x[k] : r;
+  return r;
+}
+
 __global__ void __launch_bounds__(kThreads) beam_join_kernel(BeamParams p) {
   __shared__ double lse[64];    // of a beam (dead or finished: 0)
   __shared__ float score_of[64];  // (dead: 0)
@@ -308,15 +317,14 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(BeamParams p) {
   __shared__ int kind[64];      // 0: as the logits say; 1: every continuation -inf; 2: finished
   __shared__ uint32_t sh_range[2][kThreads / 32];
   __shared__ Cand sh_bound;
-  __shared__ int sh_count, sh_sum[2], sh_widest;  // widest: the largest |score| + |lse|, as its float's bits
+  __shared__ int sh_count, sh_sum[3], sh_widest;  // widest: the largest |score| + |lse|, as its float's bits
   extern __shared__ uint64_t raw[];
   const int tid = threadIdx.x, group = blockIdx.x, w_n = p.beams, parts = p.parts, top = p.top;
-  const int lists = w_n * parts, room = room_of(top);
-  Cand *exact = reinterpret_cast<Cand *>(raw);                               // [max(lists, room)]
-  uint64_t *pool = reinterpret_cast<uint64_t *>(exact + max(lists, room));   // [room] image of the score, list, entry
+  const int lists = w_n * parts, deep = min(top, max(kSample / lists, 1));  // sampled entries of a list
+  Cand *found = reinterpret_cast<Cand *>(raw);  // [kRoom]
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
-  if (tid == 0) sh_count = sh_widest = 0;
+  if (tid == 0) sh_count = sh_widest = sh_sum[0] = sh_sum[1] = sh_sum[2] = 0;
   __syncthreads();
   {  // four threads a beam
     const int w = tid >> 2, row = group * w_n + w;
@@ -360,12 +368,13 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(BeamParams p) {
     }
   }
   __syncthreads();
-  // entry i of list (w, part): its logit (a finished or dead beam's: 0 or -inf) and its place
-  auto entry = [&](int list, int i, float &logit, uint32_t &place) {
+  // entry i of list (w, part), whose key (where its logits say) is `key`: its logit (a finished or dead
+  // beam's: 0 or -inf) and its place
+  const uint64_t *keys = p.keys + (long long)group * lists * top;
+  auto entry = [&](int list, int i, uint64_t key, float &logit, uint32_t &place) {
     const int w = list / parts, part = list - w * parts;
     const uint32_t base = (uint32_t)w * (uint32_t)p.vocab;
     if (kind[w] == 0) {
-      const uint64_t key = p.keys[((long long)group * lists + list) * top + i];
       logit = value_of((uint32_t)(key >> 32));
       place = base + ~(uint32_t)key;
       return key != 0;
@@ -389,103 +398,116 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(BeamParams p) {
     return Cand{image(((double)score_of[w] + (double)logit) - lse[w]), place};
   };
   auto about = [&](int list, float logit) { return shift[list / parts] + logit; };
-  uint32_t most = 0;  // of this thread's heads
-  for (int i = tid; i < lists; i += kThreads) {
-    float logit;
-    uint32_t place;
-    if (entry(i, 0, logit, place)) most = max(most, image(about(i, logit)));
+  // (loops stay rolled but for a few loads side by side: a kernel this short waits for its instructions)
+  uint32_t *sample = reinterpret_cast<uint32_t *>(found + kRoom), most = 0;  // [kSample]
+  const int sampled = lists * deep;
+#pragma unroll 1
+  for (int k = tid; k < sampled; k += 4 * kThreads) {
+    uint64_t key[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int at = k + u * kThreads, list = at / deep;
+      key[u] = at < sampled ? keys[(long long)list * top + (at - list * deep)] : 0;
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int at = k + u * kThreads, list = at / deep;
+      float logit;
+      uint32_t place, score = 0;
+      if (at >= sampled) break;
+      if (entry(list, at - list * deep, key[u], logit, place)) score = image(about(list, logit));
+      sample[at] = score;
+      most = max(most, score);
+    }
+  }
+  uint32_t lo = 0;
+  if (__syncthreads_count(most != 0) > top) lo = common_limit(most, top, sh_range);
+  auto reach = [&](uint32_t limit, int turn) {
+    int count = 0;
+#pragma unroll 4
+    for (int k = tid; k < sampled; k += kThreads) count += sample[k] >= limit && sample[k] != 0;
+    count = __reduce_add_sync(kAll, count);
+    if ((tid & 31) == 0 && count) atomicAdd(&sh_sum[turn], count);
+    __syncthreads();
+    count = sh_sum[turn];
+    if (tid == 0) sh_sum[turn == 0 ? 2 : turn - 1] = 0;  // (three counters in turn: this one is read, the next one free)
+    return count;
+  };
+  const int enough = top + top / 2 + 32;
+  if (reach(lo, 0) > enough) {
+    most = __reduce_max_sync(kAll, most);
+    if ((tid & 31) == 0) sh_range[0][tid >> 5] = most;
+    __syncthreads();
+    uint32_t hi = 0;
+    for (int i = 0; i < kThreads / 32; ++i) hi = max(hi, sh_range[0][i]);
+    for (int turn = 1; lo < hi; turn = turn == 2 ? 0 : turn + 1) {
+      const uint32_t mid = lo + (hi - lo + 1) / 2;
+      const int count = reach(mid, turn);
+      if (count >= top) lo = mid;
+      else hi = mid - 1;
+      if (count >= top && count <= enough) break;
+    }
   }
   // (a score in float32 is off by three roundings of 2^-24)
-  auto loosened = [&](float x) {
-    return x > -CUDART_INF_F ? x - (3.6e-7f * (fabsf(x) + __int_as_float(sh_widest)) + 1e-30f) : x;
-  };
-  float bound = -CUDART_INF_F;
-  const int busy = __syncthreads_count(most != 0);
-  if (busy > top) bound = loosened(value_of(common_limit(most, top, sh_range)));
-  // Puts what reaches the bound, and is no worse than `least`, into the pool; lists are in order.
+  const float low = lo == 0 ? -CUDART_INF_F : value_of(lo);
+  const float bound = low > -CUDART_INF_F ? low - (3.6e-7f * (fabsf(low) + __int_as_float(sh_widest)) + 1e-30f) : low;
+  // What reaches the bound and is no worse than `least`.
   auto gather = [&](const Cand *least) {
-    for (int i = tid; i < lists; i += kThreads) {
-      for (int e = 0; e < top; e += 4) {
-        float logit[4];
-        uint32_t place[4];
-        bool good[4];
+    auto put = [&](float logit, uint32_t place) {
+      const Cand c = exactly(logit, place);
+      if (least && better(*least, c)) return;
+      const int to = atomicAdd(&sh_count, 1);
+      if (to < kRoom) found[to] = c;
+    };
+#pragma unroll 1
+    for (int at = tid; at < sampled; at += kThreads) {
+      if (sample[at] == 0 || value_of(sample[at]) < bound) continue;
+      const int list = at / deep, first = at - list * deep;
+      float logit;
+      uint32_t place;
+      entry(list, first, keys[(long long)list * top + first], logit, place);
+      put(logit, place);
+      if (first < deep - 1) continue;
+#pragma unroll 1
+      for (int e = deep, more = 1; more && e < top; e += 8) {
+        uint64_t key[8];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) good[u] = e + u < top && entry(i, e + u, logit[u], place[u]);
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const float about_it = about(i, logit[u]);
-          good[u] = good[u] && about_it >= bound && !(least && better(*least, exactly(logit[u], place[u])));
-          if (!good[u]) continue;
-          const int to = atomicAdd(&sh_count, 1);
-          if (to < room) pool[to] = (uint64_t)image(about_it) << 32 | (uint32_t)(i << 6 | (e + u));
+        for (int u = 0; u < 8; ++u) key[u] = e + u < top ? keys[(long long)list * top + e + u] : 0;
+#pragma unroll 1
+        for (int u = 0; u < 8 && e + u < top; ++u) {
+          more = entry(list, e + u, pick(key, u), logit, place) && about(list, logit) >= bound;
+          if (!more) break;
+          put(logit, place);
         }
-        if (!good[3]) break;
       }
     }
     __syncthreads();
     return sh_count;
   };
   int n = gather(nullptr);
-  if (n > room) {  // equal scores: bounded by the top-th best head itself
+  if (n > kRoom) {  // equal scores: bounded by the top-th best head itself
     __syncthreads();
     if (tid == 0) sh_count = 0, sh_bound = Cand{0, ~0u};
     for (int i = tid; i < lists; i += kThreads) {
       float logit;
       uint32_t place;
-      exact[i] = entry(i, 0, logit, place) ? exactly(logit, place) : Cand{0, ~0u};
+      found[i] = entry(i, 0, keys[(long long)i * top], logit, place) ? exactly(logit, place) : Cand{0, ~0u};
     }
     __syncthreads();
     for (int i = tid; i < lists; i += kThreads) {
-      const Cand mine = exact[i];
+      const Cand mine = found[i];
       int b = 0;
-      for (int j = 0; j < lists; ++j) b += better(exact[j], mine);
+      for (int j = 0; j < lists; ++j) b += better(found[j], mine);
       if (b == top - 1 && mine.score != 0) sh_bound = mine;
     }
     __syncthreads();
     n = gather(&sh_bound);
   }
-  if (n > 2 * top + 32) {  // a bound among them
-    uint32_t lo = image(bound), hi = 0;
-    for (int i = tid; i < n; i += kThreads) hi = max(hi, (uint32_t)(pool[i] >> 32));
-    hi = __reduce_max_sync(kAll, hi);
-    if ((tid & 31) == 0) sh_range[0][tid >> 5] = hi;
-    if (tid < 2) sh_sum[tid] = 0;
-    __syncthreads();
-    for (int i = 0; i < kThreads / 32; ++i) hi = max(hi, sh_range[0][i]);
-    for (int turn = 0; lo < hi; turn ^= 1) {
-      const uint32_t mid = lo + (hi - lo + 1) / 2;
-      int count = 0;
-      for (int i = tid; i < n; i += kThreads) count += (uint32_t)(pool[i] >> 32) >= mid;
-      count = __reduce_add_sync(kAll, count);
-      if ((tid & 31) == 0 && count) atomicAdd(&sh_sum[turn], count);
-      __syncthreads();
-      count = sh_sum[turn];
-      __syncthreads();
-      if (tid == 0) sh_sum[turn] = 0;
-      if (count >= top) lo = mid;
-      else hi = mid - 1;
-      if (count >= top && count <= top + top / 2 + 8) break;
-    }
-    bound = fmaxf(bound, loosened(value_of(lo)));
-  }
-  // their scores
-  __syncthreads();
-  if (tid == 0) sh_count = 0;
-  __syncthreads();
   for (int i = tid; i < n; i += kThreads) {
-    const uint64_t it = pool[i];
-    float logit;
-    uint32_t place;
-    if (value_of((uint32_t)(it >> 32)) >= bound && entry((int)((uint32_t)it >> 6), (int)(it & 63), logit, place))
-      exact[atomicAdd(&sh_count, 1)] = exactly(logit, place);
-  }
-  __syncthreads();
-  n = sh_count;
-  for (int i = tid; i < n; i += kThreads) {
-    const Cand mine = exact[i];
+    const Cand mine = found[i];
     int b = 0;
 #pragma unroll 4
-    for (int j = 0; j < n; ++j) b += better(exact[j], mine);
+    for (int j = 0; j < n; ++j) b += better(found[j], mine);
     if (b < top) {
       const long long at = (long long)group * top + b;
       p.scores_out[at] = (float)value_of(mine.score);
@@ -499,15 +521,15 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(BeamParams p) {
 // them (2 requests of 4 beams over 32000: see below).
 int vec_of(int rows, int vocab, int per) { return (long long)rows * (vocab / (kThreads * 4 * per)) < 2 * kSms ? 1 : 4; }
 
-// Parts of a row, each of whole steps: the number that ends first if the CTAs come in waves of `slots` and a
-// CTA's start and end take as long as three steps; no more lists a request than the join takes.
+// Parts of a row, each of whole steps: the number that ends first if `slots` CTAs run at a time, the last of them
+// half a CTA's time longer than the rest, and a CTA's start and end take one and a half steps (64 x 8 rows of 150001,
+// 37 steps, in 1 to 5 parts: 61, 61, 56, 60, 63 us); no more lists a request than the join takes.
 int parts_of(int rows, int beams, int vocab, int step, int slots) {
   const int steps = (vocab + step - 1) / step, most = std::min(steps, kLists / beams);
   int best = 1;
-  long long least = 0;
+  float least = 0.f;
   for (int parts = 1; parts <= most; ++parts) {
-    const long long waves = ((long long)rows * parts + slots - 1) / slots;
-    const long long cost = waves * ((steps + parts - 1) / parts + 3);
+    const float cost = (float)rows / slots * (steps + 1.5f * parts) + 0.5f * ((float)steps / parts + 1.5f);
     if (parts == 1 || cost < least) best = parts, least = cost;
   }
   return best;
@@ -555,9 +577,9 @@ __global__ void __launch_bounds__(128) reorder_kernel(ReorderParams p) {
 template <typename T, bool ALIGNED, int VEC>
 cudaError_t select(const BeamParams &p, cudaStream_t stream) {
   const size_t rows = sizeof(uint64_t) * (size_t)p.top * (Values<T, ALIGNED, VEC>::MOST + 1);
-  const size_t join = sizeof(Cand) * std::max(p.beams * p.parts, room_of(p.top)) + sizeof(uint64_t) * room_of(p.top);
+  constexpr size_t join = sizeof(Cand) * kRoom + sizeof(uint32_t) * kSample;
   static std::atomic<uint64_t> allowed{0};
-  cudaError_t err = allow_smem(beam_join_kernel, 164 * 1024, allowed);
+  cudaError_t err = allow_smem(beam_join_kernel, join, allowed);
   if (err == cudaSuccess)
     err = launch_dependent(beam_rows_kernel<T, ALIGNED, VEC>, (unsigned)(p.groups * p.beams * p.parts), kThreads, rows, stream, 1, p);
   if (err != cudaSuccess) return err;
