@@ -85,12 +85,13 @@ __device__ __forceinline__ void tie(uint32_t (&r)[N]) {
   for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
 }
 
-// The leading bf16 of two floats, packed; the floats keep what is left of them.
+// The leading 8 bits of two floats as bf16, packed; the floats keep what is left of them (three times 8 bits
+// are all that they have).
 __device__ __forceinline__ uint32_t take_bf16(float &a, float &b) {
-  const uint32_t p = pack_bf16(a, b);
-  a -= __uint_as_float(p << 16);
-  b -= __uint_as_float(p & 0xffff0000u);
-  return p;
+  const uint32_t x = __float_as_uint(a), y = __float_as_uint(b);
+  a -= __uint_as_float(x & 0xffff0000u);
+  b -= __uint_as_float(y & 0xffff0000u);
+  return __byte_perm(x, y, 0x7632);
 }
 
 __device__ __forceinline__ void st8(uint32_t taddr, const uint32_t (&r)[8]) {
@@ -141,7 +142,7 @@ __global__ void __launch_bounds__(TreeCfg<T, C>::THREADS, TreeCfg<T, C>::CTAS) v
   constexpr int kTree = 32 * F::TREE_WARPS;
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t above[C];    // a node's ancestors, itself among them
-  __shared__ float2 path[C];       // G in two floats
+  __shared__ float2 path[C];       // G log2(e) in two floats
   __shared__ float from_state[C];  // e^G
   __shared__ float gates[C], beta[C];
   __shared__ int up[C];
@@ -170,15 +171,6 @@ __global__ void __launch_bounds__(TreeCfg<T, C>::THREADS, TreeCfg<T, C>::CTAS) v
   seq_range(p.cu_seqlens, n, p.total_tokens, bos, eos);
   const int t_n = min(eos - bos, C);
 
-  // the state's first 64 keys, then the rows of q, k and v
-  const float *state = p.state_in ? p.state_in + ((size_t)n * p.hv + h) * kD * kD + (tid & 127) : nullptr;
-  float s[2][kKeys];
-  if (state && t_n > 0 && warp < 4) {
-#pragma unroll
-    for (int c = 0; c < 2; ++c)
-#pragma unroll
-      for (int i = 0; i < kKeys; ++i) s[c][i] = __ldcs(state + (c * kKeys + i) * kD);
-  }
   const T *q = static_cast<const T *>(p.q), *k = static_cast<const T *>(p.k), *v = static_cast<const T *>(p.v);
   if (F::TERMS == 1) {
 #pragma unroll 2
@@ -211,6 +203,15 @@ __global__ void __launch_bounds__(TreeCfg<T, C>::THREADS, TreeCfg<T, C>::CTAS) v
                reinterpret_cast<const uint8_t *>(v + ((size_t)(bos + t) * p.hv + h) * kD) + unit * 16, 16);
   }
   cp_async_commit();
+  // the state's first 64 keys, then the rows of q, k and v
+  const float *state = p.state_in ? p.state_in + ((size_t)n * p.hv + h) * kD * kD + (tid & 127) : nullptr;
+  float s[2][kKeys];
+  if (state && t_n > 0 && warp < 4) {
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+      for (int i = 0; i < kKeys; ++i) s[c][i] = __ldcs(state + (c * kKeys + i) * kD);
+  }
 
   // ancestors, path sums, and the places of the lists
   const int j = tid - kColumns;  // of a thread of the tree: its node, and its key
@@ -236,8 +237,10 @@ __global__ void __launch_bounds__(TreeCfg<T, C>::THREADS, TreeCfg<T, C>::CTAS) v
     __syncwarp();
     if (j < C) {
       above[j] = mine;
-      path[j] = make_float2(hi, lo);
-      from_state[j] = expf(hi + lo);
+      const float up2 = hi * 1.44269504f;  // (and what the product and the constant lose)
+      const float low2 = fmaf(hi, 1.44269504f, -up2) + fmaf(lo, 1.44269504f, hi * 1.92596299e-8f);
+      path[j] = make_float2(up2, low2);
+      from_state[j] = ex2(up2 + low2);
       beta[j] = node ? p.beta[(size_t)(bos + j) * p.hv + h] : 0.f;
     }
   }
@@ -283,7 +286,7 @@ __global__ void __launch_bounds__(TreeCfg<T, C>::THREADS, TreeCfg<T, C>::CTAS) v
       for (int i = 0; i < 8; ++i) {
         const int t = t0 + i;
         const float2 g = path[t];
-        const float decay = expf((g.x - own.x) + (g.y - own.y));
+        const float decay = ex2((g.x - own.x) + (g.y - own.y));
         const bool on = above[t] >> j & 1;  // (its own: decay 1, and no factor of delta)
         a[i] = on ? __uint_as_float(x[i]) * decay : 0.f;
         b[i] = on && t != j ? __uint_as_float(y[i]) * decay : 0.f;
