@@ -125,7 +125,7 @@ def lib() -> ctypes.CDLL:
         L.gdn_tree_attention.restype = ctypes.c_int
         L.gdn_verify_tree.argtypes = [ctypes.POINTER(GdnShape)] + [P] * 11
         L.gdn_verify_tree.restype = ctypes.c_int
-        # several beams (beams.py)
+        # several continuations (branching.py)
         L.gdn_beam_select.argtypes = [P] * 8 + [S, P]
         L.gdn_beam_select.restype = ctypes.c_int
         L.gdn_beam_workspace_size.argtypes = [P]
@@ -469,44 +469,6 @@ def gdn_verify_block_capture(q, k, v, g, beta, state_in, state_out, cu_seqlens, 
     return o, state_out, delta
 
 
-@_on_its_stream
-def gdn_verify_tree(q, k, v, g, beta, state_in, cu_seqlens, parents, o=None, delta=None,
-                    chunk: int = 64, stream=None):
-    """Draft-verify block whose drafts form a tree: parents [T] int32, each node's parent as an
-    index into its own sequence's nodes (it stands before its child; -1: the node hangs on the
-    snapshot).  state_in [N, Hv, 128, 128] fp32 (or None) is left unchanged and no state is
-    written; delta [T, Hv, 128] fp32.  chunk (16, 32, 64): the most nodes of a tree.  The state
-    after an accepted path: gdn_state_rollback on the path's rows of k, g and delta.
-    Returns (o, delta)."""
-    torch = _torch()
-    if o is None:
-        o = torch.empty_like(v)
-    if delta is None:
-        delta = torch.empty(v.shape, dtype=torch.float32, device=v.device)
-    _check_tensors(q, k, v, g, beta, state_in, cu_seqlens, parents, o, delta)
-    T, hk, dk = q.shape
-    hv, dv = v.shape[1], v.shape[2]
-    n = cu_seqlens.numel() - 1
-    for what, t, dtype, size in (("k", k, q.dtype, q.shape), ("v", v, q.dtype, (T, hv, dv)),
-                                 ("g", g, torch.float32, (T, hv)), ("beta", beta, torch.float32, (T, hv)),
-                                 ("state_in", state_in, torch.float32, (n, hv, dk, dv)),
-                                 ("cu_seqlens", cu_seqlens, torch.int32, (n + 1,)),
-                                 ("parents", parents, torch.int32, (T,)), ("o", o, o.dtype, v.shape),
-                                 ("delta", delta, torch.float32, v.shape)):
-        if t is not None and (t.dtype != dtype or t.shape != size):
-            raise ValueError("%s must be %s of shape %s" % (what, dtype, tuple(size)))
-    code = _dtype_code(q)
-    if o.dtype != q.dtype and _dtype_code(o) != GDN_F32:
-        raise TypeError("o must have q's type or be float32")
-    shape = make_shape(n, T, hk, hv, dk, dv, chunk, code, int(o.dtype != q.dtype))
-    st = lib().gdn_verify_tree(ctypes.byref(shape), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta),
-                               _ptr(state_in), _ptr(cu_seqlens), _ptr(parents), _ptr(o), _ptr(delta),
-                               _stream(stream))
-    if st != GDN_OK:
-        raise GdnError(st, "gdn_verify_tree")
-    return o, delta
-
-
 def gdn_state_rollback(k, g, delta, state_in, prefix_len, state_out, cu_seqlens, stream=None):
     """State after the first prefix_len[n] tokens of each sequence's verified block,
     from the snapshot state_in and the captured deltas.  state_out may be state_in."""
@@ -537,19 +499,19 @@ def gdn_conv_state_rollback(q_raw, k_raw, v_raw, conv_state_in, prefix_len, conv
     return conv_state_out
 
 
-# ------------------------------------------------------------------ the attention layers, beams
+# ------------------------------------------------------------------ the attention layers, several continuations
 
 _ATTENTION = ("GdnAttnShape", "make_attn_shape", "gdn_attn_workspace_size", "gdn_attn_workspace",
               "gdn_kv_append", "gdn_paged_attention", "gdn_shared_prefix_attention",
               "gdn_add_rmsnorm", "gdn_tree_attention")
-_BEAMS = ("GdnBeamShape", "make_beam_shape", "gdn_beam_workspace_size", "gdn_beam_workspace",
-          "gdn_beam_select", "gdn_beam_reorder")
+_BRANCHING = ("gdn_verify_tree", "GdnBeamShape", "make_beam_shape", "gdn_beam_workspace_size",
+              "gdn_beam_workspace", "gdn_beam_select", "gdn_beam_reorder")
 
 
 def __getattr__(name):
-    """The attention-layer calls live in attention.py and the beams' in beams.py, which import
-    torch: loaded on use."""
-    for names, module in ((_ATTENTION, "attention"), (_BEAMS, "beams")):
+    """The attention-layer calls live in attention.py, those for several continuations in
+    branching.py, which import torch: loaded on use."""
+    for names, module in ((_ATTENTION, "attention"), (_BRANCHING, "branching")):
         if name in names:
             m = importlib.import_module("." + module, __name__)
             for n in names:

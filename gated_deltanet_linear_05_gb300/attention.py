@@ -200,7 +200,7 @@ class _Unbuilt:
     def attend(*args):
         return None
 
-    append = norm = attend
+    append = norm = verify = select = reorder = attend
 
 
 def _fast():
@@ -217,7 +217,8 @@ def _fast():
         _marshal.bind(_BF16, _F32, torch.float64, _I32, torch.empty, torch.empty_like, _raw_stream,
                       _DENSE, _current_device, *(ctypes.cast(getattr(L, f), ctypes.c_void_p).value for f in
                                 ("gdn_paged_attention", "gdn_shared_prefix_attention", "gdn_kv_append",
-                                 "gdn_add_rmsnorm")))
+                                 "gdn_add_rmsnorm", "gdn_tree_attention", "gdn_verify_tree",
+                                 "gdn_beam_select", "gdn_beam_reorder")))
         _quick = _marshal
     return _quick
 
@@ -320,13 +321,15 @@ def _attend(name, q, k_cache, v_cache, prefix_table, prefix_len, page_table, kv_
         with torch.cuda.stream(stream):
             return _attend(name, q, k_cache, v_cache, prefix_table, prefix_len, page_table, kv_lens,
                            cu_seqlens, gate, scale, o, lse, workspace, None, parents)
-    if lse is None and parents is None:
+    if lse is None:
         r = (_quick or _fast()).attend(_made, q, k_cache, v_cache, prefix_table, prefix_len, page_table,
-                                       kv_lens, cu_seqlens, gate, scale, o, workspace)
+                                       kv_lens, cu_seqlens, gate, scale, o, workspace, parents)
         if type(r) is int:
             raise GdnError(r, name)
         if r is not None:
             return r
+    if parents is not None and (cu_seqlens is None or parents.shape != q.shape[:1]):
+        raise ValueError("trees need cu_seqlens and parents [tokens]")
     device = q.get_device()
     _check(device, (q, k_cache, v_cache) if gate is None else (q, k_cache, v_cache, gate),
            (page_table, kv_lens, cu_seqlens, prefix_table, parents))
@@ -391,7 +394,7 @@ def gdn_tree_attention(q, k_cache, v_cache, page_table, kv_lens, cu_seqlens, par
     parents [T] int32: each node's parent as an index into its own sequence's nodes, which stands
     before it; -1: the node hangs on the keys before the tree.  With prefix_len > 0 every node
     also sees the shared prefix in prefix_table.  Returns o."""
-    if cu_seqlens is None or parents.shape != q.shape[:1]:
+    if parents is None:
         raise ValueError("trees need cu_seqlens and parents [tokens]")
     return _attend("gdn_tree_attention", q, k_cache, v_cache, prefix_table, prefix_len, page_table,
                    kv_lens, cu_seqlens, gate, scale, o, lse, workspace, stream, parents)

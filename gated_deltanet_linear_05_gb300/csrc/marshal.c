@@ -1,9 +1,9 @@
 /*
- * The attention calls' argument marshalling for torch tensors, for calls whose sizes and strides have
- * been seen before: a decode step's kernels take 4 to 7 us, and checking and unpacking its
+ * The argument marshalling of the attention calls and of those for several continuations, for torch tensors
+ * and calls whose sizes and strides have been seen before: a decode step's kernels take 4 to 7 us, and checking and unpacking its
  * tensors in Python took as long.  Everything else (the first call of a combination, errors) is
- * attention.py's: a function here returns None for "not seen, or not to my liking", and
- * attention.py then checks again and says what is wrong.  Tensors are seen through their Python
+ * attention.py's and branching.py's: a function here returns None for "not seen, or not to my liking",
+ * and they then check again and say what is wrong.  Tensors are seen through their Python
  * attributes only.
  *
  * The interpreter lock is let go around the library's call: a launch blocks while the stream's queue is full.
@@ -28,6 +28,14 @@ static gdn_status (*c_prefix)(const gdn_attn_shape *, const void *, const void *
 static gdn_status (*c_append)(const gdn_attn_shape *, const void *, const void *, const void *, const float *,
                               const float *, float, const double *, const int32_t *, const int32_t *, const int32_t *,
                               const int32_t *, const int32_t *, void *, void *, void *, void *);
+static gdn_status (*c_tree)(const gdn_attn_shape *, const void *, const void *, const void *, const void *,
+                            const int32_t *, const int32_t *, const int32_t *, const int32_t *, const int32_t *, void *,
+                            float *, void *, size_t, void *);
+static gdn_status (*c_verify)(const gdn_shape *, const void *, const void *, const void *, const float *, const float *,
+                              const float *, const int32_t *, const int32_t *, void *, float *, void *);
+static gdn_status (*c_select)(const gdn_beam_shape *, const void *, const float *, const uint8_t *, float *, int32_t *,
+                              int32_t *, void *, size_t, void *);
+static gdn_status (*c_reorder)(int32_t, int32_t, int32_t, int64_t, const int32_t *, void *, void *);
 static gdn_status (*c_norm)(int64_t, int32_t, gdn_dtype, const void *, const void *, const float *, float, void *,
                             void *, float *, int32_t, void *);
 
@@ -138,11 +146,25 @@ static PyObject *no(int r) {
     if (r_ != 1) return no(r_); \
   } while (0)
 
+/* A contiguous int32 vector of as many entries as `like` has rows. */
+static int one_a_row(PyObject *t, PyObject *like, long device) {
+  const int r = good(t, t_i32, device, 1, 0);
+  if (r != 1) return r;
+  PyObject *a = shape_of(t), *b = shape_of(like);
+  int same = a && b && PyTuple_GET_SIZE(a) == 1 && PyTuple_GET_SIZE(b) > 0
+                 ? PyObject_RichCompareBool(PyTuple_GET_ITEM(a, 0), PyTuple_GET_ITEM(b, 0), Py_EQ)
+                 : a && b ? 0 : -1;
+  Py_XDECREF(a);
+  Py_XDECREF(b);
+  return same;
+}
+
 /* attend(made, q, k_cache, v_cache, prefix_table, prefix_len, page_table, kv_lens, cu_seqlens, gate,
- *        scale, o, workspace) */
+ *        scale, o, workspace[, parents]): with parents (not None) gdn_tree_attention */
 static PyObject *attend(PyObject *self, PyObject *const *a, Py_ssize_t count) {
   (void)self;
-  if (count != 13) return PyErr_Format(PyExc_TypeError, "attend takes 13 arguments");
+  if (count != 13 && count != 14) return PyErr_Format(PyExc_TypeError, "attend takes 13 or 14 arguments");
+  PyObject *up = count == 14 ? a[13] : Py_None;
   PyObject *made = a[0], *q = a[1], *k = a[2], *v = a[3], *prefix = a[4], *prefix_len = a[5], *table = a[6],
            *lens = a[7], *cu = a[8], *gate = a[9], *scale = a[10], *o = a[11], *ws = a[12];
   long device;
@@ -158,6 +180,10 @@ static PyObject *attend(PyObject *self, PyObject *const *a, Py_ssize_t count) {
   NEED(good(prefix, t_i32, device, 1, 1));
   NEED(on_device(ws, device));
   NEED(is_dense(ws));
+  if (up != Py_None) {
+    if (cu == Py_None) Py_RETURN_NONE;
+    NEED(one_a_row(up, q, device));
+  }
   PyObject *key = PyTuple_New(13);
   if (!key) return NULL;
   Py_ssize_t at = 0;
@@ -197,7 +223,7 @@ static PyObject *attend(PyObject *self, PyObject *const *a, Py_ssize_t count) {
   const void *pq = (void *)address(q), *pg = (void *)address(gate), *pk = (void *)address(k),
              *pv = (void *)address(v);
   const int32_t *pt = (int32_t *)address(table), *pl = (int32_t *)address(lens), *pc = (int32_t *)address(cu),
-                *pp = (int32_t *)address(prefix);
+                *pp = (int32_t *)address(prefix), *pu = (int32_t *)address(up);
   void *po = (void *)address(out), *pw = (void *)address(ws);
   if (PyErr_Occurred()) {
     Py_DECREF(out);
@@ -205,8 +231,9 @@ static PyObject *attend(PyObject *self, PyObject *const *a, Py_ssize_t count) {
   }
   gdn_status st;
   Py_BEGIN_ALLOW_THREADS
-  st = prefix == Py_None ? c_paged(&s, pq, pg, pk, pv, pt, pl, pc, po, NULL, pw, ws_bytes, stream)
-                         : c_prefix(&s, pq, pg, pk, pv, pp, pt, pl, pc, po, NULL, pw, ws_bytes, stream);
+  st = up != Py_None     ? c_tree(&s, pq, pg, pk, pv, pp, pt, pl, pc, pu, po, NULL, pw, ws_bytes, stream)
+       : prefix == Py_None ? c_paged(&s, pq, pg, pk, pv, pt, pl, pc, po, NULL, pw, ws_bytes, stream)
+                           : c_prefix(&s, pq, pg, pk, pv, pp, pt, pl, pc, po, NULL, pw, ws_bytes, stream);
   Py_END_ALLOW_THREADS
   if (st == GDN_OK) return out;
   Py_DECREF(out);
@@ -380,20 +407,180 @@ end:
   return result;
 }
 
+/* Shape and type of a tensor, twice None for None. */
+static void put_kind(PyObject *key, Py_ssize_t *at, PyObject *t, int *bad) {
+  put(key, at, shape_of(t), bad);
+  put(key, at, t == Py_None ? Py_NewRef(Py_None) : PyObject_GetAttr(t, n_dtype), bad);
+}
+/* A contiguous tensor on this device (None passes with `maybe`); its type is in the key. */
+static int lies(PyObject *t, long device, int maybe) {
+  if (t == Py_None) return maybe;
+  const int r = on_device(t, device);
+  return r == 1 ? is_dense(t) : r;
+}
+static PyObject *like_in(PyObject *t, PyObject *type) {
+  PyObject *args[2] = {t, type};
+  return PyObject_Vectorcall(f_empty_like, args, 1, kw_dtype);
+}
+
+/* verify(made, q, k, v, g, beta, state_in, cu_seqlens, parents, o, delta, chunk) */
+static PyObject *verify(PyObject *self, PyObject *const *a, Py_ssize_t count) {
+  (void)self;
+  if (count != 12) return PyErr_Format(PyExc_TypeError, "verify takes 12 arguments");
+  static PyObject *tag;
+  if (!tag && !(tag = PyUnicode_InternFromString("verify"))) return NULL;
+  long device;
+  NEED(device_of(a[1], &device));
+  for (int i = 1; i < 11; ++i) NEED(lies(a[i], device, i == 6 || i == 9 || i == 10));
+  PyObject *key = PyTuple_New(22);
+  if (!key) return NULL;
+  Py_ssize_t at = 0;
+  int bad = 0;
+  put(key, &at, Py_NewRef(tag), &bad);
+  for (int i = 1; i < 11; ++i) put_kind(key, &at, a[i], &bad);
+  put(key, &at, Py_NewRef(a[11]), &bad);
+  PyObject *entry = look_up(a[0], key, bad);
+  if (!entry) return no(PyErr_Occurred() ? -1 : 0);
+  const gdn_shape s = *(const gdn_shape *)(uintptr_t)PyLong_AsUnsignedLongLong(PyTuple_GET_ITEM(entry, 2));
+  void *stream;
+  NEED(stream_of(device, &stream));
+  PyObject *o = a[9] == Py_None ? PyObject_CallOneArg(f_empty_like, a[3]) : Py_NewRef(a[9]);
+  PyObject *delta = !o ? NULL : a[10] == Py_None ? like_in(a[3], t_f32) : Py_NewRef(a[10]), *result = NULL;
+  if (delta) {
+    const void *p[8];
+    for (int i = 0; i < 8; ++i) p[i] = (void *)address(a[1 + i]);
+    void *po = (void *)address(o), *pd = (void *)address(delta);
+    if (!PyErr_Occurred()) {
+      gdn_status st;
+      Py_BEGIN_ALLOW_THREADS
+      st = c_verify(&s, p[0], p[1], p[2], p[3], p[4], p[5], p[6], p[7], po, pd, stream);
+      Py_END_ALLOW_THREADS
+      result = st == GDN_OK ? PyTuple_Pack(2, o, delta) : PyLong_FromLong(st);
+    }
+  }
+  Py_XDECREF(o);
+  Py_XDECREF(delta);
+  return result;
+}
+
+/* select(made, logits, scores, top, finished, pad_token, workspace): all outputs new */
+static PyObject *select_best(PyObject *self, PyObject *const *a, Py_ssize_t count) {
+  (void)self;
+  if (count != 7) return PyErr_Format(PyExc_TypeError, "select takes 7 arguments");
+  PyObject *made = a[0], *logits = a[1], *scores = a[2], *finished = a[4], *ws = a[6];
+  static PyObject *tag;
+  if (!tag && !(tag = PyUnicode_InternFromString("select"))) return NULL;
+  long device;
+  if (ws == Py_None) Py_RETURN_NONE;
+  NEED(device_of(logits, &device));
+  NEED(lies(scores, device, 0));
+  NEED(lies(finished, device, 1));
+  NEED(lies(ws, device, 0));
+  PyObject *key = PyTuple_New(10);
+  if (!key) return NULL;
+  Py_ssize_t at = 0;
+  int bad = 0;
+  put(key, &at, Py_NewRef(tag), &bad);
+  put(key, &at, shape_of(logits), &bad);
+  put(key, &at, strides_of(logits), &bad);
+  put(key, &at, PyObject_GetAttr(logits, n_dtype), &bad);
+  put_kind(key, &at, scores, &bad);
+  put_kind(key, &at, finished, &bad);
+  put(key, &at, Py_NewRef(a[3]), &bad);
+  put(key, &at, Py_NewRef(a[5]), &bad);
+  PyObject *entry = look_up(made, key, bad);
+  if (!entry) return no(PyErr_Occurred() ? -1 : 0);
+  const gdn_beam_shape s = *(const gdn_beam_shape *)(uintptr_t)PyLong_AsUnsignedLongLong(PyTuple_GET_ITEM(entry, 2));
+  PyObject *shape = Py_NewRef(PyTuple_GET_ITEM(entry, 3));
+  PyObject *out[3] = {NULL, NULL, NULL}, *result = NULL, *where = NULL, *bytes = NULL;
+  void *stream;
+  const int r = stream_of(device, &stream);
+  if (r != 1) {
+    result = no(r);
+    goto end;
+  }
+  if (!(where = PyObject_GetAttr(logits, n_device)) || !(bytes = PyObject_GetAttr(ws, n_nbytes))) goto end;
+  for (int i = 0; i < 3; ++i) {
+    PyObject *args[3] = {shape, i ? t_i32 : t_f32, where};
+    if (!(out[i] = PyObject_Vectorcall(f_empty, args, 1, kw_dtype_device))) goto end;
+  }
+  {
+    const void *px = (void *)address(logits);
+    const float *ps = (float *)address(scores);
+    const uint8_t *pf = (uint8_t *)address(finished);
+    void *po = (void *)address(out[0]), *pu = (void *)address(out[1]), *pt = (void *)address(out[2]),
+         *pw = (void *)address(ws);
+    const size_t ws_bytes = PyLong_AsSize_t(bytes);
+    if (PyErr_Occurred()) goto end;
+    gdn_status st;
+    Py_BEGIN_ALLOW_THREADS
+    st = c_select(&s, px, ps, pf, (float *)po, (int32_t *)pu, (int32_t *)pt, pw, ws_bytes, stream);
+    Py_END_ALLOW_THREADS
+    result = st == GDN_OK ? PyTuple_Pack(3, out[0], out[1], out[2]) : PyLong_FromLong(st);
+  }
+end:
+  for (int i = 0; i < 3; ++i) Py_XDECREF(out[i]);
+  Py_DECREF(shape);
+  Py_XDECREF(where);
+  Py_XDECREF(bytes);
+  return result;
+}
+
+/* reorder(made, rows, parents) */
+static PyObject *reorder(PyObject *self, PyObject *const *a, Py_ssize_t count) {
+  (void)self;
+  if (count != 3) return PyErr_Format(PyExc_TypeError, "reorder takes 3 arguments");
+  PyObject *rows = a[1], *up = a[2];
+  static PyObject *tag;
+  if (!tag && !(tag = PyUnicode_InternFromString("reorder"))) return NULL;
+  long device;
+  NEED(device_of(rows, &device));
+  NEED(is_dense(rows));
+  NEED(lies(up, device, 0));
+  PyObject *key = PyTuple_New(5);
+  if (!key) return NULL;
+  Py_ssize_t at = 0;
+  int bad = 0;
+  put(key, &at, Py_NewRef(tag), &bad);
+  put_kind(key, &at, rows, &bad);
+  put_kind(key, &at, up, &bad);
+  PyObject *entry = look_up(a[0], key, bad); /* (layers, groups, beams, bytes of a row) */
+  if (!entry) return no(PyErr_Occurred() ? -1 : 0);
+  const int32_t layers = (int32_t)PyLong_AsLong(PyTuple_GET_ITEM(entry, 0)),
+                groups = (int32_t)PyLong_AsLong(PyTuple_GET_ITEM(entry, 1)),
+                beams = (int32_t)PyLong_AsLong(PyTuple_GET_ITEM(entry, 2));
+  const int64_t row_bytes = PyLong_AsLongLong(PyTuple_GET_ITEM(entry, 3));
+  void *stream;
+  NEED(stream_of(device, &stream));
+  void *pr = (void *)address(rows);
+  const int32_t *pu = (int32_t *)address(up);
+  if (PyErr_Occurred()) return NULL;
+  gdn_status st;
+  Py_BEGIN_ALLOW_THREADS
+  st = c_reorder(layers, groups, beams, row_bytes, pu, pr, stream);
+  Py_END_ALLOW_THREADS
+  return st == GDN_OK ? Py_NewRef(rows) : PyLong_FromLong(st);
+}
+
 /* bind(bfloat16, float32, float64, int32, empty, empty_like, raw_stream, contiguous_format,
- *      current_device, gdn_paged_attention, gdn_shared_prefix_attention, gdn_kv_append, gdn_add_rmsnorm) */
+ *      current_device, gdn_paged_attention, gdn_shared_prefix_attention, gdn_kv_append, gdn_add_rmsnorm,
+ *      gdn_tree_attention, gdn_verify_tree, gdn_beam_select, gdn_beam_reorder) */
 static PyObject *bind(PyObject *self, PyObject *const *a, Py_ssize_t count) {
   (void)self;
-  if (count != 13) return PyErr_Format(PyExc_TypeError, "bind takes 13 arguments");
+  if (count != 17) return PyErr_Format(PyExc_TypeError, "bind takes 17 arguments");
   PyObject **to[9] = {&t_bf16, &t_f32, &t_f64, &t_i32, &f_empty, &f_empty_like, &f_stream, &dense_format, &f_current};
   for (int i = 0; i < 9; ++i) Py_XSETREF(*to[i], Py_NewRef(a[i]));
-  uintptr_t f[4];
-  for (int i = 0; i < 4; ++i) f[i] = (uintptr_t)PyLong_AsUnsignedLongLong(a[9 + i]);
+  uintptr_t f[8];
+  for (int i = 0; i < 8; ++i) f[i] = (uintptr_t)PyLong_AsUnsignedLongLong(a[9 + i]);
   if (PyErr_Occurred()) return NULL;
   *(uintptr_t *)&c_paged = f[0];
   *(uintptr_t *)&c_prefix = f[1];
   *(uintptr_t *)&c_append = f[2];
   *(uintptr_t *)&c_norm = f[3];
+  *(uintptr_t *)&c_tree = f[4];
+  *(uintptr_t *)&c_verify = f[5];
+  *(uintptr_t *)&c_select = f[6];
+  *(uintptr_t *)&c_reorder = f[7];
   Py_RETURN_NONE;
 }
 
@@ -402,6 +589,9 @@ static PyMethodDef methods[] = {
     {"attend", (PyCFunction)(void (*)(void))attend, METH_FASTCALL, NULL},
     {"append", (PyCFunction)(void (*)(void))append, METH_FASTCALL, NULL},
     {"norm", (PyCFunction)(void (*)(void))norm, METH_FASTCALL, NULL},
+    {"verify", (PyCFunction)(void (*)(void))verify, METH_FASTCALL, NULL},
+    {"select", (PyCFunction)(void (*)(void))select_best, METH_FASTCALL, NULL},
+    {"reorder", (PyCFunction)(void (*)(void))reorder, METH_FASTCALL, NULL},
     {NULL, NULL, 0, NULL},
 };
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", NULL, -1, methods, NULL, NULL, NULL, NULL};
