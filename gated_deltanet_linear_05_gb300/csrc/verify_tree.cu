@@ -180,19 +180,29 @@ __global__ void __launch_bounds__(TreeCfg<T, C>::THREADS, TreeCfg<T, C>::CTAS) v
       cp_async16(smem + (unit >> 3) * F::CHUNK + tile_off(row, unit & 7), src, t < t_n ? 16 : 0);
     }
   } else {
-#pragma unroll 2
-    for (int e = tid; e < 2 * C * 32; e += F::THREADS) {
-      const int row = e >> 5, quad = e & 31, t = row & (C - 1);
-      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (t < t_n)
-        x = *reinterpret_cast<const float4 *>((row < C ? q : k) + ((size_t)(bos + t) * p.hk + kh) * kD + quad * 4);
-      uint8_t *at = smem + (quad >> 4) * F::CHUNK + tile_off(row, (quad & 15) >> 1) + (quad & 1) * 8;
+    constexpr int kBatch = 8;  // loads side by side (two at a time, the rows took 13k cycles of an item's 45k)
+#pragma unroll 1
+    for (int e0 = tid; e0 < 2 * C * 32; e0 += kBatch * F::THREADS) {
+      float4 x[kBatch];
 #pragma unroll
-      for (int term = 0; term < 3; ++term) {
-        uint2 w;
-        w.x = take_bf16(x.x, x.y);
-        w.y = take_bf16(x.z, x.w);
-        *reinterpret_cast<uint2 *>(at + term * 2 * F::CHUNK) = w;
+      for (int b = 0; b < kBatch; ++b) {
+        const int e = e0 + b * F::THREADS, row = e >> 5, t = row & (C - 1);
+        x[b] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (e < 2 * C * 32 && t < t_n)
+          x[b] = *reinterpret_cast<const float4 *>((row < C ? q : k) + ((size_t)(bos + t) * p.hk + kh) * kD + (e & 31) * 4);
+      }
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) {
+        const int e = e0 + b * F::THREADS, row = e >> 5, quad = e & 31;
+        if (e >= 2 * C * 32) break;
+        uint8_t *at = smem + (quad >> 4) * F::CHUNK + tile_off(row, (quad & 15) >> 1) + (quad & 1) * 8;
+#pragma unroll
+        for (int term = 0; term < 3; ++term) {
+          uint2 w;
+          w.x = take_bf16(x[b].x, x[b].y);
+          w.y = take_bf16(x[b].z, x[b].w);
+          *reinterpret_cast<uint2 *>(at + term * 2 * F::CHUNK) = w;
+        }
       }
     }
   }
@@ -254,6 +264,23 @@ __global__ void __launch_bounds__(TreeCfg<T, C>::THREADS, TreeCfg<T, C>::CTAS) v
   const uint64_t tiles = tile_desc(uniform(smem_u32(smem)));
   constexpr uint32_t kChunk = F::CHUNK >> 4;
   constexpr uint32_t id_s = tc::idesc(128, 2 * C, 1, 0, 0);
+  // [W; T] in three terms over the tiles, which the products with S have read by then: 8-row x 16-byte
+  // core matrices, rows of a key column contiguous
+  auto put_factors = [&](int first, int step) {
+    const int keys16 = (t_n + 15) / 16 * 16;
+#pragma unroll 2
+    for (int e = first; e < keys16 * (C / 2); e += step) {
+      const int t = e & (C - 1), c = 2 * (e / C);
+      const float *a = sn + c * F::ROW + t, *b = sa + c * F::ROW + t;
+      float a0 = a[0], a1 = a[F::ROW], b0 = b[0], b1 = b[F::ROW];
+      uint8_t *at = smem + (c >> 3) * (2 * C * 16) + t * 16 + (c & 7) * 2;
+#pragma unroll
+      for (int term = 0; term < 3; ++term) {
+        *reinterpret_cast<uint32_t *>(at + term * F::WT_TERM) = take_bf16(a0, a1);
+        *reinterpret_cast<uint32_t *>(at + term * F::WT_TERM + C * 16) = take_bf16(b0, b1);
+      }
+    }
+  };
   if (t_n > 0 && warp >= 4) {
     // ---------------------------------------------------------------- the tree
     if (warp == 4) {
@@ -307,9 +334,14 @@ __global__ void __launch_bounds__(TreeCfg<T, C>::THREADS, TreeCfg<T, C>::CTAS) v
     for (int t0 = 0; t0 < t_n; t0 += 16) {
       float2 r[8] = {}, w[8] = {};
       float d[16];
+      // four at a time of the nodes before these 16, where one of them has one of these below
+      uint64_t need = above[t0 + (j & 15)];
+      need = (uint64_t)__reduce_or_sync(0xffffffffu, (uint32_t)(need >> 32)) << 32 |
+             __reduce_or_sync(0xffffffffu, (uint32_t)need);
       if (j < C) {
 #pragma unroll 1
         for (int m = 0; m < t0; m += 4) {
+          if (!(need >> m & 15)) continue;
           const float4 x = *reinterpret_cast<const float4 *>(sa + j * F::ROW + m);
           const float xs[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
@@ -331,23 +363,11 @@ __global__ void __launch_bounds__(TreeCfg<T, C>::THREADS, TreeCfg<T, C>::CTAS) v
       }
     }
     bar_sync(3, kTree);
-    // [W; T] in three terms over the tiles, which the products with S have read by then: 8-row x 16-byte
-    // core matrices, rows of a key column contiguous
-    if (state) wait_bar(&bar_s, 0, dead, p.err);
-    const int keys16 = (t_n + 15) / 16 * 16;
-#pragma unroll 2
-    for (int e = j; e < keys16 * (C / 2); e += kTree) {
-      const int t = e & (C - 1), c = 2 * (e / C);
-      const float *a = sn + c * F::ROW + t, *b = sa + c * F::ROW + t;
-      float a0 = a[0], a1 = a[F::ROW], b0 = b[0], b1 = b[F::ROW];
-      uint8_t *at = smem + (c >> 3) * (2 * C * 16) + t * 16 + (c & 7) * 2;
-#pragma unroll
-      for (int term = 0; term < 3; ++term) {
-        *reinterpret_cast<uint32_t *>(at + term * F::WT_TERM) = take_bf16(a0, a1);
-        *reinterpret_cast<uint32_t *>(at + term * F::WT_TERM + C * 16) = take_bf16(b0, b1);
-      }
+    if (C < 64) {
+      if (state) wait_bar(&bar_s, 0, dead, p.err);
+      put_factors(j, kTree);
+      tc::fence_proxy_async();
     }
-    tc::fence_proxy_async();
   } else if (t_n > 0) {
     // ---------------------------------------------------------------- D^T = S^T [Q; K]^T
     if (state) {
@@ -434,6 +454,11 @@ __global__ void __launch_bounds__(TreeCfg<T, C>::THREADS, TreeCfg<T, C>::CTAS) v
       }
     }
     tc::wait_st();
+  }
+  if (C == 64) {
+    __syncthreads();
+    put_factors(tid, F::THREADS);
+    tc::fence_proxy_async();
   }
   tc::fence_before();
   __syncthreads();
