@@ -25,7 +25,14 @@
 //   results   r, in three terms over S^T's columns, times [W; T]^T in three terms, added to
 //             diag(e^G) D^T in place.
 //
-// Bound by HBM: the 64 KB of S per head are read once.
+// The 64 KB of S per head are read once.  64 trees of 11 to 32 nodes, 32 heads: 49 us, 3.8 TB/s (floor 27);
+// bound by the chain of steps that a CTA goes through (loads under a busy HBM 6000 cycles, the state's steps
+// 11000, results 5000 of 22000) at four CTAs an SM, all that tensor memory holds (128 of 512 columns each).
+// 24 trees of 40 to 64 nodes: bf16 64 us (two CTAs), f32 124 (one).
+//
+// Tried and dropped: tf32 terms (two instructions a value in place of five and a half; q and k then go through
+// registers to become 32 bits wide: 52 -> 66 us), the next CTA's state brought to L2 meanwhile (the same), T for two
+// columns a lane and W by another warp (C = 64: 124 -> 134), the solution of 16 nodes in a rolled loop (52 -> 60).
 #include "attn_tma.cuh"
 #include "internal.h"
 #include "tc.cuh"
@@ -56,7 +63,10 @@ struct TreeCfg {
   static constexpr int COLS = A_COL + A_COLS <= 128 ? 128 : 256;
   static constexpr int TREE_WARPS = C == 64 ? 2 : 1;
   static constexpr int THREADS = kColumns + 32 * TREE_WARPS;
-  static constexpr int CTAS = C == 64 ? 2 : 4;
+  // CTAs on an SM by shared and by tensor memory; the registers are shared out for two at least (f32, C = 64: one
+  // fits, and with 254 registers a thread took 132 us for 124)
+  static constexpr int FIT = 227 * 1024 / (SMEM + 4096), MOST = 512 / COLS;
+  static constexpr int CTAS = FIT < 2 ? 2 : FIT < MOST ? FIT : MOST;
 };
 
 // 64 columns x 2 C rows of bf16, 128-byte swizzle, K-major.
@@ -264,23 +274,6 @@ __global__ void __launch_bounds__(TreeCfg<T, C>::THREADS, TreeCfg<T, C>::CTAS) v
   const uint64_t tiles = tile_desc(uniform(smem_u32(smem)));
   constexpr uint32_t kChunk = F::CHUNK >> 4;
   constexpr uint32_t id_s = tc::idesc(128, 2 * C, 1, 0, 0);
-  // [W; T] in three terms over the tiles, which the products with S have read by then: 8-row x 16-byte
-  // core matrices, rows of a key column contiguous
-  auto put_factors = [&](int first, int step) {
-    const int keys16 = (t_n + 15) / 16 * 16;
-#pragma unroll 2
-    for (int e = first; e < keys16 * (C / 2); e += step) {
-      const int t = e & (C - 1), c = 2 * (e / C);
-      const float *a = sn + c * F::ROW + t, *b = sa + c * F::ROW + t;
-      float a0 = a[0], a1 = a[F::ROW], b0 = b[0], b1 = b[F::ROW];
-      uint8_t *at = smem + (c >> 3) * (2 * C * 16) + t * 16 + (c & 7) * 2;
-#pragma unroll
-      for (int term = 0; term < 3; ++term) {
-        *reinterpret_cast<uint32_t *>(at + term * F::WT_TERM) = take_bf16(a0, a1);
-        *reinterpret_cast<uint32_t *>(at + term * F::WT_TERM + C * 16) = take_bf16(b0, b1);
-      }
-    }
-  };
   if (t_n > 0 && warp >= 4) {
     // ---------------------------------------------------------------- the tree
     if (warp == 4) {
@@ -363,11 +356,6 @@ __global__ void __launch_bounds__(TreeCfg<T, C>::THREADS, TreeCfg<T, C>::CTAS) v
       }
     }
     bar_sync(3, kTree);
-    if (C < 64) {
-      if (state) wait_bar(&bar_s, 0, dead, p.err);
-      put_factors(j, kTree);
-      tc::fence_proxy_async();
-    }
   } else if (t_n > 0) {
     // ---------------------------------------------------------------- D^T = S^T [Q; K]^T
     if (state) {
@@ -455,11 +443,23 @@ __global__ void __launch_bounds__(TreeCfg<T, C>::THREADS, TreeCfg<T, C>::CTAS) v
     }
     tc::wait_st();
   }
-  if (C == 64) {
-    __syncthreads();
-    put_factors(tid, F::THREADS);
-    tc::fence_proxy_async();
+  __syncthreads();
+  // [W; T] in three terms over the tiles, which every product has read: 8-row x 16-byte core matrices, rows of
+  // a key column contiguous
+  const int keys16 = (t_n + 15) / 16 * 16;
+#pragma unroll 2
+  for (int e = tid; e < keys16 * (C / 2); e += F::THREADS) {
+    const int t = e & (C - 1), c = 2 * (e / C);
+    const float *a = sn + c * F::ROW + t, *b = sa + c * F::ROW + t;
+    float a0 = a[0], a1 = a[F::ROW], b0 = b[0], b1 = b[F::ROW];
+    uint8_t *at = smem + (c >> 3) * (2 * C * 16) + t * 16 + (c & 7) * 2;
+#pragma unroll
+    for (int term = 0; term < 3; ++term) {
+      *reinterpret_cast<uint32_t *>(at + term * F::WT_TERM) = take_bf16(a0, a1);
+      *reinterpret_cast<uint32_t *>(at + term * F::WT_TERM + C * 16) = take_bf16(b0, b1);
+    }
   }
+  tc::fence_proxy_async();
   tc::fence_before();
   __syncthreads();
   if (t_n > 0 && warp < 4) {
