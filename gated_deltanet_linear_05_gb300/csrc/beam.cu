@@ -137,7 +137,7 @@ __device__ __forceinline__ uint32_t common_limit(uint32_t mine, int top, uint32_
 }
 
 template <typename T, bool ALIGNED, int VEC>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && ALIGNED && VEC == 4 ? 3 : 4) beam_rows_kernel(BeamParams p) {
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && ALIGNED ? 3 : 4) beam_rows_kernel(BeamParams p) {
   using V = Values<T, ALIGNED, VEC>;
   constexpr int MOST = V::MOST, STEP = MOST * kThreads;
   __shared__ uint64_t best[64];  // the best so far, largest first
@@ -517,19 +517,18 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(BeamParams p) {
   }
 }
 
-// Values of a thread and step, in 16-byte units: four; one where the rows are few, so that more CTAs share
-// them (2 requests of 4 beams over 32000: see below).
-int vec_of(int rows, int vocab, int per) { return (long long)rows * (vocab / (kThreads * 4 * per)) < 2 * kSms ? 1 : 4; }
-
 // Parts of a row, each of whole steps: the number that ends first if `slots` CTAs run at a time, the last of them
 // half a CTA's time longer than the rest, and a CTA's start and end take one and a half steps (64 x 8 rows of 150001,
-// 37 steps, in 1 to 5 parts: 61, 61, 56, 60, 63 us); no more lists a request than the join takes.
+// 37 steps, in 1 to 5 parts: 61, 61, 56, 60, 63 us; 2 x 4 rows of 32000, 4 steps, in 1 to 4: 12.4, 10.1, 9.8,
+// 7.9; steps of a quarter of the size, and so more of them: 8.7); no more lists a request than the join takes.
 int parts_of(int rows, int beams, int vocab, int step, int slots) {
   const int steps = (vocab + step - 1) / step, most = std::min(steps, kLists / beams);
   int best = 1;
   float least = 0.f;
   for (int parts = 1; parts <= most; ++parts) {
-    const float cost = (float)rows / slots * (steps + 1.5f * parts) + 0.5f * ((float)steps / parts + 1.5f);
+    const float all = (float)rows / slots * (steps + 1.5f * parts);  // (grows with the parts)
+    if (parts > 1 && all > least) break;
+    const float cost = all + 0.5f * ((steps + parts - 1) / parts + 1.5f);
     if (parts == 1 || cost < least) best = parts, least = cost;
   }
   return best;
@@ -587,10 +586,7 @@ cudaError_t select(const BeamParams &p, cudaStream_t stream) {
 }
 template <typename T>
 cudaError_t by_alignment(const BeamParams &p, cudaStream_t stream) {
-  constexpr int per = 16 / (int)sizeof(T);
-  const bool aligned = reinterpret_cast<uintptr_t>(p.logits) % 16 == 0 && p.row_stride % per == 0;
-  if (vec_of(p.groups * p.beams, p.vocab, per) == 1)
-    return aligned ? select<T, true, 1>(p, stream) : select<T, false, 1>(p, stream);
+  const bool aligned = reinterpret_cast<uintptr_t>(p.logits) % 16 == 0 && p.row_stride % (16 / (int)sizeof(T)) == 0;
   // (single values of 16 bits take a register each: half as many)
   return aligned ? select<T, true, 4>(p, stream) : select<T, false, sizeof(T) == 2 ? 2 : 4>(p, stream);
 }
@@ -598,8 +594,7 @@ cudaError_t by_alignment(const BeamParams &p, cudaStream_t stream) {
 }  // namespace
 
 int beam_parts(int groups, int beams, int vocab, bool bf16) {
-  const int rows = groups * beams, per = bf16 ? 8 : 4, vec = vec_of(rows, vocab, per);
-  return parts_of(rows, beams, vocab, kThreads * vec * per, kSms * (bf16 && vec == 4 ? 3 : 4));
+  return parts_of(groups * beams, beams, vocab, kThreads * 4 * (bf16 ? 8 : 4), kSms * (bf16 ? 3 : 4));
 }
 
 cudaError_t launch_beam_select(const BeamParams &p, gdn_dtype dtype, cudaStream_t stream) {
