@@ -243,6 +243,7 @@ gdn_status gdn_state_rollback(const gdn_shape *shape, const void *k, const float
  *     delta      [total_tokens, Hv, dv]  float32
  * o and delta must not overlap each other or an input (GDN_ERR_ALIAS).  shape->chunk (16, 32 or
  * 64) is the most nodes of a tree; a sequence with more gives unspecified results for itself alone.
+ * A NaN or an infinity among a tree's inputs may reach all of its nodes, but no other sequence's.
  * shape->algo must be GDN_ALGO_AUTO.  No state is written: the one after an accepted path follows
  * from gdn_state_rollback on the path's rows of k, g and delta.
  * q, k and v are taken exactly and the state to 24 bits on the tensor cores, sums in float32 (bf16
