@@ -312,7 +312,7 @@ cudaError_t run_tiles(const AttnParams &p, TilePlan own, const PrefixParts &part
   const size_t smem = C::SMEM + 1024;
   static std::atomic<uint64_t> allowed{0};
   err = allow_smem(tile_kernel<C>, smem, allowed);
-  // (152 blocks of 8 trees beside the plan's)
+  // (blocks of 8 trees beside the plan's)
   const int trees = C::TREE ? std::min((p.num_seqs + kTreesABlock - 1) / kTreesABlock, kSms - 1) : 0;
   if (err == cudaSuccess)
     err = launch_dependent(plan_kernel, 1 + trees, kPlanThreads, 0, stream, 1, p, own, tt);

@@ -282,13 +282,14 @@ __device__ __forceinline__ bool better(const Cand &a, const Cand &b) {
   return a.score > b.score || (a.score == b.score && a.place < b.place);
 }
 
-// Pass 2: a request.  The (beam, part) lists are in order.  Their first entries, up to kSample of them, tell a score that at least `top` reach and not many more, found by halving: first by threads'
-// largest, then by all.  What reaches it, and what follows in lists whose sampled entries all do, is ranked by
-// counting.  The halving is done on scores in float32, less what their rounding may make of them; only what passes
-// gets its score in float64 (slow on this GPU).
-constexpr int kLists = 4096;           // lists of a request at most
+// Pass 2: a request.  The (beam, part) lists are in order.  Their first entries, up to kSample of them, tell a score
+// that at least `top` reach and not many more, found by halving: first by threads' largest, then by all.  What
+// reaches it, and what follows in lists whose sampled entries all do, is ranked by counting.  The halving is done on
+// scores in float32, less what their rounding may make of them; only what passes gets its score in float64 (slow on
+// this GPU).
+constexpr int kLists = 4096;   // lists of a request at most
 constexpr int kSample = 4096;
-constexpr int kRoom = kLists;          // what may pass, but for equal scores: no less than 64 entries of 64 lists
+constexpr int kRoom = kLists;  // what may pass, but for equal scores: no less than 64 entries of 64 lists
 
 // ln(a + b), b small beside a > 0, to 2^-28: a = 2^e f with f in [1/sqrt 2, sqrt 2), ln f = 2 artanh(s) with
 // s = (f - 1) / (f + 1), |s| < 0.172; s in two floats, its series from s^3 on (to s^11) in one.

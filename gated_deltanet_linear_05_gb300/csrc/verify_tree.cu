@@ -21,14 +21,14 @@
 //             them; the thread of key j multiplies those of its descendants by the decays (exponents:
 //             differences of G in two floats).  Then thread j runs the recursion on unit vector j, 16 nodes
 //             at a time in registers.  (Down lists of the ancestors alone it took 90 cycles for each four of
-//             them, one after another: 24 trees of 40 to 64 nodes, some of them chains, in f32 237 us.)
+//             them, one after another: 24 trees of 40 to 64 nodes, some of them chains, in f32 237 us for 168.)
 //   results   r, in three terms over S^T's columns, times [W; T]^T in three terms, added to
 //             diag(e^G) D^T in place.
 //
 // The 64 KB of S per head are read once.  64 trees of 11 to 32 nodes, 32 heads: 49 us, 3.8 TB/s (floor 27);
 // bound by the chain of steps that a CTA goes through (loads under a busy HBM 6000 cycles, the state's steps
 // 11000, results 5000 of 22000) at four CTAs an SM, all that tensor memory holds (128 of 512 columns each).
-// 24 trees of 40 to 64 nodes: bf16 64 us (two CTAs), f32 124 (one).
+// 24 trees of 40 to 64 nodes: bf16 64 us, f32 86 (two CTAs).
 //
 // Tried and dropped: tf32 terms (two instructions a value in place of five and a half; q and k then go through
 // registers to become 32 bits wide: 52 -> 66 us), the next CTA's state brought to L2 meanwhile (the same), T for two
@@ -44,18 +44,22 @@ constexpr int kColumns = 128;  // threads with a value column
 constexpr int kKeys = 32;      // keys of S to a step
 
 // Shared memory: operand tiles, whose place [W; T] in three terms takes; N and A, whose place W and T
-// take; v.
+// take; v, if there is room.
 template <typename T, int C>
 struct TreeCfg {
   static constexpr int TERMS = sizeof(T) == 2 ? 1 : 3;  // bf16 terms of a value of q or k
   static constexpr int CHUNK = 2 * C * 128;             // 64 columns of [Q; K]
-  static constexpr int QK = TERMS * 2 * CHUNK;
+  // Chunks in shared memory at a time.  f32 rows of 32 and 64 nodes have 48 and 96 KB of terms, which leave an SM two
+  // CTAs and one: their chunks come one after the other, the second once more for the state's products, and v straight
+  // to registers (24 trees of 40 to 64 nodes 124 -> 86 us, 64 of 11 to 32 96 -> 86; 64 of 8 to 16 50 -> 57: not there).
+  static constexpr int HALVES = TERMS == 3 && C >= 32 ? 1 : 2;
+  static constexpr int QK = TERMS * HALVES * CHUNK;
   static constexpr int WT_TERM = 2 * C * C * 2;         // a term of [W; T]
   static constexpr int N_AT = QK > 3 * WT_TERM ? QK : 3 * WT_TERM;
   static constexpr int ROW = C + 4;                     // floats: 16-byte accesses of a column of rows spread over the banks
   static constexpr int A_AT = N_AT + C * ROW * 4;
   static constexpr int V_AT = A_AT + C * ROW * 4;
-  static constexpr int USED = V_AT + C * kD * (int)sizeof(T);
+  static constexpr int USED = V_AT + (HALVES == 2 ? C * kD * (int)sizeof(T) : 0);
   // the Gram product reads 128 rows from K's first; past the tiles they are whatever follows
   static constexpr int GRAM = QK - CHUNK + C * 128 + 16384;
   static constexpr int SMEM = 1024 + (USED > GRAM ? USED : GRAM);
@@ -63,10 +67,10 @@ struct TreeCfg {
   static constexpr int COLS = A_COL + A_COLS <= 128 ? 128 : 256;
   static constexpr int TREE_WARPS = C == 64 ? 2 : 1;
   static constexpr int THREADS = kColumns + 32 * TREE_WARPS;
-  // CTAs on an SM by shared and by tensor memory; the registers are shared out for two at least (f32, C = 64: one
-  // fits, and with 254 registers a thread took 132 us for 124)
-  static constexpr int FIT = 227 * 1024 / (SMEM + 4096), MOST = 512 / COLS;
-  static constexpr int CTAS = FIT < 2 ? 2 : FIT < MOST ? FIT : MOST;
+  // CTAs on an SM by shared and by tensor memory; three where a fourth takes too many registers from the
+  // reloading of chunks (86 for 89 us; without it, at C = 16, 52 for 50)
+  static constexpr int FIT = 227 * 1024 / (SMEM + 4096), MOST = HALVES == 1 && COLS == 128 ? 3 : 512 / COLS;
+  static constexpr int CTAS = FIT < MOST ? FIT : MOST;
 };
 
 // 64 columns x 2 C rows of bf16, 128-byte swizzle, K-major.
@@ -182,6 +186,38 @@ __global__ void __launch_bounds__(TreeCfg<T, C>::THREADS, TreeCfg<T, C>::CTAS) v
   const int t_n = min(eos - bos, C);
 
   const T *q = static_cast<const T *>(p.q), *k = static_cast<const T *>(p.k), *v = static_cast<const T *>(p.v);
+  // f32 rows of q and k in three terms, from column 64 `half` on, by `threads` threads; `ready` comes before the first
+  // of them is written
+  auto put_rows = [&](int half, int threads, auto ready) {
+    constexpr int kBatch = 8;  // loads side by side (two at a time, the rows took 13k cycles of an item's 45k)
+    constexpr int kQuads = 16 * F::HALVES;
+#pragma unroll 1
+    for (int e0 = tid; e0 < 2 * C * kQuads; e0 += kBatch * threads) {
+      float4 x[kBatch];
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) {
+        const int e = e0 + b * threads, row = e / kQuads, t = row & (C - 1);
+        x[b] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (e < 2 * C * kQuads && t < t_n)
+          x[b] = *reinterpret_cast<const float4 *>((row < C ? q : k) + ((size_t)(bos + t) * p.hk + kh) * kD + half * 64 +
+                                                   (e % kQuads) * 4);
+      }
+      if (e0 == tid) ready();
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) {
+        const int e = e0 + b * threads, row = e / kQuads, quad = e % kQuads;
+        if (e >= 2 * C * kQuads) break;
+        uint8_t *at = smem + (quad >> 4) * F::CHUNK + tile_off(row, (quad & 15) >> 1) + (quad & 1) * 8;
+#pragma unroll
+        for (int term = 0; term < 3; ++term) {
+          uint2 w;
+          w.x = take_bf16(x[b].x, x[b].y);
+          w.y = take_bf16(x[b].z, x[b].w);
+          *reinterpret_cast<uint2 *>(at + term * F::HALVES * F::CHUNK) = w;
+        }
+      }
+    }
+  };
   if (F::TERMS == 1) {
 #pragma unroll 2
     for (int e = tid; e < 2 * C * 16; e += F::THREADS) {
@@ -190,34 +226,10 @@ __global__ void __launch_bounds__(TreeCfg<T, C>::THREADS, TreeCfg<T, C>::CTAS) v
       cp_async16(smem + (unit >> 3) * F::CHUNK + tile_off(row, unit & 7), src, t < t_n ? 16 : 0);
     }
   } else {
-    constexpr int kBatch = 8;  // loads side by side (two at a time, the rows took 13k cycles of an item's 45k)
-#pragma unroll 1
-    for (int e0 = tid; e0 < 2 * C * 32; e0 += kBatch * F::THREADS) {
-      float4 x[kBatch];
-#pragma unroll
-      for (int b = 0; b < kBatch; ++b) {
-        const int e = e0 + b * F::THREADS, row = e >> 5, t = row & (C - 1);
-        x[b] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (e < 2 * C * 32 && t < t_n)
-          x[b] = *reinterpret_cast<const float4 *>((row < C ? q : k) + ((size_t)(bos + t) * p.hk + kh) * kD + (e & 31) * 4);
-      }
-#pragma unroll
-      for (int b = 0; b < kBatch; ++b) {
-        const int e = e0 + b * F::THREADS, row = e >> 5, quad = e & 31;
-        if (e >= 2 * C * 32) break;
-        uint8_t *at = smem + (quad >> 4) * F::CHUNK + tile_off(row, (quad & 15) >> 1) + (quad & 1) * 8;
-#pragma unroll
-        for (int term = 0; term < 3; ++term) {
-          uint2 w;
-          w.x = take_bf16(x[b].x, x[b].y);
-          w.y = take_bf16(x[b].z, x[b].w);
-          *reinterpret_cast<uint2 *>(at + term * 2 * F::CHUNK) = w;
-        }
-      }
-    }
+    put_rows(F::HALVES == 1 ? 1 : 0, F::THREADS, [] {});
   }
   constexpr int kUnits = kD * (int)sizeof(T) / 16;  // of a row of v
-  for (int e = tid; e < t_n * kUnits; e += F::THREADS) {
+  for (int e = tid; F::HALVES == 2 && e < t_n * kUnits; e += F::THREADS) {
     const int t = e / kUnits, unit = e % kUnits;
     cp_async16(reinterpret_cast<uint8_t *>(sv) + e * 16,
                reinterpret_cast<const uint8_t *>(v + ((size_t)(bos + t) * p.hv + h) * kD) + unit * 16, 16);
@@ -274,23 +286,35 @@ __global__ void __launch_bounds__(TreeCfg<T, C>::THREADS, TreeCfg<T, C>::CTAS) v
   const uint64_t tiles = tile_desc(uniform(smem_u32(smem)));
   constexpr uint32_t kChunk = F::CHUNK >> 4;
   constexpr uint32_t id_s = tc::idesc(128, 2 * C, 1, 0, 0);
+  // Gram products of the chunks in shared memory; by one thread
+  auto gram = [&](bool some) {
+    const uint64_t keys = tiles + (C * 128 >> 4);
+#pragma unroll
+    for (int x = F::TERMS == 1 ? kProducts - 1 : 0; x < kProducts; ++x)
+#pragma unroll
+      for (int i = 0; i < F::HALVES * 4; ++i, some = true)
+        tc::mma_ss(tmem, keys + (kTermA[x] * F::HALVES + i / 4) * kChunk + (i % 4) * 2,
+                   tiles + (kTermB[x] * F::HALVES + i / 4) * kChunk + (i % 4) * 2, id_s, some);
+    tc::commit(&bar_gram);
+  };
+  if (F::HALVES == 1 && t_n > 0) {  // the second half's, then the first half in its place
+    if (warp == 4) {
+      if (elect_one()) gram(false);
+      __syncwarp();
+    }
+    put_rows(0, F::THREADS, [&] { wait_bar(&bar_gram, 0, dead, p.err); });
+    tc::fence_proxy_async();
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+  }
   if (t_n > 0 && warp >= 4) {
     // ---------------------------------------------------------------- the tree
     if (warp == 4) {
-      if (elect_one()) {
-        const uint64_t keys = tiles + (C * 128 >> 4);
-        bool some = false;
-#pragma unroll
-        for (int x = F::TERMS == 1 ? kProducts - 1 : 0; x < kProducts; ++x)
-#pragma unroll
-          for (int i = 0; i < kD / 16; ++i, some = true)
-            tc::mma_ss(tmem, keys + (kTermA[x] * 2 + i / 4) * kChunk + (i % 4) * 2,
-                       tiles + (kTermB[x] * 2 + i / 4) * kChunk + (i % 4) * 2, id_s, some);
-        tc::commit(&bar_gram);
-      }
+      if (elect_one()) gram(F::HALVES == 1);
       __syncwarp();
     }
-    wait_bar(&bar_gram, 0, dead, p.err);
+    wait_bar(&bar_gram, F::HALVES == 1 ? 1 : 0, dead, p.err);
     tc::fence_after();
     const float2 own = path[j & (C - 1)];
 #pragma unroll 1
@@ -361,6 +385,10 @@ __global__ void __launch_bounds__(TreeCfg<T, C>::THREADS, TreeCfg<T, C>::CTAS) v
     if (state) {
 #pragma unroll 1
       for (int c0 = 0; c0 < kD / kKeys; c0 += 2) {
+        if (F::HALVES == 1 && c0 > 0) {
+          put_rows(1, kColumns, [&] { wait_bar(&bar_out, 1, dead, p.err); });
+          tc::fence_proxy_async();  // (the next barrier is before these products)
+        }
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           const int c = c0 + half;
@@ -394,7 +422,7 @@ __global__ void __launch_bounds__(TreeCfg<T, C>::THREADS, TreeCfg<T, C>::CTAS) v
 #pragma unroll
                 for (int i = 0; i < kKeys / 16; ++i, some = 1)
                   tc::mma_ts(tmem, tmem + F::A_COL + 16 * kTermA[y] + 8 * i,
-                             tiles + (kTermB[y] * 2 + (c0 >> 1)) * kChunk + (half * 2 + i) * 2, id_s, some);
+                             tiles + (kTermB[y] * F::HALVES + (F::HALVES == 2 ? c0 >> 1 : 0)) * kChunk + (half * 2 + i) * 2, id_s, some);
               }
               tc::commit(c + 1 < kD / kKeys ? &bar_out : &bar_s);
             }
@@ -410,6 +438,13 @@ __global__ void __launch_bounds__(TreeCfg<T, C>::THREADS, TreeCfg<T, C>::CTAS) v
       tc::fence_after();
     }
     // r, and what it will be added to
+    const T *v_col = v + ((size_t)bos * p.hv + h) * kD + tid;
+    float ahead[16];
+    auto load_v = [&](int t0) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) ahead[i] = t0 + i < t_n ? Elem<T>::load(v_col + (size_t)(t0 + i) * p.hv * kD) : 0.f;
+    };
+    if (F::HALVES == 1) load_v(0);
 #pragma unroll 1
     for (int t0 = 0; t0 < t_n; t0 += 16) {
       uint32_t x[16], y[16];
@@ -426,11 +461,13 @@ __global__ void __launch_bounds__(TreeCfg<T, C>::THREADS, TreeCfg<T, C>::CTAS) v
         const int t = t0 + i;
         const bool node = t < t_n;
         const float scale = node && state ? from_state[t] : 0.f;
-        r[i] = node ? Elem<T>::load(sv + t * kD + tid) : 0.f;
+        if (F::HALVES == 2) r[i] = node ? Elem<T>::load(sv + t * kD + tid) : 0.f;
+        else r[i] = ahead[i];
         if (state) r[i] = fmaf(-scale, __uint_as_float(y[i]), r[i]);
         x[i] = state ? __float_as_uint(scale * __uint_as_float(x[i])) : 0u;
         y[i] = 0u;
       }
+      if (F::HALVES == 1) load_v(t0 + 16);
       tc::st16(lanes + t0, x);
       tc::st16(lanes + C + t0, y);
 #pragma unroll
