@@ -119,13 +119,14 @@ __device__ __forceinline__ void rank_keys(const uint64_t *keys, int count, uint6
 
 // A value that at least `top` threads' reach, and not many more if it can be helped: `mine` of the threads that take
 // part (0 for the others), of which there are `top` at least.
-__device__ __forceinline__ uint32_t common_limit(uint32_t mine, int top, uint32_t (&sh)[2][kThreads / 32]) {
+template <int WARPS>
+__device__ __forceinline__ uint32_t common_limit(uint32_t mine, int top, uint32_t (&sh)[2][WARPS]) {
   const uint32_t big = __reduce_max_sync(kAll, mine), small = __reduce_min_sync(kAll, mine == 0 ? ~0u : mine);
   if ((threadIdx.x & 31) == 0) sh[0][threadIdx.x >> 5] = big, sh[1][threadIdx.x >> 5] = small;
   __syncthreads();
   uint32_t lo = ~0u, hi = 0;
 #pragma unroll
-  for (int i = 0; i < kThreads / 32; ++i) hi = max(hi, sh[0][i]), lo = min(lo, sh[1][i]);
+  for (int i = 0; i < WARPS; ++i) hi = max(hi, sh[0][i]), lo = min(lo, sh[1][i]);
   while (lo < hi) {
     const uint32_t mid = lo + (hi - lo + 1) / 2;
     const int count = __syncthreads_count(mine >= mid);
@@ -291,6 +292,12 @@ constexpr int kLists = 4096;   // lists of a request at most
 constexpr int kSample = 4096;
 constexpr int kRoom = kLists;  // what may pass, but for equal scores: no less than 64 entries of 64 lists
 
+// sampled entries of a list
+__host__ __device__ constexpr int sampled_of(int lists, int top) {
+  const int most = kSample / lists > 1 ? kSample / lists : 1;
+  return top < most ? top : most;
+}
+
 // ln(a + b), b small beside a > 0, to 2^-28: a = 2^e f with f in [1/sqrt 2, sqrt 2), ln f = 2 artanh(s) with
 // s = (f - 1) / (f + 1), |s| < 0.172; s in two floats, its series from s^3 on (to s^11) in one.
 __device__ __forceinline__ double log_of(float a, float b) {
@@ -311,17 +318,18 @@ __device__ __forceinline__ uint64_t pick(const uint64_t (&x)[8], int i) {
   return r;
 }
 
-__global__ void __launch_bounds__(kThreads) beam_join_kernel(BeamParams p) {
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS) beam_join_kernel(BeamParams p) {
   __shared__ double lse[64];    // of a beam (dead or finished: 0)
   __shared__ float score_of[64];  // (dead: 0)
   __shared__ float shift[64];     // score less lse, for the bound
   __shared__ int kind[64];      // 0: as the logits say; 1: every continuation -inf; 2: finished
-  __shared__ uint32_t sh_range[2][kThreads / 32];
+  __shared__ uint32_t sh_range[2][THREADS / 32];
   __shared__ Cand sh_bound;
   __shared__ int sh_count, sh_sum[3], sh_widest;  // widest: the largest |score| + |lse|, as its float's bits
   extern __shared__ uint64_t raw[];
   const int tid = threadIdx.x, group = blockIdx.x, w_n = p.beams, parts = p.parts, top = p.top;
-  const int lists = w_n * parts, deep = min(top, max(kSample / lists, 1));  // sampled entries of a list
+  const int lists = w_n * parts, deep = sampled_of(lists, top);
   Cand *found = reinterpret_cast<Cand *>(raw);  // [kRoom]
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
@@ -403,16 +411,16 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(BeamParams p) {
   uint32_t *sample = reinterpret_cast<uint32_t *>(found + kRoom), most = 0;  // [kSample]
   const int sampled = lists * deep;
 #pragma unroll 1
-  for (int k = tid; k < sampled; k += 4 * kThreads) {
+  for (int k = tid; k < sampled; k += 4 * THREADS) {
     uint64_t key[4];
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-      const int at = k + u * kThreads, list = at / deep;
+      const int at = k + u * THREADS, list = at / deep;
       key[u] = at < sampled ? keys[(long long)list * top + (at - list * deep)] : 0;
     }
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-      const int at = k + u * kThreads, list = at / deep;
+      const int at = k + u * THREADS, list = at / deep;
       float logit;
       uint32_t place, score = 0;
       if (at >= sampled) break;
@@ -426,7 +434,7 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(BeamParams p) {
   auto reach = [&](uint32_t limit, int turn) {
     int count = 0;
 #pragma unroll 4
-    for (int k = tid; k < sampled; k += kThreads) count += sample[k] >= limit && sample[k] != 0;
+    for (int k = tid; k < sampled; k += THREADS) count += sample[k] >= limit && sample[k] != 0;
     count = __reduce_add_sync(kAll, count);
     if ((tid & 31) == 0 && count) atomicAdd(&sh_sum[turn], count);
     __syncthreads();
@@ -440,7 +448,7 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(BeamParams p) {
     if ((tid & 31) == 0) sh_range[0][tid >> 5] = most;
     __syncthreads();
     uint32_t hi = 0;
-    for (int i = 0; i < kThreads / 32; ++i) hi = max(hi, sh_range[0][i]);
+    for (int i = 0; i < THREADS / 32; ++i) hi = max(hi, sh_range[0][i]);
     for (int turn = 1; lo < hi; turn = turn == 2 ? 0 : turn + 1) {
       const uint32_t mid = lo + (hi - lo + 1) / 2;
       const int count = reach(mid, turn);
@@ -461,7 +469,7 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(BeamParams p) {
       if (to < kRoom) found[to] = c;
     };
 #pragma unroll 1
-    for (int at = tid; at < sampled; at += kThreads) {
+    for (int at = tid; at < sampled; at += THREADS) {
       if (sample[at] == 0 || value_of(sample[at]) < bound) continue;
       const int list = at / deep, first = at - list * deep;
       float logit;
@@ -489,13 +497,13 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(BeamParams p) {
   if (n > kRoom) {  // equal scores: bounded by the top-th best head itself
     __syncthreads();
     if (tid == 0) sh_count = 0, sh_bound = Cand{0, ~0u};
-    for (int i = tid; i < lists; i += kThreads) {
+    for (int i = tid; i < lists; i += THREADS) {
       float logit;
       uint32_t place;
       found[i] = entry(i, 0, keys[(long long)i * top], logit, place) ? exactly(logit, place) : Cand{0, ~0u};
     }
     __syncthreads();
-    for (int i = tid; i < lists; i += kThreads) {
+    for (int i = tid; i < lists; i += THREADS) {
       const Cand mine = found[i];
       int b = 0;
       for (int j = 0; j < lists; ++j) b += better(found[j], mine);
@@ -504,7 +512,7 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(BeamParams p) {
     __syncthreads();
     n = gather(&sh_bound);
   }
-  for (int i = tid; i < n; i += kThreads) {
+  for (int i = tid; i < n; i += THREADS) {
     const Cand mine = found[i];
     int b = 0;
 #pragma unroll 4
@@ -578,12 +586,18 @@ template <typename T, bool ALIGNED, int VEC>
 cudaError_t select(const BeamParams &p, cudaStream_t stream) {
   const size_t rows = sizeof(uint64_t) * (size_t)p.top * (Values<T, ALIGNED, VEC>::MOST + 1);
   constexpr size_t join = sizeof(Cand) * kRoom + sizeof(uint32_t) * kSample;
-  static std::atomic<uint64_t> allowed{0};
-  cudaError_t err = allow_smem(beam_join_kernel, join, allowed);
+  const int lists = p.beams * p.parts;
+  static std::atomic<uint64_t> allowed{0}, allowed_wide{0};
+  // A CTA of 256 threads walks up to four sampled entries a thread as fast as one of 1024 (2 x 4 beams of 32000, 64 entries:
+  // 7.9 against 8.9 us a call; 16 beams of 32000, 1024: 11.2, 11.4); with more it is slower (64 beams of 32000, 8 best,
+  // 2048: 13.7, 12.2; 4 x 48 of 99999, 48 best, 4032: 48.1, 42.7).
+  const bool wide = lists * sampled_of(lists, p.top) > 1024;
+  cudaError_t err = wide ? allow_smem(beam_join_kernel<1024>, join, allowed_wide) : allow_smem(beam_join_kernel<256>, join, allowed);
   if (err == cudaSuccess)
     err = launch_dependent(beam_rows_kernel<T, ALIGNED, VEC>, (unsigned)(p.groups * p.beams * p.parts), kThreads, rows, stream, 1, p);
   if (err != cudaSuccess) return err;
-  return launch_dependent(beam_join_kernel, (unsigned)p.groups, kThreads, join, stream, 1, p);
+  return wide ? launch_dependent(beam_join_kernel<1024>, (unsigned)p.groups, 1024, join, stream, 1, p)
+              : launch_dependent(beam_join_kernel<256>, (unsigned)p.groups, 256, join, stream, 1, p);
 }
 template <typename T>
 cudaError_t by_alignment(const BeamParams &p, cudaStream_t stream) {

@@ -92,6 +92,32 @@ def test_select_orders(dtype, vocab, kind):
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("beams,top", [(16, 16), (32, 32), (64, 17), (64, 64)])
+@pytest.mark.parametrize("kind", ["any", "constant", "equal rows", "some finished or dead", "one ahead"])
+def test_select_many_lists(dtype, beams, top, kind):
+    """As many sampled entries of lists as a request can have, in the orders that are worst for a bound."""
+    vocab = 40000
+    g = torch.Generator(device="cuda").manual_seed(beams + top)
+    x = torch.randn(2, beams, vocab, generator=g, device="cuda") * 2
+    s = -9 * torch.rand(2, beams, generator=g, device="cuda")
+    fin = None
+    if kind == "constant":
+        x.fill_(0.75)
+        s.fill_(-2.0)
+    elif kind == "equal rows":
+        x[:] = x[0, 0]
+    elif kind == "some finished or dead":
+        fin = torch.rand(2, beams, generator=g, device="cuda") < 0.5
+        fin[1, 1:] = True
+        s[0, 1::5] = -math.inf
+        x[0, 2::7, 11] = math.nan
+    elif kind == "one ahead":
+        s -= 100
+        s[:, beams // 2] = 0
+    check(x.to(dtype), s, top, finished=fin, pad=7)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 def test_select_nothing_left(dtype):
     """Forbidden tokens, finished and dead beams, rows that are not finite."""
     vocab = 3000
