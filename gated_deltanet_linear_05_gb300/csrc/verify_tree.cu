@@ -51,7 +51,7 @@ struct TreeCfg {
   static constexpr int CHUNK = 2 * C * 128;             // 64 columns of [Q; K]
   // Chunks in shared memory at a time.  f32 rows of 32 and 64 nodes have 48 and 96 KB of terms, which leave an SM two
   // CTAs and one: their chunks come one after the other, the second once more for the state's products, and v straight
-  // to registers (24 trees of 40 to 64 nodes 124 -> 86 us, 64 of 11 to 32 96 -> 86; 64 of 8 to 16 50 -> 57: not there).
+  // to registers (24 trees of 40 to 64 nodes 124 -> 86 us, 64 of 11 to 32 96 -> 88; 64 of 8 to 16 50 -> 57: not there).
   static constexpr int HALVES = TERMS == 3 && C >= 32 ? 1 : 2;
   static constexpr int QK = TERMS * HALVES * CHUNK;
   static constexpr int WT_TERM = 2 * C * C * 2;         // a term of [W; T]
@@ -65,10 +65,14 @@ struct TreeCfg {
   static constexpr int SMEM = 1024 + (USED > GRAM ? USED : GRAM);
   static constexpr int A_COL = 2 * C, A_COLS = 3 * C / 2 > 48 ? 3 * C / 2 : 48;  // tensor memory: after D^T
   static constexpr int COLS = A_COL + A_COLS <= 128 ? 128 : 256;
+  // The halves' Gram products stay apart until they are added in registers, the second's in the columns of A: on top of the
+  // first's, the small terms of the second would be cut to its size (o at 32 and 64 nodes 8.0e-7 and 7.5e-7 of its rms
+  // off, against 4.8e-7 and 3.2e-7 so).
+  static_assert(HALVES == 2 || 4 * C <= COLS, "columns of the second half's Gram products");
   static constexpr int TREE_WARPS = C == 64 ? 2 : 1;
   static constexpr int THREADS = kColumns + 32 * TREE_WARPS;
   // CTAs on an SM by shared and by tensor memory; three where a fourth takes too many registers from the
-  // reloading of chunks (86 for 89 us; without it, at C = 16, 52 for 50)
+  // reloading of chunks (3 us of 64 trees of 11 to 32; without it, at C = 16, 52 for 50)
   static constexpr int FIT = 227 * 1024 / (SMEM + 4096), MOST = HALVES == 1 && COLS == 128 ? 3 : 512 / COLS;
   static constexpr int CTAS = FIT < MOST ? FIT : MOST;
 };
@@ -154,6 +158,7 @@ template <typename T, typename TO, int C>
 __global__ void __launch_bounds__(TreeCfg<T, C>::THREADS, TreeCfg<T, C>::CTAS) verify_tree_kernel(TreeParams p) {
   using F = TreeCfg<T, C>;
   constexpr int kTree = 32 * F::TREE_WARPS;
+  constexpr int kGramRead = kTree + (F::HALVES == 1 ? kColumns : 32);  // threads at that barrier
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t above[C];    // a node's ancestors, itself among them
   __shared__ float2 path[C];       // G log2(e) in two floats
@@ -286,20 +291,21 @@ __global__ void __launch_bounds__(TreeCfg<T, C>::THREADS, TreeCfg<T, C>::CTAS) v
   const uint64_t tiles = tile_desc(uniform(smem_u32(smem)));
   constexpr uint32_t kChunk = F::CHUNK >> 4;
   constexpr uint32_t id_s = tc::idesc(128, 2 * C, 1, 0, 0);
-  // Gram products of the chunks in shared memory; by one thread
-  auto gram = [&](bool some) {
+  // Gram products of the chunks in shared memory, to tensor memory at `to`; by one thread
+  auto gram = [&](uint32_t to) {
+    bool some = false;
     const uint64_t keys = tiles + (C * 128 >> 4);
 #pragma unroll
     for (int x = F::TERMS == 1 ? kProducts - 1 : 0; x < kProducts; ++x)
 #pragma unroll
       for (int i = 0; i < F::HALVES * 4; ++i, some = true)
-        tc::mma_ss(tmem, keys + (kTermA[x] * F::HALVES + i / 4) * kChunk + (i % 4) * 2,
+        tc::mma_ss(to, keys + (kTermA[x] * F::HALVES + i / 4) * kChunk + (i % 4) * 2,
                    tiles + (kTermB[x] * F::HALVES + i / 4) * kChunk + (i % 4) * 2, id_s, some);
     tc::commit(&bar_gram);
   };
   if (F::HALVES == 1 && t_n > 0) {  // the second half's, then the first half in its place
     if (warp == 4) {
-      if (elect_one()) gram(false);
+      if (elect_one()) gram(tmem);
       __syncwarp();
     }
     put_rows(0, F::THREADS, [&] { wait_bar(&bar_gram, 0, dead, p.err); });
@@ -311,7 +317,7 @@ __global__ void __launch_bounds__(TreeCfg<T, C>::THREADS, TreeCfg<T, C>::CTAS) v
   if (t_n > 0 && warp >= 4) {
     // ---------------------------------------------------------------- the tree
     if (warp == 4) {
-      if (elect_one()) gram(F::HALVES == 1);
+      if (elect_one()) gram(F::HALVES == 1 ? tmem + 2 * C : tmem);
       __syncwarp();
     }
     wait_bar(&bar_gram, F::HALVES == 1 ? 1 : 0, dead, p.err);
@@ -325,6 +331,19 @@ __global__ void __launch_bounds__(TreeCfg<T, C>::THREADS, TreeCfg<T, C>::CTAS) v
       tc::wait_ld();
       tie(x);
       tie(y);
+      if (F::HALVES == 1) {
+        uint32_t x2[8], y2[8];
+        ld8(lanes + 2 * C + t0, x2);
+        ld8(lanes + 3 * C + t0, y2);
+        tc::wait_ld();
+        tie(x2);
+        tie(y2);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          x[i] = __float_as_uint(__uint_as_float(x[i]) + __uint_as_float(x2[i]));
+          y[i] = __float_as_uint(__uint_as_float(y[i]) + __uint_as_float(y2[i]));
+        }
+      }
       float a[8], b[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
@@ -344,7 +363,7 @@ __global__ void __launch_bounds__(TreeCfg<T, C>::THREADS, TreeCfg<T, C>::CTAS) v
       }
     }
     tc::fence_before();
-    bar_arrive(1, kTree + 32);  // D^T's columns are free
+    bar_arrive(1, kGramRead);  // D^T's columns are free, and A's
     bar_sync(3, kTree);
     // column j of T and W, 16 nodes at a time; they take the place of the factors that have been used
 #pragma unroll 1
@@ -398,6 +417,10 @@ __global__ void __launch_bounds__(TreeCfg<T, C>::THREADS, TreeCfg<T, C>::CTAS) v
             uint32_t w[kKeys / 2];
 #pragma unroll
             for (int i = 0; i < kKeys / 2; ++i) w[i] = take_bf16(x[2 * i], x[2 * i + 1]);
+            if (F::HALVES == 1 && term == 0 && c == 0) {
+              bar_sync(1, kGramRead);
+              tc::fence_after();
+            }
             if (term == 0 && c > 0) {  // the products of the step before have read their operand
               wait_bar(&bar_out, (c - 1) & 1, dead, p.err);
               tc::fence_after();
@@ -412,7 +435,7 @@ __global__ void __launch_bounds__(TreeCfg<T, C>::THREADS, TreeCfg<T, C>::CTAS) v
           tc::fence_before();
           bar_sync(2, kColumns);
           if (warp == 0) {
-            if (c == 0) bar_sync(1, kTree + 32);  // the Gram products have been read
+            if (F::HALVES == 2 && c == 0) bar_sync(1, kGramRead);  // the Gram products have been read
             tc::fence_after();
             if (elect_one()) {
               uint32_t some = c > 0;
@@ -433,7 +456,7 @@ __global__ void __launch_bounds__(TreeCfg<T, C>::THREADS, TreeCfg<T, C>::CTAS) v
       wait_bar(&bar_s, 0, dead, p.err);
       tc::fence_after();
     } else {
-      if (warp == 0) bar_sync(1, kTree + 32);
+      if (F::HALVES == 1 || warp == 0) bar_sync(1, kGramRead);
       bar_sync(2, kColumns);
       tc::fence_after();
     }
