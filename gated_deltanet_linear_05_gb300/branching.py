@@ -128,6 +128,8 @@ def _select_plan(logits, scores, top, finished, pad_token):
     row = st[1] if beams > 1 else st[0] if groups > 1 else vocab
     if (vocab > 1 and st[2] != 1) or (groups > 1 and st[0] != beams * row):
         raise ValueError("the rows of logits must be contiguous, and at equal distances")
+    if row < vocab:  # (several rows: expanded logits, or views that overlap)
+        raise ValueError("the rows of logits must not lie over each other (expanded logits: give a copy)")
     for what, t, dtype in (("scores", scores, _F32), ("finished", finished, torch.bool)):
         if t is not None and (t.dtype is not dtype or t.shape != (groups, beams)):
             raise ValueError("%s must be %s of shape %s" % (what, dtype, (groups, beams)))
@@ -138,10 +140,11 @@ def _select_plan(logits, scores, top, finished, pad_token):
 def gdn_beam_select(logits, scores, top: int, finished=None, pad_token: int = 0, scores_out=None,
                     parents=None, tokens=None, workspace=None, stream=None):
     """The `top` best continuations of each group's beams by scores + log_softmax(logits): logits
-    [G, W, V] bf16 or fp32 (rows at equal distances), scores [G, W] fp32, finished [G, W] bool or
-    None (a finished beam goes on with pad_token and keeps its score).  Returns (scores [G, top]
-    fp32, parents [G, top] int32, tokens [G, top] int32), best first, equal ones in order of beam
-    and token.  workspace: from gdn_beam_workspace (None: a fresh one)."""
+    [G, W, V] bf16 or fp32 (rows at equal distances of at least V, so no expanded ones), scores
+    [G, W] fp32, finished [G, W] bool or None (a finished beam goes on with pad_token and keeps its
+    score).  Returns (scores [G, top] fp32, parents [G, top] int32, tokens [G, top] int32), best
+    first, equal ones in order of beam and token.  workspace: from gdn_beam_workspace (None: a
+    fresh one)."""
     if stream is not None:
         with torch.cuda.stream(stream):
             return gdn_beam_select(logits, scores, top, finished, pad_token, scores_out, parents, tokens,
