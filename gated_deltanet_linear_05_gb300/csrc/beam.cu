@@ -10,9 +10,9 @@ namespace {
 
 // ------------------------------------------------------------------ selection
 //
-// s(w, x) = score_w + logit_wx - lse_w.  Within a beam the order is the logits', so one pass over a
-// row finds its maximum, its sum of powers and its `top` best logits without the sum being known; the
-// second kernel puts the beams together.
+// s(w, x) = score_w + (logit_wx - m_w) - ln l_w, with m_w the row's maximum and l_w its sum of exp(logit - m_w).  Within a
+// beam the order is the logits', so one pass over a row finds its maximum, its sum of powers and its `top` best
+// logits without the sum being known; the second kernel puts the beams together.
 //
 // Pass 1: a CTA takes a part of a row, in steps of 256 threads x MOST values, the next step's loads under way
 // while this one's are looked at.  A thread keeps its own m and l with one rescaling a step.  What may still be
@@ -320,13 +320,14 @@ __device__ __forceinline__ uint64_t pick(const uint64_t (&x)[8], int i) {
 
 template <int THREADS>
 __global__ void __launch_bounds__(THREADS) beam_join_kernel(BeamParams p) {
-  __shared__ double lse[64];    // of a beam (dead or finished: 0)
+  __shared__ double ln_sum[64];   // of a beam (dead or finished: 0)
+  __shared__ float peak[64];      // its largest logit (dead or finished: 0)
   __shared__ float score_of[64];  // (dead: 0)
-  __shared__ float shift[64];     // score less lse, for the bound
+  __shared__ float shift[64];     // score less ln_sum, for the bound
   __shared__ int kind[64];      // 0: as the logits say; 1: every continuation -inf; 2: finished
   __shared__ uint32_t sh_range[2][THREADS / 32];
   __shared__ Cand sh_bound;
-  __shared__ int sh_count, sh_sum[3], sh_widest;  // widest: the largest |score| + |lse|, as its float's bits
+  __shared__ int sh_count, sh_sum[3], sh_widest;  // widest: the largest |shift|, as its float's bits
   extern __shared__ uint64_t raw[];
   const int tid = threadIdx.x, group = blockIdx.x, w_n = p.beams, parts = p.parts, top = p.top;
   const int lists = w_n * parts, deep = sampled_of(lists, top);
@@ -368,12 +369,13 @@ __global__ void __launch_bounds__(THREADS) beam_join_kernel(BeamParams p) {
     }
     if (here && (tid & 3) == 0) {
       const bool alive = isfinite(score) && l > 0.f && isfinite(l) && isfinite(m);
-      const double sum = alive && !done ? (double)m + log_of(l, low) : 0.0;
-      lse[w] = sum;
+      const double ln = alive && !done ? log_of(l, low) : 0.0;
+      ln_sum[w] = ln;
+      peak[w] = alive && !done ? m : 0.f;
       score_of[w] = done || alive ? score : 0.f;
-      shift[w] = score_of[w] - (float)sum;
+      shift[w] = (float)((double)score_of[w] - ln);
       kind[w] = done ? 2 : alive ? 0 : 1;
-      atomicMax(&sh_widest, __float_as_int(fabsf(score_of[w]) + fabsf((float)sum)));
+      atomicMax(&sh_widest, __float_as_int(fabsf(shift[w])));
     }
   }
   __syncthreads();
@@ -401,12 +403,16 @@ __global__ void __launch_bounds__(THREADS) beam_join_kernel(BeamParams p) {
     place = base + (uint32_t)i;
     return i < p.vocab;
   };
-  // (the first sum is exact but for far exponents, so that beams of equal rows tie where score and logit do)
+  // The maximum is taken off first: a row far from 0, as a mask of the lowest value leaves it, would swallow score and
+  // logarithm.  (Difference and sum are exact but for far exponents, so that beams of equal rows tie where score and logit do.)
   auto exactly = [&](float logit, uint32_t place) {
     const int w = place / (uint32_t)p.vocab;
-    return Cand{image(((double)score_of[w] + (double)logit) - lse[w]), place};
+    return Cand{image(((double)score_of[w] + ((double)logit - (double)peak[w])) - ln_sum[w]), place};
   };
-  auto about = [&](int list, float logit) { return shift[list / parts] + logit; };
+  auto about = [&](int list, float logit) {
+    const int w = list / parts;
+    return shift[w] + (logit - peak[w]);
+  };
   // (loops stay rolled but for a few loads side by side: a kernel this short waits for its instructions)
   uint32_t *sample = reinterpret_cast<uint32_t *>(found + kRoom), most = 0;  // [kSample]
   const int sampled = lists * deep;
@@ -457,9 +463,10 @@ __global__ void __launch_bounds__(THREADS) beam_join_kernel(BeamParams p) {
       if (count >= top && count <= enough) break;
     }
   }
-  // (a score in float32 is off by three roundings of 2^-24)
+  // (a score in float32 is off by three roundings of 2^-24, of shift, difference and sum: by 2^-23 (|score| + |shift|), which
+  // both that of `low` and one at the bound may be, 2.4e-7 in all; 1e-13: float64's own, ln V 2^-53 at most)
   const float low = lo == 0 ? -CUDART_INF_F : value_of(lo);
-  const float bound = low > -CUDART_INF_F ? low - (3.6e-7f * (fabsf(low) + __int_as_float(sh_widest)) + 1e-30f) : low;
+  const float bound = low > -CUDART_INF_F ? low - (3.6e-7f * (fabsf(low) + __int_as_float(sh_widest)) + 1e-13f) : low;
   // What reaches the bound and is no worse than `least`.
   auto gather = [&](const Cand *least) {
     auto put = [&](float logit, uint32_t place) {

@@ -646,7 +646,8 @@ typedef struct {
  * A continuation of probability 0 (a logit of -inf), all of a beam whose score is -inf or NaN or
  * +inf, or whose logits hold NaN or +inf or nothing but -inf, and all but one of a finished beam's
  * count as -inf: they come after the others, in order of beam and token.
- * Scores are compared in float64; the powers are summed in float32 (a few hundred at a time) and
+ * Scores are compared in float64, the row's largest logit taken off each before the beam's score is
+ * added (a row far from 0 loses nothing); the powers are summed in float32 (a few hundred at a time) and
  * then in float64.  A request's results do not depend on the others.  A level of a tree of drafts
  * is grown the same way (W = 1 at its root).
  * workspace: gdn_beam_workspace_size(shape) bytes, 256-byte aligned; it may hold anything.  Calls
