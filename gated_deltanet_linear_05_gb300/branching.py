@@ -105,7 +105,7 @@ def gdn_beam_workspace_size(shape: GdnBeamShape) -> int:
 
 
 def gdn_beam_workspace(num_groups: int, beams: int, vocab: int, top: int, device="cuda"):
-    """A workspace for gdn_beam_select at these sizes, for logits of either type, to be kept and
+    """A workspace for gdn_beam_select up to these sizes, for logits of either type, to be kept and
     given to every call (one per stream)."""
     size = max(gdn_beam_workspace_size(make_beam_shape(num_groups, beams, vocab, top, dtype))
                for dtype in (GDN_BF16, GDN_F32))

@@ -533,12 +533,18 @@ __global__ void __launch_bounds__(THREADS) beam_join_kernel(BeamParams p) {
   }
 }
 
+// Lists that are made of `rows` rows at most, whatever their length: eight waves of CTAs, which the cost below seldom wants
+// more than, and two a row.  A workspace's size goes by this, not by the parts themselves: fewer rows have more
+// parts each, and a workspace must do for them too.
+long long most_lists(int rows, int slots) { return 2ll * rows + 8 * slots; }
+
 // Parts of a row, each of whole steps: the number that ends first if `slots` CTAs run at a time, the last of them
 // half a CTA's time longer than the rest, and a CTA's start and end take one and a half steps (64 x 8 rows of 150001,
 // 37 steps, in 1 to 5 parts: 61, 61, 56, 60, 63 us; 2 x 4 rows of 32000, 4 steps, in 1 to 4: 12.4, 10.1, 9.8,
 // 7.9; steps of a quarter of the size, and so more of them: 8.7); no more lists a request than the join takes.
 int parts_of(int rows, int beams, int vocab, int step, int slots) {
-  const int steps = (vocab + step - 1) / step, most = std::min(steps, kLists / beams);
+  const int steps = (vocab + step - 1) / step;
+  const int most = std::min<long long>(std::min(steps, kLists / beams), most_lists(rows, slots) / std::max(rows, 1));
   int best = 1;
   float least = 0.f;
   for (int parts = 1; parts <= most; ++parts) {
@@ -615,8 +621,15 @@ cudaError_t by_alignment(const BeamParams &p, cudaStream_t stream) {
 
 }  // namespace
 
+constexpr int step_of(bool bf16) { return kThreads * 4 * (bf16 ? 8 : 4); }
+constexpr int slots_of(bool bf16) { return kSms * (bf16 ? 3 : 4); }
+
 int beam_parts(int groups, int beams, int vocab, bool bf16) {
-  return parts_of(groups * beams, beams, vocab, kThreads * 4 * (bf16 ? 8 : 4), kSms * (bf16 ? 3 : 4));
+  return parts_of(groups * beams, beams, vocab, step_of(bf16), slots_of(bf16));
+}
+size_t beam_lists(int groups, int beams, int vocab, bool bf16) {
+  const long long steps = (vocab + step_of(bf16) - 1) / step_of(bf16);
+  return (size_t)std::min(groups * std::min(beams * steps, (long long)kLists), groups ? most_lists(groups * beams, slots_of(bf16)) : 0);
 }
 
 cudaError_t launch_beam_select(const BeamParams &p, gdn_dtype dtype, cudaStream_t stream) {

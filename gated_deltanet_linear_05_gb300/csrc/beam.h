@@ -21,6 +21,8 @@ struct BeamParams {
   uint64_t *keys;  // [row][part][top] the best logits
 };
 int beam_parts(int groups, int beams, int vocab, bool bf16);
+// (row, part) lists at most, which more requests, beams or vocabulary never make fewer
+size_t beam_lists(int groups, int beams, int vocab, bool bf16);
 cudaError_t launch_beam_select(const BeamParams &p, gdn_dtype dtype, cudaStream_t stream);
 
 struct ReorderParams {

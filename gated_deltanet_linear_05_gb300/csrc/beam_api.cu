@@ -32,9 +32,10 @@ gdn_status check_shape(const gdn_beam_shape *s) {
 int parts(const gdn_beam_shape *s) {
   return gdn::beam_parts(s->num_groups, s->beams, s->vocab, s->dtype == GDN_BF16);
 }
-size_t sums_bytes(const gdn_beam_shape *s) {
-  return ((size_t)s->num_groups * s->beams * parts(s) * sizeof(float2) + 255) / 256 * 256;
+size_t lists(const gdn_beam_shape *s) {
+  return gdn::beam_lists(s->num_groups, s->beams, s->vocab, s->dtype == GDN_BF16);
 }
+size_t sums_bytes(const gdn_beam_shape *s) { return (lists(s) * sizeof(float2) + 255) / 256 * 256; }
 
 }  // namespace
 
@@ -42,7 +43,7 @@ extern "C" {
 
 size_t gdn_beam_workspace_size(const gdn_beam_shape *shape) {
   if (check_shape(shape) != GDN_OK) return (size_t)-1;
-  return sums_bytes(shape) + (size_t)shape->num_groups * shape->beams * parts(shape) * shape->top * sizeof(uint64_t);
+  return sums_bytes(shape) + lists(shape) * shape->top * sizeof(uint64_t);
 }
 
 gdn_status gdn_beam_select(const gdn_beam_shape *shape, const void *logits, const float *scores,

@@ -657,7 +657,8 @@ gdn_status gdn_beam_select(const gdn_beam_shape *shape, const void *logits, cons
                            const uint8_t *finished, float *scores_out, int32_t *parents,
                            int32_t *tokens, void *workspace, size_t workspace_bytes, void *stream);
 
-/* Workspace bytes for gdn_beam_select; (size_t)-1 for an invalid shape. */
+/* Workspace bytes for gdn_beam_select (num_groups, beams, vocab, top and dtype decide; larger values of
+ * any of the first four never need less); (size_t)-1 for an invalid shape. */
 size_t gdn_beam_workspace_size(const gdn_beam_shape *shape);
 
 /*
