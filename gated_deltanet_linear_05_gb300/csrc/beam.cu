@@ -15,9 +15,11 @@ namespace {
 // logits without the sum being known; the second kernel puts the beams together.
 //
 // Pass 1: a CTA takes a part of a row, in steps of 256 threads x MOST values, the next step's loads under way
-// while this one's are looked at.  A thread keeps its own m and l with one rescaling a step.  What may still be
-// among the best is told by a limit: once `top` are kept the last of them, and where more threads than that
-// reach it, a value that at least `top` threads' largest reach, found by halving the range of their largest
+// while this one's are looked at.  Each step has its own maximum and sum of powers, in an order that does not go by the
+// parts, so that a request's scores are the same to the bit in any batch: the threads' go to shared memory, and eight
+// steps' at a time are put together by a warp each (64 x 8 rows of 150001 57.4 -> 58.9 us; by shuffles in each step 61.7).
+// What may still be among the best is told by a limit: once `top` are kept the last of them, and where more threads
+// than that reach it, a value that at least `top` threads' largest reach, found by halving the range of their largest
 // (a barrier that counts for each halving; some 8 of them in a part's first step, seldom any later).  Values that
 // pass are appended to a buffer in shared memory, and the k best of it found by counting how many are better.
 // Equal logits go by index: the keys there are (value, index) in 64 bits, all different.  Where equal values
@@ -27,8 +29,16 @@ namespace {
 // Bound by HBM (the logits are read once) where rows are many; by latency where they are few.
 
 constexpr int kThreads = 256;
+constexpr int kSumSteps = kThreads / 32;  // whose sums are put together at a time
 constexpr unsigned kAll = 0xffffffffu;
 constexpr float kLog2e = 1.4426950408889634f;
+
+// The largest of a warp's floats, NaN apart.
+__device__ __forceinline__ float warp_max(float x) {
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;\n" : "=f"(r) : "f"(x));
+  return r;
+}
 
 // Order-preserving images of floats (larger float, larger image; NaN as -inf, -0 as 0).
 __device__ __forceinline__ uint32_t image(float x) {
@@ -145,7 +155,6 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && ALIGNED ? 3 : 4) b
   __shared__ uint64_t heads[kThreads], sh_limit;
   __shared__ uint32_t sh_range[2][kThreads / 32];
   __shared__ int sh_count;
-  __shared__ float2 sums[kThreads / 32];
   extern __shared__ uint64_t buffer[];  // what may count: `kept` from before, then new ones
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int row = blockIdx.x / p.parts, part = blockIdx.x - row * p.parts, top = p.top, room = top * MOST;
@@ -155,10 +164,9 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && ALIGNED ? 3 : 4) b
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   if ((p.finished && p.finished[row]) || !isfinite(p.scores[row])) return;  // (its logits do not count)
   const T *x = static_cast<const T *>(p.logits) + (long long)row * p.row_stride;
-  const int steps = (p.vocab + STEP - 1) / STEP;  // of the row: parts take whole ones
+  const int steps = p.steps;  // of the row: parts take whole ones
   const int from = (int)((long long)steps * part / p.parts) * STEP;
   const int end = (int)min((long long)((long long)steps * (part + 1) / p.parts) * STEP, (long long)p.vocab);
-  float m = -CUDART_INF_F, l = 0.f;
   int kept = 0, late = 0;  // kept: in order; late: threads (at most) that have appended since
   float last = 0.f;        // of the `top` that are kept
   // The best of what is kept and what has been appended; after a barrier, and ends with one.
@@ -173,6 +181,24 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && ALIGNED ? 3 : 4) b
     last = kept == top ? value_of((uint32_t)(best[top - 1] >> 32)) : 0.f;
     __syncthreads();
   };
+  float2 *sums = reinterpret_cast<float2 *>(buffer + top * (MOST + 1));  // [kSumSteps + 1][kThreads], in turn: the step after those that are read has one of its own
+  // The sums of up to kSumSteps steps of the row, to `step`; after its barrier.
+  auto put_sums = [&](int step) {
+    const int mine = step / kSumSteps * kSumSteps + warp;
+    if (mine > step || mine * STEP < from) return;
+    const float2 *of = sums + mine % (kSumSteps + 1) * kThreads + lane;
+    float m = of[0].x;
+#pragma unroll 4
+    for (int i = 1; i < kThreads / 32; ++i) m = fmaxf(m, of[32 * i].x);
+    m = warp_max(m);
+    const float ref = m == -CUDART_INF_F ? 0.f : m;
+    float l = 0.f;
+#pragma unroll 4
+    for (int i = 0; i < kThreads / 32; ++i) l = fmaf(of[32 * i].y, ex2((of[32 * i].x - ref) * kLog2e), l);
+#pragma unroll 4
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(kAll, l, o);
+    if (lane == 0) p.sums[(long long)row * steps + mine] = make_float2(m, l);
+  };
   V y, ahead;
   ahead.load(x, from, end);
   __syncthreads();
@@ -185,19 +211,20 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && ALIGNED ? 3 : 4) b
     for (int i = 1; i < MOST; ++i) big = fmaxf(big, y[i]);
     // The differences are taken first: a product with log2 e less its own maximum's would put the
     // rounding of that maximum, up to 1e-6, into every power alike.
-    const float m1 = fmaxf(m, big), ref = m1 == -CUDART_INF_F ? 0.f : m1;
-    float sum = 0.f, sum2 = 0.f;
+    const int step = base / STEP;
+    const float ref = big == -CUDART_INF_F ? 0.f : big;
+    float sum[4];
 #pragma unroll
-    for (int i = 0; i < MOST; i += 2) {
-      sum += ex2((y[i] - ref) * kLog2e);
-      sum2 += ex2((y[i + 1] - ref) * kLog2e);
+    for (int i = 0; i < MOST; ++i) {
+      const float e = ex2((y[i] - ref) * kLog2e);
+      sum[i % 4] = i < 4 ? e : sum[i % 4] + e;
     }
-    l = l * ex2((m - ref) * kLog2e) + (sum + sum2);
-    m = m1;
+    sums[step % (kSumSteps + 1) * kThreads + tid] = make_float2(big, (sum[0] + sum[1]) + (sum[2] + sum[3]));
 
     // Threads with a value that may count.  Equal ones from here on come after those that are kept.
     auto may = [&]() { return kept < top ? V::index(base, 0) < end : big > last; };
     int busy = __syncthreads_count(may());
+    if (step % kSumSteps == kSumSteps - 1) put_sums(step);
     if (busy == 0) continue;
     if (late > 0 && late + busy > top) {  // (the buffer holds all values of `top` threads)
       settle();
@@ -252,25 +279,10 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && ALIGNED ? 3 : 4) b
     }
     settle();
   }
+  const int last_step = (end - 1) / STEP;
+  if (last_step % kSumSteps != kSumSteps - 1) put_sums(last_step);
   __syncthreads();
   if (late > 0) settle();
-  // the part's maximum, sum of powers and best
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const float m2 = __shfl_xor_sync(kAll, m, o), l2 = __shfl_xor_sync(kAll, l, o), m1 = fmaxf(m, m2);
-    const float ref = m1 == -CUDART_INF_F ? 0.f : m1;
-    l = l * ex2((m - ref) * kLog2e) + l2 * ex2((m2 - ref) * kLog2e);
-    m = m1;
-  }
-  if (lane == 0) sums[warp] = make_float2(m, l);
-  __syncthreads();
-  if (tid == 0) {
-    for (int i = 1; i < kThreads / 32; ++i) m = fmaxf(m, sums[i].x);
-    const float ref = m == -CUDART_INF_F ? 0.f : m;
-    l = 0.f;
-    for (int i = 0; i < kThreads / 32; ++i) l += sums[i].y * ex2((sums[i].x - ref) * kLog2e);
-    p.sums[blockIdx.x] = make_float2(m, l);
-  }
   if (tid < top) p.keys[(long long)blockIdx.x * top + tid] = best[tid];
 }
 
@@ -336,16 +348,29 @@ __global__ void __launch_bounds__(THREADS) beam_join_kernel(BeamParams p) {
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   if (tid == 0) sh_count = sh_widest = sh_sum[0] = sh_sum[1] = sh_sum[2] = 0;
   __syncthreads();
-  {  // four threads a beam
-    const int w = tid >> 2, row = group * w_n + w;
+  // Beams' sums, by threads enough for four steps each (32 at most): what is added in which order goes by the steps
+  // alone, not by the threads that the kernel has.
+  const int steps = p.steps;
+  const int log_per = steps <= 16 ? 2 : steps <= 32 ? 3 : steps <= 64 ? 4 : 5, per = 1 << log_per, turn = tid & (per - 1);
+#pragma unroll 1
+  for (int w0 = 0; w0 < w_n; w0 += THREADS >> log_per) {
+    const int w = w0 + (tid >> log_per), row = group * w_n + w;
+    const float2 *sums = p.sums + (long long)row * steps;
     const bool here = w < w_n;
     const float score = here ? p.scores[row] : 0.f;
     const bool done = here && isfinite(score) && p.finished && p.finished[row];
     float m = -CUDART_INF_F;
+    float2 some[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int i = turn + u * per;
+      some[u] = here && i < steps ? sums[i] : make_float2(-CUDART_INF_F, 0.f);
+      m = fmaxf(m, some[u].x);
+    }
 #pragma unroll 4
-    for (int i = tid & 3; here && i < parts; i += 4) m = fmaxf(m, p.sums[(long long)row * parts + i].x);
-    m = fmaxf(m, __shfl_xor_sync(kAll, m, 1));
-    m = fmaxf(m, __shfl_xor_sync(kAll, m, 2));
+    for (int i = turn + 4 * per; here && i < steps; i += per) m = fmaxf(m, sums[i].x);
+#pragma unroll 1
+    for (int o = 1; o < per; o <<= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, o));
     const float ref = m == -CUDART_INF_F ? 0.f : m;
     float l = 0.f, low = 0.f;  // the sum in two floats
     auto add = [&](float x) {
@@ -353,13 +378,15 @@ __global__ void __launch_bounds__(THREADS) beam_join_kernel(BeamParams p) {
       low += (l - (y - z)) + (x - z);
       l = y;
     };
-#pragma unroll 4
-    for (int i = tid & 3; here && i < parts; i += 4) {
-      const float2 s = p.sums[(long long)row * parts + i];
-      add(s.y * expf(s.x - ref));
-    }
 #pragma unroll
-    for (int o = 1; o < 4; o <<= 1) {
+    for (int u = 0; u < 4; ++u) add(some[u].y * ex2((some[u].x - ref) * kLog2e));
+#pragma unroll 1
+    for (int i = turn + 4 * per; here && i < steps; i += per) {
+      const float2 s = sums[i];
+      add(s.y * ex2((s.x - ref) * kLog2e));
+    }
+#pragma unroll 1
+    for (int o = 1; o < per; o <<= 1) {
       const float x = __shfl_xor_sync(kAll, l, o), y = __shfl_xor_sync(kAll, low, o);
       // (both sides add the same two in the same order)
       const bool first = (tid & o) == 0;
@@ -367,7 +394,7 @@ __global__ void __launch_bounds__(THREADS) beam_join_kernel(BeamParams p) {
       low = low + y + ((a - (sum - z)) + (b - z));
       l = sum;
     }
-    if (here && (tid & 3) == 0) {
+    if (here && turn == 0) {
       const bool alive = isfinite(score) && l > 0.f && isfinite(l) && isfinite(m);
       const double ln = alive && !done ? log_of(l, low) : 0.0;
       ln_sum[w] = ln;
@@ -596,16 +623,24 @@ __global__ void __launch_bounds__(128) reorder_kernel(ReorderParams p) {
 }
 
 template <typename T, bool ALIGNED, int VEC>
-cudaError_t select(const BeamParams &p, cudaStream_t stream) {
-  const size_t rows = sizeof(uint64_t) * (size_t)p.top * (Values<T, ALIGNED, VEC>::MOST + 1);
+cudaError_t select(const BeamParams &given, cudaStream_t stream) {
+  constexpr int STEP = Values<T, ALIGNED, VEC>::MOST * kThreads;
+  static_assert(STEP >= kBeamStep, "a place in the workspace for each step's sums");
+  BeamParams p = given;
+  p.steps = (p.vocab + STEP - 1) / STEP;
+  auto rows_smem = [](int top) {
+    return sizeof(uint64_t) * (size_t)top * (Values<T, ALIGNED, VEC>::MOST + 1) + sizeof(float2) * (kSumSteps + 1) * kThreads;
+  };
+  const size_t rows = rows_smem(p.top);
   constexpr size_t join = sizeof(Cand) * kRoom + sizeof(uint32_t) * kSample;
   const int lists = p.beams * p.parts;
-  static std::atomic<uint64_t> allowed{0}, allowed_wide{0};
+  static std::atomic<uint64_t> allowed{0}, allowed_wide{0}, allowed_rows{0};
   // A CTA of 256 threads walks up to four sampled entries a thread as fast as one of 1024 (2 x 4 beams of 32000, 64 entries:
   // 7.9 against 8.9 us a call; 16 beams of 32000, 1024: 11.2, 11.4); with more it is slower (64 beams of 32000, 8 best,
   // 2048: 13.7, 12.2; 4 x 48 of 99999, 48 best, 4032: 48.1, 42.7).
   const bool wide = lists * sampled_of(lists, p.top) > 1024;
   cudaError_t err = wide ? allow_smem(beam_join_kernel<1024>, join, allowed_wide) : allow_smem(beam_join_kernel<256>, join, allowed);
+  if (err == cudaSuccess) err = allow_smem(beam_rows_kernel<T, ALIGNED, VEC>, rows_smem(64), allowed_rows);
   if (err == cudaSuccess)
     err = launch_dependent(beam_rows_kernel<T, ALIGNED, VEC>, (unsigned)(p.groups * p.beams * p.parts), kThreads, rows, stream, 1, p);
   if (err != cudaSuccess) return err;

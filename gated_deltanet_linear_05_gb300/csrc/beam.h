@@ -10,16 +10,17 @@
 namespace gdn {
 
 struct BeamParams {
-  int groups, beams, vocab, top, pad_token, parts;
+  int groups, beams, vocab, top, pad_token, parts, steps;  // steps: set by the launch
   long long row_stride;
   const void *logits;
   const float *scores;
   const uint8_t *finished;
   float *scores_out;
   int32_t *parents, *tokens;
-  float2 *sums;    // [row][part] maximum and sum of powers
+  float2 *sums;    // [row][step] maximum and sum of powers
   uint64_t *keys;  // [row][part][top] the best logits
 };
+constexpr int kBeamStep = 4096;  // tokens of a step at least
 int beam_parts(int groups, int beams, int vocab, bool bf16);
 // (row, part) lists at most, which more requests, beams or vocabulary never make fewer
 size_t beam_lists(int groups, int beams, int vocab, bool bf16);

@@ -35,7 +35,10 @@ int parts(const gdn_beam_shape *s) {
 size_t lists(const gdn_beam_shape *s) {
   return gdn::beam_lists(s->num_groups, s->beams, s->vocab, s->dtype == GDN_BF16);
 }
-size_t sums_bytes(const gdn_beam_shape *s) { return (lists(s) * sizeof(float2) + 255) / 256 * 256; }
+size_t sums_bytes(const gdn_beam_shape *s) {
+  const size_t steps = ((size_t)s->vocab + gdn::kBeamStep - 1) / gdn::kBeamStep;
+  return ((size_t)s->num_groups * s->beams * steps * sizeof(float2) + 255) / 256 * 256;
+}
 
 }  // namespace
 

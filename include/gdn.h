@@ -647,9 +647,11 @@ typedef struct {
  * +inf, or whose logits hold NaN or +inf or nothing but -inf, and all but one of a finished beam's
  * count as -inf: they come after the others, in order of beam and token.
  * Scores are compared in float64, the row's largest logit taken off each before the beam's score is
- * added (a row far from 0 loses nothing); the powers are summed in float32 (a few hundred at a time) and
- * then in float64.  A request's results do not depend on the others.  A level of a tree of drafts
- * is grown the same way (W = 1 at its root).
+ * added (a row far from 0 loses nothing).  Powers are summed in float32 over 4096 or 8192 tokens at a
+ * time, those sums in two floats: a score's error, 2.5e-6 at most beside its rounding, does not grow
+ * with V.  A request's results depend neither on the others nor on their number, to the bit; but
+ * where all rows start at multiples of 16 bytes, powers are added in another order than elsewhere.  A
+ * level of a tree of drafts is grown the same way (W = 1 at its root).
  * workspace: gdn_beam_workspace_size(shape) bytes, 256-byte aligned; it may hold anything.  Calls
  * sharing a workspace must not overlap on the GPU.  Two launches.
  */
