@@ -649,7 +649,8 @@ cudaError_t select(const BeamParams &given, cudaStream_t stream) {
 }
 template <typename T>
 cudaError_t by_alignment(const BeamParams &p, cudaStream_t stream) {
-  const bool aligned = reinterpret_cast<uintptr_t>(p.logits) % 16 == 0 && p.row_stride % (16 / (int)sizeof(T)) == 0;
+  const bool alone = p.groups * p.beams == 1;  // (its stride says nothing)
+  const bool aligned = reinterpret_cast<uintptr_t>(p.logits) % 16 == 0 && (alone || p.row_stride % (16 / (int)sizeof(T)) == 0);
   // (single values of 16 bits take a register each: half as many)
   return aligned ? select<T, true, 4>(p, stream) : select<T, false, sizeof(T) == 2 ? 2 : 4>(p, stream);
 }

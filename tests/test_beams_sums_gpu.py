@@ -24,6 +24,21 @@ def test_a_request_alone_and_in_a_batch(dtype, groups, beams, vocab, top):
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("pad", [0, 5, 8])
+def test_a_row_alone_and_among_others(dtype, pad):
+    """A row's order of sums goes by where it starts, also where its stride has no meaning: of the rows here some or all
+    start at multiples of 16 bytes."""
+    buf = torch.randn(64, 1, 20011 + pad, generator=torch.Generator(device="cuda").manual_seed(6), device="cuda").to(dtype)
+    x, s = buf[..., :20011], torch.zeros(64, 1, device="cuda")
+    every = gdn.gdn_beam_select(x, s, 64)
+    for i in range(64):
+        start = x[i].data_ptr() % 16
+        if pad == 5 or start:  # 20016: every row starts at a multiple of 16 bytes
+            assert start == 0 or pad != 5
+            assert all(torch.equal(a[0], b[i]) for a, b in zip(gdn.gdn_beam_select(x[i:i + 1], s[i:i + 1], 64), every))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("groups,beams,vocab", [(1, 1, 1 << 24), (3, 2, (1 << 22) + 1), (500, 1, 1 << 20), (150, 32, 131072)])
 @pytest.mark.parametrize("kind", ["flat", "rising", "falling", "normal"])
 def test_long_rows(dtype, groups, beams, vocab, kind):
