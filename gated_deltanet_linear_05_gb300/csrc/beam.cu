@@ -565,10 +565,13 @@ __global__ void __launch_bounds__(THREADS) beam_join_kernel(BeamParams p) {
 // parts each, and a workspace must do for them too.
 long long most_lists(int rows, int slots) { return 2ll * rows + 8 * slots; }
 
-// Parts of a row, each of whole steps: the number that ends first if `slots` CTAs run at a time, the last of them
-// half a CTA's time longer than the rest, and a CTA's start and end take one and a half steps (64 x 8 rows of 150001,
-// 37 steps, in 1 to 5 parts: 61, 61, 56, 60, 63 us; 2 x 4 rows of 32000, 4 steps, in 1 to 4: 12.4, 10.1, 9.8,
-// 7.9; steps of a quarter of the size, and so more of them: 8.7); no more lists a request than the join takes.
+// Parts of a row, each of whole steps: the number that by its cost ends first if `slots` CTAs run at a time, the last of
+// them half a CTA's time longer than the rest, and a CTA's start and end take one and a half steps; no more lists a
+// request than the join takes.  In 1, 2, ... parts: 64 x 8 rows of 150001 in f32 (37 steps) 61.6, 60.1, 55.8, 58.7,
+// 62.7 us, of which it takes 4, not the best; 64 x 8 of 151936 in bf16 (19 steps) 55.6, 55.4, 60.5, of which 2; 4 x 48 of
+// 99999 52.7, 45.7, 43.8, 50.1, of which 3; 2 x 4 of 32000 (4 steps) 11.9, 10.1, 9.3, 8.1, of which 4.  It does not
+// go by where rows start: for bf16 it counts steps of 8192 tokens and three CTAs an SM, also where rows that start
+// anywhere are read in steps of 4096 by four.
 int parts_of(int rows, int beams, int vocab, int step, int slots) {
   const int steps = (vocab + step - 1) / step;
   const int most = std::min<long long>(std::min(steps, kLists / beams), most_lists(rows, slots) / std::max(rows, 1));
@@ -636,8 +639,8 @@ cudaError_t select(const BeamParams &given, cudaStream_t stream) {
   const int lists = p.beams * p.parts;
   static std::atomic<uint64_t> allowed{0}, allowed_wide{0}, allowed_rows{0};
   // A CTA of 256 threads walks up to four sampled entries a thread as fast as one of 1024 (2 x 4 beams of 32000, 64 entries:
-  // 7.9 against 8.9 us a call; 16 beams of 32000, 1024: 11.2, 11.4); with more it is slower (64 beams of 32000, 8 best,
-  // 2048: 13.7, 12.2; 4 x 48 of 99999, 48 best, 4032: 48.1, 42.7).
+  // 8.1 against 9.3 us a call; 16 beams of 32000, 1024: 11.2, 11.8); with more it is slower (64 beams of 32000, 8 best,
+  // 2048: 13.8, 12.7; 4 x 48 of 99999, 48 best, 4032: 50.7, 43.9).
   const bool wide = lists * sampled_of(lists, p.top) > 1024;
   cudaError_t err = wide ? allow_smem(beam_join_kernel<1024>, join, allowed_wide) : allow_smem(beam_join_kernel<256>, join, allowed);
   if (err == cudaSuccess) err = allow_smem(beam_rows_kernel<T, ALIGNED, VEC>, rows_smem(64), allowed_rows);
